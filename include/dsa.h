@@ -84,7 +84,8 @@ typedef enum dsa_status {
     DSA_ERR_TIMEOUT = 5,     /* device: a bounded wait inside a kernel expired */
     DSA_ERR_BAD_BATCH = 6,   /* device: q_off / ctx_len outside the host bounds */
     DSA_ERR_BAD_INDEX = 7,   /* device: a selected index outside [-1, t] */
-    DSA_ERR_INTERNAL = 8     /* device: an internal consistency check failed (a bug); the write was skipped */
+    DSA_ERR_INTERNAL = 8,    /* device: an internal consistency check failed (a bug); the write was skipped */
+    DSA_ERR_NO_PAGES = 9     /* device: a step needs more pages than the free list holds */
 } dsa_status;
 
 /* One call's batch.  q_off and ctx_len are DEVICE int32 arrays, read by the
@@ -324,6 +325,142 @@ DSA_API dsa_status dsa_forward_fp8(const dsa_batch* batch, const uint8_t* q8, co
                                    const uint8_t* k8, const float* ks, const uint16_t* q, const uint16_t* kv, int k,
                                    float sm_scale, uint16_t* out, float* lse, int32_t* idx_out, float* scores_out,
                                    int64_t ld, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- A step of drafted tokens (a tree per sequence) over a cache.
+ * Sequence b holds c_b committed cache rows and gets n_b new ones (n_b <= 64
+ * where masks are involved); the batch describes the lengths after the step,
+ * so c_b = ctx_len[b] - n_b and new row i is packed row r = q_off[b] + i at
+ * cache position c_b + i.  Row r sees every committed position, and the new
+ * row j <= i of its own sequence if bit j of mask[r] is set; higher bits are
+ * ignored.  A tree's mask[r] holds the row's ancestors and itself; a chain's
+ * is (2 << i) - 1.  mask is uint64 [total_q], 8-byte aligned.
+ *
+ *   dsa_step_tables    lengths (and parent links) -> q_off, ctx_len, block
+ *                      table, slot map, positions, masks
+ *   dsa_latent_append  the new tokens' latent rows into their slots
+ *   dsa_tree_mla_fwd   attention over everything a row sees (contexts of at
+ *                      most index_topk rows, layers without an indexer)
+ *   dsa_tree_topk      the DSA selection of a row among what it sees, between
+ *                      dsa_indexer_scores and dsa_sparse_mla_fwd
+ *   dsa_tree_commit    the accepted path's rows moved behind the committed
+ *
+ * Paged caches: with a dsa_pages, position s of sequence b is cache row
+ * block_table[b * max_pages + s / page_size] * page_size + s % page_size of a
+ * cache of pool_pages * page_size rows, and cache_stride plays no part (it
+ * must still be >= max_ctx).  Without one (NULL) it is row
+ * b * cache_stride + s, as in every other call.
+ * Every launch is sized from the host arguments alone.  Calls that may run at
+ * the same time (two streams, or two captured graphs) need a workspace each.
+ * The calls' results do not depend on timing: the same inputs give the same
+ * bits. */
+
+#define DSA_MAX_TREE 64      /* new rows per sequence under a mask */
+
+typedef struct dsa_pages {
+    int32_t page_size;       /* cache rows per page: a power of two, 16 .. 1024 */
+    int32_t max_pages;       /* entries per block-table row, >= ceil(max_ctx / page_size) */
+    int32_t pool_pages;      /* pages of the caches; pool_pages * page_size < 2^31 */
+    int32_t* block_table;    /* device [batch, max_pages]; written by dsa_step_tables only */
+} dsa_pages;
+
+/* Bytes of workspace that the calls of this section need for `batch` (the
+ * largest of them); NULL: dsa_latent_append alone (256).  Host only. */
+DSA_API dsa_status dsa_tree_workspace_size(const dsa_batch* batch, size_t* bytes);
+
+/* The tables of a step, on the device, from the sequences' lengths:
+ *   batch->q_off[b+1]   = n_new[0] + .. + n_new[b], q_off[0] = 0      (written)
+ *   batch->ctx_len[b]   = ctx_old[b] + n_new[b]                       (written)
+ *   slots[r]            = cache row of new token r
+ *   positions[r]        = its rotary position: ctx_old[b] + i, or
+ *                         ctx_old[b] + depth of node i when parent is given
+ *   mask[r]             = its visibility bits (NULL: not wanted)
+ * Rows r >= q_off[batch] (behind the last sequence) get slots = positions =
+ * -1 and mask = 0.  batch->total_q is the length of the per-row arrays, an
+ * upper bound of the step's tokens; max_q, max_ctx bound n_new and ctx_len.
+ *   n_new, ctx_old  int32 [batch]
+ *   parent          int32 [total_q] or NULL (a chain): parent[r] is the
+ *                   node's parent within its sequence, -1 for a root, else
+ *                   less than its own index
+ * With pages (all of the following are NULL without):
+ *   n_pages_old     int32 [batch]  pages that the block table already holds
+ *   n_pages         int32 [batch]  out: max(n_pages_old, ceil(ctx_len / page_size))
+ *   free_pages      int32 [pool_pages]; entries [free_range[0], free_range[1])
+ *                   are free pages; sequence 0 takes its new pages first
+ *   free_range      int32 [2] in, free_range_out int32 [2] out
+ * The new block-table entries are written behind the held ones; the others
+ * are left as they were.  An output may be the input it advances (ctx_len
+ * and ctx_old, n_pages and n_pages_old, free_range and free_range_out).
+ * Bad lengths (negative, past max_q, max_ctx or total_q; n_new > 64 with a
+ * mask or parent; n_pages_old outside [0, max_pages]; free_range outside the
+ * list) latch DSA_ERR_BAD_BATCH; pages that run out, DSA_ERR_NO_PAGES.  Then
+ * no sequence advances: q_off = 0, ctx_len = ctx_old, n_pages and
+ * free_range_out as they came in, every row as behind the last sequence.
+ * A held or free page outside [0, pool_pages) that a new row falls on
+ * latches DSA_ERR_BAD_INDEX and gives slots = -1.  A parent outside [-1, i) latches DSA_ERR_BAD_INDEX;
+ * the node counts as a root. */
+DSA_API dsa_status dsa_step_tables(const dsa_batch* batch, const dsa_pages* pages, const int32_t* n_new,
+                                   const int32_t* ctx_old, const int32_t* parent, const int32_t* n_pages_old,
+                                   int32_t* n_pages, const int32_t* free_pages, const int32_t* free_range,
+                                   int32_t* free_range_out, int32_t* slots, int32_t* positions, uint64_t* mask,
+                                   void* ws, size_t ws_bytes, void* stream);
+
+/* The latent cache rows of new tokens ("GLM-5.1 架构深度拆解", section 4.5
+ * Step 2: kv_a_proj_with_mqa -> split 512 | 64 -> kv_a_layernorm, RoPE):
+ *   kv[slots[r], 0:512]   = x[r, 0:512] / sqrt(mean(x[r, 0:512]^2) + eps) * gamma
+ *   kv[slots[r], 512:576] = RoPE(x[r, 512:576]) at positions[r], rotate-half
+ *                           pairs (i, i + 32) as in dsa_index_key_producer
+ * fp32 arithmetic on the bf16 inputs, one rounding to bf16 at the end.
+ *   x       bf16 [total_q, x_stride]  the first 576 of each row; x_stride a
+ *                                     multiple of 8, >= 576
+ *   gamma   fp32 [512]
+ *   cos, sin fp32 [table_rows, 64]    rotary table, row = position
+ *   positions, slots int32 [total_q]
+ *   kv      bf16 [cache_rows, 576]
+ * A slot of -1 skips the row; another slot outside [0, cache_rows) or a
+ * position outside [0, table_rows) skips it and latches DSA_ERR_BAD_INDEX.
+ * Two rows with one slot: one of them is kept, which is not defined.
+ * ws: at least 256 bytes. */
+DSA_API dsa_status dsa_latent_append(int32_t total_q, const uint16_t* x, int64_t x_stride, const float* gamma,
+                                     float eps, const float* cos, const float* sin, int32_t table_rows,
+                                     const int32_t* positions, const int32_t* slots, int64_t cache_rows,
+                                     uint16_t* kv, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of every new row over everything it sees, absorbed form:
+ *   q, kv, out, lse, sm_scale as dsa_sparse_mla_fwd (kv paged or contiguous)
+ * A row that sees nothing gets out = 0 and lse = -inf.  Cache rows past
+ * ctx_len and new rows that a row does not see do not reach its results,
+ * whatever they hold; a row that sees a new row with a NaN or infinity gets
+ * NaN.  A block-table entry outside [0, pool_pages) latches
+ * DSA_ERR_BAD_INDEX, a sequence with more than 64 new rows
+ * DSA_ERR_BAD_BATCH, and the outputs of the sequence's affected rows are
+ * left unwritten.  max_q > 64 -> DSA_ERR_UNSUPPORTED. */
+DSA_API dsa_status dsa_tree_mla_fwd(const dsa_batch* batch, const dsa_pages* pages, const uint16_t* q,
+                                    const uint16_t* kv, const uint64_t* mask, float sm_scale, uint16_t* out,
+                                    float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Step 2 under a mask: idx int32 [total_q, k] gets the min(k, seen) positions
+ * with the largest scores among those that the row sees, ascending, -1 past
+ * them.  scores, ld, k, ties as dsa_topk; scores of positions that a row does
+ * not see are not read as values.  max_q > 64 -> DSA_ERR_UNSUPPORTED. */
+DSA_API dsa_status dsa_tree_topk(const dsa_batch* batch, const float* scores, int64_t ld, const uint64_t* mask,
+                                 int k, int32_t* idx, void* ws, size_t ws_bytes, void* stream);
+
+/* Accepts a path of each sequence's tree.  accepted[b] is the index of the
+ * path's last node, or -1 (nothing accepted).  The path is what the node
+ * sees: the set bits j_0 < j_1 < .. of mask[q_off[b] + accepted[b]] at or
+ * below accepted[b].  Cache row c_b + j_i moves to c_b + i in each of the
+ * `layers` layers, and ctx_new[b] = c_b + the path's length.
+ *   kv      bf16 [layers, cache_rows, 576] or NULL
+ *   k_idx   bf16 [layers, cache_rows, 128] or NULL
+ *   ctx_new int32 [batch]; may be batch->ctx_len
+ * cache_rows: pool_pages * page_size, or at least batch * cache_stride.
+ * Rows behind the path keep what they hold; pages are kept too.  An index
+ * outside [-1, n_b), or a bad block-table entry on the path, latches
+ * DSA_ERR_BAD_INDEX, moves nothing of that sequence and gives
+ * ctx_new = c_b. */
+DSA_API dsa_status dsa_tree_commit(const dsa_batch* batch, const dsa_pages* pages, const uint64_t* mask,
+                                   const int32_t* accepted, int32_t layers, int64_t cache_rows, uint16_t* kv,
+                                   uint16_t* k_idx, int32_t* ctx_new, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -28,12 +28,15 @@ H_IDX, D_IDX, H, D_QK, D_V, MAX_TOPK = 32, 128, 64, 576, 512, 2048
 STATUS = {
     0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED", 3: "DSA_ERR_WORKSPACE",
     4: "DSA_ERR_CUDA", 5: "DSA_ERR_TIMEOUT", 6: "DSA_ERR_BAD_BATCH", 7: "DSA_ERR_BAD_INDEX", 8: "DSA_ERR_INTERNAL",
+    9: "DSA_ERR_NO_PAGES",
 }
 
 EXPORTS = ("dsa_status_string", "dsa_last_cuda_error", "dsa_kernel_launch_count", "dsa_workspace_size", "dsa_reset_device_status", "dsa_read_device_status",
            "dsa_selftest_wait_timeout", "dsa_indexer_scores", "dsa_topk", "dsa_sparse_mla_fwd",
            "dsa_sparse_mla_fwd_noalloc", "dsa_forward", "dsa_mla_absorb_q", "dsa_mla_workspace_size", "dsa_mla_output", "dsa_index_key_workspace_size",
-           "dsa_index_key_producer", "dsa_quantize_fp8", "dsa_indexer_scores_fp8", "dsa_forward_fp8")
+           "dsa_index_key_producer", "dsa_quantize_fp8", "dsa_indexer_scores_fp8", "dsa_forward_fp8",
+           "dsa_tree_workspace_size", "dsa_step_tables", "dsa_latent_append", "dsa_tree_mla_fwd", "dsa_tree_topk",
+           "dsa_tree_commit")
 
 
 class DsaError(RuntimeError):
@@ -49,6 +52,11 @@ class DsaBatch(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("total_q", ctypes.c_int32), ("max_q", ctypes.c_int32),
                 ("max_ctx", ctypes.c_int32), ("cache_stride", ctypes.c_int64),
                 ("q_off", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p)]
+
+
+class DsaPages(ctypes.Structure):
+    _fields_ = [("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("pool_pages", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p)]
 
 
 _lib = None
@@ -88,6 +96,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dsa_quantize_fp8.argtypes = [i64, P, P, P, P]
     lib.dsa_indexer_scores_fp8.argtypes = [BP, P, P, P, P, P, P, i64, P, sz, P]
     lib.dsa_forward_fp8.argtypes = [BP, P, P, P, P, P, P, P, i32, f32, P, P, P, P, i64, P, sz, P]
+    GP = ctypes.POINTER(DsaPages)
+    lib.dsa_tree_workspace_size.argtypes = [BP, ctypes.POINTER(sz)]
+    lib.dsa_step_tables.argtypes = [BP, GP, P, P, P, P, P, P, P, P, P, P, P, P, sz, P]
+    lib.dsa_latent_append.argtypes = [i32, P, i64, P, f32, P, P, i32, P, P, i64, P, P, sz, P]
+    lib.dsa_tree_mla_fwd.argtypes = [BP, GP, P, P, P, f32, P, P, P, sz, P]
+    lib.dsa_tree_topk.argtypes = [BP, P, i64, P, i32, P, P, sz, P]
+    lib.dsa_tree_commit.argtypes = [BP, GP, P, P, i32, i64, P, P, P, P, sz, P]
     for name in EXPORTS:
         if name not in ("dsa_status_string", "dsa_last_cuda_error", "dsa_kernel_launch_count"):
             getattr(lib, name).restype = ctypes.c_int
@@ -320,3 +335,155 @@ def forward_fp8(batch: Batch, q8, qs, w, k8, ks, q, kv, k: int, sm_scale: float,
                                           _p(scores_out), int(ld), _p(ws), ws.numel() if ws is not None else 0,
                                           _stream(stream)), "dsa_forward_fp8")
     return out
+
+
+# ---- A step of drafted tokens over a paged or contiguous cache --------------
+
+class Pages:
+    """Host handle of a dsa_pages.  Keeps the device block table alive."""
+
+    def __init__(self, block_table: torch.Tensor, page_size: int, pool_pages: int):
+        if block_table.dtype != torch.int32 or block_table.dim() != 2:
+            raise TypeError("block_table: int32 [batch, max_pages] expected")
+        self.block_table, self.page_size, self.pool_pages = block_table, int(page_size), int(pool_pages)
+        self.c = DsaPages(self.page_size, block_table.shape[1], self.pool_pages, _p(block_table))
+
+
+def make_pages(block_table: torch.Tensor, page_size: int, pool_pages: int) -> Pages:
+    return Pages(block_table, page_size, pool_pages)
+
+
+def tree_workspace(batch: Optional[Batch] = None, device="cuda") -> torch.Tensor:
+    """A workspace of the drafted-step calls with a cleared status word (no
+    batch: for latent_append alone)."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().dsa_tree_workspace_size(ctypes.byref(batch.c) if batch is not None else None,
+                                                  ctypes.byref(n)), "dsa_tree_workspace_size")
+    ws = torch.empty(int(n.value), dtype=torch.uint8, device=device)
+    reset_device_status(ws)
+    return ws
+
+
+def _typed(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, numel: int, device: torch.device):
+    """Pointer of a contiguous tensor of `dtype` with at least `numel` elements on `device` (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} tensor expected, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous tensor expected")
+    if t.numel() < numel:
+        raise ValueError(f"{name}: {numel} elements expected, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _here(ws: torch.Tensor) -> torch.device:
+    """The device of a call: the workspace's, which has to be the current one."""
+    dev = ws.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"workspace on {dev}: expected on the current CUDA device")
+    return dev
+
+
+def _paged(batch: Batch, pages: Optional[Pages], dev: torch.device):
+    """The dsa_pages argument, and the cache rows that a call may reach."""
+    if batch.q_off.device != dev or (pages is not None and pages.block_table.device != dev):
+        raise ValueError(f"batch or block table: expected on {dev}")
+    if pages is None:
+        return None, batch.c.batch * batch.c.cache_stride
+    if pages.block_table.shape[0] < batch.c.batch:
+        raise ValueError("block_table: a row for each sequence expected")
+    return ctypes.byref(pages.c), pages.pool_pages * pages.page_size
+
+
+def step_tables(batch: Batch, n_new, ctx_old, slots, positions, mask=None, parent=None, pages: Optional[Pages] = None,
+                n_pages_old=None, n_pages=None, free_pages=None, free_range=None, free_range_out=None, ws=None,
+                stream=None):
+    """q_off and ctx_len of `batch`, block table, slot map, positions and
+    masks of a step from its lengths (see dsa_step_tables).  mask: int64
+    tensor holding the 64 bits."""
+    dev, i32 = _here(ws), torch.int32
+    c = batch.c
+    pg, _ = _paged(batch, pages, dev)
+    _check(load_library().dsa_step_tables(
+        ctypes.byref(c), pg, _typed("n_new", n_new, i32, c.batch, dev), _typed("ctx_old", ctx_old, i32, c.batch, dev),
+        _typed("parent", parent, i32, c.total_q, dev), _typed("n_pages_old", n_pages_old, i32, c.batch, dev),
+        _typed("n_pages", n_pages, i32, c.batch, dev),
+        _typed("free_pages", free_pages, i32, pages.pool_pages if pages is not None else 0, dev),
+        _typed("free_range", free_range, i32, 2, dev), _typed("free_range_out", free_range_out, i32, 2, dev),
+        _typed("slots", slots, i32, c.total_q, dev), _typed("positions", positions, i32, c.total_q, dev),
+        _typed("mask", mask, torch.int64, c.total_q, dev), ws.data_ptr(), ws.numel(), _stream(stream)),
+        "dsa_step_tables")
+    return slots
+
+
+def latent_append(x, gamma, eps: float, cos, sin, positions, slots, kv, ws, stream=None):
+    """RMSNorm | RoPE of the new tokens' compressed rows x [total_q, >= 576]
+    (rows may be strided), written to kv at slots (see dsa_latent_append)."""
+    dev, f32, i32 = _here(ws), torch.float32, torch.int32
+    if x.dtype != torch.bfloat16 or x.device != dev:
+        raise TypeError(f"x: bf16 tensor on {dev} expected")
+    if x.dim() != 2 or x.shape[1] != D_QK or x.stride(1) != 1:
+        raise ValueError("x: [total_q, 576] with unit column stride expected")
+    total_q, rows = x.shape[0], cos.shape[0]
+    if kv.dim() < 2 or kv.shape[-1] != D_QK:
+        raise ValueError("kv: [cache_rows, 576] expected")
+    _check(load_library().dsa_latent_append(
+        total_q, x.data_ptr(), x.stride(0) if total_q > 1 else D_QK, _typed("gamma", gamma, f32, D_V, dev), float(eps),
+        _typed("cos", cos, f32, rows * 64, dev), _typed("sin", sin, f32, rows * 64, dev), rows,
+        _typed("positions", positions, i32, total_q, dev), _typed("slots", slots, i32, total_q, dev),
+        kv.numel() // D_QK, _typed("kv", kv, torch.bfloat16, 0, dev), ws.data_ptr(), ws.numel(), _stream(stream)),
+        "dsa_latent_append")
+    return kv
+
+
+def tree_mla_fwd(batch: Batch, q, kv, mask, sm_scale: float, out, lse=None, pages: Optional[Pages] = None, ws=None,
+                 stream=None):
+    """Attention of every new row over the committed rows and the new rows of
+    its mask (see dsa_tree_mla_fwd)."""
+    dev, bf16 = _here(ws), torch.bfloat16
+    c = batch.c
+    pg, rows = _paged(batch, pages, dev)
+    _check(load_library().dsa_tree_mla_fwd(
+        ctypes.byref(c), pg, _typed("q", q, bf16, c.total_q * H * D_QK, dev), _typed("kv", kv, bf16, rows * D_QK, dev),
+        _typed("mask", mask, torch.int64, c.total_q, dev), float(sm_scale),
+        _typed("out", out, bf16, c.total_q * H * D_V, dev), _typed("lse", lse, torch.float32, c.total_q * H, dev),
+        ws.data_ptr(), ws.numel(), _stream(stream)), "dsa_tree_mla_fwd")
+    return out
+
+
+def tree_topk(batch: Batch, scores, mask, k: int, idx, ld: Optional[int] = None, ws=None, stream=None):
+    """Causal top-k among what every new row sees (see dsa_tree_topk)."""
+    dev = _here(ws)
+    c = batch.c
+    ld = int(ld if ld is not None else scores.shape[-1])
+    _paged(batch, None, dev)
+    _check(load_library().dsa_tree_topk(
+        ctypes.byref(c), _typed("scores", scores, torch.float32, c.total_q * ld, dev), ld,
+        _typed("mask", mask, torch.int64, c.total_q, dev), int(k),
+        _typed("idx", idx, torch.int32, c.total_q * int(k), dev), ws.data_ptr(), ws.numel(), _stream(stream)),
+        "dsa_tree_topk")
+    return idx
+
+
+def tree_commit(batch: Batch, mask, accepted, ctx_new, kv=None, k_idx=None, pages: Optional[Pages] = None, ws=None,
+                stream=None):
+    """Moves the accepted paths' rows behind the committed ones in every layer
+    of kv [layers, rows, 576] and k_idx [layers, rows, 128] (one layer without
+    the first dimension; see dsa_tree_commit)."""
+    dev, bf16 = _here(ws), torch.bfloat16
+    c = batch.c
+    pg, need = _paged(batch, pages, dev)
+    shapes = {(t.shape[0] if t.dim() == 3 else 1, t.shape[-2]) for t in (kv, k_idx) if t is not None}
+    if len(shapes) > 1:
+        raise ValueError("kv and k_idx: the same layers and rows expected")
+    layers, rows = shapes.pop() if shapes else (1, need)
+    _check(load_library().dsa_tree_commit(
+        ctypes.byref(c), pg, _typed("mask", mask, torch.int64, c.total_q, dev),
+        _typed("accepted", accepted, torch.int32, c.batch, dev), layers, rows,
+        _typed("kv", kv, bf16, layers * rows * D_QK, dev), _typed("k_idx", k_idx, bf16, layers * rows * D_IDX, dev),
+        _typed("ctx_new", ctx_new, torch.int32, c.batch, dev), ws.data_ptr(), ws.numel(), _stream(stream)),
+        "dsa_tree_commit")
+    return ctx_new

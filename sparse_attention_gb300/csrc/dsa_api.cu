@@ -183,6 +183,7 @@ const char* dsa_status_string(int s) {
         case DSA_ERR_BAD_BATCH: return "DSA_ERR_BAD_BATCH: q_off/ctx_len outside the host bounds";
         case DSA_ERR_BAD_INDEX: return "DSA_ERR_BAD_INDEX: a selected index outside [-1, t]";
         case DSA_ERR_INTERNAL: return "DSA_ERR_INTERNAL: an internal consistency check failed in a kernel";
+        case DSA_ERR_NO_PAGES: return "DSA_ERR_NO_PAGES: the free list holds too few pages for the step";
         default: return "unknown dsa_status";
     }
 }

@@ -1,0 +1,327 @@
+// step_tables.cu -- the tables of a decoding step, built on the device from
+// the sequences' lengths: query offsets, new context lengths, block-table
+// entries taken from a free list, the slot map, rotary positions and the
+// visibility masks of drafted trees.
+//
+// With n_b new tokens on c_b committed rows, q_off is the exclusive prefix sum
+// of n_b, and sequence b takes max(0, ceil((c_b + n_b) / P) - held_b) pages
+// from the free list behind those of the sequences before it (a second
+// prefix sum).  Both sums run in one CTA, which alone can refuse the whole step
+// (bad lengths, no pages) before anything advances.  The rows and the new
+// block-table entries are then independent of one another: a few thousand are
+// written by the same CTA (one launch; a step is bound by latency, not by its
+// some 20 KB), more by a second launch over the whole GPU.
+// A row's page is looked up in the held part of the block table or, behind
+// it, in the free list itself, so rows do not wait for the new entries.
+//
+// A tree's mask is built by pointer jumping, a warp per sequence with two
+// nodes per lane: after round s a node's mask holds its nearest 2^s
+// ancestors-or-self and its link points 2^s up, so six rounds reach 64 nodes.
+#include <algorithm>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "tree.h"
+
+namespace dsa {
+namespace {
+
+constexpr int kThreads = 1024;
+
+struct TablesArgs {
+    int32_t B, total_q, max_q, max_ctx;
+    int64_t stride;
+    PagesDev pg;
+    const int32_t *n_new, *ctx_old, *parent, *held_old, *free_pages, *free_range;
+    int32_t *held, *free_out, *q_off, *ctx_len, *slots, *positions, *table;
+    uint64_t* mask;
+    int32_t *first_new, *held_kept;   // workspace: [B + 1] prefix of new pages, [B] pages held before
+    int32_t* head;                    // workspace: the free list's head before
+    int32_t* status;
+};
+
+__device__ __forceinline__ int64_t warp_scan_i64(int64_t v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if ((threadIdx.x & 31) >= o) v += u;
+    }
+    return v;
+}
+
+struct SeqNeed {
+    int32_t n, c, held, fresh;
+    int code;
+};
+
+__device__ __forceinline__ SeqNeed seq_need(const TablesArgs& a, int b) {
+    SeqNeed s{0, 0, 0, 0, DSA_OK};
+    if (b >= a.B) return s;
+    s.n = __ldg(a.n_new + b);
+    s.c = a.ctx_old[b];              // may be an output too: no read-only path
+    const int32_t most = (a.mask || a.parent) ? min(a.max_q, DSA_MAX_TREE) : a.max_q;
+    if (s.n < 0 || s.n > most || s.c < 0 || (int64_t)s.c + s.n > a.max_ctx) {
+        s.code = DSA_ERR_BAD_BATCH;
+        s.n = 0;
+        return s;
+    }
+    if (a.pg.table) {
+        s.held = a.held_old[b];
+        const int32_t need = (int32_t)(((int64_t)s.c + s.n + (1 << a.pg.shift) - 1) >> a.pg.shift);
+        if (s.held < 0 || s.held > a.pg.max_pages) s.code = DSA_ERR_BAD_BATCH;
+        else s.fresh = max(need - s.held, 0);    // need <= max_pages: c + n <= max_ctx
+    }
+    return s;
+}
+
+// The last b with start[b] <= v (start ascending from start[0] <= v).
+__device__ __forceinline__ int find_seq(const int32_t* start, int B, int32_t v) {
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (start[mid] <= v) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int32_t slot_of(const TablesArgs& a, int b, int32_t pos, int32_t head) {
+    if (!a.pg.table) return (int32_t)(b * a.stride + pos);
+    const int32_t p = pos >> a.pg.shift, held = a.held_kept[b];
+    const int32_t page = p < held ? a.table[(int64_t)b * a.pg.max_pages + p]
+                                  : __ldg(a.free_pages + head + a.first_new[b] + (p - held));
+    if ((uint32_t)page >= (uint32_t)a.pg.pool_pages) {
+        latch_status(a.status, DSA_ERR_BAD_INDEX);
+        return -1;
+    }
+    return (page << a.pg.shift) + (pos & ((1 << a.pg.shift) - 1));
+}
+
+// Rows and new block-table entries, by thread `me` of `threads`.
+__device__ void write_rows(const TablesArgs& a, int64_t me, int64_t threads) {
+    const int32_t rows = a.q_off[a.B], head = a.pg.table ? *a.head : 0;
+    const int64_t first_row = a.parent ? (int64_t)rows : 0;      // a tree's rows are written below
+    for (int64_t r = first_row + me; r < a.total_q; r += threads) {
+        if (r >= rows) {
+            a.slots[r] = -1;
+            a.positions[r] = -1;
+            if (a.mask) a.mask[r] = 0u;
+            continue;
+        }
+        const int b = find_seq(a.q_off, a.B, (int32_t)r);
+        const int32_t i = (int32_t)r - a.q_off[b], n = a.q_off[b + 1] - a.q_off[b];
+        const int32_t pos = a.ctx_len[b] - n + i;
+        a.slots[r] = slot_of(a, b, pos, head);
+        a.positions[r] = pos;
+        if (a.mask) a.mask[r] = ~0ull >> (63 - i);
+    }
+    if (a.parent) {
+        const int lane = (int)(me & 31);
+        for (int64_t b = me >> 5; b < a.B; b += threads >> 5) {
+            const int32_t q0 = a.q_off[b], n = a.q_off[b + 1] - q0, c = a.ctx_len[b] - n;
+            int32_t up[2];
+            uint64_t m[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int32_t i = lane + 32 * h;
+                up[h] = i < n ? __ldg(a.parent + q0 + i) : -1;
+                if (up[h] < -1 || up[h] >= i) {
+                    if (i < n) latch_status(a.status, DSA_ERR_BAD_INDEX);
+                    up[h] = -1;
+                }
+                m[h] = 1ull << i;
+            }
+#pragma unroll 1
+            for (int s = 0; s < 6; ++s) {
+                uint64_t m2[2];
+                int32_t u2[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int from = up[h] & 31;
+                    const uint64_t lo = __shfl_sync(0xffffffffu, m[0], from), hi = __shfl_sync(0xffffffffu, m[1], from);
+                    const int32_t ulo = __shfl_sync(0xffffffffu, up[0], from), uhi = __shfl_sync(0xffffffffu, up[1], from);
+                    m2[h] = up[h] < 0 ? 0u : up[h] < 32 ? lo : hi;
+                    u2[h] = up[h] < 0 ? -1 : up[h] < 32 ? ulo : uhi;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    m[h] |= m2[h];
+                    up[h] = u2[h];
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int32_t i = lane + 32 * h;
+                if (i >= n) continue;
+                a.slots[q0 + i] = slot_of(a, (int)b, c + i, head);
+                a.positions[q0 + i] = c + __popcll(m[h]) - 1;
+                if (a.mask) a.mask[q0 + i] = m[h];
+            }
+        }
+    }
+    if (a.pg.table) {
+        const int32_t fresh = a.first_new[a.B];
+        for (int64_t e = me; e < fresh; e += threads) {
+            const int b = find_seq(a.first_new, a.B, (int32_t)e);
+            a.table[(int64_t)b * a.pg.max_pages + a.held_kept[b] + ((int32_t)e - a.first_new[b])] =
+                __ldg(a.free_pages + head + e);
+        }
+    }
+}
+
+template <bool kRows>
+__global__ void __launch_bounds__(kThreads) step_lengths_kernel(const TablesArgs a) {
+    __shared__ int64_t s_n[32], s_f[32];
+    __shared__ int s_code;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    if (tid == 0) s_code = DSA_OK;
+    int32_t head = 0, tail = 0;
+    if (a.pg.table) {
+        head = a.free_range[0];
+        tail = a.free_range[1];
+    }
+    __syncthreads();
+    // pass 1: does the whole step fit?
+    int64_t n_sum = 0, f_sum = 0;
+    SeqNeed s{};
+    for (int b = tid; b < a.B; b += kThreads) {
+        s = seq_need(a, b);
+        n_sum += s.n;
+        f_sum += s.fresh;
+        if (s.code != DSA_OK) atomicMax(&s_code, s.code);
+    }
+    n_sum = warp_scan_i64(n_sum);
+    f_sum = warp_scan_i64(f_sum);
+    if (lane == 31) {
+        s_n[warp] = n_sum;
+        s_f[warp] = f_sum;
+    }
+    __syncthreads();
+    const int64_t all_n = __shfl_sync(0xffffffffu, warp_scan_i64(s_n[lane]), 31);
+    const int64_t all_f = __shfl_sync(0xffffffffu, warp_scan_i64(s_f[lane]), 31);
+    int code = s_code;
+    if (code == DSA_OK && all_n > a.total_q) code = DSA_ERR_BAD_BATCH;
+    if (code == DSA_OK && a.pg.table) {
+        if (head < 0 || tail < head || tail > a.pg.pool_pages) code = DSA_ERR_BAD_BATCH;
+        else if (all_f > tail - head) code = DSA_ERR_NO_PAGES;
+    }
+    const bool go = code == DSA_OK;
+    if (!go && tid == 0) latch_status(a.status, code);
+    __syncthreads();
+    // pass 2: the prefix sums and what advances, 1024 sequences at a time
+    int64_t n_base = 0, f_base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        if (a.B > kThreads) s = seq_need(a, b);
+        if (!go) s.n = s.fresh = 0;
+        const int64_t ni = warp_scan_i64(s.n), fi = warp_scan_i64(s.fresh);
+        if (lane == 31) {
+            s_n[warp] = ni;
+            s_f[warp] = fi;
+        }
+        __syncthreads();
+        const int64_t nw = warp_scan_i64(s_n[lane]), fw = warp_scan_i64(s_f[lane]);
+        const int64_t n_before = warp ? __shfl_sync(0xffffffffu, nw, (warp - 1) & 31) : 0;
+        const int64_t f_before = warp ? __shfl_sync(0xffffffffu, fw, (warp - 1) & 31) : 0;
+        if (b < a.B) {
+            // the outputs may be the inputs' own arrays: an element is read
+            // (above, or here for a refused step) before it is written
+            const int32_t c = go ? s.c : a.ctx_old[b];
+            a.q_off[b + 1] = (int32_t)(n_base + n_before + ni);
+            a.ctx_len[b] = c + s.n;
+            if (a.pg.table) {
+                const int32_t held = go ? s.held : a.held_old[b];
+                a.held_kept[b] = held;
+                a.held[b] = held + s.fresh;
+                a.first_new[b] = (int32_t)(f_base + f_before + fi - s.fresh);
+            }
+        }
+        n_base += __shfl_sync(0xffffffffu, nw, 31);
+        f_base += __shfl_sync(0xffffffffu, fw, 31);
+        __syncthreads();
+    }
+    if (tid == 0) {
+        a.q_off[0] = 0;
+        if (a.pg.table) {
+            a.first_new[a.B] = (int32_t)f_base;
+            *a.head = head;
+            a.free_out[0] = head + (int32_t)f_base;
+            a.free_out[1] = tail;
+        }
+    }
+    if (kRows) {
+        __syncthreads();
+        write_rows(a, tid, kThreads);
+    }
+}
+
+__global__ void __launch_bounds__(256) step_rows_kernel(const TablesArgs a) {
+    pdl_wait();
+    write_rows(a, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x);
+}
+
+}  // namespace
+
+size_t step_tables_bytes(int32_t batch) { return sizeof(int32_t) * ((size_t)2 * batch + 2); }
+
+cudaError_t launch_step_tables(const BatchDev& bd, const PagesDev& pg, const int32_t* n_new, const int32_t* ctx_old,
+                               const int32_t* parent, const int32_t* held_old, int32_t* held,
+                               const int32_t* free_pages, const int32_t* free_range, int32_t* free_out,
+                               int32_t* slots, int32_t* positions, uint64_t* mask, int32_t* scratch, int32_t* status,
+                               cudaStream_t stream) {
+    TablesArgs a{};
+    a.B = bd.B;
+    a.total_q = bd.total_q;
+    a.max_q = bd.max_q;
+    a.max_ctx = bd.max_ctx;
+    a.stride = bd.stride;
+    a.pg = pg;
+    a.n_new = n_new;
+    a.ctx_old = ctx_old;
+    a.parent = parent;
+    a.held_old = held_old;
+    a.held = held;
+    a.free_pages = free_pages;
+    a.free_range = free_range;
+    a.free_out = free_out;
+    a.q_off = const_cast<int32_t*>(bd.q_off);       // outputs of this call
+    a.ctx_len = const_cast<int32_t*>(bd.ctx_len);
+    a.slots = slots;
+    a.positions = positions;
+    a.mask = mask;
+    a.table = const_cast<int32_t*>(pg.table);
+    a.first_new = scratch;
+    a.held_kept = scratch + bd.B + 1;
+    a.head = scratch + 2 * (int64_t)bd.B + 1;
+    a.status = status;
+    // what the rows and entries can come to: the step's rows, and the pages
+    // that sequences may take (all of max_ctx for a fresh prompt)
+    const int64_t per_seq = pg.table ? std::min<int64_t>(pg.max_pages, ((int64_t)bd.max_q >> pg.shift) + 2) : 0;
+    const int64_t items = std::max<int64_t>(bd.total_q, per_seq * bd.B);
+    const bool one = items <= 4 * kThreads;
+    if (one) {
+        step_lengths_kernel<true><<<1, kThreads, 0, stream>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e == cudaSuccess) count_launches(1);
+        return e;
+    }
+    step_lengths_kernel<false><<<1, kThreads, 0, stream>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>((items + 255) / 256, 8 * num_sms()));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, step_rows_kernel, a);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+}  // namespace dsa

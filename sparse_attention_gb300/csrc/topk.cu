@@ -31,12 +31,20 @@
 // candidates in the cluster, or a full region) steps 3-4 run over the whole
 // slices instead.  Atomics only count; the result is the same bit for bit
 // on every run.
+//
+// Under a visibility mask (a tree of drafted tokens) a row's candidates are
+// its committed positions, then the new positions whose bit is set, taken as
+// one row without gaps: the at most 64 visible new scores are packed in
+// shared memory and stand in for the row's end wherever it is read, and
+// positions are mapped back as they are written.  The selection itself is the
+// same code, so -inf scores and ties come out as they would on such a row.
 #include <cooperative_groups.h>
 
 #include <algorithm>
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "tree.h"
 
 namespace cg = cooperative_groups;
 
@@ -342,11 +350,11 @@ __device__ __forceinline__ void put(int32_t* out, uint32_t pos, int k, int32_t v
     else latch_status(status, DSA_ERR_INTERNAL);
 }
 
-template <int NT>
+template <int NT, bool MASKED>
 __global__ void __launch_bounds__(NT, NT <= 512 ? 2 : 1)
     topk_kernel(const BatchDev bd, const RowRange rr, const float* __restrict__ scores, const int64_t ld,
                 const int scores_local, const int k, int32_t* __restrict__ idx, const int idx_local,
-                const int csize, int32_t* status) {
+                const int csize, int32_t* status, const uint64_t* __restrict__ mask) {
     constexpr int kThreads = NT, kWarps = NT / 32, kBinsPerThread = kBins / NT;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     TopkSmem<NT>& S = *reinterpret_cast<TopkSmem<NT>*>(smem_raw);
@@ -363,10 +371,32 @@ __global__ void __launch_bounds__(NT, NT <= 512 ? 2 : 1)
     const int32_t i = rr.i0 + (int32_t)(blockIdx.x / (unsigned)csize);
     if (i >= min(rr.i1, sq.nq)) return;
     const int32_t t = sq.ctx - sq.nq + i;
-    const int32_t n = t + 1;
     const float* row = scores + buf_row(scores_local, sq, b, i, rr) * ld;
     int32_t* out = idx + buf_row(idx_local, sq, b, i, rr) * (int64_t)k;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // the row's end under a mask: visible new scores and their positions
+    __shared__ float end_score[MASKED ? DSA_MAX_TREE : 1];
+    __shared__ int32_t end_pos[MASKED ? DSA_MAX_TREE : 1];
+    const int32_t c = MASKED ? sq.ctx - sq.nq : 0;
+    int32_t n = t + 1;
+    if constexpr (MASKED) {
+        if (sq.nq > DSA_MAX_TREE) {
+            latch_status(status, DSA_ERR_BAD_BATCH);
+            return;
+        }
+        const uint64_t bits = visible_bits(__ldg(reinterpret_cast<const unsigned long long*>(mask) + sq.q0 + i), i);
+        n = c + __popcll(bits);
+        if (tid < DSA_MAX_TREE && (bits >> tid) & 1u) {
+            const int e = __popcll(bits & ((1ull << tid) - 1u));
+            end_score[e] = __ldg(row + c + tid);
+            end_pos[e] = c + tid;
+        }
+        __syncthreads();
+    }
+    auto position = [&](int32_t j) -> int32_t {
+        if constexpr (MASKED) return j < c ? j : end_pos[j - c];
+        else return j;
+    };
     // a barrier over every thread that shares this row
     auto sync_row = [&]() {
         if (csize == 1) __syncthreads();
@@ -375,10 +405,14 @@ __global__ void __launch_bounds__(NT, NT <= 512 ? 2 : 1)
 
     if (n <= k) {  // every causal position is selected
         if (crank == 0)
-            for (int j = tid; j < k; j += kThreads) out[j] = j < n ? j : -1;
+            for (int j = tid; j < k; j += kThreads) out[j] = j < n ? position(j) : -1;
         return;
     }
-    auto row_key = [&](int32_t j) -> uint32_t { return order_key(__ldg(row + j)); };
+    auto row_key = [&](int32_t j) -> uint32_t {
+        if constexpr (MASKED)
+            if (j >= c) return order_key(end_score[j - c]);
+        return order_key(__ldg(row + j));
+    };
 
     // this CTA's slice [s_lo, s_hi) of the row (slices start on multiples of 128)
     const int32_t span = ((n + csize - 1) / csize + 127) & ~127;
@@ -442,6 +476,13 @@ __global__ void __launch_bounds__(NT, NT <= 512 ? 2 : 1)
 #pragma unroll
         for (int u = 0; u < kPrefetch; ++u) {
             float x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            if constexpr (MASKED) {
+                const int32_t j = jb + 128 * u + 4 * (int32_t)lane;
+                if (j + 3 >= c && j < w_hi)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (j + e >= c && j + e < w_hi) x[e] = end_score[j + e - c];
+            }
             uint32_t bu = 0u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -587,8 +628,8 @@ __global__ void __launch_bounds__(NT, NT <= 512 ? 2 : 1)
             const bool isg = s < c && key > tau, ise = s < c && key == tau;
             const uint32_t bg = __ballot_sync(0xffffffffu, isg), be = __ballot_sync(0xffffffffu, ise);
             const uint32_t gtb = gt_run + __popc(bg & lower), eqb = eq_run + __popc(be & lower);
-            if (isg) put(out, gtb + min(eqb, need), k, rp[s], status);
-            else if (ise && eqb < need) put(out, gtb + eqb, k, rp[s], status);
+            if (isg) put(out, gtb + min(eqb, need), k, position(rp[s]), status);
+            else if (ise && eqb < need) put(out, gtb + eqb, k, position(rp[s]), status);
             gt_run += __popc(bg);
             eq_run += __popc(be);
         }
@@ -654,10 +695,10 @@ __global__ void __launch_bounds__(NT, NT <= 512 ? 2 : 1)
             for (int x = 0; x < kE; ++x) {
                 if (j0 + x < len) {
                     if (kk[x] > tau) {
-                        put(out, gtb + min(eqb, need), k, s_lo + j0 + x, status);
+                        put(out, gtb + min(eqb, need), k, position(s_lo + j0 + x), status);
                         ++gtb;
                     } else if (kk[x] == tau) {
-                        if (eqb < need) put(out, gtb + eqb, k, s_lo + j0 + x, status);
+                        if (eqb < need) put(out, gtb + eqb, k, position(s_lo + j0 + x), status);
                         ++eqb;
                     }
                 }
@@ -670,12 +711,13 @@ __global__ void __launch_bounds__(NT, NT <= 512 ? 2 : 1)
     if (csize > 1) cluster.sync();                 // the cluster may still read this CTA's counts
 }
 
-template <int NT>
+template <int NT, bool MASKED>
 cudaError_t launch_nt(const BatchDev& bd, RowRange rr, const float* scores, int64_t ld, bool scores_local, int k,
                       int32_t* idx, bool idx_local, int csize, int32_t rows_per_seq, int32_t* status,
-                      cudaStream_t stream, bool after_previous) {
+                      cudaStream_t stream, bool after_previous, const uint64_t* mask) {
     const size_t smem = sizeof(TopkSmem<NT>);
-    cudaError_t e = cudaFuncSetAttribute(topk_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(topk_kernel<NT, MASKED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows_per_seq * csize), (unsigned)bd.B);
@@ -691,17 +733,16 @@ cudaError_t launch_nt(const BatchDev& bd, RowRange rr, const float* scores, int6
     attr[1].val.programmaticStreamSerializationAllowed = after_previous ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, topk_kernel<NT>, bd, rr, scores, ld, scores_local ? 1 : 0, k, idx,
-                           idx_local ? 1 : 0, csize, status);
+    e = cudaLaunchKernelEx(&cfg, topk_kernel<NT, MASKED>, bd, rr, scores, ld, scores_local ? 1 : 0, k, idx,
+                           idx_local ? 1 : 0, csize, status, mask);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
 
-}  // namespace
-
-cudaError_t launch_topk(const BatchDev& bd, RowRange rr, const float* scores, int64_t ld, bool scores_local,
-                        int k, int32_t* idx, bool idx_local, int32_t* status, cudaStream_t stream,
-                        bool after_previous) {
+template <bool MASKED>
+cudaError_t launch_rows(const BatchDev& bd, RowRange rr, const float* scores, int64_t ld, bool scores_local, int k,
+                        int32_t* idx, bool idx_local, int32_t* status, cudaStream_t stream, bool after_previous,
+                        const uint64_t* mask) {
     const int32_t rows_per_seq = min(rr.i1, bd.max_q) - rr.i0;
     if (rows_per_seq <= 0) return cudaSuccess;
     // long rows, few of them: split each row over a cluster
@@ -709,10 +750,24 @@ cudaError_t launch_topk(const BatchDev& bd, RowRange rr, const float* scores, in
     int csize = 1;
     if (bd.max_ctx > kLongRow && rows < 2 * num_sms())
         csize = (int)std::min<int64_t>(kMaxCluster, ((int64_t)bd.max_ctx + kKeysPerCta - 1) / kKeysPerCta);
-    return rows < num_sms() ? launch_nt<1024>(bd, rr, scores, ld, scores_local, k, idx, idx_local, csize, rows_per_seq,
-                                            status, stream, after_previous)
-                          : launch_nt<512>(bd, rr, scores, ld, scores_local, k, idx, idx_local, csize, rows_per_seq,
-                                           status, stream, after_previous);
+    return rows < num_sms() ? launch_nt<1024, MASKED>(bd, rr, scores, ld, scores_local, k, idx, idx_local, csize,
+                                                      rows_per_seq, status, stream, after_previous, mask)
+                            : launch_nt<512, MASKED>(bd, rr, scores, ld, scores_local, k, idx, idx_local, csize,
+                                                     rows_per_seq, status, stream, after_previous, mask);
+}
+
+}  // namespace
+
+cudaError_t launch_topk(const BatchDev& bd, RowRange rr, const float* scores, int64_t ld, bool scores_local,
+                        int k, int32_t* idx, bool idx_local, int32_t* status, cudaStream_t stream,
+                        bool after_previous) {
+    return launch_rows<false>(bd, rr, scores, ld, scores_local, k, idx, idx_local, status, stream, after_previous,
+                              nullptr);
+}
+
+cudaError_t launch_tree_topk(const BatchDev& bd, const float* scores, int64_t ld, const uint64_t* mask, int k,
+                             int32_t* idx, int32_t* status, cudaStream_t stream) {
+    return launch_rows<true>(bd, RowRange{0, bd.max_q}, scores, ld, false, k, idx, false, status, stream, false, mask);
 }
 
 }  // namespace dsa
