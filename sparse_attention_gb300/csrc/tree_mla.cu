@@ -2,9 +2,43 @@
 // see in a (paged or contiguous) cache: the committed rows and, by a bit mask,
 // the drafted rows of the same sequence.
 //
-// A warp per (row, head) walks the visible positions with a running maximum
-// and sum (fp32), 18 query and 16 value dims per lane.
-#include <cfloat>
+// With 64 heads on one cached stream, two new rows (nodes) make 128 query
+// rows: the M of a CTA pair's tcgen05 tile.  A pair takes an item (sequence,
+// node pair) and walks its cache in tiles of 128 positions:
+//   S[128 q, 128 pos] = Q K^T     9 chunks of 64 dims; each CTA stages its
+//                                 node's 64 query rows (72 KiB, resident) and
+//                                 64 of the tile's positions
+//   P = 2^(S c - m)               the running maximum m of a row moves only
+//                                 when a score exceeds it by 2^8 (then O is
+//                                 rescaled), so sums and weights stay far from
+//                                 both ends of fp32
+//   O[128 q, 512] += P V          two N = 256 halves; each CTA stages, for all
+//                                 128 positions, the 128 dims of each half
+//                                 whose columns it supplies
+// O (256 TMEM columns) and two S tiles (64 columns each) live in each CTA's
+// TMEM: rows of its node, lanes 0-63 the first half of the columns, lanes
+// 64-127 the second.  Nothing but barriers crosses between the CTAs, and each
+// cached row feeds 128 query rows.  S of tile g + 1 is issued before PV of
+// tile g, so the softmax of a tile runs under the tensor work of the next.
+//
+// The value half of a CTA's positions is staged twice (once as K, once in
+// V's dims-by-position split): a pair's K and V differ in which operand half
+// a CTA has to hold, and descriptors mean the same offset in both.
+//
+// Roles of a CTA's 9 warps: K and Q loads, MMA (rank 0 only), V loads,
+// fix-up, four softmax / epilogue warps (a thread per TMEM lane, so two
+// threads share a query row, 64 positions each).  Tiles that reach
+// past the committed rows go through the fix-up warp, which zeroes V rows past
+// the sequence (a page's leftovers may hold anything, and 0 * NaN is NaN) and
+// values of drafted rows that are not finite: a row that sees such a row gets
+// NaN through its score, the others nothing.
+//
+// Work: the items' tiles, plus kItemCost tiles per item for its start and
+// end, laid end to end and cut into equal chunks, one per pair.  An item cut
+// by a chunk's end leaves fp32 partial results, which merge_kernel joins in
+// order.
+#include <algorithm>
+#include <atomic>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -13,75 +47,684 @@
 namespace dsa {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kTile = 128;                   // positions per tile
+constexpr int kItemCost = 4;                 // an item's start and end, in tiles
+constexpr int kMinChunk = kItemCost + 4;     // least work cut off for a pair
+constexpr int kThreads = 288;
+constexpr int kChunkBytes = 64 * 128;        // 64 rows x 64 dims
+constexpr int kQChunks = kDQK / 64;          // 9
+constexpr int kKStages = 7;                  // chunks
+constexpr int kVStages = 5;                  // granules: 64 positions x 128 dims
+constexpr int kVBytes = 2 * kChunkBytes;
+constexpr uint32_t kOCol = 0, kSCol = 256;   // TMEM columns
+constexpr float kRescale = 8.f;              // log2
 
-__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+struct Plan {
+    int64_t lo, hi, start_u, chunk;
+    int32_t start_b;
+};
 
-__global__ void __launch_bounds__(32 * kWarps)
-    tree_mla_kernel(const BatchDev bd, const PagesDev pg, const uint16_t* __restrict__ q,
-                    const uint16_t* __restrict__ kv, const uint64_t* __restrict__ mask, float scale_log2,
-                    uint16_t* __restrict__ out, float* __restrict__ lse, int32_t* status) {
-    const int b = blockIdx.y, lane = threadIdx.x & 31;
-    SeqInfo sq;
-    if (!load_seq(bd, b, status, sq)) return;
-    if (sq.nq > DSA_MAX_TREE) {
+struct Smem {
+    alignas(1024) uint8_t q[kQChunks * kChunkBytes];
+    alignas(1024) uint8_t k[kKStages * kChunkBytes];
+    alignas(1024) uint8_t v[kVStages * kVBytes];
+    alignas(1024) uint8_t p[2 * kChunkBytes];
+    alignas(8) uint64_t kfull[kKStages], kempty[kKStages], vfull[kVStages], vempty[kVStages], vloc[kVStages];
+    uint64_t qfull, qempty, sfull[2], sempty[2], pfull, pvdone, ofree;
+    Plan plan;
+    int64_t scan[kThreads / 32];
+    float xch[2][128];
+    int32_t bad[4];
+    uint32_t tmem;
+};
+static_assert(sizeof(Smem) <= 232448, "one CTA's shared memory");
+
+struct Args {
+    BatchDev bd;
+    PagesDev pg;
+    const uint64_t* mask;
+    float scale_log2;
+    uint16_t* out;
+    float* lse;
+    int4* meta;          // [pairs]: row, rows, last pair of the item that a pair begins and another ends
+    float* part_lse;     // [2 * pairs][128]
+    float* part_o;       // [2 * pairs][128][512]
+    int32_t* status;
+    int32_t rows_total;  // cache rows
+    int32_t box;         // positions per TMA box
+};
+
+// One item's tiles [t0, t1) of a pair's chunk.
+struct Seg {
+    int32_t b, row, c, len, i0, rows, t0, t1, tiles;
+    int64_t u_end;
+    __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+__device__ __forceinline__ bool seq_ok(const BatchDev& bd, int b, int32_t* status, SeqInfo& s) {
+    if (!load_seq(bd, b, status, s)) return false;
+    if (s.nq > DSA_MAX_TREE) {
         latch_status(status, DSA_ERR_BAD_BATCH);
-        return;
+        return false;
     }
-    const int i = blockIdx.x >> 3;
-    if (i >= sq.nq) return;
-    const int h = (blockIdx.x & 7) * kWarps + (threadIdx.x >> 5);
-    const int64_t r = sq.q0 + i;
-    const int32_t c = sq.ctx - sq.nq;
-    const uint64_t bits = visible_bits(mask[r], i);
-    const uint16_t* qr = q + (r * kH + h) * kDQK;
-    float qv[18], o[16];
-#pragma unroll
-    for (int k = 0; k < 18; ++k) qv[k] = bf(qr[lane + 32 * k]);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    for (int32_t s = 0; s < sq.ctx; ++s) {
-        if (s >= c && !((bits >> (s - c)) & 1u)) continue;
-        const int32_t row = cache_row(bd, pg, b, s);
-        if (row < 0) {
-            latch_status(status, DSA_ERR_BAD_INDEX);
-            return;
+    return true;
+}
+
+__device__ __forceinline__ int64_t seq_units(const SeqInfo& s) {
+    return (int64_t)((s.nq + 1) >> 1) * (((s.ctx + kTile - 1) / kTile) + kItemCost);
+}
+
+// Walks the segments of a pair's chunk; every warp walks for itself (lanes
+// hold 32 sequences' lengths).
+struct SegIter {
+    const Args& a;
+    const Plan& plan;
+    int32_t b, p = 0, b0 = -64;
+    int64_t u;
+    int32_t w_q0 = 0, w_nq = 0, w_ctx = 0;
+    __device__ SegIter(const Args& args, const Plan& pl) : a(args), plan(pl), b(pl.start_b), u(pl.start_u) {}
+
+    __device__ bool next(Seg& s) {
+        const int64_t lo = plan.lo, hi = plan.hi;
+        for (; b < a.bd.B; ++b, p = 0) {
+            if (b >= b0 + 32) {
+                b0 = b;
+                const int mine = b0 + (int)lane_id();
+                SeqInfo q{0, 0, 0};
+                if (mine >= a.bd.B || !seq_ok(a.bd, mine, nullptr, q)) q.nq = 0;
+                w_q0 = q.q0, w_nq = q.nq, w_ctx = q.ctx;
+            }
+            const int32_t nq = __shfl_sync(0xffffffffu, w_nq, b - b0);
+            if (nq == 0) continue;
+            const int32_t ctx = __shfl_sync(0xffffffffu, w_ctx, b - b0), q0 = __shfl_sync(0xffffffffu, w_q0, b - b0);
+            const int32_t tiles = (ctx + kTile - 1) / kTile, per = tiles + kItemCost, pairs = (nq + 1) >> 1;
+            if (p == 0 && lo > u) p = (int32_t)min((lo - u) / per, (int64_t)pairs);
+            while (p < pairs) {
+                const int64_t u0 = u + (int64_t)p * per + kItemCost;
+                if (u0 - kItemCost >= hi) return false;
+                s.t0 = (int32_t)max((int64_t)0, min((int64_t)tiles, lo - u0));
+                s.t1 = (int32_t)max((int64_t)0, min((int64_t)tiles, hi - u0));
+                s.i0 = 2 * p;
+                ++p;
+                if (s.t1 > s.t0) {
+                    s.b = b;
+                    s.row = q0 + s.i0;
+                    s.rows = min(2, nq - s.i0);
+                    s.c = ctx - nq;
+                    s.len = ctx;
+                    s.tiles = tiles;
+                    s.u_end = u0 + tiles - 1;
+                    return true;
+                }
+            }
+            u += (int64_t)pairs * per;
         }
-        const uint16_t* kr = kv + (int64_t)row * kDQK;
-        float kvv[18], dot = 0.f;
-#pragma unroll
-        for (int k = 0; k < 18; ++k) {
-            kvv[k] = bf(kr[lane + 32 * k]);
-            dot += qv[k] * kvv[k];
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
-        dot *= scale_log2;
-        const float mn = fmaxf(m, dot), f = exp2f(m - mn), p = exp2f(dot - mn);
-        m = mn;
-        l = l * f + p;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = o[k] * f + p * kvv[k];
+        return false;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+};
+
+// The pair's chunk of the work, by all threads of the CTA.
+__device__ void make_plan(const Args& a, Smem& S, int pair, int pairs) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.bd.B + kThreads - 1) / kThreads;
+    const int b_lo = min(a.bd.B, tid * per), b_hi = min(a.bd.B, b_lo + per);
+    int64_t sum = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        SeqInfo q;
+        if (seq_ok(a.bd, b, a.status, q)) sum += seq_units(q);
+    }
+    int64_t incl = sum;
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-        out[(r * kH + h) * kDV + lane + 32 * k] = (uint16_t)(pack_bf16x2(o[k] * inv, 0.f) & 0xFFFFu);
-    if (lse && lane == 0) lse[r * kH + h] = (m + log2f(l)) * kLn2;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) S.scan[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - sum, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += S.scan[w];
+        all += S.scan[w];
+    }
+    const int64_t chunk = max((all + pairs - 1) / pairs, (int64_t)kMinChunk);
+    const int64_t lo = min(all, pair * chunk);
+    if (tid == 0) {
+        S.plan.lo = lo;
+        S.plan.hi = min(all, lo + chunk);
+        S.plan.chunk = chunk;
+        if (lo >= all) S.plan.start_b = a.bd.B;
+    }
+    if (before <= lo && lo < before + sum) {
+        int64_t u = before;
+        for (int b = b_lo; b < b_hi; ++b) {
+            SeqInfo q;
+            const int64_t w = seq_ok(a.bd, b, nullptr, q) ? seq_units(q) : 0;
+            if (lo < u + w) {
+                S.plan.start_b = b;
+                S.plan.start_u = u;
+                break;
+            }
+            u += w;
+        }
+    }
+}
+
+// First cache row of a box of positions at pos; past the sequence, or on a
+// page outside the pool, the rows behind the cache (TMA fills zeros).
+__device__ __forceinline__ int32_t box_row(const Args& a, const Seg& s, int32_t pos, bool& bad) {
+    if (pos >= s.len) return a.rows_total;
+    const int32_t r = cache_row(a.bd, a.pg, s.b, pos);
+    if (r >= 0) return r;
+    bad = true;
+    return a.rows_total;
+}
+
+__device__ __forceinline__ bool past_committed(const Seg& s, int32_t t) { return (t + 1) * kTile > s.c; }
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    tree_mla_kernel(const Args a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Smem& S = *reinterpret_cast<Smem*>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    pdl_launch_dependents();
+    if (smem_u32(smem_raw) & 1023u) {            // the swizzle goes by address bits
+        if (tid == 0) latch_status(a.status, DSA_ERR_INTERNAL);
+        return;                                  // both CTAs: the same launch, the same offset
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kKStages; ++i) {
+            mbar_init(smem_u32(&S.kfull[i]), 2);
+            mbar_init(smem_u32(&S.kempty[i]), 1);
+        }
+        for (int i = 0; i < kVStages; ++i) {
+            mbar_init(smem_u32(&S.vfull[i]), 2);
+            mbar_init(smem_u32(&S.vempty[i]), 1);
+            mbar_init(smem_u32(&S.vloc[i]), 1);
+        }
+        mbar_init(smem_u32(&S.qfull), 2);
+        mbar_init(smem_u32(&S.qempty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&S.sfull[i]), 1);
+            mbar_init(smem_u32(&S.sempty[i]), 8);
+        }
+        mbar_init(smem_u32(&S.pfull), 8);
+        mbar_init(smem_u32(&S.pvdone), 1);
+        mbar_init(smem_u32(&S.ofree), 8);
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(&S.tmem), 512);
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_kv);
+    }
+    make_plan(a, S, pair, pairs);
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    SegIter it(a, S.plan);
+    Seg s;
+    bool ok = true;
+    // the barrier at `b`'s offset in the CTA of rank 0
+    auto lead = [&](uint64_t& b) -> uint32_t { return map_to_cluster_rank(smem_u32(&b), 0); };
+    // bounded; the warp agrees, so that no lane is left behind in a vote
+    auto wait = [&](uint64_t& b, uint32_t parity) {
+        if (ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&b), parity))) {
+            ok = false;
+            latch_status(a.status, DSA_ERR_TIMEOUT);
+        }
+        return ok;
+    };
+    const int boxes = 64 / a.box;                // per 64 positions
+
+    if (warp == 0) {
+        // Q and K loads
+        uint32_t kc = 0, seg = 0;
+        while (ok && it.next(s)) {
+            if (seg > 0 && !wait(S.qempty, (seg - 1) & 1)) break;
+            const bool mine = (int)rank < s.rows;
+            if (lane == 0) mbar_arrive_expect_tx_pair(lead(S.qfull), mine ? (uint32_t)sizeof(S.q) : 0u);
+            __syncwarp();
+            if (mine && lane < kQChunks)
+                tma_load_2d_pair(smem_u32(S.q + lane * kChunkBytes), &tm_q, lead(S.qfull), 64 * lane,
+                                 (s.row + (int)rank) * kH);
+            ++seg;
+            bool bad = false;
+            const int32_t at = 64 * (int)rank + (lane & 3) * a.box;
+            int32_t row = box_row(a, s, s.t0 * kTile + at, bad);
+            for (int32_t t = s.t0; ok && t < s.t1; ++t) {
+                const int32_t next = t + 1 < s.t1 ? box_row(a, s, (t + 1) * kTile + at, bad) : 0;
+                for (int ch = 0; ch < kQChunks; ++ch, ++kc) {
+                    const uint32_t st = kc % kKStages;
+                    if (kc >= kKStages && !wait(S.kempty[st], (kc / kKStages - 1) & 1)) break;
+                    if (lane == 0) mbar_arrive_expect_tx_pair(lead(S.kfull[st]), kChunkBytes);
+                    if (lane < boxes)
+                        tma_load_2d_pair(smem_u32(S.k + st * kChunkBytes + lane * a.box * 128), &tm_kv,
+                                         lead(S.kfull[st]), 64 * ch, row);
+                }
+                row = next;
+            }
+        }
+    } else if (warp == 1) {
+        // MMA: S of tile g + 1, then PV of tile g
+        if (rank == 0) {
+            constexpr uint32_t kIdS = idesc_bf16_f32(128, kTile), kIdO = idesc_bf16_f32(128, 256, false, true);
+            SegIter itq(a, S.plan);
+            Seg sq;
+            uint32_t kc = 0, vc = 0, gq = 0, gp = 0, segq = 0, segp = 0;
+            int32_t tq = 0, tp = 0;
+            bool more_q = itq.next(sq);
+            if (more_q) tq = sq.t0;
+            auto issue_s = [&]() {
+                if (tq == sq.t0 && !wait(S.qfull, segq & 1)) return;
+                const uint32_t buf = gq & 1;
+                if (gq >= 2 && !wait(S.sempty[buf], ((gq >> 1) - 1) & 1)) return;
+                tc_fence_after();
+                for (int ch = 0; ch < kQChunks; ++ch, ++kc) {
+                    const uint32_t st = kc % kKStages;
+                    if (!wait(S.kfull[st], (kc / kKStages) & 1)) return;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t da = sdesc_sw128(smem_u32(S.q + ch * kChunkBytes), 0, 1024);
+                        const uint64_t db = sdesc_sw128(smem_u32(S.k + st * kChunkBytes), 0, 1024);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_ss_pair(tmem + kSCol + 64 * buf, da + 2 * k, db + 2 * k, kIdS, (ch | k) != 0);
+                        mma_commit_pair(smem_u32(&S.kempty[st]));
+                    }
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    mma_commit_pair(smem_u32(&S.sfull[buf]));
+                    if (tq + 1 == sq.t1) mma_commit_pair(smem_u32(&S.qempty));
+                }
+                __syncwarp();
+                ++gq;
+                if (++tq == sq.t1) {
+                    ++segq;
+                    more_q = itq.next(sq);
+                    if (more_q) tq = sq.t0;
+                }
+            };
+            if (more_q) issue_s();
+            while (ok && it.next(s)) {
+                for (tp = s.t0; ok && tp < s.t1; ++tp, ++gp) {
+                    if (more_q) issue_s();
+                    if (tp == s.t0 && segp > 0 && !wait(S.ofree, (segp - 1) & 1)) break;
+                    if (!wait(S.pfull, gp & 1)) break;
+                    tc_fence_after();
+                    for (int gr = 0; gr < 4; ++gr, ++vc) {
+                        const uint32_t st = vc % kVStages;
+                        if (!wait(S.vfull[st], (vc / kVStages) & 1)) break;
+                        tc_fence_after();
+                        if (lane == 0) {
+                            const int j = gr >> 1, h = gr & 1;
+                            const uint64_t da = sdesc_sw128(smem_u32(S.p + h * kChunkBytes), 0, 1024);
+                            const uint64_t db = sdesc_sw128(smem_u32(S.v + st * kVBytes), kChunkBytes, 1024);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_bf16_ss_pair(tmem + kOCol + 128 * j, da + 2 * k, db + 128 * k, kIdO,
+                                                 tp != s.t0 || h != 0 || k != 0);
+                            mma_commit_pair(smem_u32(&S.vempty[st]));
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) mma_commit_pair(smem_u32(&S.pvdone));
+                    __syncwarp();
+                }
+                ++segp;
+            }
+        }
+    } else if (warp == 2) {
+        // V loads
+        uint32_t vc = 0, seg = 0;
+        while (ok && it.next(s)) {
+            bool bad = false;
+            int32_t row = box_row(a, s, s.t0 * kTile + (lane & 7) * a.box, bad);
+            for (int32_t t = s.t0; ok && t < s.t1; ++t) {
+                const bool any_bad = __any_sync(0xffffffffu, bad);
+                if (lane == 0) S.bad[seg & 3] = any_bad;
+                if (any_bad && lane == 0) latch_status(a.status, DSA_ERR_BAD_INDEX);
+                __syncwarp();
+                const int32_t next = t + 1 < s.t1 ? box_row(a, s, (t + 1) * kTile + (lane & 7) * a.box, bad) : 0;
+                const bool fix = past_committed(s, t);
+                for (int gr = 0; gr < 4; ++gr, ++vc) {
+                    const int j = gr >> 1, h = gr & 1;
+                    const uint32_t st = vc % kVStages;
+                    if (vc >= kVStages && !wait(S.vempty[st], (vc / kVStages - 1) & 1)) break;
+                    const uint32_t bar = fix ? map_to_cluster_rank(smem_u32(&S.vloc[st]), rank) : lead(S.vfull[st]);
+                    if (lane == 0) mbar_arrive_expect_tx_pair(bar, kVBytes);
+                    const int e = lane % boxes, blk = lane / boxes;
+                    const int32_t r = __shfl_sync(0xffffffffu, row, h * boxes + e);
+                    if (blk < 2)
+                        tma_load_2d_pair(smem_u32(S.v + st * kVBytes + blk * kChunkBytes + e * a.box * 128), &tm_kv, bar,
+                                         256 * j + 128 * (int)rank + 64 * blk, r);
+                }
+                row = next;
+            }
+            ++seg;
+        }
+    } else if (warp == 3) {
+        // fix-up of V tiles that reach past the committed rows
+        uint32_t vc = 0, parity = 0;
+        while (ok && it.next(s)) {
+            for (int32_t t = s.t0; ok && t < s.t1; ++t, vc += 4) {
+                if (!past_committed(s, t)) continue;
+                for (int gr = 0; gr < 4; ++gr) {
+                    const uint32_t st = (vc + gr) % kVStages;
+                    if (!wait(S.vloc[st], (parity >> st) & 1)) break;
+                    parity ^= 1u << st;
+                    const int32_t pos0 = t * kTile + 64 * (gr & 1);
+                    for (int32_t x = max(0, s.c - pos0) + (lane >> 4); x < 64; x += 2) {
+                        uint4* at = reinterpret_cast<uint4*>(S.v + st * kVBytes + ((lane >> 3) & 1) * kChunkBytes +
+                                                             x * 128 + (lane & 7) * 16);
+                        if (pos0 + x >= s.len) {
+                            *at = make_uint4(0, 0, 0, 0);
+                        } else {
+                            uint4 v = *at;
+                            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+                            bool hit = false;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u, hit = true;
+                                if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0xFFFFu, hit = true;
+                            }
+                            if (hit) *at = v;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(lead(S.vfull[st]));
+                }
+            }
+        }
+    } else if (warp < 8) {
+        // softmax and epilogue: TMEM lane = tid - 128
+        const int ln = tid - 128, x = ln & 63, half = ln >> 6;
+        const uint32_t tl = tmem + ((uint32_t)(ln & ~31) << 16);
+        uint32_t g = 0, seg = 0, xb = 0;
+        auto exchange = [&](float v) -> float {
+            xb ^= 1;
+            S.xch[xb][ln] = v;
+            named_bar_sync(1, 128);
+            return S.xch[xb][ln ^ 64];
+        };
+        while (it.next(s)) {
+            const bool mine = (int)rank < s.rows;
+            const uint64_t bits =
+                mine ? visible_bits(__ldg(reinterpret_cast<const unsigned long long*>(a.mask) + s.row + rank),
+                                    s.i0 + (int)rank)
+                     : 0u;
+            float m = -INFINITY, l = 0.f;
+            for (int32_t t = s.t0; t < s.t1; ++t, ++g) {
+                const uint32_t buf = g & 1;
+                wait(S.sfull[buf], (g >> 1) & 1);
+                tc_fence_after();
+                if (!mine) {
+                    // no node here: its rows of S, P and O are nobody's
+                    if (lane == 0) mbar_arrive_pair(lead(S.sempty[buf]));
+                    if (g > 0) wait(S.pvdone, (g - 1) & 1);
+                    if (lane == 0) mbar_arrive_pair(lead(S.pfull));
+                    continue;
+                }
+                uint32_t r[2][32];
+                tmem_ld_32x32b_x32(tl + kSCol + 64 * buf, r[0]);
+                tmem_ld_32x32b_x32(tl + kSCol + 64 * buf + 32, r[1]);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(lead(S.sempty[buf]));
+                if (past_committed(s, t)) {
+                    const int32_t d = s.c - (t * kTile + 64 * half);     // committed columns of this thread's 64
+                    uint64_t vis = d >= 64 ? ~0ull : d > 0 ? (1ull << d) - 1u : 0u;
+                    vis |= d >= 64 ? 0u : d >= 0 ? bits << d : d > -64 ? bits >> -d : 0u;
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        if (!((vis >> k) & 1u)) r[k >> 5][k & 31] = 0xFF800000u;
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 64; ++k) mx = fmaxf(mx, __uint_as_float(r[k >> 5][k & 31]));
+                mx = fmaxf(mx, exchange(mx)) * a.scale_log2;
+                const bool move = mx > m + kRescale || (m == -INFINITY && mx > m);
+                const float m_new = move ? mx : m;
+                const float f = move ? ex2_approx(m - m_new) : 1.f;
+                const float off = m_new == -INFINITY ? 0.f : m_new;
+                m = m_new;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t pk[32];
+#pragma unroll
+                for (int k = 0; k < 64; k += 2) {
+                    const float p0 = ex2_approx(fmaf(__uint_as_float(r[k >> 5][k & 31]), a.scale_log2, -off));
+                    const float p1 = ex2_approx(fmaf(__uint_as_float(r[k >> 5][(k & 31) + 1]), a.scale_log2, -off));
+                    sum[(k >> 1) & 3] += p0 + p1;
+                    pk[k >> 1] = pack_bf16x2(p0, p1);
+                }
+                l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                if (g > 0) wait(S.pvdone, (g - 1) & 1);
+                tc_fence_after();
+                if (t > s.t0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+                    for (uint32_t c = 0; c < 256; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld_32x32b_x16(tl + kOCol + c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st_32x32b_x16(tl + kOCol + c, o);
+                    }
+                    tmem_st_wait();
+                }
+                uint8_t* pr = S.p + half * kChunkBytes + x * 128;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<uint4*>(pr + ((k ^ (x & 7)) << 4)) =
+                        make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(lead(S.pfull));
+            }
+            wait(S.pvdone, (g - 1) & 1);
+            tc_fence_after();
+            const bool bad = *reinterpret_cast<volatile int32_t*>(&S.bad[seg & 3]) != 0;
+            if (mine) {
+                l += exchange(l);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float ls = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                const int64_t head = (int64_t)(s.row + (int)rank) * kH + x;
+                const bool whole = s.whole();
+                const int64_t slot = 2 * (int64_t)pair + (s.t0 == 0 ? 1 : 0);
+                const int64_t prow = slot * 128 + 64 * (int)rank + x;
+                uint16_t* ob = a.out + head * kDV + 128 * half;
+                float* of = a.part_o + prow * kDV + 128 * half;
+                if (half == 0 && ok) {
+                    if (!whole) a.part_lse[prow] = bad ? INFINITY : ls;
+                    else if (a.lse && !bad) a.lse[head] = ls;
+                }
+#pragma unroll 1
+                for (uint32_t c = 0; c < 256; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(tl + kOCol + c, o);
+                    tmem_ld_wait();
+                    const uint32_t col = (c & 127) + 2 * (c & 128);   // dims 256 j + 128 half + ..
+                    if (ok && whole && !bad) {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = pack_bf16x2(__uint_as_float(o[8 * v + 2 * k]) * inv,
+                                                   __uint_as_float(o[8 * v + 2 * k + 1]) * inv);
+                            *reinterpret_cast<uint4*>(ob + col + 8 * v) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else if (ok && !whole) {
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            *reinterpret_cast<float4*>(of + col + 4 * v) =
+                                make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                                            __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+                    }
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(lead(S.ofree));
+            ++seg;
+        }
+    } else if (rank == 0) {
+        // what merge_kernel has to know of this pair's cut items
+        int4 meta = make_int4(0, 0, 0, 0);
+        while (it.next(s))
+            if (s.t0 == 0 && !s.whole()) meta = make_int4(s.row, s.rows, (int)(s.u_end / S.plan.chunk), 0);
+        if (lane == 0) a.meta[pair] = meta;
+    }
+    if (!ok) {
+        // let copies in flight land before the CTA's shared memory goes
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000u) __nanosleep(1000);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// Joins the partial results of an item: block (pair, y) takes 8 of the 128
+// query rows of the item that the pair begins.
+__global__ void __launch_bounds__(128)
+    tree_merge_kernel(const int4* __restrict__ meta, const float* __restrict__ part_lse,
+                      const float* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
+    pdl_wait();
+    const int pair = blockIdx.x, tid = threadIdx.x;
+    const int4 it = meta[pair];
+    const int first = 8 * blockIdx.y;
+    if (first >= 64 * it.y) return;
+    // the item's pieces: this pair's slot 2 pair + 1, then slots 2 p of the
+    // pairs behind it
+    const int pieces = it.z - pair + 1;
+    auto slot = [&](int e) -> int64_t { return e == 0 ? 2 * (int64_t)pair + 1 : 2 * ((int64_t)pair + e); };
+    for (int r = first; r < first + 8; ++r) {
+        float mx = -INFINITY, sum = 0.f;
+        bool bad = false;
+        for (int e = 0; e < pieces; ++e) {
+            const float v = part_lse[slot(e) * 128 + r];
+            bad = bad || v == INFINITY;
+            mx = (v > mx || v != v) ? v : mx;
+        }
+        if (bad) continue;
+        const float base = mx == -INFINITY ? 0.f : mx;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int e = 0; e < pieces; ++e) {
+            const float w = ex2_approx((part_lse[slot(e) * 128 + r] - base) * kLog2e);
+            const float4 o = *reinterpret_cast<const float4*>(part_o + (slot(e) * 128 + r) * kDV + 4 * tid);
+            sum += w;
+            acc.x += w * o.x;
+            acc.y += w * o.y;
+            acc.z += w * o.z;
+            acc.w += w * o.w;
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t head = (int64_t)it.x * kH + r;
+        *reinterpret_cast<uint2*>(out + head * kDV + 4 * tid) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (lse && tid == 0) lse[head] = sum == 0.f ? -INFINITY : base + log2f(sum) * kLn2;
+    }
+}
+
+// CTA pairs that can be resident at once on the current device.
+int max_pairs() {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> cache[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return kDefaultSMs / 2;
+    }
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * num_sms());
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(tree_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem)) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, tree_mla_kernel, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        return num_sms() / 2;
+    }
+    n = std::min(n, num_sms() / 2);
+    cache[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Pairs that a call launches: no more than its bounds can give kMinChunk of
+// work each.
+int pairs_for(const BatchDev& bd) {
+    const int64_t items = (int64_t)bd.B * ((std::min(bd.max_q, DSA_MAX_TREE) + 1) / 2);
+    const int64_t units = items * ((bd.max_ctx + kTile - 1) / kTile + kItemCost);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2, (units + kMinChunk - 1) / kMinChunk));
 }
 
 }  // namespace
 
-size_t tree_mla_scratch_bytes(const BatchDev&) { return 0; }
+size_t tree_mla_scratch_bytes(const BatchDev& bd) {
+    const size_t pairs = (size_t)pairs_for(bd);
+    return pairs * (sizeof(int4) + 2 * 128 * sizeof(float) * (1 + (size_t)kDV)) + 256;
+}
 
 cudaError_t launch_tree_mla(const BatchDev& bd, const PagesDev& pg, const uint16_t* q, const uint16_t* kv,
-                            const uint64_t* mask, float sm_scale, uint16_t* out, float* lse, void*, int32_t* status,
-                            cudaStream_t stream) {
-    tree_mla_kernel<<<dim3((unsigned)bd.max_q * 8, (unsigned)bd.B), 32 * kWarps, 0, stream>>>(
-        bd, pg, q, kv, mask, sm_scale * kLog2e, out, lse, status);
-    const cudaError_t e = cudaGetLastError();
+                            const uint64_t* mask, float sm_scale, uint16_t* out, float* lse, void* scratch,
+                            int32_t* status, cudaStream_t stream) {
+    const size_t slots = 2 * (size_t)pairs_for(bd);
+    const int pairs = std::min(pairs_for(bd), max_pairs());
+    Args a{};
+    a.bd = bd;
+    a.pg = pg;
+    a.mask = mask;
+    a.scale_log2 = sm_scale * kLog2e;
+    a.out = out;
+    a.lse = lse;
+    a.status = status;
+    a.part_o = static_cast<float*>(scratch);
+    a.part_lse = a.part_o + slots * 128 * kDV;
+    a.meta = reinterpret_cast<int4*>(a.part_lse + slots * 128);
+    a.rows_total = pg.table ? pg.pool_pages << pg.shift : (int32_t)(bd.B * bd.stride);
+    a.box = pg.table ? std::min(1 << pg.shift, 64) : 64;
+    CUtensorMap tm_q, tm_kv;
+    if (!make_tmap_bf16_2d(&tm_q, q, kDQK, (uint64_t)bd.total_q * kH, 64, 64) ||
+        !make_tmap_bf16_2d(&tm_kv, kv, kDQK, (uint64_t)a.rows_total, 64, (uint32_t)a.box))
+        return cudaErrorInvalidValue;
+    cudaError_t e =
+        cudaFuncSetAttribute(tree_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+    if (e != cudaSuccess) return e;
+    tree_mla_kernel<<<2 * pairs, kThreads, sizeof(Smem), stream>>>(a, tm_q, tm_kv);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    count_launches(1);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pairs, 16);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, (const int4*)a.meta, (const float*)a.part_lse,
+                           (const float*)a.part_o, out, lse);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
