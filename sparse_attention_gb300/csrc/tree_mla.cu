@@ -271,9 +271,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     // the barrier at `b`'s offset in the CTA of rank 0
     auto lead = [&](uint64_t& b) -> uint32_t { return map_to_cluster_rank(smem_u32(&b), 0); };
-    // bounded; the warp agrees, so that no lane is left behind in a vote
-    auto wait = [&](uint64_t& b, uint32_t parity) {
-        if (ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&b), parity))) {
+    // bounded; a thread whose wait expired waits for nothing any more
+    auto wait = [&](uint64_t& b, uint32_t parity) -> bool {
+        if (ok && !mbar_wait(smem_u32(&b), parity)) {
             ok = false;
             latch_status(a.status, DSA_ERR_TIMEOUT);
         }
@@ -281,142 +281,170 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     const int boxes = 64 / a.box;                // per 64 positions
 
+    // Loads and MMAs are issued by one elected lane, which also waits: the
+    // tensor pipe takes a chunk's four MMAs in 150 cycles, less than a warp
+    // that waits together, votes and branches to its issuing lane needs
+    // (4.5 us a tile that way, of 1.3 us in the pipe).
     if (warp == 0) {
         // Q and K loads
-        uint32_t kc = 0, seg = 0;
-        while (ok && it.next(s)) {
-            if (seg > 0 && !wait(S.qempty, (seg - 1) & 1)) break;
-            const bool mine = (int)rank < s.rows;
-            if (lane == 0) mbar_arrive_expect_tx_pair(lead(S.qfull), mine ? (uint32_t)sizeof(S.q) : 0u);
-            __syncwarp();
-            if (mine && lane < kQChunks)
-                tma_load_2d_pair(smem_u32(S.q + lane * kChunkBytes), &tm_q, lead(S.qfull), 64 * lane,
-                                 (s.row + (int)rank) * kH);
-            ++seg;
-            bool bad = false;
-            const int32_t at = 64 * (int)rank + (lane & 3) * a.box;
-            int32_t row = box_row(a, s, s.t0 * kTile + at, bad);
-            for (int32_t t = s.t0; ok && t < s.t1; ++t) {
-                const int32_t next = t + 1 < s.t1 ? box_row(a, s, (t + 1) * kTile + at, bad) : 0;
-                for (int ch = 0; ch < kQChunks; ++ch, ++kc) {
-                    const uint32_t st = kc % kKStages;
-                    if (kc >= kKStages && !wait(S.kempty[st], (kc / kKStages - 1) & 1)) break;
-                    if (lane == 0) mbar_arrive_expect_tx_pair(lead(S.kfull[st]), kChunkBytes);
-                    if (lane < boxes)
-                        tma_load_2d_pair(smem_u32(S.k + st * kChunkBytes + lane * a.box * 128), &tm_kv,
-                                         lead(S.kfull[st]), 64 * ch, row);
+        uint32_t g0 = 0, seg = 0;                // tiles and segments before this one
+        for (; ok && it.next(s); g0 += s.t1 - s.t0, ++seg) {
+            // rows of the segment's boxes, 32 boxes of this CTA's positions at a time
+            const int32_t n = (s.t1 - s.t0) * boxes;
+            for (int32_t x0 = 0; ok && x0 < n; x0 += 32) {
+                bool bad = false;
+                const int32_t x = x0 + lane;
+                const int32_t row = box_row(a, s, (s.t0 + x / boxes) * kTile + 64 * (int)rank + (x % boxes) * a.box, bad);
+                for (int32_t y = 0; y < 32 && x0 + y < n; y += boxes) {
+                    int32_t r[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) r[e] = __shfl_sync(0xffffffffu, row, (y + e) & 31);
+                    if (elect_one()) {
+                        if (x0 + y == 0 && (seg == 0 || wait(S.qempty, (seg - 1) & 1))) {
+                            const bool mine = (int)rank < s.rows;
+                            mbar_arrive_expect_tx_pair(lead(S.qfull), mine ? (uint32_t)sizeof(S.q) : 0u);
+                            if (mine)
+                                for (int ch = 0; ch < kQChunks; ++ch)
+                                    tma_load_2d_pair(smem_u32(S.q + ch * kChunkBytes), &tm_q, lead(S.qfull), 64 * ch,
+                                                     (s.row + (int)rank) * kH);
+                        }
+                        uint32_t kc = (g0 + (x0 + y) / boxes) * kQChunks;
+                        for (int ch = 0; ch < kQChunks; ++ch, ++kc) {
+                            const uint32_t st = kc % kKStages;
+                            if (kc >= kKStages && !wait(S.kempty[st], (kc / kKStages - 1) & 1)) break;
+                            const uint32_t bar = lead(S.kfull[st]), dst = smem_u32(S.k + st * kChunkBytes);
+                            mbar_arrive_expect_tx_pair(bar, kChunkBytes);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (e < boxes) tma_load_2d_pair(dst + e * a.box * 128, &tm_kv, bar, 64 * ch, r[e]);
+                        }
+                    }
+                    __syncwarp();
                 }
-                row = next;
+                ok = __all_sync(0xffffffffu, ok);
             }
         }
     } else if (warp == 1) {
-        // MMA: S of tile g + 1, then PV of tile g
         if (rank == 0) {
+            // MMA: S of tile g + 1, then PV of tile g
             constexpr uint32_t kIdS = idesc_bf16_f32(128, kTile), kIdO = idesc_bf16_f32(128, 256, false, true);
-            SegIter itq(a, S.plan);
-            Seg sq;
-            uint32_t kc = 0, vc = 0, gq = 0, gp = 0, segq = 0, segp = 0;
-            int32_t tq = 0, tp = 0;
-            bool more_q = itq.next(sq);
-            if (more_q) tq = sq.t0;
-            auto issue_s = [&]() {
-                if (tq == sq.t0 && !wait(S.qfull, segq & 1)) return;
-                const uint32_t buf = gq & 1;
-                if (gq >= 2 && !wait(S.sempty[buf], ((gq >> 1) - 1) & 1)) return;
-                tc_fence_after();
+            // S of tile g; first / last of its segment (number seg)
+            auto issue_s = [&](uint32_t g, bool first, bool last, uint32_t seg) {
+                if (first && !wait(S.qfull, seg & 1)) return;
+                const uint32_t buf = g & 1;
+                if (g >= 2 && !wait(S.sempty[buf], ((g >> 1) - 1) & 1)) return;
+                uint32_t kc = g * kQChunks;
+                const uint64_t dq = sdesc_sw128(smem_u32(S.q), 0, 1024), dk = sdesc_sw128(smem_u32(S.k), 0, 1024);
                 for (int ch = 0; ch < kQChunks; ++ch, ++kc) {
                     const uint32_t st = kc % kKStages;
                     if (!wait(S.kfull[st], (kc / kKStages) & 1)) return;
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t da = sdesc_sw128(smem_u32(S.q + ch * kChunkBytes), 0, 1024);
-                        const uint64_t db = sdesc_sw128(smem_u32(S.k + st * kChunkBytes), 0, 1024);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16_ss_pair(tmem + kSCol + 64 * buf, da + 2 * k, db + 2 * k, kIdS, (ch | k) != 0);
-                        mma_commit_pair(smem_u32(&S.kempty[st]));
-                    }
-                    __syncwarp();
+                    const uint64_t da = dq + ch * (kChunkBytes >> 4), db = dk + st * (kChunkBytes >> 4);
+    #pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16_ss_pair(tmem + kSCol + 64 * buf, da + 2 * k, db + 2 * k, kIdS, (ch | k) != 0);
+                    mma_commit_pair(smem_u32(&S.kempty[st]));
                 }
-                if (lane == 0) {
-                    mma_commit_pair(smem_u32(&S.sfull[buf]));
-                    if (tq + 1 == sq.t1) mma_commit_pair(smem_u32(&S.qempty));
+                mma_commit_pair(smem_u32(&S.sfull[buf]));
+                if (last) mma_commit_pair(smem_u32(&S.qempty));
+            };
+            auto issue_pv = [&](uint32_t g, bool first, uint32_t seg) {
+                if (first && seg > 0 && !wait(S.ofree, (seg - 1) & 1)) return;
+                if (!wait(S.pfull, g & 1)) return;
+                tc_fence_after();
+                uint32_t vc = 4 * g;
+                const uint64_t dp = sdesc_sw128(smem_u32(S.p), 0, 1024), dv = sdesc_sw128(smem_u32(S.v), kChunkBytes, 1024);
+                for (int gr = 0; gr < 4; ++gr, ++vc) {
+                    const uint32_t st = vc % kVStages;
+                    if (!wait(S.vfull[st], (vc / kVStages) & 1)) return;
+                    tc_fence_after();
+                    const int j = gr >> 1, h = gr & 1;
+                    const uint64_t da = dp + h * (kChunkBytes >> 4), db = dv + st * (kVBytes >> 4);
+    #pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16_ss_pair(tmem + kOCol + 128 * j, da + 2 * k, db + 128 * k, kIdO,
+                                         !first || h != 0 || k != 0);
+                    mma_commit_pair(smem_u32(&S.vempty[st]));
+                }
+                mma_commit_pair(smem_u32(&S.pvdone));
+            };
+            Seg n;
+            bool more = it.next(n);
+            uint32_t g = 0;
+            for (uint32_t seg = 0; ok && more; ++seg) {
+                s = n;
+                more = it.next(n);
+                const int32_t tiles = s.t1 - s.t0;
+                if (elect_one()) {
+                    if (seg == 0) issue_s(0, true, tiles == 1, 0);
+                    for (int32_t t = 0; ok && t < tiles; ++t) {
+                        if (t + 1 < tiles) issue_s(g + t + 1, false, t + 2 == tiles, seg);
+                        else if (more) issue_s(g + t + 1, true, n.t1 - n.t0 == 1, seg + 1);
+                        if (ok) issue_pv(g + t, t == 0, seg);
+                    }
                 }
                 __syncwarp();
-                ++gq;
-                if (++tq == sq.t1) {
-                    ++segq;
-                    more_q = itq.next(sq);
-                    if (more_q) tq = sq.t0;
-                }
-            };
-            if (more_q) issue_s();
-            while (ok && it.next(s)) {
-                for (tp = s.t0; ok && tp < s.t1; ++tp, ++gp) {
-                    if (more_q) issue_s();
-                    if (tp == s.t0 && segp > 0 && !wait(S.ofree, (segp - 1) & 1)) break;
-                    if (!wait(S.pfull, gp & 1)) break;
-                    tc_fence_after();
-                    for (int gr = 0; gr < 4; ++gr, ++vc) {
-                        const uint32_t st = vc % kVStages;
-                        if (!wait(S.vfull[st], (vc / kVStages) & 1)) break;
-                        tc_fence_after();
-                        if (lane == 0) {
-                            const int j = gr >> 1, h = gr & 1;
-                            const uint64_t da = sdesc_sw128(smem_u32(S.p + h * kChunkBytes), 0, 1024);
-                            const uint64_t db = sdesc_sw128(smem_u32(S.v + st * kVBytes), kChunkBytes, 1024);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_bf16_ss_pair(tmem + kOCol + 128 * j, da + 2 * k, db + 128 * k, kIdO,
-                                                 tp != s.t0 || h != 0 || k != 0);
-                            mma_commit_pair(smem_u32(&S.vempty[st]));
-                        }
-                        __syncwarp();
-                    }
-                    if (lane == 0) mma_commit_pair(smem_u32(&S.pvdone));
-                    __syncwarp();
-                }
-                ++segp;
+                ok = __all_sync(0xffffffffu, ok);
+                g += tiles;
             }
         }
     } else if (warp == 2) {
         // V loads
-        uint32_t vc = 0, seg = 0;
-        while (ok && it.next(s)) {
+        uint32_t g0 = 0, seg = 0;
+        for (; ok && it.next(s); g0 += s.t1 - s.t0, ++seg) {
+            const int32_t per = 2 * boxes, n = (s.t1 - s.t0) * per;
             bool bad = false;
-            int32_t row = box_row(a, s, s.t0 * kTile + (lane & 7) * a.box, bad);
-            for (int32_t t = s.t0; ok && t < s.t1; ++t) {
+            for (int32_t x0 = 0; ok && x0 < n; x0 += 32) {
+                const int32_t x = x0 + lane;
+                const int32_t row = box_row(a, s, s.t0 * kTile + x * a.box, bad);
                 const bool any_bad = __any_sync(0xffffffffu, bad);
-                if (lane == 0) S.bad[seg & 3] = any_bad;
-                if (any_bad && lane == 0) latch_status(a.status, DSA_ERR_BAD_INDEX);
-                __syncwarp();
-                const int32_t next = t + 1 < s.t1 ? box_row(a, s, (t + 1) * kTile + (lane & 7) * a.box, bad) : 0;
-                const bool fix = past_committed(s, t);
-                for (int gr = 0; gr < 4; ++gr, ++vc) {
-                    const int j = gr >> 1, h = gr & 1;
-                    const uint32_t st = vc % kVStages;
-                    if (vc >= kVStages && !wait(S.vempty[st], (vc / kVStages - 1) & 1)) break;
-                    const uint32_t bar = fix ? map_to_cluster_rank(smem_u32(&S.vloc[st]), rank) : lead(S.vfull[st]);
-                    if (lane == 0) mbar_arrive_expect_tx_pair(bar, kVBytes);
-                    const int e = lane % boxes, blk = lane / boxes;
-                    const int32_t r = __shfl_sync(0xffffffffu, row, h * boxes + e);
-                    if (blk < 2)
-                        tma_load_2d_pair(smem_u32(S.v + st * kVBytes + blk * kChunkBytes + e * a.box * 128), &tm_kv, bar,
-                                         256 * j + 128 * (int)rank + 64 * blk, r);
+                if (lane == 0) {
+                    S.bad[seg & 3] = any_bad;
+                    if (any_bad) latch_status(a.status, DSA_ERR_BAD_INDEX);
                 }
-                row = next;
+                __syncwarp();
+                for (int32_t y = 0; y < 32 && x0 + y < n; y += per) {
+                    int32_t r[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) r[e] = __shfl_sync(0xffffffffu, row, (y + e) & 31);
+                    if (elect_one()) {
+                        const int32_t tile = (x0 + y) / per;
+                        const bool fix = past_committed(s, s.t0 + tile);
+                        uint32_t vc = 4 * (g0 + tile);
+#pragma unroll
+                        for (int gr = 0; gr < 4; ++gr, ++vc) {
+                            const int j = gr >> 1, h = gr & 1;
+                            const uint32_t st = vc % kVStages;
+                            if (vc >= kVStages && !wait(S.vempty[st], (vc / kVStages - 1) & 1)) break;
+                            const uint32_t bar =
+                                fix ? map_to_cluster_rank(smem_u32(&S.vloc[st]), rank) : lead(S.vfull[st]);
+                            const uint32_t dst = smem_u32(S.v + st * kVBytes);
+                            const int32_t dim = 256 * j + 128 * (int)rank;
+                            mbar_arrive_expect_tx_pair(bar, kVBytes);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (e >= boxes) continue;
+                                const int32_t rr = h == 0 ? r[e] : boxes == 1 ? r[1] : boxes == 2 ? r[2 + (e & 1)] : r[4 + e];
+                                tma_load_2d_pair(dst + e * a.box * 128, &tm_kv, bar, dim, rr);
+                                tma_load_2d_pair(dst + kChunkBytes + e * a.box * 128, &tm_kv, bar, dim + 64, rr);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+                ok = __all_sync(0xffffffffu, ok);
             }
-            ++seg;
         }
     } else if (warp == 3) {
         // fix-up of V tiles that reach past the committed rows
         uint32_t vc = 0, parity = 0;
-        while (ok && it.next(s)) {
-            for (int32_t t = s.t0; ok && t < s.t1; ++t, vc += 4) {
+        while (it.next(s)) {
+            for (int32_t t = s.t0; t < s.t1; ++t, vc += 4) {
                 if (!past_committed(s, t)) continue;
                 for (int gr = 0; gr < 4; ++gr) {
                     const uint32_t st = (vc + gr) % kVStages;
-                    if (!wait(S.vloc[st], (parity >> st) & 1)) break;
+                    wait(S.vloc[st], (parity >> st) & 1);
+                    __syncwarp();
                     parity ^= 1u << st;
                     const int32_t pos0 = t * kTile + 64 * (gr & 1);
                     for (int32_t x = max(0, s.c - pos0) + (lane >> 4); x < 64; x += 2) {
@@ -463,11 +491,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int32_t t = s.t0; t < s.t1; ++t, ++g) {
                 const uint32_t buf = g & 1;
                 wait(S.sfull[buf], (g >> 1) & 1);
+                __syncwarp();
                 tc_fence_after();
                 if (!mine) {
                     // no node here: its rows of S, P and O are nobody's
+                    __syncwarp();
                     if (lane == 0) mbar_arrive_pair(lead(S.sempty[buf]));
                     if (g > 0) wait(S.pvdone, (g - 1) & 1);
+                    __syncwarp();
                     if (lane == 0) mbar_arrive_pair(lead(S.pfull));
                     continue;
                 }
@@ -506,6 +537,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
                 if (g > 0) wait(S.pvdone, (g - 1) & 1);
+                __syncwarp();
                 tc_fence_after();
                 if (t > s.t0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
@@ -530,6 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive_pair(lead(S.pfull));
             }
             wait(S.pvdone, (g - 1) & 1);
+            __syncwarp();
             tc_fence_after();
             const bool bad = *reinterpret_cast<volatile int32_t*>(&S.bad[seg & 3]) != 0;
             if (mine) {
