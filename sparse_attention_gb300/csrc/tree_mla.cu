@@ -54,9 +54,10 @@ constexpr int kMinChunk = kItemCost + 4;     // least work cut off for a pair
 constexpr int kThreads = 288;
 constexpr int kChunkBytes = 64 * 128;        // 64 rows x 64 dims
 constexpr int kQChunks = kDQK / 64;          // 9
-constexpr int kKStages = 7;                  // chunks
-constexpr int kVStages = 5;                  // granules: 64 positions x 128 dims
-constexpr int kVBytes = 2 * kChunkBytes;
+constexpr int kGroup = 3;                    // chunks per K stage
+constexpr int kKStages = 3;                  // a whole tile of K ..
+constexpr int kVStages = 2;                  // .. and of V: a stage is 128 positions x 128 dims of one half
+constexpr int kKBytes = kGroup * kChunkBytes, kVBytes = 4 * kChunkBytes;
 constexpr uint32_t kOCol = 0, kSCol = 256;   // TMEM columns
 constexpr float kRescale = 8.f;              // log2
 
@@ -67,7 +68,7 @@ struct Plan {
 
 struct Smem {
     alignas(1024) uint8_t q[kQChunks * kChunkBytes];
-    alignas(1024) uint8_t k[kKStages * kChunkBytes];
+    alignas(1024) uint8_t k[kKStages * kKBytes];
     alignas(1024) uint8_t v[kVStages * kVBytes];
     alignas(1024) uint8_t p[2 * kChunkBytes];
     alignas(8) uint64_t kfull[kKStages], kempty[kKStages], vfull[kVStages], vempty[kVStages], vloc[kVStages];
@@ -308,15 +309,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                     tma_load_2d_pair(smem_u32(S.q + ch * kChunkBytes), &tm_q, lead(S.qfull), 64 * ch,
                                                      (s.row + (int)rank) * kH);
                         }
-                        uint32_t kc = (g0 + (x0 + y) / boxes) * kQChunks;
-                        for (int ch = 0; ch < kQChunks; ++ch, ++kc) {
-                            const uint32_t st = kc % kKStages;
-                            if (kc >= kKStages && !wait(S.kempty[st], (kc / kKStages - 1) & 1)) break;
-                            const uint32_t bar = lead(S.kfull[st]), dst = smem_u32(S.k + st * kChunkBytes);
-                            mbar_arrive_expect_tx_pair(bar, kChunkBytes);
+                        const uint32_t g = g0 + (x0 + y) / boxes;
+                        for (int gr = 0; gr < kKStages; ++gr) {
+                            if (g > 0 && !wait(S.kempty[gr], (g - 1) & 1)) break;
+                            const uint32_t bar = lead(S.kfull[gr]), dst = smem_u32(S.k + gr * kKBytes);
+                            mbar_arrive_expect_tx_pair(bar, kKBytes);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (e < boxes) tma_load_2d_pair(dst + e * a.box * 128, &tm_kv, bar, 64 * ch, r[e]);
+                            for (int c = 0; c < kGroup; ++c)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (e < boxes)
+                                        tma_load_2d_pair(dst + c * kChunkBytes + e * a.box * 128, &tm_kv, bar,
+                                                         64 * (kGroup * gr + c), r[e]);
                         }
                     }
                     __syncwarp();
@@ -333,17 +337,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (first && !wait(S.qfull, seg & 1)) return;
                 const uint32_t buf = g & 1;
                 if (g >= 2 && !wait(S.sempty[buf], ((g >> 1) - 1) & 1)) return;
-                uint32_t kc = g * kQChunks;
                 const uint64_t dq = sdesc_sw128(smem_u32(S.q), 0, 1024), dk = sdesc_sw128(smem_u32(S.k), 0, 1024);
-                for (int ch = 0; ch < kQChunks; ++ch, ++kc) {
-                    const uint32_t st = kc % kKStages;
-                    if (!wait(S.kfull[st], (kc / kKStages) & 1)) return;
+                for (int gr = 0; gr < kKStages; ++gr) {
+                    if (!wait(S.kfull[gr], g & 1)) return;
                     tc_fence_after();
-                    const uint64_t da = dq + ch * (kChunkBytes >> 4), db = dk + st * (kChunkBytes >> 4);
-    #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16_ss_pair(tmem + kSCol + 64 * buf, da + 2 * k, db + 2 * k, kIdS, (ch | k) != 0);
-                    mma_commit_pair(smem_u32(&S.kempty[st]));
+#pragma unroll
+                    for (int c = 0; c < kGroup; ++c) {
+                        const uint32_t at = (kGroup * gr + c) * (kChunkBytes >> 4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_ss_pair(tmem + kSCol + 64 * buf, dq + at + 2 * k, dk + at + 2 * k, kIdS,
+                                             (gr | c | k) != 0);
+                    }
+                    mma_commit_pair(smem_u32(&S.kempty[gr]));
                 }
                 mma_commit_pair(smem_u32(&S.sfull[buf]));
                 if (last) mma_commit_pair(smem_u32(&S.qempty));
@@ -352,19 +358,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (first && seg > 0 && !wait(S.ofree, (seg - 1) & 1)) return;
                 if (!wait(S.pfull, g & 1)) return;
                 tc_fence_after();
-                uint32_t vc = 4 * g;
-                const uint64_t dp = sdesc_sw128(smem_u32(S.p), 0, 1024), dv = sdesc_sw128(smem_u32(S.v), kChunkBytes, 1024);
-                for (int gr = 0; gr < 4; ++gr, ++vc) {
-                    const uint32_t st = vc % kVStages;
-                    if (!wait(S.vfull[st], (vc / kVStages) & 1)) return;
+                const uint64_t dp = sdesc_sw128(smem_u32(S.p), 0, 1024), dv = sdesc_sw128(smem_u32(S.v), kVBytes / 2, 1024);
+                for (int j = 0; j < kVStages; ++j) {
+                    if (!wait(S.vfull[j], g & 1)) return;
                     tc_fence_after();
-                    const int j = gr >> 1, h = gr & 1;
-                    const uint64_t da = dp + h * (kChunkBytes >> 4), db = dv + st * (kVBytes >> 4);
-    #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16_ss_pair(tmem + kOCol + 128 * j, da + 2 * k, db + 128 * k, kIdO,
-                                         !first || h != 0 || k != 0);
-                    mma_commit_pair(smem_u32(&S.vempty[st]));
+                    const uint64_t db = dv + j * (kVBytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_bf16_ss_pair(tmem + kOCol + 128 * j, dp + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3),
+                                         db + 128 * k, kIdO, !first || k != 0);
+                    mma_commit_pair(smem_u32(&S.vempty[j]));
                 }
                 mma_commit_pair(smem_u32(&S.pvdone));
             };
@@ -410,23 +413,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (elect_one()) {
                         const int32_t tile = (x0 + y) / per;
                         const bool fix = past_committed(s, s.t0 + tile);
-                        uint32_t vc = 4 * (g0 + tile);
+                        const uint32_t g = g0 + tile;
 #pragma unroll
-                        for (int gr = 0; gr < 4; ++gr, ++vc) {
-                            const int j = gr >> 1, h = gr & 1;
-                            const uint32_t st = vc % kVStages;
-                            if (vc >= kVStages && !wait(S.vempty[st], (vc / kVStages - 1) & 1)) break;
+                        for (int j = 0; j < kVStages; ++j) {
+                            if (g > 0 && !wait(S.vempty[j], (g - 1) & 1)) break;
                             const uint32_t bar =
-                                fix ? map_to_cluster_rank(smem_u32(&S.vloc[st]), rank) : lead(S.vfull[st]);
-                            const uint32_t dst = smem_u32(S.v + st * kVBytes);
+                                fix ? map_to_cluster_rank(smem_u32(&S.vloc[j]), rank) : lead(S.vfull[j]);
+                            const uint32_t dst = smem_u32(S.v + j * kVBytes);
                             const int32_t dim = 256 * j + 128 * (int)rank;
                             mbar_arrive_expect_tx_pair(bar, kVBytes);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (e >= boxes) continue;
-                                const int32_t rr = h == 0 ? r[e] : boxes == 1 ? r[1] : boxes == 2 ? r[2 + (e & 1)] : r[4 + e];
-                                tma_load_2d_pair(dst + e * a.box * 128, &tm_kv, bar, dim, rr);
-                                tma_load_2d_pair(dst + kChunkBytes + e * a.box * 128, &tm_kv, bar, dim + 64, rr);
+                            for (int e = 0; e < 8; ++e) {
+                                if (e >= per) continue;
+                                tma_load_2d_pair(dst + e * a.box * 128, &tm_kv, bar, dim, r[e]);
+                                tma_load_2d_pair(dst + kVBytes / 2 + e * a.box * 128, &tm_kv, bar, dim + 64, r[e]);
                             }
                         }
                     }
@@ -437,18 +437,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 3) {
         // fix-up of V tiles that reach past the committed rows
-        uint32_t vc = 0, parity = 0;
+        uint32_t fixed = 0;
         while (it.next(s)) {
-            for (int32_t t = s.t0; t < s.t1; ++t, vc += 4) {
+            for (int32_t t = s.t0; t < s.t1; ++t) {
                 if (!past_committed(s, t)) continue;
-                for (int gr = 0; gr < 4; ++gr) {
-                    const uint32_t st = (vc + gr) % kVStages;
-                    wait(S.vloc[st], (parity >> st) & 1);
+                const int32_t pos0 = t * kTile;
+                for (int j = 0; j < kVStages; ++j) {
+                    wait(S.vloc[j], fixed & 1);
                     __syncwarp();
-                    parity ^= 1u << st;
-                    const int32_t pos0 = t * kTile + 64 * (gr & 1);
-                    for (int32_t x = max(0, s.c - pos0) + (lane >> 4); x < 64; x += 2) {
-                        uint4* at = reinterpret_cast<uint4*>(S.v + st * kVBytes + ((lane >> 3) & 1) * kChunkBytes +
+                    for (int32_t x = max(0, s.c - pos0) + (lane >> 4); x < kTile; x += 2) {
+                        uint4* at = reinterpret_cast<uint4*>(S.v + j * kVBytes + ((lane >> 3) & 1) * (kVBytes / 2) +
                                                              x * 128 + (lane & 7) * 16);
                         if (pos0 + x >= s.len) {
                             *at = make_uint4(0, 0, 0, 0);
@@ -466,8 +464,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_pair(lead(S.vfull[st]));
+                    if (lane == 0) mbar_arrive_pair(lead(S.vfull[j]));
                 }
+                ++fixed;
             }
         }
     } else if (warp < 8) {
