@@ -27,7 +27,8 @@
 //
 // Roles of a CTA's 9 warps: K and Q loads, MMA (rank 0 only), V loads,
 // fix-up, four softmax / epilogue warps (a thread per TMEM lane, so two
-// threads share a query row, 64 positions each).  Tiles that reach
+// threads share a query row, 64 positions each), and one that walks the
+// pair's share of the work and publishes its segments.  Tiles that reach
 // past the committed rows go through the fix-up warp, which zeroes V rows past
 // the sequence (a page's leftovers may hold anything, and 0 * NaN is NaN) and
 // values of drafted rows that are not finite: a row that sees such a row gets
@@ -59,11 +60,19 @@ constexpr int kKStages = 3;                  // a whole tile of K ..
 constexpr int kVStages = 2;                  // .. and of V: a stage is 128 positions x 128 dims of one half
 constexpr int kKBytes = kGroup * kChunkBytes, kVBytes = 4 * kChunkBytes;
 constexpr uint32_t kOCol = 0, kSCol = 256;   // TMEM columns
+constexpr int kSegs = 4;                     // segments published ahead
 constexpr float kRescale = 8.f;              // log2
 
 struct Plan {
     int64_t lo, hi, start_u, chunk;
     int32_t start_b;
+};
+
+// One item's tiles [t0, t1) of a pair's chunk.
+struct Seg {
+    int32_t b, row, c, len, i0, rows, t0, t1, tiles;
+    int64_t u_end;
+    __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
 struct Smem {
@@ -72,8 +81,9 @@ struct Smem {
     alignas(1024) uint8_t v[kVStages * kVBytes];
     alignas(1024) uint8_t p[2 * kChunkBytes];
     alignas(8) uint64_t kfull[kKStages], kempty[kKStages], vfull[kVStages], vempty[kVStages], vloc[kVStages];
-    uint64_t qfull, qempty, sfull[2], sempty[2], pfull, pvdone, ofree;
+    uint64_t qfull, qempty, sfull[2], sempty[2], pfull, pvdone, ofree, segfull[kSegs], segempty[kSegs];
     Plan plan;
+    Seg seg[kSegs];
     int64_t scan[kThreads / 32];
     float xch[2][128];
     int32_t bad[4];
@@ -90,17 +100,10 @@ struct Args {
     float* lse;
     int4* meta;          // [pairs]: row, rows, last pair of the item that a pair begins and another ends
     float* part_lse;     // [2 * pairs][128]
-    float* part_o;       // [2 * pairs][128][512]
+    float* part_o;       // [2 * pairs][2 CTAs][4 warps][64 groups of 4 columns][32 lanes][4]
     int32_t* status;
     int32_t rows_total;  // cache rows
     int32_t box;         // positions per TMA box
-};
-
-// One item's tiles [t0, t1) of a pair's chunk.
-struct Seg {
-    int32_t b, row, c, len, i0, rows, t0, t1, tiles;
-    int64_t u_end;
-    __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
 __device__ __forceinline__ bool seq_ok(const BatchDev& bd, int b, int32_t* status, SeqInfo& s) {
@@ -116,8 +119,8 @@ __device__ __forceinline__ int64_t seq_units(const SeqInfo& s) {
     return (int64_t)((s.nq + 1) >> 1) * (((s.ctx + kTile - 1) / kTile) + kItemCost);
 }
 
-// Walks the segments of a pair's chunk; every warp walks for itself (lanes
-// hold 32 sequences' lengths).
+// Walks the segments of a pair's chunk (a warp; lanes hold 32 sequences'
+// lengths).
 struct SegIter {
     const Args& a;
     const Plan& plan;
@@ -140,7 +143,7 @@ struct SegIter {
             if (nq == 0) continue;
             const int32_t ctx = __shfl_sync(0xffffffffu, w_ctx, b - b0), q0 = __shfl_sync(0xffffffffu, w_q0, b - b0);
             const int32_t tiles = (ctx + kTile - 1) / kTile, per = tiles + kItemCost, pairs = (nq + 1) >> 1;
-            if (p == 0 && lo > u) p = (int32_t)min((lo - u) / per, (int64_t)pairs);
+            if (p == 0 && lo > u) p = (uint32_t)(lo - u) / (uint32_t)per;   // < pairs: lo lies in the chunk's first sequence
             while (p < pairs) {
                 const int64_t u0 = u + (int64_t)p * per + kItemCost;
                 if (u0 - kItemCost >= hi) return false;
@@ -188,7 +191,9 @@ __device__ void make_plan(const Args& a, Smem& S, int pair, int pairs) {
         if (w < warp) before += S.scan[w];
         all += S.scan[w];
     }
-    const int64_t chunk = max((all + pairs - 1) / pairs, (int64_t)kMinChunk);
+    const int64_t even = all < (int64_t(1) << 30) ? (int64_t)(((uint32_t)all + pairs - 1) / (uint32_t)pairs)
+                                                  : (all + pairs - 1) / pairs;
+    const int64_t chunk = max(even, (int64_t)kMinChunk);
     const int64_t lo = min(all, pair * chunk);
     if (tid == 0) {
         S.plan.lo = lo;
@@ -198,15 +203,15 @@ __device__ void make_plan(const Args& a, Smem& S, int pair, int pairs) {
     }
     if (before <= lo && lo < before + sum) {
         int64_t u = before;
-        for (int b = b_lo; b < b_hi; ++b) {
+        S.plan.start_b = b_lo;
+        S.plan.start_u = u;
+        for (int b = b_lo; b + 1 < b_hi; ++b) {
             SeqInfo q;
             const int64_t w = seq_ok(a.bd, b, nullptr, q) ? seq_units(q) : 0;
-            if (lo < u + w) {
-                S.plan.start_b = b;
-                S.plan.start_u = u;
-                break;
-            }
+            if (lo < u + w) break;
             u += w;
+            S.plan.start_b = b + 1;
+            S.plan.start_u = u;
         }
     }
 }
@@ -254,6 +259,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&S.pfull), 8);
         mbar_init(smem_u32(&S.pvdone), 1);
         mbar_init(smem_u32(&S.ofree), 8);
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(smem_u32(&S.segfull[i]), 1);
+            mbar_init(smem_u32(&S.segempty[i]), rank == 0 ? 8 : 7);   // the warps that read segments
+        }
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc_pair(smem_u32(&S.tmem), 512);
@@ -267,7 +276,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_barrier();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    SegIter it(a, S.plan);
     Seg s;
     bool ok = true;
     // the barrier at `b`'s offset in the CTA of rank 0
@@ -280,52 +288,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         return ok;
     };
+    // the next segment that warp 8 published; false behind the last
+    uint32_t segs_read = 0;
+    auto next_seg = [&](Seg& to) -> bool {
+        const uint32_t slot = segs_read & (kSegs - 1);
+        wait(S.segfull[slot], (segs_read / kSegs) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        to = S.seg[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&S.segempty[slot]));
+        ++segs_read;
+        return ok && to.t1 > to.t0;
+    };
     const int boxes = 64 / a.box;                // per 64 positions
 
-    // Loads and MMAs are issued by one elected lane, which also waits: the
-    // tensor pipe takes a chunk's four MMAs in 150 cycles, less than a warp
-    // that waits together, votes and branches to its issuing lane needs
-    // (4.5 us a tile that way, of 1.3 us in the pipe).
+    // MMAs are issued by one elected lane, which also waits: the tensor pipe
+    // takes a K chunk's four MMAs in 150 cycles, less than a warp that waits
+    // together, votes and branches to its issuing lane needs (4.5 us a tile
+    // that way, of 1.3 us in the pipe).  Loads have that time: lane 0 waits,
+    // then each lane issues a box.
     if (warp == 0) {
         // Q and K loads
         uint32_t g0 = 0, seg = 0;                // tiles and segments before this one
-        for (; ok && it.next(s); g0 += s.t1 - s.t0, ++seg) {
+        for (; next_seg(s); g0 += s.t1 - s.t0, ++seg) {
             // rows of the segment's boxes, 32 boxes of this CTA's positions at a time
             const int32_t n = (s.t1 - s.t0) * boxes;
             for (int32_t x0 = 0; ok && x0 < n; x0 += 32) {
                 bool bad = false;
                 const int32_t x = x0 + lane;
                 const int32_t row = box_row(a, s, (s.t0 + x / boxes) * kTile + 64 * (int)rank + (x % boxes) * a.box, bad);
-                for (int32_t y = 0; y < 32 && x0 + y < n; y += boxes) {
-                    int32_t r[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) r[e] = __shfl_sync(0xffffffffu, row, (y + e) & 31);
-                    if (elect_one()) {
-                        if (x0 + y == 0 && (seg == 0 || wait(S.qempty, (seg - 1) & 1))) {
-                            const bool mine = (int)rank < s.rows;
+                for (int32_t y = 0; ok && y < 32 && x0 + y < n; y += boxes) {
+                    if (x0 + y == 0) {
+                        const bool mine = (int)rank < s.rows;
+                        if (lane == 0 && (seg == 0 || wait(S.qempty, (seg - 1) & 1)))
                             mbar_arrive_expect_tx_pair(lead(S.qfull), mine ? (uint32_t)sizeof(S.q) : 0u);
-                            if (mine)
-                                for (int ch = 0; ch < kQChunks; ++ch)
-                                    tma_load_2d_pair(smem_u32(S.q + ch * kChunkBytes), &tm_q, lead(S.qfull), 64 * ch,
-                                                     (s.row + (int)rank) * kH);
-                        }
-                        const uint32_t g = g0 + (x0 + y) / boxes;
-                        for (int gr = 0; gr < kKStages; ++gr) {
-                            if (g > 0 && !wait(S.kempty[gr], (g - 1) & 1)) break;
-                            const uint32_t bar = lead(S.kfull[gr]), dst = smem_u32(S.k + gr * kKBytes);
-                            mbar_arrive_expect_tx_pair(bar, kKBytes);
-#pragma unroll
-                            for (int c = 0; c < kGroup; ++c)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (e < boxes)
-                                        tma_load_2d_pair(dst + c * kChunkBytes + e * a.box * 128, &tm_kv, bar,
-                                                         64 * (kGroup * gr + c), r[e]);
-                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (ok && mine && lane < kQChunks)
+                            tma_load_2d_pair(smem_u32(S.q + lane * kChunkBytes), &tm_q, lead(S.qfull), 64 * lane,
+                                             (s.row + (int)rank) * kH);
                     }
-                    __syncwarp();
+                    const uint32_t g = g0 + (x0 + y) / boxes;
+                    const int e = lane % boxes, c = lane / boxes;      // a box of a chunk each
+                    const int32_t r = __shfl_sync(0xffffffffu, row, y + e);
+#pragma unroll 1
+                    for (int gr = 0; ok && gr < kKStages; ++gr) {
+                        const uint32_t bar = lead(S.kfull[gr]);
+                        if (lane == 0 && (g == 0 || wait(S.kempty[gr], (g - 1) & 1)))
+                            mbar_arrive_expect_tx_pair(bar, kKBytes);
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (ok && c < kGroup)
+                            tma_load_2d_pair(smem_u32(S.k + gr * kKBytes + c * kChunkBytes + e * a.box * 128), &tm_kv,
+                                             bar, 64 * (kGroup * gr + c), r);
+                    }
                 }
-                ok = __all_sync(0xffffffffu, ok);
             }
         }
     } else if (warp == 1) {
@@ -372,14 +387,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mma_commit_pair(smem_u32(&S.pvdone));
             };
             Seg n;
-            bool more = it.next(n);
+            bool more = next_seg(n);
             uint32_t g = 0;
+            if (more && elect_one()) issue_s(0, true, n.t1 - n.t0 == 1, 0);
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
             for (uint32_t seg = 0; ok && more; ++seg) {
                 s = n;
-                more = it.next(n);
+                more = next_seg(n);
                 const int32_t tiles = s.t1 - s.t0;
                 if (elect_one()) {
-                    if (seg == 0) issue_s(0, true, tiles == 1, 0);
                     for (int32_t t = 0; ok && t < tiles; ++t) {
                         if (t + 1 < tiles) issue_s(g + t + 1, false, t + 2 == tiles, seg);
                         else if (more) issue_s(g + t + 1, true, n.t1 - n.t0 == 1, seg + 1);
@@ -394,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 2) {
         // V loads
         uint32_t g0 = 0, seg = 0;
-        for (; ok && it.next(s); g0 += s.t1 - s.t0, ++seg) {
+        for (; next_seg(s); g0 += s.t1 - s.t0, ++seg) {
             const int32_t per = 2 * boxes, n = (s.t1 - s.t0) * per;
             bool bad = false;
             for (int32_t x0 = 0; ok && x0 < n; x0 += 32) {
@@ -406,39 +423,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (any_bad) latch_status(a.status, DSA_ERR_BAD_INDEX);
                 }
                 __syncwarp();
-                for (int32_t y = 0; y < 32 && x0 + y < n; y += per) {
-                    int32_t r[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) r[e] = __shfl_sync(0xffffffffu, row, (y + e) & 31);
-                    if (elect_one()) {
-                        const int32_t tile = (x0 + y) / per;
-                        const bool fix = past_committed(s, s.t0 + tile);
-                        const uint32_t g = g0 + tile;
-#pragma unroll
-                        for (int j = 0; j < kVStages; ++j) {
-                            if (g > 0 && !wait(S.vempty[j], (g - 1) & 1)) break;
-                            const uint32_t bar =
-                                fix ? map_to_cluster_rank(smem_u32(&S.vloc[j]), rank) : lead(S.vfull[j]);
-                            const uint32_t dst = smem_u32(S.v + j * kVBytes);
-                            const int32_t dim = 256 * j + 128 * (int)rank;
+                for (int32_t y = 0; ok && y < 32 && x0 + y < n; y += per) {
+                    const int32_t tile = (x0 + y) / per;
+                    const bool fix = past_committed(s, s.t0 + tile);
+                    const uint32_t g = g0 + tile;
+                    const int e = lane % per, blk = lane / per;        // a box of 64 dims each
+                    const int32_t r = __shfl_sync(0xffffffffu, row, y + e);
+#pragma unroll 1
+                    for (int j = 0; ok && j < kVStages; ++j) {
+                        const uint32_t bar =
+                            fix ? map_to_cluster_rank(smem_u32(&S.vloc[j]), rank) : lead(S.vfull[j]);
+                        if (lane == 0 && (g == 0 || wait(S.vempty[j], (g - 1) & 1)))
                             mbar_arrive_expect_tx_pair(bar, kVBytes);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                if (e >= per) continue;
-                                tma_load_2d_pair(dst + e * a.box * 128, &tm_kv, bar, dim, r[e]);
-                                tma_load_2d_pair(dst + kVBytes / 2 + e * a.box * 128, &tm_kv, bar, dim + 64, r[e]);
-                            }
-                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (ok && blk < 2)
+                            tma_load_2d_pair(smem_u32(S.v + j * kVBytes + blk * (kVBytes / 2) + e * a.box * 128),
+                                             &tm_kv, bar, 256 * j + 128 * (int)rank + 64 * blk, r);
                     }
-                    __syncwarp();
                 }
-                ok = __all_sync(0xffffffffu, ok);
             }
         }
     } else if (warp == 3) {
         // fix-up of V tiles that reach past the committed rows
         uint32_t fixed = 0;
-        while (it.next(s)) {
+        while (next_seg(s)) {
             for (int32_t t = s.t0; t < s.t1; ++t) {
                 if (!past_committed(s, t)) continue;
                 const int32_t pos0 = t * kTile;
@@ -480,7 +488,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             named_bar_sync(1, 128);
             return S.xch[xb][ln ^ 64];
         };
-        while (it.next(s)) {
+        // the four warps agree on each segment, since they meet at barriers
+        while (!named_bar_or(1, 128, !next_seg(s))) {
             const bool mine = (int)rank < s.rows;
             const uint64_t bits =
                 mine ? visible_bits(__ldg(reinterpret_cast<const unsigned long long*>(a.mask) + s.row + rank),
@@ -561,43 +570,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive_pair(lead(S.pfull));
             }
             wait(S.pvdone, (g - 1) & 1);
-            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
             const bool bad = *reinterpret_cast<volatile int32_t*>(&S.bad[seg & 3]) != 0;
             if (mine) {
                 l += exchange(l);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const float ls = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-                const int64_t head = (int64_t)(s.row + (int)rank) * kH + x;
+                const int64_t head = (int64_t)(s.row + (int)rank) * kH;
                 const bool whole = s.whole();
                 const int64_t slot = 2 * (int64_t)pair + (s.t0 == 0 ? 1 : 0);
-                const int64_t prow = slot * 128 + 64 * (int)rank + x;
-                uint16_t* ob = a.out + head * kDV + 128 * half;
-                float* of = a.part_o + prow * kDV + 128 * half;
                 if (half == 0 && ok) {
-                    if (!whole) a.part_lse[prow] = bad ? INFINITY : ls;
-                    else if (a.lse && !bad) a.lse[head] = ls;
+                    if (!whole) a.part_lse[slot * 128 + 64 * (int)rank + x] = bad ? INFINITY : ls;
+                    else if (a.lse && !bad) a.lse[head + x] = ls;
                 }
-#pragma unroll 1
-                for (uint32_t c = 0; c < 256; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32(tl + kOCol + c, o);
-                    tmem_ld_wait();
-                    const uint32_t col = (c & 127) + 2 * (c & 128);   // dims 256 j + 128 half + ..
-                    if (ok && whole && !bad) {
+                // O through a 4 KiB piece of P's buffer per warp, so that a
+                // store covers whole 128-byte lines of 4 rows (16 bytes of 32
+                // rows at a time: 5.7 us an item instead of 1)
+                uint8_t* stage = S.p + (warp - 4) * 4096;
+                uint8_t* mine_at = stage + lane * 128;
+                const int x0 = x & 32;
+                auto flush = [&](uint8_t* to, int64_t pitch) {
+                    __syncwarp();
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
+                    for (int k = 0; k < 8; ++k) {
+                        const int row = 4 * k + (lane >> 3), at = lane & 7;
+                        *reinterpret_cast<uint4*>(to + row * pitch + 16 * at) =
+                            *reinterpret_cast<const uint4*>(stage + row * 128 + ((at ^ (row & 7)) << 4));
+                    }
+                    __syncwarp();
+                };
+                if (ok && whole && !bad) {
+#pragma unroll 1
+                    for (uint32_t c = 0; c < 256; c += 64) {
+                        uint32_t o[2][32];
+                        tmem_ld_32x32b_x32(tl + kOCol + c, o[0]);
+                        tmem_ld_32x32b_x32(tl + kOCol + c + 32, o[1]);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) {
                             uint32_t w[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                w[k] = pack_bf16x2(__uint_as_float(o[8 * v + 2 * k]) * inv,
-                                                   __uint_as_float(o[8 * v + 2 * k + 1]) * inv);
-                            *reinterpret_cast<uint4*>(ob + col + 8 * v) = make_uint4(w[0], w[1], w[2], w[3]);
+                                w[k] = pack_bf16x2(__uint_as_float(o[v >> 2][8 * (v & 3) + 2 * k]) * inv,
+                                                   __uint_as_float(o[v >> 2][8 * (v & 3) + 2 * k + 1]) * inv);
+                            *reinterpret_cast<uint4*>(mine_at + ((v ^ (lane & 7)) << 4)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                    } else if (ok && !whole) {
+                        // dims 256 j + 128 half + ..
+                        const uint32_t dim = 128 * half + (c & 127) + 2 * (c & 128);
+                        flush(reinterpret_cast<uint8_t*>(a.out + (head + x0) * kDV + dim), 2 * kDV);
+                    }
+                } else if (ok && !whole) {
+                    // partial results stay in TMEM's order, four columns of a
+                    // warp's 32 lanes side by side
+                    float4* part = reinterpret_cast<float4*>(a.part_o) +
+                                   ((slot * 2 + (int)rank) * 4 + (warp - 4)) * 64 * 32 + lane;
+#pragma unroll 1
+                    for (uint32_t c = 0; c < 256; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(tl + kOCol + c, o);
+                        tmem_ld_wait();
 #pragma unroll
                         for (int v = 0; v < 8; ++v)
-                            *reinterpret_cast<float4*>(of + col + 4 * v) =
+                            part[(c / 4 + v) * 32] =
                                 make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
                                             __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
                     }
@@ -608,12 +644,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_pair(lead(S.ofree));
             ++seg;
         }
-    } else if (rank == 0) {
-        // what merge_kernel has to know of this pair's cut items
+    } else {
+        // the segments, and what tree_merge_kernel has to know of a cut item
+        SegIter it(a, S.plan);
         int4 meta = make_int4(0, 0, 0, 0);
-        while (it.next(s))
-            if (s.t0 == 0 && !s.whole()) meta = make_int4(s.row, s.rows, (int)(s.u_end / S.plan.chunk), 0);
-        if (lane == 0) a.meta[pair] = meta;
+        bool more = true;
+        for (uint32_t n = 0; ok && more; ++n) {
+            more = it.next(s);
+            const uint32_t slot = n & (kSegs - 1);
+            if (n >= kSegs) wait(S.segempty[slot], (n / kSegs - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!more) s.t0 = s.t1 = 0;
+            if (lane == 0) {
+                S.seg[slot] = s;
+                mbar_arrive(smem_u32(&S.segfull[slot]));
+            }
+            __syncwarp();
+            if (more && s.t0 == 0 && !s.whole()) meta = make_int4(s.row, s.rows, (int)(s.u_end / S.plan.chunk), 0);
+        }
+        if (rank == 0 && lane == 0) a.meta[pair] = meta;
     }
     if (!ok) {
         // let copies in flight land before the CTA's shared memory goes
@@ -628,46 +677,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-// Joins the partial results of an item: block (pair, y) takes 8 of the 128
-// query rows of the item that the pair begins.
-__global__ void __launch_bounds__(128)
+// Joins the partial results of the item that a pair begins (blockIdx.x): a
+// warp per 16 TMEM columns of a CTA's 32 lanes, a lane per query row.
+__global__ void __launch_bounds__(256)
     tree_merge_kernel(const int4* __restrict__ meta, const float* __restrict__ part_lse,
-                      const float* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
+                      const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
     pdl_wait();
-    const int pair = blockIdx.x, tid = threadIdx.x;
+    const int pair = blockIdx.x, lane = threadIdx.x & 31;
+    const int unit = 8 * blockIdx.y + (threadIdx.x >> 5);
+    const int rank = unit >> 6, w = (unit >> 4) & 3, c = 16 * (unit & 15);
     const int4 it = meta[pair];
-    const int first = 8 * blockIdx.y;
-    if (first >= 64 * it.y) return;
+    if (rank >= it.y) return;
+    const int x = 32 * (w & 1) + lane;           // the lane's head
     // the item's pieces: this pair's slot 2 pair + 1, then slots 2 p of the
     // pairs behind it
     const int pieces = it.z - pair + 1;
     auto slot = [&](int e) -> int64_t { return e == 0 ? 2 * (int64_t)pair + 1 : 2 * ((int64_t)pair + e); };
-    for (int r = first; r < first + 8; ++r) {
-        float mx = -INFINITY, sum = 0.f;
-        bool bad = false;
-        for (int e = 0; e < pieces; ++e) {
-            const float v = part_lse[slot(e) * 128 + r];
-            bad = bad || v == INFINITY;
-            mx = (v > mx || v != v) ? v : mx;
-        }
-        if (bad) continue;
-        const float base = mx == -INFINITY ? 0.f : mx;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int e = 0; e < pieces; ++e) {
-            const float w = ex2_approx((part_lse[slot(e) * 128 + r] - base) * kLog2e);
-            const float4 o = *reinterpret_cast<const float4*>(part_o + (slot(e) * 128 + r) * kDV + 4 * tid);
-            sum += w;
-            acc.x += w * o.x;
-            acc.y += w * o.y;
-            acc.z += w * o.z;
-            acc.w += w * o.w;
-        }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t head = (int64_t)it.x * kH + r;
-        *reinterpret_cast<uint2*>(out + head * kDV + 4 * tid) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (lse && tid == 0) lse[head] = sum == 0.f ? -INFINITY : base + log2f(sum) * kLn2;
+    auto piece_lse = [&](int e) -> float { return part_lse[slot(e) * 128 + 64 * rank + x]; };
+    float mx = -INFINITY;
+    bool bad = false, nan = false;
+#pragma unroll 4
+    for (int e = 0; e < pieces; ++e) {
+        const float v = piece_lse(e);
+        bad = bad || v == INFINITY;
+        nan = nan || v != v;
+        mx = fmaxf(mx, v);
     }
+    if (nan) mx = NAN;
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float acc[16], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+#pragma unroll 2
+    for (int e = 0; e < pieces; ++e) {
+        const float f = ex2_approx((piece_lse(e) - base) * kLog2e);
+        const float4* o = part_o + (((slot(e) * 2 + rank) * 4 + w) * 64 + c / 4) * 32 + lane;
+        sum += f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 v = o[32 * k];
+            acc[4 * k] += f * v.x;
+            acc[4 * k + 1] += f * v.y;
+            acc[4 * k + 2] += f * v.z;
+            acc[4 * k + 3] += f * v.w;
+        }
+    }
+    if (bad) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t head = (int64_t)(it.x + rank) * kH + x;
+    uint4* to = reinterpret_cast<uint4*>(out + head * kDV + 128 * (w >> 1) + (c & 127) + 2 * (c & 128));
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        to[k] = make_uint4(pack_bf16x2(acc[8 * k] * inv, acc[8 * k + 1] * inv),
+                           pack_bf16x2(acc[8 * k + 2] * inv, acc[8 * k + 3] * inv),
+                           pack_bf16x2(acc[8 * k + 4] * inv, acc[8 * k + 5] * inv),
+                           pack_bf16x2(acc[8 * k + 6] * inv, acc[8 * k + 7] * inv));
+    if (lse && (w >> 1) == 0 && c == 0) lse[head] = sum == 0.f ? -INFINITY : base + log2f(sum) * kLn2;
 }
 
 // CTA pairs that can be resident at once on the current device.
@@ -748,7 +813,7 @@ cudaError_t launch_tree_mla(const BatchDev& bd, const PagesDev& pg, const uint16
     count_launches(1);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)pairs, 16);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -756,7 +821,7 @@ cudaError_t launch_tree_mla(const BatchDev& bd, const PagesDev& pg, const uint16
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, (const int4*)a.meta, (const float*)a.part_lse,
-                           (const float*)a.part_o, out, lse);
+                           (const float4*)a.part_o, out, lse);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
