@@ -72,7 +72,13 @@ __device__ __forceinline__ int64_t buf_row(bool local, const SeqInfo& s, int b, 
 bool make_tmap_bf16_2d(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner,
                        uint32_t box_rows);
 
-// The same for a 2-D tensor of bytes (row stride inner bytes).
+// A row-major bf16 tensor [rows, 64 * chunks] seen as [chunks][rows][64], so
+// that one box brings box_rows rows of box_chunks 64-column chunks, each chunk
+// an operand block of its own: box {64, box_rows, box_chunks}.
+bool make_tmap_bf16_chunks(CUtensorMap* tm, const void* base, uint64_t chunks, uint64_t rows, uint32_t box_rows,
+                           uint32_t box_chunks);
+
+// make_tmap_bf16_2d for a 2-D tensor of bytes (row stride inner bytes).
 bool make_tmap_u8_2d(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner,
                      uint32_t box_rows);
 

@@ -50,8 +50,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTile = 128;                   // positions per tile
-constexpr int kItemCost = 4;                 // an item's start and end, in tiles
-constexpr int kMinChunk = kItemCost + 4;     // least work cut off for a pair
+constexpr int kItemCost = 3;                 // an item's start and end, in tiles
+constexpr int kMinChunk = kItemCost + 1;     // least work cut off for a pair
 constexpr int kThreads = 288;
 constexpr int kChunkBytes = 64 * 128;        // 64 rows x 64 dims
 constexpr int kQChunks = kDQK / 64;          // 9
@@ -98,12 +98,11 @@ struct Args {
     float scale_log2;
     uint16_t* out;
     float* lse;
-    int4* meta;          // [pairs]: row, rows, last pair of the item that a pair begins and another ends
+    int4* meta;          // [pairs]: row, rows, last and first pair of the cut item that a pair begins or lies in
     float* part_lse;     // [2 * pairs][128]
     float* part_o;       // [2 * pairs][2 CTAs][4 warps][64 groups of 4 columns][32 lanes][4]
     int32_t* status;
     int32_t rows_total;  // cache rows
-    int32_t box;         // positions per TMA box
 };
 
 __device__ __forceinline__ bool seq_ok(const BatchDev& bd, int b, int32_t* status, SeqInfo& s) {
@@ -228,8 +227,16 @@ __device__ __forceinline__ int32_t box_row(const Args& a, const Seg& s, int32_t 
 
 __device__ __forceinline__ bool past_committed(const Seg& s, int32_t t) { return (t + 1) * kTile > s.c; }
 
+// kKRows, kVRows: positions of a K box (of one chunk, or of a stage's three)
+// and of a V box (of two).  Pages of 64 rows and more, and contiguous caches:
+// boxes of 64; pages of 32: of 32; pages of 16: K boxes of 8 rows x 3 chunks,
+// whose 8-row groups stay evenly spaced in a stage as a descriptor needs them
+// (24 K and 16 V boxes a tile; boxes of one chunk of 16 rows, 36 and 32: 0.94
+// instead of 0.89 ms for 16 trees of 64 over 8,192 rows).
+template <int kKRows, int kVRows>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    tree_mla_kernel(const Args a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv) {
+    tree_mla_kernel(const Args a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem& S = *reinterpret_cast<Smem*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -268,7 +275,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_alloc_pair(smem_u32(&S.tmem), 512);
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&tm_q);
-        prefetch_tmap(&tm_kv);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
     }
     make_plan(a, S, pair, pairs);
     tc_fence_before();
@@ -300,7 +308,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++segs_read;
         return ok && to.t1 > to.t0;
     };
-    const int boxes = 64 / a.box;                // per 64 positions
+    constexpr int kboxes = 64 / kKRows, vboxes = kTile / kVRows;     // per stage's positions
+    constexpr int kChunksPerBox = kKRows == 32 ? 1 : kGroup;
 
     // MMAs are issued by one elected lane, which also waits: the tensor pipe
     // takes a K chunk's four MMAs in 150 cycles, less than a warp that waits
@@ -311,13 +320,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Q and K loads
         uint32_t g0 = 0, seg = 0;                // tiles and segments before this one
         for (; next_seg(s); g0 += s.t1 - s.t0, ++seg) {
-            // rows of the segment's boxes, 32 boxes of this CTA's positions at a time
-            const int32_t n = (s.t1 - s.t0) * boxes;
+            // first rows of the segment's boxes, 32 at a time
+            const int32_t n = (s.t1 - s.t0) * kboxes;
             for (int32_t x0 = 0; ok && x0 < n; x0 += 32) {
                 bool bad = false;
                 const int32_t x = x0 + lane;
-                const int32_t row = box_row(a, s, (s.t0 + x / boxes) * kTile + 64 * (int)rank + (x % boxes) * a.box, bad);
-                for (int32_t y = 0; ok && y < 32 && x0 + y < n; y += boxes) {
+                const int32_t row =
+                    box_row(a, s, (s.t0 + x / kboxes) * kTile + 64 * (int)rank + (x % kboxes) * kKRows, bad);
+                for (int32_t y = 0; ok && y < 32 && x0 + y < n; y += kboxes) {
                     if (x0 + y == 0) {
                         const bool mine = (int)rank < s.rows;
                         if (lane == 0 && (seg == 0 || wait(S.qempty, (seg - 1) & 1)))
@@ -327,8 +337,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tma_load_2d_pair(smem_u32(S.q + lane * kChunkBytes), &tm_q, lead(S.qfull), 64 * lane,
                                              (s.row + (int)rank) * kH);
                     }
-                    const uint32_t g = g0 + (x0 + y) / boxes;
-                    const int e = lane % boxes, c = lane / boxes;      // a box of a chunk each
+                    const uint32_t g = g0 + (x0 + y) / kboxes;
+                    const int e = lane % kboxes, c = (lane / kboxes) * kChunksPerBox;    // a box each
                     const int32_t r = __shfl_sync(0xffffffffu, row, y + e);
 #pragma unroll 1
                     for (int gr = 0; ok && gr < kKStages; ++gr) {
@@ -337,8 +347,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             mbar_arrive_expect_tx_pair(bar, kKBytes);
                         ok = __shfl_sync(0xffffffffu, ok, 0);
                         if (ok && c < kGroup)
-                            tma_load_2d_pair(smem_u32(S.k + gr * kKBytes + c * kChunkBytes + e * a.box * 128), &tm_kv,
-                                             bar, 64 * (kGroup * gr + c), r);
+                            tma_load_3d_pair(smem_u32(S.k + gr * kKBytes + c * kChunkBytes +
+                                                      e * kKRows * 128 * kChunksPerBox),
+                                             &tm_k, bar, 0, r, kGroup * gr + c);
                     }
                 }
             }
@@ -347,21 +358,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rank == 0) {
             // MMA: S of tile g + 1, then PV of tile g
             constexpr uint32_t kIdS = idesc_bf16_f32(128, kTile), kIdO = idesc_bf16_f32(128, 256, false, true);
+            // K stages: three chunks of 64 rows, or (boxes of 8 rows) eight
+            // groups of 8 rows x three chunks; V stages: boxes of two 64-dim
+            // blocks of vrows rows
+            constexpr uint32_t ksbo = kKRows == 8 ? 1024 * kGroup : 1024;
+            constexpr uint32_t kcstep = (kKRows == 8 ? 1024 : kChunkBytes) >> 4;
             // S of tile g; first / last of its segment (number seg)
             auto issue_s = [&](uint32_t g, bool first, bool last, uint32_t seg) {
                 if (first && !wait(S.qfull, seg & 1)) return;
                 const uint32_t buf = g & 1;
                 if (g >= 2 && !wait(S.sempty[buf], ((g >> 1) - 1) & 1)) return;
-                const uint64_t dq = sdesc_sw128(smem_u32(S.q), 0, 1024), dk = sdesc_sw128(smem_u32(S.k), 0, 1024);
+                const uint64_t dq = sdesc_sw128(smem_u32(S.q), 0, 1024), dk = sdesc_sw128(smem_u32(S.k), 0, ksbo);
                 for (int gr = 0; gr < kKStages; ++gr) {
                     if (!wait(S.kfull[gr], g & 1)) return;
                     tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < kGroup; ++c) {
-                        const uint32_t at = (kGroup * gr + c) * (kChunkBytes >> 4);
+                        const uint64_t da = dq + (kGroup * gr + c) * (kChunkBytes >> 4);
+                        const uint64_t db = dk + gr * (kKBytes >> 4) + c * kcstep;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_bf16_ss_pair(tmem + kSCol + 64 * buf, dq + at + 2 * k, dk + at + 2 * k, kIdS,
+                            mma_bf16_ss_pair(tmem + kSCol + 64 * buf, da + 2 * k, db + 2 * k, kIdS,
                                              (gr | c | k) != 0);
                     }
                     mma_commit_pair(smem_u32(&S.kempty[gr]));
@@ -373,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (first && seg > 0 && !wait(S.ofree, (seg - 1) & 1)) return;
                 if (!wait(S.pfull, g & 1)) return;
                 tc_fence_after();
-                const uint64_t dp = sdesc_sw128(smem_u32(S.p), 0, 1024), dv = sdesc_sw128(smem_u32(S.v), kVBytes / 2, 1024);
+                const uint64_t dp = sdesc_sw128(smem_u32(S.p), 0, 1024), dv = sdesc_sw128(smem_u32(S.v), kVRows * 128, 1024);
                 for (int j = 0; j < kVStages; ++j) {
                     if (!wait(S.vfull[j], g & 1)) return;
                     tc_fence_after();
@@ -381,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
                         mma_bf16_ss_pair(tmem + kOCol + 128 * j, dp + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3),
-                                         db + 128 * k, kIdO, !first || k != 0);
+                                         db + 128 * k + 128 * ((16 * k) & -kVRows) / 16, kIdO, !first || k != 0);
                     mma_commit_pair(smem_u32(&S.vempty[j]));
                 }
                 mma_commit_pair(smem_u32(&S.pvdone));
@@ -412,23 +429,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // V loads
         uint32_t g0 = 0, seg = 0;
         for (; next_seg(s); g0 += s.t1 - s.t0, ++seg) {
-            const int32_t per = 2 * boxes, n = (s.t1 - s.t0) * per;
+            const int32_t n = (s.t1 - s.t0) * vboxes;
             bool bad = false;
             for (int32_t x0 = 0; ok && x0 < n; x0 += 32) {
                 const int32_t x = x0 + lane;
-                const int32_t row = box_row(a, s, s.t0 * kTile + x * a.box, bad);
+                const int32_t row = box_row(a, s, s.t0 * kTile + x * kVRows, bad);
                 const bool any_bad = __any_sync(0xffffffffu, bad);
                 if (lane == 0) {
                     S.bad[seg & 3] = any_bad;
                     if (any_bad) latch_status(a.status, DSA_ERR_BAD_INDEX);
                 }
                 __syncwarp();
-                for (int32_t y = 0; ok && y < 32 && x0 + y < n; y += per) {
-                    const int32_t tile = (x0 + y) / per;
+                for (int32_t y = 0; ok && y < 32 && x0 + y < n; y += vboxes) {
+                    const int32_t tile = (x0 + y) / vboxes;
                     const bool fix = past_committed(s, s.t0 + tile);
                     const uint32_t g = g0 + tile;
-                    const int e = lane % per, blk = lane / per;        // a box of 64 dims each
-                    const int32_t r = __shfl_sync(0xffffffffu, row, y + e);
+                    const int32_t r = __shfl_sync(0xffffffffu, row, (y + lane) & 31);     // a box each
 #pragma unroll 1
                     for (int j = 0; ok && j < kVStages; ++j) {
                         const uint32_t bar =
@@ -436,9 +452,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (lane == 0 && (g == 0 || wait(S.vempty[j], (g - 1) & 1)))
                             mbar_arrive_expect_tx_pair(bar, kVBytes);
                         ok = __shfl_sync(0xffffffffu, ok, 0);
-                        if (ok && blk < 2)
-                            tma_load_2d_pair(smem_u32(S.v + j * kVBytes + blk * (kVBytes / 2) + e * a.box * 128),
-                                             &tm_kv, bar, 256 * j + 128 * (int)rank + 64 * blk, r);
+                        if (ok && lane < vboxes)
+                            tma_load_3d_pair(smem_u32(S.v + j * kVBytes + lane * kVRows * 256), &tm_v, bar, 0, r,
+                                             4 * j + 2 * (int)rank);
                     }
                 }
             }
@@ -454,8 +470,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     wait(S.vloc[j], fixed & 1);
                     __syncwarp();
                     for (int32_t x = max(0, s.c - pos0) + (lane >> 4); x < kTile; x += 2) {
-                        uint4* at = reinterpret_cast<uint4*>(S.v + j * kVBytes + ((lane >> 3) & 1) * (kVBytes / 2) +
-                                                             x * 128 + (lane & 7) * 16);
+                        const int32_t in = x & (kVRows - 1), blk = (lane >> 3) & 1;
+                        uint4* at = reinterpret_cast<uint4*>(S.v + j * kVBytes + (x - in) * 256 +
+                                                             (blk * kVRows + in) * 128 + (lane & 7) * 16);
                         if (pos0 + x >= s.len) {
                             *at = make_uint4(0, 0, 0, 0);
                         } else {
@@ -660,7 +677,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mbar_arrive(smem_u32(&S.segfull[slot]));
             }
             __syncwarp();
-            if (more && s.t0 == 0 && !s.whole()) meta = make_int4(s.row, s.rows, (int)(s.u_end / S.plan.chunk), 0);
+            if (more && !s.whole())
+                meta = make_int4(s.row, s.rows, (int)(s.u_end / S.plan.chunk),
+                                 (int)((s.u_end - s.tiles + 1) / S.plan.chunk));
         }
         if (rank == 0 && lane == 0) a.meta[pair] = meta;
     }
@@ -677,62 +696,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-// Joins the partial results of the item that a pair begins (blockIdx.x): a
-// warp per 16 TMEM columns of a CTA's 32 lanes, a lane per query row.
-__global__ void __launch_bounds__(256)
+// Joins the partial results of the items that chunks cut.  A unit is 16 TMEM
+// columns of a CTA's 32 lanes, a lane per query row.  Items of few pieces: the
+// 16 blocks of the pair that begins the item take a unit per warp.  Items of
+// many (one long sequence over the whole GPU: 10 MB of pieces): the blocks of
+// the pairs inside it, which begin nothing, help; a block takes a unit, its
+// warps every 8th piece (1 x 100,000 rows: 83 -> 30 us, merge included).
+constexpr int kMergeBlocks = 16, kMergeWarps = 8;
+
+__global__ void __launch_bounds__(32 * kMergeWarps)
     tree_merge_kernel(const int4* __restrict__ meta, const float* __restrict__ part_lse,
                       const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
+    __shared__ float acc_s[kMergeWarps][17][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
-    const int pair = blockIdx.x, lane = threadIdx.x & 31;
-    const int unit = 8 * blockIdx.y + (threadIdx.x >> 5);
-    const int rank = unit >> 6, w = (unit >> 4) & 3, c = 16 * (unit & 15);
-    const int4 it = meta[pair];
-    if (rank >= it.y) return;
-    const int x = 32 * (w & 1) + lane;           // the lane's head
-    // the item's pieces: this pair's slot 2 pair + 1, then slots 2 p of the
-    // pairs behind it
+    const int4 it = meta[blockIdx.x];
+    const int pair = it.w, helper = (int)blockIdx.x - pair;
+    if (it.y == 0) return;
+    // its pieces: the first pair's slot 2 pair + 1, then slots 2 p of the pairs
+    // behind it
     const int pieces = it.z - pair + 1;
+    const bool wide = pieces > kMergeWarps;
+    if (!wide && helper > 0) return;
+    const int helpers = wide ? it.z - pair + (meta[it.z].w == pair ? 1 : 0) : 1;
+    const int e0 = wide ? warp : 0, step = wide ? kMergeWarps : 1;
+    const int units = 64 * it.y, stride = wide ? kMergeBlocks * helpers : units;
     auto slot = [&](int e) -> int64_t { return e == 0 ? 2 * (int64_t)pair + 1 : 2 * ((int64_t)pair + e); };
-    auto piece_lse = [&](int e) -> float { return part_lse[slot(e) * 128 + 64 * rank + x]; };
-    float mx = -INFINITY;
-    bool bad = false, nan = false;
+    for (int unit = wide ? kMergeBlocks * helper + (int)blockIdx.y : kMergeWarps * (int)blockIdx.y + warp; unit < units;
+         unit += stride) {
+        const int rank = unit >> 6, w = (unit >> 4) & 3, c = 16 * (unit & 15);
+        const int x = 32 * (w & 1) + lane;           // the lane's head
+        auto piece_lse = [&](int e) -> float { return part_lse[slot(e) * 128 + 64 * rank + x]; };
+        float mx = -INFINITY;
+        bool bad = false, nan = false;
 #pragma unroll 4
-    for (int e = 0; e < pieces; ++e) {
-        const float v = piece_lse(e);
-        bad = bad || v == INFINITY;
-        nan = nan || v != v;
-        mx = fmaxf(mx, v);
-    }
-    if (nan) mx = NAN;
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float acc[16], sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-#pragma unroll 2
-    for (int e = 0; e < pieces; ++e) {
-        const float f = ex2_approx((piece_lse(e) - base) * kLog2e);
-        const float4* o = part_o + (((slot(e) * 2 + rank) * 4 + w) * 64 + c / 4) * 32 + lane;
-        sum += f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 v = o[32 * k];
-            acc[4 * k] += f * v.x;
-            acc[4 * k + 1] += f * v.y;
-            acc[4 * k + 2] += f * v.z;
-            acc[4 * k + 3] += f * v.w;
+        for (int e = 0; e < pieces; ++e) {
+            const float v = piece_lse(e);
+            bad = bad || v == INFINITY;
+            nan = nan || v != v;
+            mx = fmaxf(mx, v);
         }
-    }
-    if (bad) return;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t head = (int64_t)(it.x + rank) * kH + x;
-    uint4* to = reinterpret_cast<uint4*>(out + head * kDV + 128 * (w >> 1) + (c & 127) + 2 * (c & 128));
+        if (nan) mx = NAN;
+        const float base = mx == -INFINITY ? 0.f : mx;
+        float acc[16], sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-        to[k] = make_uint4(pack_bf16x2(acc[8 * k] * inv, acc[8 * k + 1] * inv),
-                           pack_bf16x2(acc[8 * k + 2] * inv, acc[8 * k + 3] * inv),
-                           pack_bf16x2(acc[8 * k + 4] * inv, acc[8 * k + 5] * inv),
-                           pack_bf16x2(acc[8 * k + 6] * inv, acc[8 * k + 7] * inv));
-    if (lse && (w >> 1) == 0 && c == 0) lse[head] = sum == 0.f ? -INFINITY : base + log2f(sum) * kLn2;
+        for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+#pragma unroll 2
+        for (int e = e0; e < pieces; e += step) {
+            const float f = ex2_approx((piece_lse(e) - base) * kLog2e);
+            const float4* o = part_o + (((slot(e) * 2 + rank) * 4 + w) * 64 + c / 4) * 32 + lane;
+            sum += f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 v = o[32 * k];
+                acc[4 * k] += f * v.x;
+                acc[4 * k + 1] += f * v.y;
+                acc[4 * k + 2] += f * v.z;
+                acc[4 * k + 3] += f * v.w;
+            }
+        }
+        if (wide) {
+            // the warps' sums, in order
+#pragma unroll
+            for (int k = 0; k < 16; ++k) acc_s[warp][k][lane] = acc[k];
+            acc_s[warp][16][lane] = sum;
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int v = 1; v < kMergeWarps; ++v) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) acc[k] += acc_s[v][k][lane];
+                    sum += acc_s[v][16][lane];
+                }
+            }
+            __syncthreads();
+            if (warp != 0) continue;
+        }
+        if (bad) continue;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t head = (int64_t)(it.x + rank) * kH + x;
+        uint4* to = reinterpret_cast<uint4*>(out + head * kDV + 128 * (w >> 1) + (c & 127) + 2 * (c & 128));
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            to[k] = make_uint4(pack_bf16x2(acc[8 * k] * inv, acc[8 * k + 1] * inv),
+                               pack_bf16x2(acc[8 * k + 2] * inv, acc[8 * k + 3] * inv),
+                               pack_bf16x2(acc[8 * k + 4] * inv, acc[8 * k + 5] * inv),
+                               pack_bf16x2(acc[8 * k + 6] * inv, acc[8 * k + 7] * inv));
+        if (lse && (w >> 1) == 0 && c == 0) lse[head] = sum == 0.f ? -INFINITY : base + log2f(sum) * kLn2;
+    }
 }
 
 // CTA pairs that can be resident at once on the current device.
@@ -757,9 +808,9 @@ int max_pairs() {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(tree_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem)) !=
+    if (cudaFuncSetAttribute(tree_mla_kernel<64, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem)) !=
             cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, tree_mla_kernel, &cfg) != cudaSuccess || n <= 0) {
+        cudaOccupancyMaxActiveClusters(&n, tree_mla_kernel<64, 64>, &cfg) != cudaSuccess || n <= 0) {
         cudaGetLastError();
         return num_sms() / 2;
     }
@@ -800,20 +851,25 @@ cudaError_t launch_tree_mla(const BatchDev& bd, const PagesDev& pg, const uint16
     a.part_lse = a.part_o + slots * 128 * kDV;
     a.meta = reinterpret_cast<int4*>(a.part_lse + slots * 128);
     a.rows_total = pg.table ? pg.pool_pages << pg.shift : (int32_t)(bd.B * bd.stride);
-    a.box = pg.table ? std::min(1 << pg.shift, 64) : 64;
-    CUtensorMap tm_q, tm_kv;
+    const int page = pg.table ? 1 << pg.shift : kTile;
+    const uint32_t krows = page >= 64 ? 64 : page == 32 ? 32 : 8, kchunks = krows == 32 ? 1 : kGroup;
+    const uint32_t vrows = (uint32_t)std::min(page, 64);
+    CUtensorMap tm_q, tm_k, tm_v;
     if (!make_tmap_bf16_2d(&tm_q, q, kDQK, (uint64_t)bd.total_q * kH, 64, 64) ||
-        !make_tmap_bf16_2d(&tm_kv, kv, kDQK, (uint64_t)a.rows_total, 64, (uint32_t)a.box))
+        !make_tmap_bf16_chunks(&tm_k, kv, kQChunks, (uint64_t)a.rows_total, krows, kchunks) ||
+        !make_tmap_bf16_chunks(&tm_v, kv, kQChunks, (uint64_t)a.rows_total, vrows, 2))
         return cudaErrorInvalidValue;
-    cudaError_t e =
-        cudaFuncSetAttribute(tree_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+    auto kernel = krows == 64   ? tree_mla_kernel<64, 64>
+                  : krows == 32 ? tree_mla_kernel<32, 32>
+                                : tree_mla_kernel<8, 16>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
     if (e != cudaSuccess) return e;
-    tree_mla_kernel<<<2 * pairs, kThreads, sizeof(Smem), stream>>>(a, tm_q, tm_kv);
+    kernel<<<2 * pairs, kThreads, sizeof(Smem), stream>>>(a, tm_q, tm_k, tm_v);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     count_launches(1);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)pairs, 16);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)pairs, kMergeBlocks);
+    cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
