@@ -171,7 +171,8 @@ def _bf16(t: torch.Tensor):
 
 def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle: building a Stream object takes 3 us of a 13 us call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -364,33 +365,33 @@ def tree_workspace(batch: Optional[Batch] = None, device="cuda") -> torch.Tensor
     return ws
 
 
-def _typed(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, numel: int, device: torch.device):
-    """Pointer of a contiguous tensor of `dtype` with at least `numel` elements on `device` (None stays None)."""
+def _typed(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, numel: int, dev: int):
+    """Pointer of a contiguous tensor of `dtype` with at least `numel` elements on device `dev` (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: {dtype} tensor expected, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected on {device}, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected on cuda:{dev}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: contiguous tensor expected")
-    if t.numel() < numel:
-        raise ValueError(f"{name}: {numel} elements expected, got {t.numel()}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: {numel} elements expected, got {t.numel()}")
 
 
-def _here(ws: torch.Tensor) -> torch.device:
-    """The device of a call: the workspace's, which has to be the current one."""
-    dev = ws.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"workspace on {dev}: expected on the current CUDA device")
+def _here(ws: torch.Tensor, stream) -> int:
+    """The device of a call: the workspace's, which has to be the current one and the stream's."""
+    dev = ws.get_device()
+    if dev < 0 or dev != torch.cuda.current_device() or (stream is not None and stream.device_index != dev):
+        raise ValueError(f"workspace on {ws.device}: expected on the current CUDA device, and the stream's")
     return dev
 
 
-def _paged(batch: Batch, pages: Optional[Pages], dev: torch.device):
+def _paged(batch: Batch, pages: Optional[Pages], dev: int):
     """The dsa_pages argument, and the cache rows that a call may reach."""
-    if batch.q_off.device != dev or (pages is not None and pages.block_table.device != dev):
-        raise ValueError(f"batch or block table: expected on {dev}")
+    if batch.q_off.get_device() != dev or (pages is not None and pages.block_table.get_device() != dev):
+        raise ValueError(f"batch or block table: expected on cuda:{dev}")
     if pages is None:
         return None, batch.c.batch * batch.c.cache_stride
     if pages.block_table.shape[0] < batch.c.batch:
@@ -404,7 +405,7 @@ def step_tables(batch: Batch, n_new, ctx_old, slots, positions, mask=None, paren
     """q_off and ctx_len of `batch`, block table, slot map, positions and
     masks of a step from its lengths (see dsa_step_tables).  mask: int64
     tensor holding the 64 bits."""
-    dev, i32 = _here(ws), torch.int32
+    dev, i32 = _here(ws, stream), torch.int32
     c = batch.c
     pg, _ = _paged(batch, pages, dev)
     _check(load_library().dsa_step_tables(
@@ -422,9 +423,9 @@ def step_tables(batch: Batch, n_new, ctx_old, slots, positions, mask=None, paren
 def latent_append(x, gamma, eps: float, cos, sin, positions, slots, kv, ws, stream=None):
     """RMSNorm | RoPE of the new tokens' compressed rows x [total_q, >= 576]
     (rows may be strided), written to kv at slots (see dsa_latent_append)."""
-    dev, f32, i32 = _here(ws), torch.float32, torch.int32
-    if x.dtype != torch.bfloat16 or x.device != dev:
-        raise TypeError(f"x: bf16 tensor on {dev} expected")
+    dev, f32, i32 = _here(ws, stream), torch.float32, torch.int32
+    if x.dtype is not torch.bfloat16 or x.get_device() != dev:
+        raise TypeError(f"x: bf16 tensor on cuda:{dev} expected")
     if x.dim() != 2 or x.shape[1] != D_QK or x.stride(1) != 1:
         raise ValueError("x: [total_q, 576] with unit column stride expected")
     total_q, rows = x.shape[0], cos.shape[0]
@@ -443,7 +444,7 @@ def tree_mla_fwd(batch: Batch, q, kv, mask, sm_scale: float, out, lse=None, page
                  stream=None):
     """Attention of every new row over the committed rows and the new rows of
     its mask (see dsa_tree_mla_fwd)."""
-    dev, bf16 = _here(ws), torch.bfloat16
+    dev, bf16 = _here(ws, stream), torch.bfloat16
     c = batch.c
     pg, rows = _paged(batch, pages, dev)
     _check(load_library().dsa_tree_mla_fwd(
@@ -456,7 +457,7 @@ def tree_mla_fwd(batch: Batch, q, kv, mask, sm_scale: float, out, lse=None, page
 
 def tree_topk(batch: Batch, scores, mask, k: int, idx, ld: Optional[int] = None, ws=None, stream=None):
     """Causal top-k among what every new row sees (see dsa_tree_topk)."""
-    dev = _here(ws)
+    dev = _here(ws, stream)
     c = batch.c
     ld = int(ld if ld is not None else scores.shape[-1])
     _paged(batch, None, dev)
@@ -473,7 +474,7 @@ def tree_commit(batch: Batch, mask, accepted, ctx_new, kv=None, k_idx=None, page
     """Moves the accepted paths' rows behind the committed ones in every layer
     of kv [layers, rows, 576] and k_idx [layers, rows, 128] (one layer without
     the first dimension; see dsa_tree_commit)."""
-    dev, bf16 = _here(ws), torch.bfloat16
+    dev, bf16 = _here(ws, stream), torch.bfloat16
     c = batch.c
     pg, need = _paged(batch, pages, dev)
     shapes = {(t.shape[0] if t.dim() == 3 else 1, t.shape[-2]) for t in (kv, k_idx) if t is not None}
