@@ -16,7 +16,8 @@
 //
 // A tree's mask is built by pointer jumping, a warp per sequence with two
 // nodes per lane: after round s a node's mask holds its nearest 2^s
-// ancestors-or-self and its link points 2^s up, so six rounds reach 64 nodes.
+// ancestors-or-self and its link points 2^s up, so log2 of the nodes, at most
+// six rounds, do.
 #include <algorithm>
 
 #include "internal.h"
@@ -25,8 +26,6 @@
 
 namespace dsa {
 namespace {
-
-constexpr int kThreads = 1024;
 
 struct TablesArgs {
     int32_t B, total_q, max_q, max_ctx;
@@ -39,15 +38,6 @@ struct TablesArgs {
     int32_t* head;                    // workspace: the free list's head before
     int32_t* status;
 };
-
-__device__ __forceinline__ int64_t warp_scan_i64(int64_t v) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if ((threadIdx.x & 31) >= o) v += u;
-    }
-    return v;
-}
 
 struct SeqNeed {
     int32_t n, c, held, fresh;
@@ -97,6 +87,62 @@ __device__ __forceinline__ int32_t slot_of(const TablesArgs& a, int b, int32_t p
     return (page << a.pg.shift) + (pos & ((1 << a.pg.shift) - 1));
 }
 
+// The trees' rows, a warp per sequence, H nodes per lane (node lane + 32 h).
+template <int H>
+__device__ __forceinline__ void write_trees(const TablesArgs& a, int64_t me, int64_t threads, int32_t head) {
+    const int lane = (int)(me & 31);
+    const int rounds = 32 - __clz(max(a.max_q, 2) - 1);
+    for (int64_t b = me >> 5; b < a.B; b += threads >> 5) {
+        const int32_t q0 = a.q_off[b], n = a.q_off[b + 1] - q0, c = a.ctx_len[b] - n;
+        int32_t up[H], slot[H];
+        uint64_t m[H];
+        // parents and pages are on their way together
+#pragma unroll
+        for (int h = 0; h < H; ++h) up[h] = lane + 32 * h < n ? __ldg(a.parent + q0 + lane + 32 * h) : -1;
+#pragma unroll
+        for (int h = 0; h < H; ++h) slot[h] = lane + 32 * h < n ? slot_of(a, (int)b, c + lane + 32 * h, head) : -1;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int32_t i = lane + 32 * h;
+            if (up[h] < -1 || up[h] >= i) {
+                if (i < n) latch_status(a.status, DSA_ERR_BAD_INDEX);
+                up[h] = -1;
+            }
+            m[h] = 1ull << i;
+        }
+#pragma unroll 1
+        for (int s = 0; s < rounds; ++s) {
+            uint64_t m2[H];
+            int32_t u2[H];
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int from = up[h] & 31;
+                m2[h] = __shfl_sync(0xffffffffu, m[0], from);
+                u2[h] = __shfl_sync(0xffffffffu, up[0], from);
+                if (H > 1) {
+                    const uint64_t high = __shfl_sync(0xffffffffu, m[H - 1], from);
+                    const int32_t uhigh = __shfl_sync(0xffffffffu, up[H - 1], from);
+                    if (up[h] >= 32) m2[h] = high, u2[h] = uhigh;
+                }
+                if (up[h] < 0) m2[h] = 0u, u2[h] = -1;
+            }
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                m[h] |= m2[h];
+                up[h] = u2[h];
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int32_t i = lane + 32 * h;
+            if (i >= n) continue;
+            a.slots[q0 + i] = slot[h];
+            a.positions[q0 + i] = c + __popcll(m[h]) - 1;
+            if (a.mask) a.mask[q0 + i] = m[h];
+        }
+    }
+}
+
 // Rows and new block-table entries, by thread `me` of `threads`.
 __device__ void write_rows(const TablesArgs& a, int64_t me, int64_t threads) {
     const int32_t rows = a.q_off[a.B], head = a.pg.table ? *a.head : 0;
@@ -116,48 +162,8 @@ __device__ void write_rows(const TablesArgs& a, int64_t me, int64_t threads) {
         if (a.mask) a.mask[r] = ~0ull >> (63 - i);
     }
     if (a.parent) {
-        const int lane = (int)(me & 31);
-        for (int64_t b = me >> 5; b < a.B; b += threads >> 5) {
-            const int32_t q0 = a.q_off[b], n = a.q_off[b + 1] - q0, c = a.ctx_len[b] - n;
-            int32_t up[2];
-            uint64_t m[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int32_t i = lane + 32 * h;
-                up[h] = i < n ? __ldg(a.parent + q0 + i) : -1;
-                if (up[h] < -1 || up[h] >= i) {
-                    if (i < n) latch_status(a.status, DSA_ERR_BAD_INDEX);
-                    up[h] = -1;
-                }
-                m[h] = 1ull << i;
-            }
-#pragma unroll 1
-            for (int s = 0; s < 6; ++s) {
-                uint64_t m2[2];
-                int32_t u2[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int from = up[h] & 31;
-                    const uint64_t lo = __shfl_sync(0xffffffffu, m[0], from), hi = __shfl_sync(0xffffffffu, m[1], from);
-                    const int32_t ulo = __shfl_sync(0xffffffffu, up[0], from), uhi = __shfl_sync(0xffffffffu, up[1], from);
-                    m2[h] = up[h] < 0 ? 0u : up[h] < 32 ? lo : hi;
-                    u2[h] = up[h] < 0 ? -1 : up[h] < 32 ? ulo : uhi;
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    m[h] |= m2[h];
-                    up[h] = u2[h];
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int32_t i = lane + 32 * h;
-                if (i >= n) continue;
-                a.slots[q0 + i] = slot_of(a, (int)b, c + i, head);
-                a.positions[q0 + i] = c + __popcll(m[h]) - 1;
-                if (a.mask) a.mask[q0 + i] = m[h];
-            }
-        }
+        if (a.max_q <= 32) write_trees<1>(a, me, threads, head);
+        else write_trees<2>(a, me, threads, head);
     }
     if (a.pg.table) {
         const int32_t fresh = a.first_new[a.B];
@@ -169,9 +175,17 @@ __device__ void write_rows(const TablesArgs& a, int64_t me, int64_t threads) {
     }
 }
 
-template <bool kRows>
-__global__ void __launch_bounds__(kThreads) step_lengths_kernel(const TablesArgs a) {
-    __shared__ int64_t s_n[32], s_f[32];
+// NT threads: all of them walk the same few hundred instructions, so a small
+// batch is faster with fewer (256 prompts: 6.4 us with 256, 8.2 with 1024).
+template <int NT, bool kRows>
+__global__ void __launch_bounds__(NT) step_lengths_kernel(const TablesArgs a) {
+    constexpr int kWarps = NT / 32;
+    // the tables again for this CTA's own rows, which would read them back
+    // from L2 otherwise
+    __shared__ int32_t s_off[kRows ? NT + 1 : 1], s_ctx[kRows ? NT : 1];
+    __shared__ int32_t s_first[kRows ? NT + 1 : 1], s_held[kRows ? NT : 1], s_head;
+    __shared__ int64_t s_n[kWarps], s_f[kWarps];
+    __shared__ uint64_t s_both[kWarps];
     __shared__ int s_code;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();
@@ -181,25 +195,34 @@ __global__ void __launch_bounds__(kThreads) step_lengths_kernel(const TablesArgs
         head = a.free_range[0];
         tail = a.free_range[1];
     }
-    __syncthreads();
     // pass 1: does the whole step fit?
     int64_t n_sum = 0, f_sum = 0;
     SeqNeed s{};
-    for (int b = tid; b < a.B; b += kThreads) {
+    int worst = DSA_OK;
+    for (int b = tid; b < a.B; b += NT) {
         s = seq_need(a, b);
         n_sum += s.n;
         f_sum += s.fresh;
-        if (s.code != DSA_OK) atomicMax(&s_code, s.code);
+        worst = max(worst, s.code);
     }
-    n_sum = warp_scan_i64(n_sum);
-    f_sum = warp_scan_i64(f_sum);
-    if (lane == 31) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        n_sum += __shfl_xor_sync(0xffffffffu, n_sum, o);
+        f_sum += __shfl_xor_sync(0xffffffffu, f_sum, o);
+    }
+    if (lane == 0) {
         s_n[warp] = n_sum;
         s_f[warp] = f_sum;
     }
     __syncthreads();
-    const int64_t all_n = __shfl_sync(0xffffffffu, warp_scan_i64(s_n[lane]), 31);
-    const int64_t all_f = __shfl_sync(0xffffffffu, warp_scan_i64(s_f[lane]), 31);
+    if (worst != DSA_OK) atomicMax(&s_code, worst);
+    int64_t all_n = lane < kWarps ? s_n[lane] : 0, all_f = lane < kWarps ? s_f[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        all_n += __shfl_xor_sync(0xffffffffu, all_n, o);
+        all_f += __shfl_xor_sync(0xffffffffu, all_f, o);
+    }
+    __syncthreads();
     int code = s_code;
     if (code == DSA_OK && all_n > a.total_q) code = DSA_ERR_BAD_BATCH;
     if (code == DSA_OK && a.pg.table) {
@@ -208,51 +231,80 @@ __global__ void __launch_bounds__(kThreads) step_lengths_kernel(const TablesArgs
     }
     const bool go = code == DSA_OK;
     if (!go && tid == 0) latch_status(a.status, code);
-    __syncthreads();
-    // pass 2: the prefix sums and what advances, 1024 sequences at a time
-    int64_t n_base = 0, f_base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    // pass 2: the prefix sums and what advances, NT sequences at a time; both
+    // sums fit 32 bits now and share one scan
+    uint64_t base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += NT) {
         const int b = b0 + tid;
-        if (a.B > kThreads) s = seq_need(a, b);
+        if (a.B > NT || b >= a.B) s = seq_need(a, b);
         if (!go) s.n = s.fresh = 0;
-        const int64_t ni = warp_scan_i64(s.n), fi = warp_scan_i64(s.fresh);
-        if (lane == 31) {
-            s_n[warp] = ni;
-            s_f[warp] = fi;
+        const uint64_t mine = (uint64_t)(uint32_t)s.n | (uint64_t)(uint32_t)s.fresh << 32;
+        uint64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
         }
+        if (lane == 31) s_both[warp] = incl;
         __syncthreads();
-        const int64_t nw = warp_scan_i64(s_n[lane]), fw = warp_scan_i64(s_f[lane]);
-        const int64_t n_before = warp ? __shfl_sync(0xffffffffu, nw, (warp - 1) & 31) : 0;
-        const int64_t f_before = warp ? __shfl_sync(0xffffffffu, fw, (warp - 1) & 31) : 0;
+        uint64_t sums = lane < kWarps ? s_both[lane] : 0u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t up = __shfl_up_sync(0xffffffffu, sums, o);
+            if (lane >= o) sums += up;
+        }
+        const uint64_t lower = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
+        const uint64_t before = base + (warp ? lower : 0u);
+        base += __shfl_sync(0xffffffffu, sums, 31);
         if (b < a.B) {
             // the outputs may be the inputs' own arrays: an element is read
             // (above, or here for a refused step) before it is written
-            const int32_t c = go ? s.c : a.ctx_old[b];
-            a.q_off[b + 1] = (int32_t)(n_base + n_before + ni);
-            a.ctx_len[b] = c + s.n;
+            const int32_t off = (int32_t)(uint32_t)(before + incl);
+            const int32_t first = (int32_t)((before + incl - mine) >> 32);
+            const int32_t ctx = (go ? s.c : a.ctx_old[b]) + s.n;
+            const int32_t held = go || !a.pg.table ? s.held : a.held_old[b];
+            a.q_off[b + 1] = off;
+            a.ctx_len[b] = ctx;
             if (a.pg.table) {
-                const int32_t held = go ? s.held : a.held_old[b];
                 a.held_kept[b] = held;
                 a.held[b] = held + s.fresh;
-                a.first_new[b] = (int32_t)(f_base + f_before + fi - s.fresh);
+                a.first_new[b] = first;
+            }
+            if (kRows && b < NT) {
+                s_off[b + 1] = off;
+                s_ctx[b] = ctx;
+                s_held[b] = held;
+                s_first[b] = first;
             }
         }
-        n_base += __shfl_sync(0xffffffffu, nw, 31);
-        f_base += __shfl_sync(0xffffffffu, fw, 31);
         __syncthreads();
     }
+    const int32_t fresh = (int32_t)(base >> 32);
     if (tid == 0) {
         a.q_off[0] = 0;
         if (a.pg.table) {
-            a.first_new[a.B] = (int32_t)f_base;
+            a.first_new[a.B] = fresh;
             *a.head = head;
-            a.free_out[0] = head + (int32_t)f_base;
+            a.free_out[0] = head + fresh;
             a.free_out[1] = tail;
+        }
+        if (kRows) {
+            s_off[0] = 0;
+            s_head = head;
+            if (a.B <= NT) s_first[a.B] = fresh;
         }
     }
     if (kRows) {
         __syncthreads();
-        write_rows(a, tid, kThreads);
+        TablesArgs l = a;
+        if (a.B <= NT) {
+            l.q_off = s_off;
+            l.ctx_len = s_ctx;
+            l.first_new = s_first;
+            l.held_kept = s_held;
+            l.head = &s_head;
+        }
+        write_rows(l, tid, NT);
     }
 }
 
@@ -298,17 +350,21 @@ cudaError_t launch_step_tables(const BatchDev& bd, const PagesDev& pg, const int
     // what the rows and entries can come to: the step's rows, and the pages
     // that sequences may take (all of max_ctx for a fresh prompt)
     const int64_t per_seq = pg.table ? std::min<int64_t>(pg.max_pages, ((int64_t)bd.max_q >> pg.shift) + 2) : 0;
-    const int64_t items = std::max<int64_t>(bd.total_q, per_seq * bd.B);
-    const bool one = items <= 4 * kThreads;
-    if (one) {
-        step_lengths_kernel<true><<<1, kThreads, 0, stream>>>(a);
-        const cudaError_t e = cudaGetLastError();
+    const int64_t items = std::max<int64_t>(std::max<int64_t>(bd.total_q, per_seq * bd.B), parent ? 32 * bd.B : 0);
+    // A few rows and entries are written by the CTA of the sums (the second
+    // launch takes the host 2 us), with 1024 threads where there are more trees
+    // than warps of 256.
+    cudaError_t e;
+    if (bd.B <= 256 && items <= 4096) {
+        if (parent && bd.B > 8) step_lengths_kernel<1024, true><<<1, 1024, 0, stream>>>(a);
+        else step_lengths_kernel<256, true><<<1, 256, 0, stream>>>(a);
+        e = cudaGetLastError();
         if (e == cudaSuccess) count_launches(1);
         return e;
     }
-    step_lengths_kernel<false><<<1, kThreads, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (bd.B <= 256) step_lengths_kernel<256, false><<<1, 256, 0, stream>>>(a);
+    else step_lengths_kernel<1024, false><<<1, 1024, 0, stream>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     count_launches(1);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::min<int64_t>((items + 255) / 256, 8 * num_sms()));

@@ -85,9 +85,9 @@ __device__ __forceinline__ uint32_t warp_inclusive_scan(uint32_t v) {
     return v;
 }
 
-template <int NT>
+template <int NT, int REGION = kRegion>
 struct alignas(16) TopkSmem {
-    static constexpr int kMaxCand = NT / 32 * kRegion;
+    static constexpr int kMaxCand = NT / 32 * REGION;
     uint32_t hist[kBins];                 // zero between selects
     uint32_t sample[kSample];
     uint32_t cand_key[kMaxCand];          // warp w: [w * kRegion, w * kRegion + count)
@@ -113,8 +113,8 @@ struct alignas(16) TopkSmem {
 // bins (few atomic collisions).  Once at most 64 keys (over the cluster)
 // remain in the boundary bin, they are gathered and ranked directly.  S.hist must
 // be zero on entry; zero on return.
-template <int NT, typename Visit>
-__device__ uint32_t radix_select(cg::cluster_group& cluster, int nranks, TopkSmem<NT>& S, uint32_t k, int hi,
+template <int NT, int REGION, typename Visit>
+__device__ uint32_t radix_select(cg::cluster_group& cluster, int nranks, TopkSmem<NT, REGION>& S, uint32_t k, int hi,
                                  uint32_t prefix0, int passes, Visit visit, uint32_t& need_out) {
     constexpr int kWarps = NT / 32, kBinsPerThread = kBins / NT;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -255,7 +255,7 @@ __device__ uint32_t radix_select(cg::cluster_group& cluster, int nranks, TopkSme
             if (nranks == 1) __syncthreads();
             else cluster.sync();
             // every rank's list, concatenated in rank order
-            auto rank_smem = [&](int r) -> const TopkSmem<NT>* {
+            auto rank_smem = [&](int r) -> const TopkSmem<NT, REGION>* {
                 return nranks == 1 ? &S : cluster.map_shared_rank(&S, r);
             };
             if (tid < 64 * nranks) {
@@ -350,6 +350,26 @@ __device__ __forceinline__ void put(int32_t* out, uint32_t pos, int k, int32_t v
     else latch_status(status, DSA_ERR_INTERNAL);
 }
 
+// A masked row's end: packs its visible new scores and their positions
+// (threads 0-63 write; the caller synchronises) and returns the row's length
+// without gaps, c committed positions first; -1 for too many new rows.
+__device__ __forceinline__ int32_t masked_end(const SeqInfo& sq, int32_t i, const float* row, const uint64_t* mask,
+                                              float* end_score, int32_t* end_pos, int32_t* status) {
+    if (sq.nq > DSA_MAX_TREE) {
+        latch_status(status, DSA_ERR_BAD_BATCH);
+        return -1;
+    }
+    const int tid = threadIdx.x;
+    const int32_t c = sq.ctx - sq.nq;
+    const uint64_t bits = visible_bits(__ldg(reinterpret_cast<const unsigned long long*>(mask) + sq.q0 + i), i);
+    if (tid < DSA_MAX_TREE && (bits >> tid) & 1u) {
+        const int e = __popcll(bits & ((1ull << tid) - 1u));
+        end_score[e] = __ldg(row + c + tid);
+        end_pos[e] = c + tid;
+    }
+    return c + __popcll(bits);
+}
+
 template <int NT, bool MASKED>
 __global__ void __launch_bounds__(NT, NT <= 512 ? 2 : 1)
     topk_kernel(const BatchDev bd, const RowRange rr, const float* __restrict__ scores, const int64_t ld,
@@ -380,17 +400,8 @@ __global__ void __launch_bounds__(NT, NT <= 512 ? 2 : 1)
     const int32_t c = MASKED ? sq.ctx - sq.nq : 0;
     int32_t n = t + 1;
     if constexpr (MASKED) {
-        if (sq.nq > DSA_MAX_TREE) {
-            latch_status(status, DSA_ERR_BAD_BATCH);
-            return;
-        }
-        const uint64_t bits = visible_bits(__ldg(reinterpret_cast<const unsigned long long*>(mask) + sq.q0 + i), i);
-        n = c + __popcll(bits);
-        if (tid < DSA_MAX_TREE && (bits >> tid) & 1u) {
-            const int e = __popcll(bits & ((1ull << tid) - 1u));
-            end_score[e] = __ldg(row + c + tid);
-            end_pos[e] = c + tid;
-        }
+        n = masked_end(sq, i, row, mask, end_score, end_pos, status);
+        if (n < 0) return;
         __syncthreads();
     }
     auto position = [&](int32_t j) -> int32_t {
@@ -739,6 +750,283 @@ cudaError_t launch_nt(const BatchDev& bd, RowRange rr, const float* scores, int6
     return e;
 }
 
+// Masked rows of up to NT * KPT positions: the whole row stays in registers
+// (warp w owns a contiguous segment, read as coalesced 16-byte groups while
+// the mask and the row's end are on their way), so there is no sampled bound,
+// no candidate region and no second read.
+//   1. One histogram over 2048 equal intervals of [min, max]: scores of a row
+//      spread over it, so few atomics meet and few keys stay.  Subtraction, product and truncation are monotone, so the
+//      interval of the k-th largest is exact whatever the rounding.
+//   2. At most 64 keys in it: gathered and ranked.  More (ties, outliers that
+//      stretch the range, infinities): radix_select over all keys.
+//   3. Output in position order from packed warp scans; ties at tau are
+//      counted only if not all of them are taken.
+// Bound by instructions.  64 trees of up to 32 rows over up to 9,001
+// positions, k = 2048: 28.7 us (topk_kernel 72); 8 trees of 8 over 32,768:
+// 12.2 us (21.7).
+template <int NT, int KPT>
+__global__ void __launch_bounds__(NT, NT == 1024 ? 1 : KPT <= 8 ? 3 : 2)
+    topk_short_kernel(const BatchDev bd, const float* __restrict__ scores, const int64_t ld, const int k,
+                      int32_t* __restrict__ idx, int32_t* status, const uint64_t* __restrict__ mask) {
+    constexpr int kWarps = NT / 32, kGroups = KPT / 4, kBinsPerThread = kBins / NT;
+    static_assert(kGroups <= 8, "a lane's counts fill one 64-bit word");
+    __shared__ TopkSmem<NT, 1> S;
+    __shared__ float end_score[DSA_MAX_TREE];
+    __shared__ int32_t end_pos[DSA_MAX_TREE];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int b = blockIdx.y, i = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    SeqInfo sq;
+    if (!load_seq(bd, b, status, sq) || i >= sq.nq) return;
+    const float* row = scores + ((int64_t)sq.q0 + i) * ld;
+    int32_t* out = idx + ((int64_t)sq.q0 + i) * k;
+    const int32_t c = sq.ctx - sq.nq;
+    const int32_t seg = ((sq.ctx + kWarps - 1) / kWarps + 127) & ~127;
+    const int32_t w_lo = min(sq.ctx, warp * seg), w_end = min(sq.ctx, w_lo + seg);
+    float4 v[kGroups];
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) {
+        const int32_t j = w_lo + 128 * u + 4 * lane;
+        v[u] = sq.ctx > k && j < w_end ? __ldg(reinterpret_cast<const float4*>(row + j))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const int32_t n = masked_end(sq, i, row, mask, end_score, end_pos, status);
+    if (n < 0) return;
+#pragma unroll
+    for (int x = 0; x < kBinsPerThread; ++x) S.hist[NT * x + tid] = 0u;
+    if (tid == 0) {
+        S.small_n = 0u;
+        S.sel_count = 0xFFFFFFFFu;
+    }
+    __syncthreads();
+    auto position = [&](int32_t j) -> int32_t { return j < c ? j : end_pos[j - c]; };
+    if (n <= k) {
+        for (int j = tid; j < k; j += NT) out[j] = j < n ? position(j) : -1;
+        return;
+    }
+    const int32_t w_hi = min(n, w_end);
+    // The lane's scores; NaN behind the row's end, which is above, below and
+    // equal to nothing.  Groups past the segment's length are skipped
+    // everywhere (the same branch for the whole CTA): the kernel is bound by
+    // its instructions, and a row is often much shorter than NT * KPT.
+    float x[KPT], low = INFINITY, high = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) {
+        if (128 * u >= seg) break;
+        const float y[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int32_t j = w_lo + 128 * u + 4 * lane + e;
+            x[4 * u + e] = j < w_hi ? (j < c ? y[e] : end_score[j - c]) : NAN;
+            low = fminf(low, x[4 * u + e]);
+            high = fmaxf(high, x[4 * u + e]);
+        }
+    }
+    low = -warp_max_f32(-low);
+    high = warp_max_f32(high);
+    if (lane == 0) {
+        S.wgt[warp] = __float_as_uint(low);
+        S.wmax[warp] = __float_as_uint(high);
+    }
+    __syncthreads();
+    low = -warp_max_f32(lane < kWarps ? -__uint_as_float(S.wgt[lane]) : -INFINITY);
+    high = warp_max_f32(lane < kWarps ? __uint_as_float(S.wmax[lane]) : -INFINITY);
+
+    const float span = high - low, scale = (float)kBins / span;
+    const bool linear = span > 0.f && span < INFINITY && scale < INFINITY;   // false for NaN too
+    float tf = 0.f;
+    uint32_t tau = 0u, need = 0u;
+    bool ties = true, ranked = false;
+    auto bin = [&](float f) -> uint32_t { return (uint32_t)min(kBins - 1, (int)((f - low) * scale)); };
+    if (linear) {
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+            if (128 * u >= seg) break;
+#pragma unroll
+            for (int q = 4 * u; q < 4 * u + 4; ++q)
+                if (x[q] == x[q]) atomicAdd(&S.hist[bin(x[q])], 1u);
+        }
+        __syncthreads();
+        uint32_t cnt[kBinsPerThread], mine = 0u;
+#pragma unroll
+        for (int q = 0; q < kBinsPerThread; ++q) {
+            cnt[q] = S.hist[kBinsPerThread * tid + q];
+            S.hist[kBinsPerThread * tid + q] = 0u;
+            mine += cnt[q];
+        }
+        const uint32_t incl = warp_inclusive_scan(mine);
+        if (lane == 31) S.warp_sums[warp] = incl;
+        __syncthreads();
+        const uint32_t sums = warp_inclusive_scan(lane < kWarps ? S.warp_sums[lane] : 0u);
+        const uint32_t before = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
+        // keys in higher bins
+        uint32_t above = __shfl_sync(0xffffffffu, sums, 31) - (incl + (warp ? before : 0u));
+#pragma unroll
+        for (int q = kBinsPerThread - 1; q >= 0; --q) {
+            if (above < (uint32_t)k && (uint32_t)k <= above + cnt[q]) {
+                S.sel_digit = (uint32_t)(kBinsPerThread * tid + q);
+                S.sel_above = above;
+                S.sel_count = cnt[q];
+            }
+            above += cnt[q];
+        }
+        __syncthreads();
+        if (S.sel_count <= 64u) {
+            const uint32_t digit = S.sel_digit;
+#pragma unroll
+            for (int u = 0; u < kGroups; ++u) {
+                if (128 * u >= seg) break;
+#pragma unroll
+                for (int q = 4 * u; q < 4 * u + 4; ++q)
+                    if (x[q] == x[q] && bin(x[q]) == digit)
+                        S.small[atomicAdd(&S.small_n, 1u) & 63u] = __float_as_uint(x[q]);
+            }
+            __syncthreads();
+            // eight threads rank a score against eight each
+            const uint32_t m = min(S.small_n, 64u), want = (uint32_t)k - S.sel_above;
+            if (tid < 512) {
+                const uint32_t q = (uint32_t)tid >> 3, sub = (uint32_t)tid & 7u;
+                const float f = q < m ? __uint_as_float(S.small[q]) : NAN;
+                uint32_t gt = 0u, eq = 0u;
+#pragma unroll
+                for (uint32_t o = 0; o < 8u; ++o) {
+                    const float y = sub * 8u + o < m ? __uint_as_float(S.small[sub * 8u + o]) : NAN;
+                    gt += y > f ? 1u : 0u;
+                    eq += y == f ? 1u : 0u;
+                }
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) {
+                    gt += __shfl_xor_sync(0xffffffffu, gt, o);
+                    eq += __shfl_xor_sync(0xffffffffu, eq, o);
+                }
+                if (sub == 0 && q < m && gt < want && want <= gt + eq) {
+                    // equal scores (both zeros) write the same values but this one
+                    S.small_tau = __float_as_uint(f);
+                    S.small_need = want - gt;
+                    S.total = eq;
+                }
+            }
+            __syncthreads();
+            tf = __uint_as_float(S.small_tau);
+            need = S.small_need;
+            ties = S.total != need;
+            ranked = true;
+        }
+    }
+    if (!ranked) {
+        uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
+#pragma unroll 1
+        for (int32_t j = w_lo + lane; j < w_hi; j += 32) {
+            const uint32_t q = order_key(j < c ? __ldg(row + j) : end_score[j - c]);
+            kmin = min(kmin, q);
+            kmax = max(kmax, q);
+        }
+        kmin = __reduce_min_sync(0xffffffffu, kmin);
+        kmax = __reduce_max_sync(0xffffffffu, kmax);
+        __syncthreads();
+        if (lane == 0) {
+            S.wgt[warp] = kmin;
+            S.wmax[warp] = kmax;
+        }
+        __syncthreads();
+        kmin = __reduce_min_sync(0xffffffffu, lane < kWarps ? S.wgt[lane] : 0xFFFFFFFFu);
+        kmax = __reduce_max_sync(0xffffffffu, lane < kWarps ? S.wmax[lane] : 0u);
+        tau = radix_select(cluster, 1, S, (uint32_t)k, varying_bits(kmin, kmax), kmin, 3,
+                           [&](auto&& f) {
+#pragma unroll 1
+                               for (int32_t j = w_lo + lane; j < w_hi; j += 32)
+                                   f(order_key(j < c ? __ldg(row + j) : end_score[j - c]));
+                           },
+                           need);
+    }
+
+    // scores above the k-th, and equal to it; without a cut among the equal
+    // ones they count as above.  A byte per 128-key group for the warp's scan.
+    uint32_t bg = 0u, be = 0u;
+    if (ranked) {
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+            if (128 * u >= seg) break;
+#pragma unroll
+            for (int q = 4 * u; q < 4 * u + 4; ++q) {
+                if (ties) {
+                    bg |= (x[q] > tf ? 1u : 0u) << q;
+                    be |= (x[q] == tf ? 1u : 0u) << q;
+                } else {
+                    bg |= (x[q] >= tf ? 1u : 0u) << q;
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < KPT; ++q) {
+            const bool in = w_lo + 128 * (q >> 2) + 4 * lane + (q & 3) < w_hi;
+            const uint32_t key = in ? order_key(x[q]) : 0u;
+            bg |= (in && key > tau ? 1u : 0u) << q;
+            be |= (in && key == tau ? 1u : 0u) << q;
+        }
+    }
+    auto scan = [&](uint32_t bits, uint64_t& excl, uint64_t& total) -> uint32_t {
+        uint64_t p = 0u;
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) p |= (uint64_t)__popc((bits >> (4 * u)) & 0xFu) << (8 * u);
+        uint64_t incl = p;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        total = __shfl_sync(0xffffffffu, incl, 31);
+        excl = incl - p;
+        uint32_t sum = 0u;
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) sum += (uint32_t)(total >> (8 * u)) & 0xFFu;
+        return sum;
+    };
+    uint64_t xg, tg, xe = 0u, te = 0u;
+    const uint32_t sg = scan(bg, xg, tg), se = ties ? scan(be, xe, te) : 0u;
+    __syncthreads();
+    if (lane == 0) {
+        S.wcnt[warp] = sg;
+        S.weq[warp] = se;
+    }
+    __syncthreads();
+    const uint32_t all_g = warp_inclusive_scan(lane < kWarps ? S.wcnt[lane] : 0u);
+    uint32_t g0 = __shfl_sync(0xffffffffu, all_g, warp) - sg;
+    if (!ties) {
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+            if (128 * u >= seg) break;
+            uint32_t g = g0 + ((uint32_t)(xg >> (8 * u)) & 0xFFu);
+            const int32_t j = w_lo + 128 * u + 4 * lane;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if ((bg >> (4 * u + e)) & 1u) put(out, g++, k, position(j + e), status);
+            g0 += (uint32_t)(tg >> (8 * u)) & 0xFFu;
+        }
+        return;
+    }
+    const uint32_t all_e = warp_inclusive_scan(lane < kWarps ? S.weq[lane] : 0u);
+    uint32_t e0 = __shfl_sync(0xffffffffu, all_e, warp) - se;
+#pragma unroll 1
+    for (int u = 0; u < kGroups; ++u) {
+        uint32_t g = g0 + ((uint32_t)(xg >> (8 * u)) & 0xFFu), e = e0 + ((uint32_t)(xe >> (8 * u)) & 0xFFu);
+        for (uint32_t both = ((bg | be) >> (4 * u)) & 0xFu; both; both &= both - 1u) {
+            const int q = __ffs(both) - 1;
+            const int32_t j = w_lo + 128 * u + 4 * lane + q;
+            if ((bg >> (4 * u + q)) & 1u) {
+                put(out, g + min(e, need), k, position(j), status);
+                ++g;
+            } else {
+                if (e < need) put(out, g + e, k, position(j), status);
+                ++e;
+            }
+        }
+        g0 += (uint32_t)(tg >> (8 * u)) & 0xFFu;
+        e0 += (uint32_t)(te >> (8 * u)) & 0xFFu;
+    }
+}
+
 template <bool MASKED>
 cudaError_t launch_rows(const BatchDev& bd, RowRange rr, const float* scores, int64_t ld, bool scores_local, int k,
                         int32_t* idx, bool idx_local, int32_t* status, cudaStream_t stream, bool after_previous,
@@ -767,6 +1055,23 @@ cudaError_t launch_topk(const BatchDev& bd, RowRange rr, const float* scores, in
 
 cudaError_t launch_tree_topk(const BatchDev& bd, const float* scores, int64_t ld, const uint64_t* mask, int k,
                              int32_t* idx, int32_t* status, cudaStream_t stream) {
+    // Rows that fit a CTA's registers.  With fewer rows than SMs a CTA has an
+    // SM to itself: 1024 threads; else 512 and two or three CTAs per SM.
+    const bool few = (int64_t)bd.B * bd.max_q < num_sms();
+    const int per = (bd.max_ctx + (few ? 1023 : 511)) / (few ? 1024 : 512);
+    if (per <= 32) {
+        auto kernel = few ? (per <= 8    ? topk_short_kernel<1024, 8>
+                             : per <= 16 ? topk_short_kernel<1024, 16>
+                                         : topk_short_kernel<1024, 32>)
+                          : (per <= 8    ? topk_short_kernel<512, 8>
+                             : per <= 16 ? topk_short_kernel<512, 16>
+                                         : topk_short_kernel<512, 32>);
+        kernel<<<dim3((unsigned)bd.max_q, (unsigned)bd.B), few ? 1024 : 512, 0, stream>>>(bd, scores, ld, k, idx, status,
+                                                                                      mask);
+        const cudaError_t e = cudaGetLastError();
+        if (e == cudaSuccess) count_launches(1);
+        return e;
+    }
     return launch_rows<true>(bd, RowRange{0, bd.max_q}, scores, ld, false, k, idx, false, status, stream, false, mask);
 }
 
