@@ -51,7 +51,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTile = 128;                   // positions per tile
 constexpr int kItemCost = 3;                 // an item's start and end, in tiles
-constexpr int kMinChunk = kItemCost + 1;     // least work cut off for a pair
 constexpr int kThreads = 288;
 constexpr int kChunkBytes = 64 * 128;        // 64 rows x 64 dims
 constexpr int kQChunks = kDQK / 64;          // 9
@@ -85,6 +84,7 @@ struct Smem {
     Plan plan;
     Seg seg[kSegs];
     int64_t scan[kThreads / 32];
+    int32_t longest[kThreads / 32];
     float xch[2][128];
     int32_t bad[4];
     uint32_t tmem;
@@ -167,16 +167,32 @@ struct SegIter {
     }
 };
 
+// The least work worth a pair of its own, in units: a tile takes 1.2 us (2 us
+// among the first) and a piece 0.17 us more in the merge, so an item of N
+// tiles alone on the GPU is done soonest in pieces of about sqrt(N / 4)
+// (1 x 8,000 rows: 18.9 us in pieces of 4 tiles, 23.6 of 1; 1 x 1,500: 14.7 in
+// pieces of 1, 16.9 of 2 and of 4).
+__device__ __forceinline__ int least_chunk(int tiles) {
+    int c = 1;
+    while (4 * (c + 1) * (c + 1) <= tiles + 2) ++c;
+    return c;
+}
+
 // The pair's chunk of the work, by all threads of the CTA.
 __device__ void make_plan(const Args& a, Smem& S, int pair, int pairs) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.bd.B + kThreads - 1) / kThreads;
     const int b_lo = min(a.bd.B, tid * per), b_hi = min(a.bd.B, b_lo + per);
     int64_t sum = 0;
+    int tiles = 0;
     for (int b = b_lo; b < b_hi; ++b) {
         SeqInfo q;
-        if (seq_ok(a.bd, b, a.status, q)) sum += seq_units(q);
+        if (!seq_ok(a.bd, b, a.status, q) || q.nq == 0) continue;
+        sum += seq_units(q);
+        tiles = max(tiles, (q.ctx + kTile - 1) / kTile);
     }
+    tiles = __reduce_max_sync(0xffffffffu, tiles);
+    if (lane == 0) S.longest[warp] = tiles;
     int64_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -192,7 +208,9 @@ __device__ void make_plan(const Args& a, Smem& S, int pair, int pairs) {
     }
     const int64_t even = all < (int64_t(1) << 30) ? (int64_t)(((uint32_t)all + pairs - 1) / (uint32_t)pairs)
                                                   : (all + pairs - 1) / pairs;
-    const int64_t chunk = max(even, (int64_t)kMinChunk);
+    int longest = 0;
+    for (int w = 0; w < kThreads / 32; ++w) longest = max(longest, S.longest[w]);
+    const int64_t chunk = max(even, (int64_t)least_chunk(longest));
     const int64_t lo = min(all, pair * chunk);
     if (tid == 0) {
         S.plan.lo = lo;
@@ -247,7 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (tid == 0) latch_status(a.status, DSA_ERR_INTERNAL);
         return;                                  // both CTAs: the same launch, the same offset
     }
-    if (tid == 0) {
+    if (tid == kThreads - 32) {
         for (int i = 0; i < kKStages; ++i) {
             mbar_init(smem_u32(&S.kfull[i]), 2);
             mbar_init(smem_u32(&S.kempty[i]), 1);
@@ -278,10 +296,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
+    __syncwarp();
+    cluster_arrive();                            // the peer may use this CTA's barriers and TMEM ..
     make_plan(a, S, pair, pairs);
     tc_fence_before();
     __syncthreads();
-    cluster_barrier();
+    cluster_wait();                              // .. and this CTA the peer's
     tc_fence_after();
     const uint32_t tmem = S.tmem;
     Seg s;
@@ -618,7 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 };
                 if (ok && whole && !bad) {
-#pragma unroll 1
+#pragma unroll 2
                     for (uint32_t c = 0; c < 256; c += 64) {
                         uint32_t o[2][32];
                         tmem_ld_32x32b_x32(tl + kOCol + c, o[0]);
@@ -643,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     // warp's 32 lanes side by side
                     float4* part = reinterpret_cast<float4*>(a.part_o) +
                                    ((slot * 2 + (int)rank) * 4 + (warp - 4)) * 64 * 32 + lane;
-#pragma unroll 1
+#pragma unroll 2
                     for (uint32_t c = 0; c < 256; c += 32) {
                         uint32_t o[32];
                         tmem_ld_32x32b_x32(tl + kOCol + c, o);
@@ -691,7 +711,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    cluster_barrier();
+    cluster_arrive();
+    cluster_wait();
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
@@ -819,12 +840,11 @@ int max_pairs() {
     return n;
 }
 
-// Pairs that a call launches: no more than its bounds can give kMinChunk of
-// work each.
+// Pairs that a call launches: no more than its bounds give work to.
 int pairs_for(const BatchDev& bd) {
     const int64_t items = (int64_t)bd.B * ((std::min(bd.max_q, DSA_MAX_TREE) + 1) / 2);
     const int64_t units = items * ((bd.max_ctx + kTile - 1) / kTile + kItemCost);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2, (units + kMinChunk - 1) / kMinChunk));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2, units));
 }
 
 }  // namespace
