@@ -728,7 +728,7 @@ constexpr int kMergeBlocks = 16, kMergeWarps = 8;
 __global__ void __launch_bounds__(32 * kMergeWarps)
     tree_merge_kernel(const int4* __restrict__ meta, const float* __restrict__ part_lse,
                       const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
-    __shared__ float acc_s[kMergeWarps][17][32];
+    __shared__ float acc_s[kMergeWarps][18][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     const int4 it = meta[blockIdx.x];
@@ -748,52 +748,77 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
         const int rank = unit >> 6, w = (unit >> 4) & 3, c = 16 * (unit & 15);
         const int x = 32 * (w & 1) + lane;           // the lane's head
         auto piece_lse = [&](int e) -> float { return part_lse[slot(e) * 128 + 64 * rank + x]; };
-        float mx = -INFINITY;
+        // eight pieces' sums at a time, with a running maximum
+        float acc[16], sum = 0.f, top = -INFINITY;
         bool bad = false, nan = false;
-#pragma unroll 4
-        for (int e = 0; e < pieces; ++e) {
-            const float v = piece_lse(e);
-            bad = bad || v == INFINITY;
-            nan = nan || v != v;
-            mx = fmaxf(mx, v);
-        }
-        if (nan) mx = NAN;
-        const float base = mx == -INFINITY ? 0.f : mx;
-        float acc[16], sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-#pragma unroll 2
-        for (int e = e0; e < pieces; e += step) {
-            const float f = ex2_approx((piece_lse(e) - base) * kLog2e);
-            const float4* o = part_o + (((slot(e) * 2 + rank) * 4 + w) * 64 + c / 4) * 32 + lane;
-            sum += f;
+#pragma unroll 1
+        for (int e1 = e0; e1 < pieces; e1 += 8 * step) {
+            float ls[8], mx = top;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float4 v = o[32 * k];
-                acc[4 * k] += f * v.x;
-                acc[4 * k + 1] += f * v.y;
-                acc[4 * k + 2] += f * v.z;
-                acc[4 * k + 3] += f * v.w;
+            for (int q = 0; q < 8; ++q) ls[q] = e1 + q * step < pieces ? piece_lse(e1 + q * step) : -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                bad = bad || ls[q] == INFINITY;
+                nan = nan || ls[q] != ls[q];
+                mx = fmaxf(mx, ls[q]);
+            }
+            const float base = mx == -INFINITY ? 0.f : mx, down = ex2_approx((top - base) * kLog2e);
+            top = mx;
+            sum *= down;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) acc[k] *= down;
+#pragma unroll 2
+            for (int q = 0; q < 8; ++q) {
+                if (e1 + q * step >= pieces) break;
+                const float f = ex2_approx((ls[q] - base) * kLog2e);
+                const float4* o = part_o + (((slot(e1 + q * step) * 2 + rank) * 4 + w) * 64 + c / 4) * 32 + lane;
+                sum += f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 v = o[32 * k];
+                    acc[4 * k] += f * v.x;
+                    acc[4 * k + 1] += f * v.y;
+                    acc[4 * k + 2] += f * v.z;
+                    acc[4 * k + 3] += f * v.w;
+                }
             }
         }
+        if (bad) top = INFINITY;
+        else if (nan) top = NAN;
         if (wide) {
             // the warps' sums, in order
 #pragma unroll
             for (int k = 0; k < 16; ++k) acc_s[warp][k][lane] = acc[k];
             acc_s[warp][16][lane] = sum;
+            acc_s[warp][17][lane] = top;
             __syncthreads();
             if (warp == 0) {
+                float mx = top;
 #pragma unroll
                 for (int v = 1; v < kMergeWarps; ++v) {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) acc[k] += acc_s[v][k][lane];
-                    sum += acc_s[v][16][lane];
+                    const float m = acc_s[v][17][lane];
+                    if (mx != INFINITY) mx = m == INFINITY || m != m ? m : mx != mx ? mx : fmaxf(mx, m);
                 }
+                const float base = mx == -INFINITY ? 0.f : mx;
+                const float own = ex2_approx((top - base) * kLog2e);
+                sum *= own;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) acc[k] *= own;
+#pragma unroll
+                for (int v = 1; v < kMergeWarps; ++v) {
+                    const float f = ex2_approx((acc_s[v][17][lane] - base) * kLog2e);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) acc[k] += f * acc_s[v][k][lane];
+                    sum += f * acc_s[v][16][lane];
+                }
+                top = mx;
             }
             __syncthreads();
             if (warp != 0) continue;
         }
-        if (bad) continue;
+        if (top == INFINITY) continue;           // a bad page in one of the pieces
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int64_t head = (int64_t)(it.x + rank) * kH + x;
         uint4* to = reinterpret_cast<uint4*>(out + head * kDV + 128 * (w >> 1) + (c & 127) + 2 * (c & 128));
@@ -803,7 +828,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
                                pack_bf16x2(acc[8 * k + 2] * inv, acc[8 * k + 3] * inv),
                                pack_bf16x2(acc[8 * k + 4] * inv, acc[8 * k + 5] * inv),
                                pack_bf16x2(acc[8 * k + 6] * inv, acc[8 * k + 7] * inv));
-        if (lse && (w >> 1) == 0 && c == 0) lse[head] = sum == 0.f ? -INFINITY : base + log2f(sum) * kLn2;
+        if (lse && (w >> 1) == 0 && c == 0) lse[head] = sum == 0.f ? -INFINITY : top + log2f(sum) * kLn2;
     }
 }
 
