@@ -430,10 +430,13 @@ DSA_API dsa_status dsa_latent_append(int32_t total_q, const uint16_t* x, int64_t
  * A row that sees nothing gets out = 0 and lse = -inf.  Cache rows past
  * ctx_len and new rows that a row does not see do not reach its results,
  * whatever they hold; a row that sees a new row with a NaN or infinity gets
- * NaN.  A block-table entry outside [0, pool_pages) latches
- * DSA_ERR_BAD_INDEX, a sequence with more than 64 new rows
- * DSA_ERR_BAD_BATCH, and the outputs of the sequence's affected rows are
- * left unwritten.  max_q > 64 -> DSA_ERR_UNSUPPORTED. */
+ * NaN.  A block-table entry outside [0, pool_pages) among the sequence's
+ * pages latches DSA_ERR_BAD_INDEX and leaves the sequence's rows unwritten.
+ * max_q > 64 -> DSA_ERR_UNSUPPORTED.
+ * fp32 scores, softmax statistics and sums; the softmax weights are rounded
+ * to bf16 for the product with the values (as in dsa_sparse_mla_fwd) and the
+ * result once more.  Reads a cached row once per two new rows of its
+ * sequence; two launches. */
 DSA_API dsa_status dsa_tree_mla_fwd(const dsa_batch* batch, const dsa_pages* pages, const uint16_t* q,
                                     const uint16_t* kv, const uint64_t* mask, float sm_scale, uint16_t* out,
                                     float* lse, void* ws, size_t ws_bytes, void* stream);

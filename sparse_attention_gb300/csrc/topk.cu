@@ -352,13 +352,9 @@ __device__ __forceinline__ void put(int32_t* out, uint32_t pos, int k, int32_t v
 
 // A masked row's end: packs its visible new scores and their positions
 // (threads 0-63 write; the caller synchronises) and returns the row's length
-// without gaps, c committed positions first; -1 for too many new rows.
+// without gaps, c committed positions first.
 __device__ __forceinline__ int32_t masked_end(const SeqInfo& sq, int32_t i, const float* row, const uint64_t* mask,
-                                              float* end_score, int32_t* end_pos, int32_t* status) {
-    if (sq.nq > DSA_MAX_TREE) {
-        latch_status(status, DSA_ERR_BAD_BATCH);
-        return -1;
-    }
+                                              float* end_score, int32_t* end_pos) {
     const int tid = threadIdx.x;
     const int32_t c = sq.ctx - sq.nq;
     const uint64_t bits = visible_bits(__ldg(reinterpret_cast<const unsigned long long*>(mask) + sq.q0 + i), i);
@@ -400,8 +396,7 @@ __global__ void __launch_bounds__(NT, NT <= 512 ? 2 : 1)
     const int32_t c = MASKED ? sq.ctx - sq.nq : 0;
     int32_t n = t + 1;
     if constexpr (MASKED) {
-        n = masked_end(sq, i, row, mask, end_score, end_pos, status);
-        if (n < 0) return;
+        n = masked_end(sq, i, row, mask, end_score, end_pos);
         __syncthreads();
     }
     auto position = [&](int32_t j) -> int32_t {
@@ -790,8 +785,7 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : KPT <= 8 ? 3 : 2)
         v[u] = sq.ctx > k && j < w_end ? __ldg(reinterpret_cast<const float4*>(row + j))
                                        : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const int32_t n = masked_end(sq, i, row, mask, end_score, end_pos, status);
-    if (n < 0) return;
+    const int32_t n = masked_end(sq, i, row, mask, end_score, end_pos);
 #pragma unroll
     for (int x = 0; x < kBinsPerThread; ++x) S.hist[NT * x + tid] = 0u;
     if (tid == 0) {

@@ -105,15 +105,6 @@ struct Args {
     int32_t rows_total;  // cache rows
 };
 
-__device__ __forceinline__ bool seq_ok(const BatchDev& bd, int b, int32_t* status, SeqInfo& s) {
-    if (!load_seq(bd, b, status, s)) return false;
-    if (s.nq > DSA_MAX_TREE) {
-        latch_status(status, DSA_ERR_BAD_BATCH);
-        return false;
-    }
-    return true;
-}
-
 __device__ __forceinline__ int64_t seq_units(const SeqInfo& s) {
     return (int64_t)((s.nq + 1) >> 1) * (((s.ctx + kTile - 1) / kTile) + kItemCost);
 }
@@ -135,7 +126,7 @@ struct SegIter {
                 b0 = b;
                 const int mine = b0 + (int)lane_id();
                 SeqInfo q{0, 0, 0};
-                if (mine >= a.bd.B || !seq_ok(a.bd, mine, nullptr, q)) q.nq = 0;
+                if (mine >= a.bd.B || !load_seq(a.bd, mine, nullptr, q)) q.nq = 0;
                 w_q0 = q.q0, w_nq = q.nq, w_ctx = q.ctx;
             }
             const int32_t nq = __shfl_sync(0xffffffffu, w_nq, b - b0);
@@ -187,7 +178,7 @@ __device__ void make_plan(const Args& a, Smem& S, int pair, int pairs) {
     int tiles = 0;
     for (int b = b_lo; b < b_hi; ++b) {
         SeqInfo q;
-        if (!seq_ok(a.bd, b, a.status, q) || q.nq == 0) continue;
+        if (!load_seq(a.bd, b, a.status, q) || q.nq == 0) continue;
         sum += seq_units(q);
         tiles = max(tiles, (q.ctx + kTile - 1) / kTile);
     }
@@ -224,7 +215,7 @@ __device__ void make_plan(const Args& a, Smem& S, int pair, int pairs) {
         S.plan.start_u = u;
         for (int b = b_lo; b + 1 < b_hi; ++b) {
             SeqInfo q;
-            const int64_t w = seq_ok(a.bd, b, nullptr, q) ? seq_units(q) : 0;
+            const int64_t w = load_seq(a.bd, b, nullptr, q) ? seq_units(q) : 0;
             if (lo < u + w) break;
             u += w;
             S.plan.start_b = b + 1;

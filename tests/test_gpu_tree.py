@@ -265,6 +265,84 @@ def test_attention_masks(page):
     assert (out[:5] == 0).all() and torch.isinf(lse[:5]).all()
 
 
+def test_attention_pieces_that_a_row_does_not_see():
+    """Contexts that end on a tile: the last tile holds new rows alone, which some rows do not see."""
+    masks = [[0, 2, 1, 0, 31], [0] * 3, [1], [0, 0, 7]]
+    st = Step([1280, 128, 0, 0], [5, 3, 1, 3], 64, seed=13, masks=masks)
+    q, kv = st.inputs()
+    out, lse = st.attention(q, kv)
+    assert st.status() == 0
+    check_attention(st, q, kv, out, lse)
+
+
+@pytest.mark.parametrize("way", ["rising", "falling", "flat", "spikes"])
+def test_attention_moving_maximum(way):
+    """Scores whose running maximum moves at every tile, never, or by hundreds at once."""
+    st = Step([3500, 650], [2, 3], 16, seed=14)
+    q, kv = st.inputs()
+    q[:] = torch.randn((1, H, D_QK), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    along = q[0, 0].double() / (q[0, 0].double() ** 2).sum()
+    for b in range(2):
+        n = st.L[b]
+        want = {"rising": torch.linspace(-300, 300, n), "falling": torch.linspace(300, -300, n),
+                "flat": torch.zeros(n), "spikes": torch.where(torch.arange(n) % 500 == 499, 400.0, -100.0)}[way]
+        rows = torch.from_numpy(st.row(b, np.arange(n)))
+        kv[rows] = (kv[rows].double() * 0.05 + want.double()[:, None] / SCALE * along).to(torch.bfloat16)
+    out, lse = st.attention(q, kv)
+    assert st.status() == 0
+    check_attention(st, q, kv, out, lse)
+
+
+@pytest.mark.parametrize("what", ["page", "nan"])
+def test_attention_of_a_long_sequence_cut_into_many_pieces(what):
+    """A bad page leaves the rows unwritten, a NaN in a new row reaches its seers, whichever piece holds it."""
+    st = Step([30000, 40], [3, 1], 64, seed=15, masks=[[1, 2, 7], [1]])
+    q, kv = st.inputs()
+    if what == "page":
+        st.pages.block_table[0, 200] = -1
+    else:
+        kv[int(st.row(0, 30001)), 7] = float("nan")
+    out, lse = st.attention(q, kv)
+    assert st.status() == (7 if what == "page" else 0)
+    if what == "page":
+        assert (out[:3] == 7).all() and (lse[:3] == 7).all()
+        check_attention(st, q, kv, out, lse, {3})
+    else:
+        assert torch.isnan(out[1:3]).all() and torch.isnan(lse[1:3]).all()
+        check_attention(st, q, kv, out, lse, {0, 3})
+
+
+def test_thousands_of_sequences():
+    """Every call on 65,535 sequences, most of them empty."""
+    rng = np.random.default_rng(8)
+    B = 65535
+    c, m = np.zeros(B, np.int64), np.zeros(B, np.int64)
+    some = np.sort(rng.choice(B, 300, replace=False))
+    some[-1] = B - 1
+    c[some], m[some] = rng.integers(0, 60, 300), rng.integers(1, 4, 300)
+    st = Step(c, m, 16, seed=16)
+    q, kv = st.inputs()
+    out, lse = st.attention(q, kv)
+    assert st.status() == 0
+    rows = set(rng.choice(st.T, 40, replace=False).tolist()) | {0, st.T - 1}
+    check_attention(st, q, kv, out, lse, rows)
+    t = Tables(c, m, 16, True, pad=3)
+    assert t.run() == 0
+    t.check()
+    flat = Step(c, m, 0, seed=17)
+    sc = torch.randn((flat.T, 64), generator=torch.Generator().manual_seed(2))
+    idx = torch.full((flat.T, 20), -7, dtype=I32, device="cuda")
+    dsa.tree_topk(flat.b, sc.cuda(), flat.mask, 20, idx, ws=flat.ws)
+    assert flat.status() == 0
+    assert np.array_equal(idx.cpu().numpy(), _topk_ref(flat, sc.numpy(), 20))
+    kv1 = kv.clone().cuda()
+    new = torch.zeros(B, dtype=I32, device="cuda")
+    dsa.tree_commit(st.b, st.mask, _dev(m - 1), new, kv1, pages=st.pages, ws=st.ws)
+    assert st.status() == 0
+    want = [int(c[b]) + (bin(int(st.masks[b][-1])).count("1") if m[b] else 0) for b in range(B)]
+    assert new.tolist() == want
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_attention_ignores_what_a_row_does_not_see(bad):
     """A new row with NaN or infinities reaches the rows that see it, and no others."""
