@@ -59,18 +59,23 @@ constexpr int kKStages = 3;                  // a whole tile of K ..
 constexpr int kVStages = 2;                  // .. and of V: a stage is 128 positions x 128 dims of one half
 constexpr int kKBytes = kGroup * kChunkBytes, kVBytes = 4 * kChunkBytes;
 constexpr uint32_t kOCol = 0, kSCol = 256;   // TMEM columns
+constexpr int kMaxPairs = 96;                 // CTA pairs of a launch
+constexpr int kPlanSeqs = 256;               // sequences of a call whose items may go round the pairs
 constexpr int kSegs = 4;                     // segments published ahead
+constexpr int64_t kSharedBytes = int64_t(48) << 20;   // cached rows that L2 keeps for pairs apart in a sequence
+constexpr int kRoundPart = 48;               // units per pair below which rounds do not pay
 constexpr float kRescale = 8.f;              // log2
 
 struct Plan {
-    int64_t lo, hi, start_u, chunk;
-    int32_t start_b;
+    int64_t lo[kMaxPairs + 1];   // pair k's share of the cut items: units [lo[k], lo[k + 1])
+    int64_t start_u;             // the share's first sequence, and where its items begin
+    int32_t start_b, rounds;     // whole items that every pair takes before
 };
 
 // One item's tiles [t0, t1) of a pair's chunk.
 struct Seg {
     int32_t b, row, c, len, i0, rows, t0, t1, tiles;
-    int64_t u_end;
+    int64_t u0;                  // the unit of tile 0, for a piece of a cut item
     __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
@@ -103,56 +108,98 @@ struct Args {
     float* part_o;       // [2 * pairs][2 CTAs][4 warps][64 groups of 4 columns][32 lanes][4]
     int32_t* status;
     int32_t rows_total;  // cache rows
+    bool may_round;      // the bounds allow plan_rounds
 };
 
 __device__ __forceinline__ int64_t seq_units(const SeqInfo& s) {
     return (int64_t)((s.nq + 1) >> 1) * (((s.ctx + kTile - 1) / kTile) + kItemCost);
 }
 
-// Walks the segments of a pair's chunk (a warp; lanes hold 32 sequences'
-// lengths).
+// Walks the segments of a pair (a warp; lanes hold 32 sequences' lengths):
+// first every pairs-th item, whole, then its share of the others.
 struct SegIter {
     const Args& a;
     const Plan& plan;
-    int32_t b, p = 0, b0 = -64;
-    int64_t u;
+    const int32_t pair, pairs;
+    int32_t round = 0, first = 0;        // round, and the first item of sequence b, while items are whole
+    int32_t b = 0, p = 0, b0 = -64;
+    int64_t u = 0;
     int32_t w_q0 = 0, w_nq = 0, w_ctx = 0;
-    __device__ SegIter(const Args& args, const Plan& pl) : a(args), plan(pl), b(pl.start_b), u(pl.start_u) {}
+    __device__ SegIter(const Args& args, const Plan& pl, int32_t pair_, int32_t pairs_)
+        : a(args), plan(pl), pair(pair_), pairs(pairs_) {
+        if (plan.rounds == 0) begin_share();
+    }
+
+    __device__ void begin_share() {
+        b = plan.start_b;
+        u = plan.start_u;
+        p = 0;
+    }
+
+    // new rows, length and first packed row of sequence b
+    __device__ void lengths(int32_t& nq, int32_t& ctx, int32_t& q0) {
+        if (b < b0 || b >= b0 + 32) {
+            b0 = b;
+            const int mine = b0 + (int)lane_id();
+            SeqInfo q{0, 0, 0};
+            if (mine >= a.bd.B || !load_seq(a.bd, mine, nullptr, q)) q.nq = 0;
+            w_q0 = q.q0, w_nq = q.nq, w_ctx = q.ctx;
+        }
+        nq = __shfl_sync(0xffffffffu, w_nq, b - b0);
+        ctx = __shfl_sync(0xffffffffu, w_ctx, b - b0);
+        q0 = __shfl_sync(0xffffffffu, w_q0, b - b0);
+    }
+
+    __device__ void fill(Seg& s, int32_t item, int32_t nq, int32_t ctx, int32_t q0) const {
+        s.b = b;
+        s.i0 = 2 * item;
+        s.row = q0 + s.i0;
+        s.rows = min(2, nq - s.i0);
+        s.c = ctx - nq;
+        s.len = ctx;
+        s.tiles = (ctx + kTile - 1) / kTile;
+    }
 
     __device__ bool next(Seg& s) {
-        const int64_t lo = plan.lo, hi = plan.hi;
-        for (; b < a.bd.B; ++b, p = 0) {
-            if (b >= b0 + 32) {
-                b0 = b;
-                const int mine = b0 + (int)lane_id();
-                SeqInfo q{0, 0, 0};
-                if (mine >= a.bd.B || !load_seq(a.bd, mine, nullptr, q)) q.nq = 0;
-                w_q0 = q.q0, w_nq = q.nq, w_ctx = q.ctx;
+        int32_t nq, ctx, q0;
+        while (round < plan.rounds) {
+            if (b >= a.bd.B) {                   // lengths that change under the call
+                round = plan.rounds;
+                begin_share();
+                break;
             }
-            const int32_t nq = __shfl_sync(0xffffffffu, w_nq, b - b0);
+            lengths(nq, ctx, q0);
+            const int32_t item = round * pairs + pair - first, items = (nq + 1) >> 1;
+            if (item >= items) {
+                first += items;
+                ++b;
+                continue;
+            }
+            fill(s, item, nq, ctx, q0);
+            s.t0 = 0;
+            s.t1 = s.tiles;
+            if (++round == plan.rounds) begin_share();
+            return true;
+        }
+        const int64_t lo = plan.lo[pair], hi = plan.lo[pair + 1];
+        for (; b < a.bd.B; ++b, p = 0) {
+            lengths(nq, ctx, q0);
             if (nq == 0) continue;
-            const int32_t ctx = __shfl_sync(0xffffffffu, w_ctx, b - b0), q0 = __shfl_sync(0xffffffffu, w_q0, b - b0);
-            const int32_t tiles = (ctx + kTile - 1) / kTile, per = tiles + kItemCost, pairs = (nq + 1) >> 1;
-            if (p == 0 && lo > u) p = (uint32_t)(lo - u) / (uint32_t)per;   // < pairs: lo lies in the chunk's first sequence
-            while (p < pairs) {
+            const int32_t tiles = (ctx + kTile - 1) / kTile, per = tiles + kItemCost, items = (nq + 1) >> 1;
+            if (p == 0 && lo > u) p = (uint32_t)(lo - u) / (uint32_t)per;   // < items: lo lies in the share's first sequence
+            while (p < items) {
                 const int64_t u0 = u + (int64_t)p * per + kItemCost;
                 if (u0 - kItemCost >= hi) return false;
                 s.t0 = (int32_t)max((int64_t)0, min((int64_t)tiles, lo - u0));
                 s.t1 = (int32_t)max((int64_t)0, min((int64_t)tiles, hi - u0));
-                s.i0 = 2 * p;
                 ++p;
                 if (s.t1 > s.t0) {
-                    s.b = b;
-                    s.row = q0 + s.i0;
-                    s.rows = min(2, nq - s.i0);
-                    s.c = ctx - nq;
-                    s.len = ctx;
-                    s.tiles = tiles;
-                    s.u_end = u0 + tiles - 1;
+                    fill(s, p - 1, nq, ctx, q0);
+                    s.u0 = u0;
                     return true;
                 }
             }
-            u += (int64_t)pairs * per;
+            u += (int64_t)items * per;
         }
         return false;
     }
@@ -169,18 +216,127 @@ __device__ __forceinline__ int least_chunk(int tiles) {
     return c;
 }
 
-// The pair's chunk of the work, by all threads of the CTA.
+__device__ __forceinline__ int32_t warp_scan_i32(int32_t v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t n = __shfl_up_sync(0xffffffffu, v, o);
+        if ((int)lane_id() >= o) v += n;
+    }
+    return v;
+}
+
+// Whole items go round the pairs first when several node pairs share a
+// sequence and the caches exceed what L2 keeps: the pairs then walk the same
+// one or two sequences side by side, and a cached row comes from HBM once (in
+// equal contiguous shares every sequence is being read at the same time: 3.0
+// GB of HBM reads for 0.23 GB of inputs, 16 trees of 64 over 8,192 rows 0.79
+// ms; 0.66 with rounds; 64 trees of 4 over 1,000 rows, 18 units a pair, lose 4
+// of 50 us).  The shares of the items left over even out what the rounds gave.
+// All threads; kPlanSeqs sequences at most, a thread each.  Sets S.plan's rounds, shares and start; false: no rounds.
+__device__ bool plan_rounds(const Args& a, Smem& S, const SeqInfo& q, int64_t all, int pair, int pairs) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // the V ring is not in use yet
+    int32_t* first = reinterpret_cast<int32_t*>(S.v);            // [B + 1] items before a sequence
+    int32_t* per = first + kThreads + 1;                         // [B] units of its items
+    int32_t* sums = per + kThreads;                              // [3][warps]
+    const int32_t items = (q.nq + 1) >> 1;
+    const int32_t incl = warp_scan_i32(items);
+    // cached rows (64 at a time) of sequences that several items read
+    const uint32_t rows = __reduce_add_sync(0xffffffffu, items > 1 ? (uint32_t)q.ctx >> 6 : 0u);
+    if (lane == 31) {
+        sums[warp] = incl;
+        sums[16 + warp] = (int32_t)min(rows, 1u << 26);
+    }
+    __syncthreads();
+    int32_t before = 0, total = 0, cached = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+        cached += sums[16 + w];
+    }
+    // (all the same for every thread)
+    const int64_t part = (all + pairs - 1) / pairs;
+    if ((int64_t)cached * 64 * 2 * kDQK <= kSharedBytes || total < pairs || part < kRoundPart) return false;
+    first[tid] = before + incl - items;
+    per[tid] = (q.ctx + kTile - 1) / kTile + kItemCost;
+    if (tid == 0) first[kThreads] = total;
+    __syncthreads();
+    // thread k: what the rounds give pair k; one round less if some pair gets
+    // more than its part of all
+    int rounds = total / pairs;
+    int64_t load = 0, last = 0;
+    if (tid < pairs) {
+        int b = 0;
+        for (int r = 0; r < rounds; ++r) {
+            const int32_t item = r * pairs + tid;
+            while (first[b + 1] <= item) ++b;
+            last = per[b];
+            load += last;
+        }
+    }
+    if (__syncthreads_or(tid < pairs && load > part)) {
+        if (--rounds == 0) return false;
+        load -= last;
+    }
+    // shares of the rest, one behind the other
+    if (tid < kMaxPairs) {
+        // one unit at least, so that no pair inside a cut item is without a piece
+        int64_t sum = tid < pairs ? max((int64_t)1, part - load) : 0, given = tid < pairs ? load : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t n = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += n;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) given += __shfl_xor_sync(0xffffffffu, given, o);
+        if (lane == 31) {
+            S.scan[warp] = sum;
+            S.scan[4 + warp] = given;
+        }
+        S.plan.lo[tid + 1] = sum;
+    }
+    __syncthreads();
+    if (tid < kMaxPairs) {
+        int64_t rest = all, lower = 0;
+        for (int w = 0; w < kMaxPairs / 32; ++w) {
+            rest -= S.scan[4 + w];
+            if (w < warp) lower += S.scan[w];
+        }
+        S.plan.lo[tid + 1] = min(rest, S.plan.lo[tid + 1] + lower);
+    }
+    if (tid == 0) S.plan.lo[0] = 0;
+    __syncthreads();
+    if (tid == 0) {
+        // the sequence of the first item left over, then of this pair's share
+        const int32_t item = rounds * pairs;
+        int b = 0;
+        while (b < a.bd.B && first[b + 1] <= item) ++b;
+        int64_t u = b < a.bd.B ? -(int64_t)(item - first[b]) * per[b] : 0;
+        while (b < a.bd.B && u + (int64_t)(first[b + 1] - first[b]) * per[b] <= S.plan.lo[pair]) {
+            u += (int64_t)(first[b + 1] - first[b]) * per[b];
+            ++b;
+        }
+        S.plan.start_b = b;
+        S.plan.start_u = u;
+        S.plan.rounds = rounds;
+    }
+    return true;
+}
+
+// The pair's part of the work, by all threads of the CTA.
 __device__ void make_plan(const Args& a, Smem& S, int pair, int pairs) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.bd.B + kThreads - 1) / kThreads;
     const int b_lo = min(a.bd.B, tid * per), b_hi = min(a.bd.B, b_lo + per);
     int64_t sum = 0;
     int tiles = 0;
+    SeqInfo mine{0, 0, 0};
     for (int b = b_lo; b < b_hi; ++b) {
         SeqInfo q;
         if (!load_seq(a.bd, b, a.status, q) || q.nq == 0) continue;
         sum += seq_units(q);
         tiles = max(tiles, (q.ctx + kTile - 1) / kTile);
+        mine = q;
     }
     tiles = __reduce_max_sync(0xffffffffu, tiles);
     if (lane == 0) S.longest[warp] = tiles;
@@ -197,16 +353,16 @@ __device__ void make_plan(const Args& a, Smem& S, int pair, int pairs) {
         if (w < warp) before += S.scan[w];
         all += S.scan[w];
     }
+    if (a.may_round && plan_rounds(a, S, mine, all, pair, pairs)) return;
     const int64_t even = all < (int64_t(1) << 30) ? (int64_t)(((uint32_t)all + pairs - 1) / (uint32_t)pairs)
                                                   : (all + pairs - 1) / pairs;
     int longest = 0;
     for (int w = 0; w < kThreads / 32; ++w) longest = max(longest, S.longest[w]);
     const int64_t chunk = max(even, (int64_t)least_chunk(longest));
     const int64_t lo = min(all, pair * chunk);
+    if (tid <= pairs) S.plan.lo[tid] = min(all, tid * chunk);
     if (tid == 0) {
-        S.plan.lo = lo;
-        S.plan.hi = min(all, lo + chunk);
-        S.plan.chunk = chunk;
+        S.plan.rounds = 0;
         if (lo >= all) S.plan.start_b = a.bd.B;
     }
     if (before <= lo && lo < before + sum) {
@@ -290,6 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_arrive();                            // the peer may use this CTA's barriers and TMEM ..
     make_plan(a, S, pair, pairs);
+    if (a.may_round) fence_proxy_async_smem();   // plan_rounds used the V ring
     tc_fence_before();
     __syncthreads();
     cluster_wait();                              // .. and this CTA the peer's
@@ -674,7 +831,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         // the segments, and what tree_merge_kernel has to know of a cut item
-        SegIter it(a, S.plan);
+        SegIter it(a, S.plan, pair, pairs);
+        // the pair whose share holds unit u: the last with lo <= u
+        auto holder = [&](int64_t u) -> int {
+            int k = 0;
+            for (int x = 0; x < pairs; x += 32)
+                k += __popc(__ballot_sync(0xffffffffu, x + lane < pairs && S.plan.lo[x + lane] <= u));
+            return k - 1;
+        };
         int4 meta = make_int4(0, 0, 0, 0);
         bool more = true;
         for (uint32_t n = 0; ok && more; ++n) {
@@ -688,9 +852,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mbar_arrive(smem_u32(&S.segfull[slot]));
             }
             __syncwarp();
-            if (more && !s.whole())
-                meta = make_int4(s.row, s.rows, (int)(s.u_end / S.plan.chunk),
-                                 (int)((s.u_end - s.tiles + 1) / S.plan.chunk));
+            if (more && !s.whole()) meta = make_int4(s.row, s.rows, holder(s.u0 + s.tiles - 1), holder(s.u0));
         }
         if (rank == 0 && lane == 0) a.meta[pair] = meta;
     }
@@ -851,7 +1013,7 @@ int max_pairs() {
         cudaGetLastError();
         return num_sms() / 2;
     }
-    n = std::min(n, num_sms() / 2);
+    n = std::min(n, std::min(num_sms() / 2, kMaxPairs));
     cache[dev].store(n, std::memory_order_relaxed);
     return n;
 }
@@ -860,7 +1022,7 @@ int max_pairs() {
 int pairs_for(const BatchDev& bd) {
     const int64_t items = (int64_t)bd.B * ((std::min(bd.max_q, DSA_MAX_TREE) + 1) / 2);
     const int64_t units = items * ((bd.max_ctx + kTile - 1) / kTile + kItemCost);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2, units));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(num_sms() / 2, kMaxPairs), units));
 }
 
 }  // namespace
@@ -886,6 +1048,8 @@ cudaError_t launch_tree_mla(const BatchDev& bd, const PagesDev& pg, const uint16
     a.part_o = static_cast<float*>(scratch);
     a.part_lse = a.part_o + slots * 128 * kDV;
     a.meta = reinterpret_cast<int4*>(a.part_lse + slots * 128);
+    a.may_round = bd.B <= kPlanSeqs && bd.max_q > 2 && pairs <= kMaxPairs &&
+                  (int64_t)bd.B * bd.max_ctx * 2 * kDQK > kSharedBytes;
     a.rows_total = pg.table ? pg.pool_pages << pg.shift : (int32_t)(bd.B * bd.stride);
     const int page = pg.table ? 1 << pg.shift : kTile;
     const uint32_t krows = page >= 64 ? 64 : page == 32 ? 32 : 8, kchunks = krows == 32 ? 1 : kGroup;
