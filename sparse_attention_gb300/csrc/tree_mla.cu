@@ -637,22 +637,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < kVStages; ++j) {
                     wait(S.vloc[j], fixed & 1);
                     __syncwarp();
-                    for (int32_t x = max(0, s.c - pos0) + (lane >> 4); x < kTile; x += 2) {
+                    // two rows at a time; boxes behind the last row are zero
+                    const int32_t from = max(0, s.c - pos0) + (lane >> 4), live = min(kTile, s.len - pos0);
+                    const int32_t end = (live + kVRows - 1) & -kVRows;
+                    auto piece = [&](int32_t x) -> uint4* {
                         const int32_t in = x & (kVRows - 1), blk = (lane >> 3) & 1;
-                        uint4* at = reinterpret_cast<uint4*>(S.v + j * kVBytes + (x - in) * 256 +
-                                                             (blk * kVRows + in) * 128 + (lane & 7) * 16);
-                        if (pos0 + x >= s.len) {
-                            *at = make_uint4(0, 0, 0, 0);
-                        } else {
-                            uint4 v = *at;
-                            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+                        return reinterpret_cast<uint4*>(S.v + j * kVBytes + (x - in) * 256 +
+                                                        (blk * kVRows + in) * 128 + (lane & 7) * 16);
+                    };
+#pragma unroll 1
+                    for (int32_t x = max(from, live + ((live ^ from) & 1)); x < end; x += 2)
+                        *piece(x) = make_uint4(0, 0, 0, 0);
+                    // (four reads in flight; with one, 64 drafted rows held up
+                    // an item's end by 13 K cycles)
+#pragma unroll 1
+                    for (int32_t x0 = from; x0 < live; x0 += 8) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (x0 + 2 * k < live) v[k] = *piece(x0 + 2 * k);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (x0 + 2 * k >= live) break;
+                            uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
                             bool hit = false;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u, hit = true;
-                                if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0xFFFFu, hit = true;
+                            for (int q = 0; q < 4; ++q) {
+                                if ((w[q] & 0x7F80u) == 0x7F80u) w[q] &= 0xFFFF0000u, hit = true;
+                                if ((w[q] & 0x7F800000u) == 0x7F800000u) w[q] &= 0xFFFFu, hit = true;
                             }
-                            if (hit) *at = v;
+                            if (hit) *piece(x0 + 2 * k) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
                     fence_proxy_async_smem();
