@@ -6,11 +6,11 @@
 // With n_b new tokens on c_b committed rows, q_off is the exclusive prefix sum
 // of n_b, and sequence b takes max(0, ceil((c_b + n_b) / P) - held_b) pages
 // from the free list behind those of the sequences before it (a second
-// prefix sum).  Both sums run in one CTA, which alone can refuse the whole step
-// (bad lengths, no pages) before anything advances.  The rows and the new
-// block-table entries are then independent of one another: a few thousand are
-// written by the same CTA (one launch; a step is bound by latency, not by its
-// some 20 KB), more by a second launch over the whole GPU.
+// prefix sum).  Only a CTA that has both sums can tell whether the whole step
+// fits, before anything advances; up to 256 sequences every CTA forms them
+// for itself and then writes its part of the rows (one launch, bound by latency:
+// a step reads and writes some 20 KB), more are summed by one CTA, with the
+// rows in a second launch.
 // A row's page is looked up in the held part of the block table or, behind
 // it, in the free list itself, so rows do not wait for the new entries.
 //
@@ -177,6 +177,9 @@ __device__ void write_rows(const TablesArgs& a, int64_t me, int64_t threads) {
 
 // NT threads: all of them walk the same few hundred instructions, so a small
 // batch is faster with fewer (256 prompts: 6.4 us with 256, 8.2 with 1024).
+// kRows (at most NT sequences): the CTAs also write the rows.  Each forms all
+// sums for itself, the first writes them, and each writes its part of the
+// rows; with more than one CTA no output may be an input.
 template <int NT, bool kRows>
 __global__ void __launch_bounds__(NT) step_lengths_kernel(const TablesArgs a) {
     constexpr int kWarps = NT / 32;
@@ -229,8 +232,8 @@ __global__ void __launch_bounds__(NT) step_lengths_kernel(const TablesArgs a) {
         if (head < 0 || tail < head || tail > a.pg.pool_pages) code = DSA_ERR_BAD_BATCH;
         else if (all_f > tail - head) code = DSA_ERR_NO_PAGES;
     }
-    const bool go = code == DSA_OK;
-    if (!go && tid == 0) latch_status(a.status, code);
+    const bool go = code == DSA_OK, first_cta = !kRows || blockIdx.x == 0;
+    if (!go && tid == 0 && first_cta) latch_status(a.status, code);
     // pass 2: the prefix sums and what advances, NT sequences at a time; both
     // sums fit 32 bits now and share one scan
     uint64_t base = 0;
@@ -263,14 +266,16 @@ __global__ void __launch_bounds__(NT) step_lengths_kernel(const TablesArgs a) {
             const int32_t first = (int32_t)((before + incl - mine) >> 32);
             const int32_t ctx = (go ? s.c : a.ctx_old[b]) + s.n;
             const int32_t held = go || !a.pg.table ? s.held : a.held_old[b];
-            a.q_off[b + 1] = off;
-            a.ctx_len[b] = ctx;
-            if (a.pg.table) {
+            if (first_cta) {
+                a.q_off[b + 1] = off;
+                a.ctx_len[b] = ctx;
+            }
+            if (a.pg.table && first_cta) {
                 a.held_kept[b] = held;
                 a.held[b] = held + s.fresh;
                 a.first_new[b] = first;
             }
-            if (kRows && b < NT) {
+            if (kRows) {
                 s_off[b + 1] = off;
                 s_ctx[b] = ctx;
                 s_held[b] = held;
@@ -281,8 +286,8 @@ __global__ void __launch_bounds__(NT) step_lengths_kernel(const TablesArgs a) {
     }
     const int32_t fresh = (int32_t)(base >> 32);
     if (tid == 0) {
-        a.q_off[0] = 0;
-        if (a.pg.table) {
+        if (first_cta) a.q_off[0] = 0;
+        if (a.pg.table && first_cta) {
             a.first_new[a.B] = fresh;
             *a.head = head;
             a.free_out[0] = head + fresh;
@@ -291,20 +296,18 @@ __global__ void __launch_bounds__(NT) step_lengths_kernel(const TablesArgs a) {
         if (kRows) {
             s_off[0] = 0;
             s_head = head;
-            if (a.B <= NT) s_first[a.B] = fresh;
+            s_first[a.B] = fresh;
         }
     }
     if (kRows) {
         __syncthreads();
         TablesArgs l = a;
-        if (a.B <= NT) {
-            l.q_off = s_off;
-            l.ctx_len = s_ctx;
-            l.first_new = s_first;
-            l.held_kept = s_held;
-            l.head = &s_head;
-        }
-        write_rows(l, tid, NT);
+        l.q_off = s_off;
+        l.ctx_len = s_ctx;
+        l.first_new = s_first;
+        l.held_kept = s_held;
+        l.head = &s_head;
+        write_rows(l, (int64_t)blockIdx.x * NT + tid, (int64_t)gridDim.x * NT);
     }
 }
 
@@ -351,13 +354,14 @@ cudaError_t launch_step_tables(const BatchDev& bd, const PagesDev& pg, const int
     // that sequences may take (all of max_ctx for a fresh prompt)
     const int64_t per_seq = pg.table ? std::min<int64_t>(pg.max_pages, ((int64_t)bd.max_q >> pg.shift) + 2) : 0;
     const int64_t items = std::max<int64_t>(std::max<int64_t>(bd.total_q, per_seq * bd.B), parent ? 32 * bd.B : 0);
-    // A few rows and entries are written by the CTA of the sums (the second
-    // launch takes the host 2 us), with 1024 threads where there are more trees
-    // than warps of 256.
+    // One launch where every CTA can form the sums for itself (a second one
+    // takes the host 2 us): up to 256 sequences, and no array that one CTA may
+    // still have to read when the first has advanced it.
     cudaError_t e;
-    if (bd.B <= 256 && items <= 4096) {
-        if (parent && bd.B > 8) step_lengths_kernel<1024, true><<<1, 1024, 0, stream>>>(a);
-        else step_lengths_kernel<256, true><<<1, 256, 0, stream>>>(a);
+    const bool apart = ctx_old != a.ctx_len && (!pg.table || (held_old != held && free_range != free_out));
+    if (bd.B <= 256 && (apart || items <= 1024)) {
+        const int64_t ctas = apart ? std::min<int64_t>((items + 255) / 256, 2 * num_sms()) : 1;
+        step_lengths_kernel<256, true><<<(unsigned)std::max<int64_t>(ctas, 1), 256, 0, stream>>>(a);
         e = cudaGetLastError();
         if (e == cudaSuccess) count_launches(1);
         return e;
