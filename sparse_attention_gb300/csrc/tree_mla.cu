@@ -241,8 +241,10 @@ __device__ __forceinline__ int32_t warp_scan_i32(int32_t v) {
 // GB of HBM reads for 0.23 GB of inputs, 16 trees of 64 over 8,192 rows 0.79
 // ms; 0.66 with rounds; 64 trees of 4 over 1,000 rows, 18 units a pair, lose 4
 // of 50 us).  The shares of the items left over even out what the rounds gave.
-// All threads; kPlanSeqs sequences at most, a thread each.  Sets S.plan's rounds, shares and start; false: no rounds.
-__device__ bool plan_rounds(const Args& a, Smem& S, const SeqInfo& q, int64_t all, int pair, int pairs) {
+// All threads; kPlanSeqs sequences at most, a thread each with its units and
+// those before it.  Sets S.plan's rounds, shares and start; false: no rounds.
+__device__ bool plan_rounds(const Args& a, Smem& S, const SeqInfo& q, int64_t units_before, int64_t units, int64_t all,
+                            int pair, int pairs) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // the V ring is not in use yet
     int32_t* first = reinterpret_cast<int32_t*>(S.v);            // [B + 1] items before a sequence
@@ -271,11 +273,17 @@ __device__ bool plan_rounds(const Args& a, Smem& S, const SeqInfo& q, int64_t al
     if (tid == 0) first[kThreads] = total;
     __syncthreads();
     // thread k: what the rounds give pair k; one round less if some pair gets
-    // more than its part of all
+    // a quarter more than its part of all (up to there the saved reads are worth
+    // more: 24 ragged trees of up to 13 over 7,001 rows 119 -> 113 us)
     int rounds = total / pairs;
     int64_t load = 0, last = 0;
     if (tid < pairs) {
-        int b = 0;
+        int b = 0, top = a.bd.B;
+        while (b + 1 < top) {                    // the sequence of item tid
+            const int mid = (b + top) >> 1;
+            if (first[mid] <= tid) b = mid;
+            else top = mid;
+        }
         for (int r = 0; r < rounds; ++r) {
             const int32_t item = r * pairs + tid;
             while (first[b + 1] <= item) ++b;
@@ -283,7 +291,7 @@ __device__ bool plan_rounds(const Args& a, Smem& S, const SeqInfo& q, int64_t al
             load += last;
         }
     }
-    if (__syncthreads_or(tid < pairs && load > part)) {
+    if (__syncthreads_or(tid < pairs && load > part + part / 4)) {
         if (--rounds == 0) return false;
         load -= last;
     }
@@ -313,21 +321,23 @@ __device__ bool plan_rounds(const Args& a, Smem& S, const SeqInfo& q, int64_t al
         }
         S.plan.lo[tid + 1] = min(rest, S.plan.lo[tid + 1] + lower);
     }
-    if (tid == 0) S.plan.lo[0] = 0;
     __syncthreads();
+    // units before the first item left over, then the sequence in which the
+    // pair's share begins
+    const int32_t rest_item = rounds * pairs;
+    if (first[tid] <= rest_item && rest_item < first[tid + 1])
+        S.scan[0] = units_before + (int64_t)(rest_item - first[tid]) * per[tid];
     if (tid == 0) {
-        // the sequence of the first item left over, then of this pair's share
-        const int32_t item = rounds * pairs;
-        int b = 0;
-        while (b < a.bd.B && first[b + 1] <= item) ++b;
-        int64_t u = b < a.bd.B ? -(int64_t)(item - first[b]) * per[b] : 0;
-        while (b < a.bd.B && u + (int64_t)(first[b + 1] - first[b]) * per[b] <= S.plan.lo[pair]) {
-            u += (int64_t)(first[b + 1] - first[b]) * per[b];
-            ++b;
-        }
-        S.plan.start_b = b;
-        S.plan.start_u = u;
+        S.plan.lo[0] = 0;
         S.plan.rounds = rounds;
+        S.plan.start_b = a.bd.B;
+        if (rest_item >= total) S.scan[0] = all;
+    }
+    __syncthreads();
+    const int64_t u = units_before - S.scan[0], lo = S.plan.lo[pair];
+    if (u <= lo && lo < u + units) {
+        S.plan.start_b = tid;
+        S.plan.start_u = u;
     }
     return true;
 }
@@ -362,7 +372,7 @@ __device__ void make_plan(const Args& a, Smem& S, int pair, int pairs) {
         if (w < warp) before += S.scan[w];
         all += S.scan[w];
     }
-    if (a.may_round && plan_rounds(a, S, mine, all, pair, pairs)) return;
+    if (a.may_round && plan_rounds(a, S, mine, before, sum, all, pair, pairs)) return;
     const int64_t even = all < (int64_t(1) << 30) ? (int64_t)(((uint32_t)all + pairs - 1) / (uint32_t)pairs)
                                                   : (all + pairs - 1) / pairs;
     int longest = 0;
