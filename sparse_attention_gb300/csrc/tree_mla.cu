@@ -477,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto lead = [&](uint64_t& b) -> uint32_t { return map_to_cluster_rank(smem_u32(&b), 0); };
     // bounded; a thread whose wait expired waits for nothing any more
     auto wait = [&](uint64_t& b, uint32_t parity) -> bool {
-        if (ok && !mbar_wait(smem_u32(&b), parity)) {
+        if (ok && !mbar_wait_rolled(smem_u32(&b), parity)) {
             ok = false;
             latch_status(a.status, DSA_ERR_TIMEOUT);
         }
@@ -556,6 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t buf = g & 1;
                 if (g >= 2 && !wait(S.sempty[buf], ((g >> 1) - 1) & 1)) return;
                 const uint64_t dq = sdesc_sw128(smem_u32(S.q), 0, 1024), dk = sdesc_sw128(smem_u32(S.k), 0, ksbo);
+#pragma unroll 1
                 for (int gr = 0; gr < kKStages; ++gr) {
                     if (!wait(S.kfull[gr], g & 1)) return;
                     tc_fence_after();
@@ -578,6 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!wait(S.pfull, g & 1)) return;
                 tc_fence_after();
                 const uint64_t dp = sdesc_sw128(smem_u32(S.p), 0, 1024), dv = sdesc_sw128(smem_u32(S.v), kVRows * 128, 1024);
+#pragma unroll 1
                 for (int j = 0; j < kVStages; ++j) {
                     if (!wait(S.vfull[j], g & 1)) return;
                     tc_fence_after();
