@@ -46,7 +46,7 @@
 // Measured: 16 trees of 64 over 8,192 rows 0.64-0.66 ms = 1,770-1,820 TFLOP/s
 // (1,907 measured peak; the power cap holds the clock at 1.8 GHz); 64 single
 // rows over 32,768 each 0.40 ms = 6.05 TB/s (6.78 measured copy); one tree of
-// 8 over 1,500 rows 17.7 us with the merge.
+// 8 over 1,500 rows 17 us with the merge.
 #include <algorithm>
 #include <atomic>
 
