@@ -464,6 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     cluster_arrive();                            // the peer may use this CTA's barriers and TMEM ..
+    pdl_wait();                                  // lengths, tables and inputs, and the scratch of an earlier call
     make_plan(a, S, pair, pairs);
     if (a.may_round) fence_proxy_async_smem();   // plan_rounds used the V ring
     tc_fence_before();
@@ -918,6 +919,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
                       const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
     __shared__ float acc_s[kMergeWarps][18][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_launch_dependents();
     pdl_wait();
     const int4 it = meta[blockIdx.x];
     const int pair = it.w, helper = (int)blockIdx.x - pair;
@@ -1099,18 +1101,23 @@ cudaError_t launch_tree_mla(const BatchDev& bd, const PagesDev& pg, const uint16
                                 : tree_mla_kernel<8, 16>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
     if (e != cudaSuccess) return e;
-    kernel<<<2 * pairs, kThreads, sizeof(Smem), stream>>>(a, tm_q, tm_k, tm_v);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    count_launches(1);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)pairs, kMergeBlocks);
-    cfg.blockDim = dim3(32 * kMergeWarps);
-    cfg.stream = stream;
+    // Both are programmatic dependents of the launch before them: they set up
+    // while it drains and wait for it before they read anything.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Smem);
+    cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, a, tm_q, tm_k, tm_v)) != cudaSuccess) return e;
+    count_launches(1);
+    cfg.gridDim = dim3((unsigned)pairs, kMergeBlocks);
+    cfg.blockDim = dim3(32 * kMergeWarps);
+    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, (const int4*)a.meta, (const float*)a.part_lse,
                            (const float4*)a.part_o, out, lse);
     if (e == cudaSuccess) count_launches(1);
