@@ -388,6 +388,10 @@ def _here(ws: torch.Tensor, stream) -> int:
     return dev
 
 
+def _raw_stream(stream, dev: int) -> int:
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+
+
 def _paged(batch: Batch, pages: Optional[Pages], dev: int):
     """The dsa_pages argument, and the cache rows that a call may reach."""
     if batch.q_off.get_device() != dev or (pages is not None and pages.block_table.get_device() != dev):
@@ -415,7 +419,7 @@ def step_tables(batch: Batch, n_new, ctx_old, slots, positions, mask=None, paren
         _typed("free_pages", free_pages, i32, pages.pool_pages if pages is not None else 0, dev),
         _typed("free_range", free_range, i32, 2, dev), _typed("free_range_out", free_range_out, i32, 2, dev),
         _typed("slots", slots, i32, c.total_q, dev), _typed("positions", positions, i32, c.total_q, dev),
-        _typed("mask", mask, torch.int64, c.total_q, dev), ws.data_ptr(), ws.numel(), _stream(stream)),
+        _typed("mask", mask, torch.int64, c.total_q, dev), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)),
         "dsa_step_tables")
     return slots
 
@@ -435,7 +439,7 @@ def latent_append(x, gamma, eps: float, cos, sin, positions, slots, kv, ws, stre
         total_q, x.data_ptr(), x.stride(0) if total_q > 1 else D_QK, _typed("gamma", gamma, f32, D_V, dev), float(eps),
         _typed("cos", cos, f32, rows * 64, dev), _typed("sin", sin, f32, rows * 64, dev), rows,
         _typed("positions", positions, i32, total_q, dev), _typed("slots", slots, i32, total_q, dev),
-        kv.numel() // D_QK, _typed("kv", kv, torch.bfloat16, 0, dev), ws.data_ptr(), ws.numel(), _stream(stream)),
+        kv.numel() // D_QK, _typed("kv", kv, torch.bfloat16, 0, dev), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)),
         "dsa_latent_append")
     return kv
 
@@ -451,7 +455,7 @@ def tree_mla_fwd(batch: Batch, q, kv, mask, sm_scale: float, out, lse=None, page
         ctypes.byref(c), pg, _typed("q", q, bf16, c.total_q * H * D_QK, dev), _typed("kv", kv, bf16, rows * D_QK, dev),
         _typed("mask", mask, torch.int64, c.total_q, dev), float(sm_scale),
         _typed("out", out, bf16, c.total_q * H * D_V, dev), _typed("lse", lse, torch.float32, c.total_q * H, dev),
-        ws.data_ptr(), ws.numel(), _stream(stream)), "dsa_tree_mla_fwd")
+        ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "dsa_tree_mla_fwd")
     return out
 
 
@@ -464,7 +468,7 @@ def tree_topk(batch: Batch, scores, mask, k: int, idx, ld: Optional[int] = None,
     _check(load_library().dsa_tree_topk(
         ctypes.byref(c), _typed("scores", scores, torch.float32, c.total_q * ld, dev), ld,
         _typed("mask", mask, torch.int64, c.total_q, dev), int(k),
-        _typed("idx", idx, torch.int32, c.total_q * int(k), dev), ws.data_ptr(), ws.numel(), _stream(stream)),
+        _typed("idx", idx, torch.int32, c.total_q * int(k), dev), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)),
         "dsa_tree_topk")
     return idx
 
@@ -485,6 +489,6 @@ def tree_commit(batch: Batch, mask, accepted, ctx_new, kv=None, k_idx=None, page
         ctypes.byref(c), pg, _typed("mask", mask, torch.int64, c.total_q, dev),
         _typed("accepted", accepted, torch.int32, c.batch, dev), layers, rows,
         _typed("kv", kv, bf16, layers * rows * D_QK, dev), _typed("k_idx", k_idx, bf16, layers * rows * D_IDX, dev),
-        _typed("ctx_new", ctx_new, torch.int32, c.batch, dev), ws.data_ptr(), ws.numel(), _stream(stream)),
+        _typed("ctx_new", ctx_new, torch.int32, c.batch, dev), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)),
         "dsa_tree_commit")
     return ctx_new

@@ -801,19 +801,27 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : KPT <= 8 ? 3 : 2)
     const int32_t w_hi = min(n, w_end);
     // The lane's scores; NaN behind the row's end, which is above, below and
     // equal to nothing.  Groups past the segment's length are skipped
-    // everywhere (the same branch for the whole CTA): the kernel is bound by
-    // its instructions, and a row is often much shorter than NT * KPT.
+    // everywhere (the same branch for the whole CTA), and groups that lie
+    // before the packed end take no test per score (the same for a warp): the
+    // kernel is bound by its instructions.
+    const int32_t plain = min(c, w_hi) - w_lo;   // this warp's scores before the packed end
     float x[KPT], low = INFINITY, high = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kGroups; ++u) {
         if (128 * u >= seg) break;
-        const float y[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        float y[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        if (128 * u + 128 > plain) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int32_t j = w_lo + 128 * u + 4 * lane + e;
+                y[e] = j < w_hi ? (j < c ? y[e] : end_score[j - c]) : NAN;
+            }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int32_t j = w_lo + 128 * u + 4 * lane + e;
-            x[4 * u + e] = j < w_hi ? (j < c ? y[e] : end_score[j - c]) : NAN;
-            low = fminf(low, x[4 * u + e]);
-            high = fmaxf(high, x[4 * u + e]);
+            x[4 * u + e] = y[e];
+            low = fminf(low, y[e]);
+            high = fmaxf(high, y[e]);
         }
     }
     low = -warp_max_f32(-low);
@@ -826,19 +834,21 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : KPT <= 8 ? 3 : 2)
     low = -warp_max_f32(lane < kWarps ? -__uint_as_float(S.wgt[lane]) : -INFINITY);
     high = warp_max_f32(lane < kWarps ? __uint_as_float(S.wmax[lane]) : -INFINITY);
 
-    const float span = high - low, scale = (float)kBins / span;
+    // a little less than kBins intervals, so that `high` falls into the last
+    const float span = high - low, scale = ((float)kBins - 0.125f) / span;
     const bool linear = span > 0.f && span < INFINITY && scale < INFINITY;   // false for NaN too
     float tf = 0.f;
     uint32_t tau = 0u, need = 0u;
     bool ties = true, ranked = false;
-    auto bin = [&](float f) -> uint32_t { return (uint32_t)min(kBins - 1, (int)((f - low) * scale)); };
+    auto bin = [&](float f) -> uint32_t { return (uint32_t)(int)((f - low) * scale); };
     if (linear) {
 #pragma unroll
         for (int u = 0; u < kGroups; ++u) {
             if (128 * u >= seg) break;
+            const bool all = 128 * u + 128 <= plain;
 #pragma unroll
             for (int q = 4 * u; q < 4 * u + 4; ++q)
-                if (x[q] == x[q]) atomicAdd(&S.hist[bin(x[q])], 1u);
+                if (all || x[q] == x[q]) atomicAdd(&S.hist[min(bin(x[q]), (uint32_t)kBins - 1u)], 1u);
         }
         __syncthreads();
         uint32_t cnt[kBinsPerThread], mine = 0u;
@@ -963,7 +973,10 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : KPT <= 8 ? 3 : 2)
     auto scan = [&](uint32_t bits, uint64_t& excl, uint64_t& total) -> uint32_t {
         uint64_t p = 0u;
 #pragma unroll
-        for (int u = 0; u < kGroups; ++u) p |= (uint64_t)__popc((bits >> (4 * u)) & 0xFu) << (8 * u);
+        for (int u = 0; u < kGroups; ++u) {
+            if (128 * u >= seg) break;
+            p |= (uint64_t)__popc((bits >> (4 * u)) & 0xFu) << (8 * u);
+        }
         uint64_t incl = p;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -972,10 +985,9 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : KPT <= 8 ? 3 : 2)
         }
         total = __shfl_sync(0xffffffffu, incl, 31);
         excl = incl - p;
-        uint32_t sum = 0u;
-#pragma unroll
-        for (int u = 0; u < kGroups; ++u) sum += (uint32_t)(total >> (8 * u)) & 0xFFu;
-        return sum;
+        // the bytes' sum
+        const uint64_t pairs = (total & 0x00FF00FF00FF00FFull) + ((total >> 8) & 0x00FF00FF00FF00FFull);
+        return (uint32_t)((pairs * 0x0001000100010001ull) >> 48);
     };
     uint64_t xg, tg, xe = 0u, te = 0u;
     const uint32_t sg = scan(bg, xg, tg), se = ties ? scan(be, xe, te) : 0u;
@@ -993,9 +1005,10 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : KPT <= 8 ? 3 : 2)
             if (128 * u >= seg) break;
             uint32_t g = g0 + ((uint32_t)(xg >> (8 * u)) & 0xFFu);
             const int32_t j = w_lo + 128 * u + 4 * lane;
+            const bool all = 128 * u + 128 <= plain;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if ((bg >> (4 * u + e)) & 1u) put(out, g++, k, position(j + e), status);
+                if ((bg >> (4 * u + e)) & 1u) put(out, g++, k, all ? j + e : position(j + e), status);
             g0 += (uint32_t)(tg >> (8 * u)) & 0xFFu;
         }
         return;

@@ -624,6 +624,20 @@ def test_two_streams_at_once():
             s.check()
 
 
+def test_a_stream_of_the_caller():
+    st = Step([300, 41], [4, 7], 16, seed=22)
+    q, kv = st.inputs()
+    q, kv = q.cuda(), kv.cuda()
+    out = torch.full((st.T, H, D_V), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((st.T, H), 7.0, dtype=torch.float32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    dsa.tree_mla_fwd(st.b, q, kv, st.mask, SCALE, out, lse, pages=st.pages, ws=st.ws, stream=side)
+    side.synchronize()
+    assert dsa.read_device_status(st.ws, stream=side) == 0
+    check_attention(st, q.cpu(), kv.cpu(), out, lse)
+
+
 def test_same_bits_every_time():
     st = Step([5000, 100, 2047, 0], [3, 64, 1, 9], 64, seed=21)
     q, kv = st.inputs()
