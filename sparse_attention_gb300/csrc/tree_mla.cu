@@ -45,7 +45,7 @@
 // row leaves rank 1's half empty and is bound by HBM (121 flop a byte).
 // Measured: 16 trees of 64 over 8,192 rows 0.64-0.66 ms = 1,770-1,820 TFLOP/s
 // (1,907 measured peak; the power cap holds the clock at 1.8 GHz); 64 single
-// rows over 32,768 each 0.40 ms = 6.05 TB/s (6.78 measured copy); one tree of
+// rows over 32,768 each 0.396 ms = 6.1 TB/s (6.78 measured copy); one tree of
 // 8 over 1,500 rows 17 us with the merge.
 #include <algorithm>
 #include <atomic>
@@ -109,6 +109,7 @@ struct Args {
     BatchDev bd;
     PagesDev pg;
     const uint64_t* mask;
+    const uint16_t* kv;
     float scale_log2;
     uint16_t* out;
     float* lse;
@@ -118,6 +119,7 @@ struct Args {
     int32_t* status;
     int32_t rows_total;  // cache rows
     bool may_round;      // the bounds allow plan_rounds
+    bool ahead;          // a sequence's rows are read by one pair only
 };
 
 __device__ __forceinline__ int64_t seq_units(const SeqInfo& s) {
@@ -538,6 +540,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tma_load_3d_pair(smem_u32(S.k + gr * kKBytes + c * kChunkBytes +
                                                       e * kKRows * 128 * kChunksPerBox),
                                              &tm_k, bar, 0, r, kGroup * gr + c);
+                    }
+                    // Rows that no other pair reads come from HBM: the next
+                    // tile's are brought to L2 while this one's are loaded
+                    // (64 x 1 row over 32,768: 416 -> 399 us; with rows that
+                    // several pairs share the same costs 4-7 %).
+                    if (a.ahead) {
+                        const int32_t next = y + kboxes + lane;
+                        const int32_t r2 = __shfl_sync(0xffffffffu, row, next & 31);
+                        if (lane < kboxes && next < 32 && x0 + next < n && r2 < a.rows_total)
+                            prefetch_l2_bulk(a.kv + (int64_t)r2 * kDQK, min(kKRows, a.rows_total - r2) * 2 * kDQK);
                     }
                 }
             }
@@ -1078,6 +1090,8 @@ cudaError_t launch_tree_mla(const BatchDev& bd, const PagesDev& pg, const uint16
     a.bd = bd;
     a.pg = pg;
     a.mask = mask;
+    a.kv = kv;
+    a.ahead = bd.max_q <= 2;
     a.scale_log2 = sm_scale * kLog2e;
     a.out = out;
     a.lse = lse;
