@@ -519,13 +519,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     box_row(a, s, (s.t0 + x / kboxes) * kTile + 64 * (int)rank + (x % kboxes) * kKRows, bad);
                 for (int32_t y = 0; ok && y < 32 && x0 + y < n; y += kboxes) {
                     if (x0 + y == 0) {
-                        const bool mine = (int)rank < s.rows;
+                        // No row for this CTA: zeros, from behind the queries.
+                        // Whatever lay there would do as well, but its products
+                        // cost power, which holds the clock (64 x 1 row over
+                        // 32,768 in a long loop: 438 us, 407 with zeros).
+                        const int32_t q_row = (int)rank < s.rows ? (s.row + (int)rank) * kH : a.bd.total_q * kH;
                         if (lane == 0 && (seg == 0 || wait(S.qempty, (seg - 1) & 1)))
-                            mbar_arrive_expect_tx_pair(lead(S.qfull), mine ? (uint32_t)sizeof(S.q) : 0u);
+                            mbar_arrive_expect_tx_pair(lead(S.qfull), (uint32_t)sizeof(S.q));
                         ok = __shfl_sync(0xffffffffu, ok, 0);
-                        if (ok && mine && lane < kQChunks)
-                            tma_load_2d_pair(smem_u32(S.q + lane * kChunkBytes), &tm_q, lead(S.qfull), 64 * lane,
-                                             (s.row + (int)rank) * kH);
+                        if (ok && lane < kQChunks)
+                            tma_load_2d_pair(smem_u32(S.q + lane * kChunkBytes), &tm_q, lead(S.qfull), 64 * lane, q_row);
                     }
                     const uint32_t g = g0 + (x0 + y) / kboxes;
                     const int e = lane % kboxes, c = (lane / kboxes) * kChunksPerBox;    // a box each
@@ -728,6 +731,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mine ? visible_bits(__ldg(reinterpret_cast<const unsigned long long*>(a.mask) + s.row + rank),
                                     s.i0 + (int)rank)
                      : 0u;
+            if (!mine) {
+                // P of the last segment is read; zeros for this one
+#pragma unroll
+                for (int k = 0; k < 8; ++k) reinterpret_cast<uint4*>(S.p)[128 * k + ln] = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
             float m = -INFINITY, l = 0.f;
             for (int32_t t = s.t0; t < s.t1; ++t, ++g) {
                 const uint32_t buf = g & 1;
