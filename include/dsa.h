@@ -432,7 +432,7 @@ DSA_API dsa_status dsa_latent_append(int32_t total_q, const uint16_t* x, int64_t
  * whatever they hold; a row that sees a new row with a NaN or infinity gets
  * NaN.  A block-table entry outside [0, pool_pages) among the sequence's
  * pages latches DSA_ERR_BAD_INDEX and leaves the sequence's rows unwritten.
- * max_q > 64 -> DSA_ERR_UNSUPPORTED.
+ * max_q > 64 or total_q >= 2^25 -> DSA_ERR_UNSUPPORTED.
  * fp32 scores, softmax statistics and sums; the softmax weights are rounded
  * to bf16 for the product with the values (as in dsa_sparse_mla_fwd) and the
  * result once more.  Reads a cached row once per two new rows of its

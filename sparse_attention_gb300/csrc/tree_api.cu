@@ -113,6 +113,7 @@ dsa_status dsa_tree_mla_fwd(const dsa_batch* batch, const dsa_pages* pages, cons
     dsa_status st = check(batch, pages);
     if (st != DSA_OK) return st;
     if (batch->max_q > DSA_MAX_TREE) return DSA_ERR_UNSUPPORTED;
+    if (batch->total_q >= (1 << 25)) return DSA_ERR_UNSUPPORTED;     // 64 query rows each, in int32 TMA coordinates
     if ((st = check_ws(batch, ws, ws_bytes)) != DSA_OK) return st;
     if (batch->total_q == 0 || batch->max_q == 0) return DSA_OK;
     if (!given(q) || !given(kv) || !given(mask, 8) || !given(out) || !aligned(lse, 16)) return DSA_ERR_INVALID_ARG;

@@ -51,7 +51,7 @@ def test_workspace(lib):
 @pytest.mark.parametrize("b,g,code", [
     (dict(B=0), None, 1), (dict(B=65536), None, 1), (dict(total_q=-1), None, 1), (dict(max_q=65), None, 2),
     (dict(stride=99), None, 1), (dict(q_off=0), None, 1), (dict(ctx=0x20002), None, 1),
-    (dict(stride=1 << 30), None, 2), (dict(total_q=1 << 26), None, 2),
+    (dict(stride=1 << 30), None, 2), (dict(total_q=1 << 26), None, 2), (dict(total_q=1 << 25), None, 2),
     ({}, dict(size=8), 1), ({}, dict(size=2048), 1), ({}, dict(size=48), 1), ({}, dict(width=6), 1),
     ({}, dict(pool=0), 1), ({}, dict(table=0), 1), ({}, dict(pool=1 << 27), 2),
 ])
