@@ -38,6 +38,7 @@
 // shared memory and stand in for the row's end wherever it is read, and
 // positions are mapped back as they are written.  The selection itself is the
 // same code, so -inf scores and ties come out as they would on such a row.
+// Masked rows that fit shared memory take a kernel of their own (below).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -61,6 +62,10 @@ static_assert(kPrefetch <= 8, "a lane's candidate flags fill one 32-bit word, it
 constexpr int kMaxCluster = 8;
 constexpr int kLongRow = 65536;              // rows above this may be split over a cluster
 constexpr int kKeysPerCta = 32768;
+constexpr int kShortRow = 49152;             // masked rows up to this stay in shared memory (192 KB)
+constexpr int kRowOf256 = 10240;             // and take a CTA of 256 threads up to this (four or five per SM),
+constexpr int kRowOf512 = 24576;             // of 512 up to this (two or three per SM),
+constexpr int kFewRowOf512 = 16384;          // or this when there are few (one per SM)
 
 __device__ __forceinline__ uint32_t order_key(float f) {
     uint32_t u = __float_as_uint(f);
@@ -89,7 +94,7 @@ template <int NT, int REGION = kRegion>
 struct alignas(16) TopkSmem {
     static constexpr int kMaxCand = NT / 32 * REGION;
     uint32_t hist[kBins];                 // zero between selects
-    uint32_t sample[kSample];
+    uint32_t sample[REGION > 1 ? kSample : 1];
     uint32_t cand_key[kMaxCand];          // warp w: [w * kRegion, w * kRegion + count)
     int32_t cand_pos[kMaxCand];
     uint32_t warp_sums[32];
@@ -278,9 +283,9 @@ __device__ uint32_t radix_select(cg::cluster_group& cluster, int nranks, TopkSme
             __syncthreads();
             // thread t ranks key t / 8 against keys 8 (t % 8) .. 8 (t % 8) + 7;
             // eight lanes sum their counts
-            if (tid < 512) {
+            for (uint32_t ranker = (uint32_t)tid; ranker < 512u; ranker += NT) {
                 const uint32_t nb = S.small_all_n;
-                const uint32_t q = (uint32_t)tid >> 3, sub = (uint32_t)tid & 7u;
+                const uint32_t q = ranker >> 3, sub = ranker & 7u;
                 const uint32_t x = q < nb ? S.small_all[q] : 0u;
                 uint32_t gt = 0u, eq = 0u;
 #pragma unroll
@@ -745,84 +750,101 @@ cudaError_t launch_nt(const BatchDev& bd, RowRange rr, const float* scores, int6
     return e;
 }
 
-// Masked rows of up to NT * KPT positions: the whole row stays in registers
-// (warp w owns a contiguous segment, read as coalesced 16-byte groups while
-// the mask and the row's end are on their way), so there is no sampled bound,
-// no candidate region and no second read.
-//   1. One histogram over 2048 equal intervals of [min, max]: scores of a row
-//      spread over it, so few atomics meet and few keys stay.  Subtraction, product and truncation are monotone, so the
-//      interval of the k-th largest is exact whatever the rounding.
-//   2. At most 64 keys in it: gathered and ranked.  More (ties, outliers that
-//      stretch the range, infinities): radix_select over all keys.
-//   3. Output in position order from packed warp scans; ties at tau are
-//      counted only if not all of them are taken.
-// Bound by instructions.  64 trees of up to 32 rows over up to 9,001
-// positions, k = 2048: 29-35 us (topk_kernel 72); 8 trees of 8 over 32,768:
-// 12-14 us (21.7).
-template <int NT, int KPT>
-__global__ void __launch_bounds__(NT, NT == 1024 ? 1 : KPT <= 8 ? 3 : 2)
+// Masked rows that fit a CTA's shared memory (committed scores, then the visible
+// new ones without a gap, -inf behind them): one read of the row, no sampled
+// bound, no candidate region.
+//   1. min and max as the row arrives (BATCH 16-byte loads in flight per thread).
+//   2. One histogram over about 2040 equal intervals of [min, max]: scores of a
+//      row spread over it, so few atomics meet and few scores share the k-th's
+//      interval.  The interval is read off the low bits of f * per + off, a
+//      float in [2^21, 2^22) whose steps are quarters.
+//   3. In position order, a segment per warp: scores above a window a little
+//      wider than that interval are counted, those in it gathered and ranked.
+//      Whatever the rounding, the counts prove the k-th to be in the window; if
+//      they do not, or it holds more than 64 (ties, outliers that stretch the
+//      range, infinities): radix_select over all scores and a count.
+//   4. The selected indices, in order from packed warp scans, into shared
+//      memory, and from there to idx; ties at the k-th are told apart only if
+//      not all of them are taken.
+// Bound by instructions (37 a score in 32, 4.7 K a row of 256 threads; a
+// scheduler issues in 60 % of the cycles).  k = 2048, 64 trees of up to 32 rows
+// over up to 9,001 positions: 18-21 us (topk_kernel 72, the row in registers
+// instead of shared memory 23-29); 64 x 32 over 2,500: 18 us; 8 x 8 over
+// 32,768: 10.7 us.
+template <int NT, int BATCH, int MINB>
+__global__ void __launch_bounds__(NT, MINB)
     topk_short_kernel(const BatchDev bd, const float* __restrict__ scores, const int64_t ld, const int k,
                       int32_t* __restrict__ idx, int32_t* status, const uint64_t* __restrict__ mask) {
-    constexpr int kWarps = NT / 32, kGroups = KPT / 4, kBinsPerThread = kBins / NT;
-    static_assert(kGroups <= 8, "a lane's counts fill one 64-bit word");
+    constexpr int kWarps = NT / 32, kBinsPerThread = kBins / NT, kBlock = 4;   // 128-score groups per scan
+    static_assert(kMaxTopk <= kBins, "the selected indices take the histogram's place");
+    static_assert(kWarps <= 32 && NT >= DSA_MAX_TREE * 2, "one lane per warp's sum; new scores and padding by one thread each");
+    extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ TopkSmem<NT, 1> S;
-    __shared__ float end_score[DSA_MAX_TREE];
     __shared__ int32_t end_pos[DSA_MAX_TREE];
+    float* row_s = reinterpret_cast<float*>(smem_raw);
+    float4* row4 = reinterpret_cast<float4*>(smem_raw);
     cg::cluster_group cluster = cg::this_cluster();
     const int b = blockIdx.y, i = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();                  // the scores of the previous launch are complete
     SeqInfo sq;
     if (!load_seq(bd, b, status, sq) || i >= sq.nq) return;
     const float* row = scores + ((int64_t)sq.q0 + i) * ld;
     int32_t* out = idx + ((int64_t)sq.q0 + i) * k;
-    const int32_t c = sq.ctx - sq.nq;
-    const int32_t seg = ((sq.ctx + kWarps - 1) / kWarps + 127) & ~127;
-    const int32_t w_lo = min(sq.ctx, warp * seg), w_end = min(sq.ctx, w_lo + seg);
-    float4 v[kGroups];
+    const int32_t c = sq.ctx - sq.nq, old4 = (c + 3) >> 2;
+    const unsigned long long word = __ldg(reinterpret_cast<const unsigned long long*>(mask) + sq.q0 + i);
+    auto load = [&](int32_t g) -> float4 {
+        return sq.ctx > k && g < old4 ? __ldg(reinterpret_cast<const float4*>(row) + g) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float4 v[BATCH];
 #pragma unroll
-    for (int u = 0; u < kGroups; ++u) {
-        const int32_t j = w_lo + 128 * u + 4 * lane;
-        v[u] = sq.ctx > k && j < w_end ? __ldg(reinterpret_cast<const float4*>(row + j))
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u = 0; u < BATCH; ++u) v[u] = load(NT * u + tid);
+    const uint64_t bits = visible_bits(word, i);
+    const int32_t n = c + __popcll(bits);
+    // the new position of a visible bit, its place in the row, and its score
+    const bool seen = tid < DSA_MAX_TREE && (bits >> (tid & 63)) & 1u;
+    const int32_t place = c + __popcll(bits & ((1ull << (tid & 63)) - 1u));
+    if (n <= k) {
+        for (int j = tid; j < k; j += NT)
+            if (j < c || j >= n) out[j] = j < c ? j : -1;
+        if (seen) out[place] = c + tid;
+        return;
     }
-    const int32_t n = masked_end(sq, i, row, mask, end_score, end_pos);
+    float low = INFINITY, high = -INFINITY;
+    if (seen) {
+        low = high = __ldg(row + c + tid);
+        row_s[place] = low;
+        end_pos[place - c] = c + tid;
+    }
+    if (n + tid < ((n + 127) & ~127)) row_s[n + tid] = -INFINITY;
 #pragma unroll
     for (int x = 0; x < kBinsPerThread; ++x) S.hist[NT * x + tid] = 0u;
+    if (tid < 32) S.weq[tid] = 0u;
     if (tid == 0) {
         S.small_n = 0u;
         S.sel_count = 0xFFFFFFFFu;
     }
-    __syncthreads();
-    auto position = [&](int32_t j) -> int32_t { return j < c ? j : end_pos[j - c]; };
-    if (n <= k) {
-        for (int j = tid; j < k; j += NT) out[j] = j < n ? position(j) : -1;
-        return;
-    }
-    const int32_t w_hi = min(n, w_end);
-    // The lane's scores; NaN behind the row's end, which is above, below and
-    // equal to nothing.  Groups past the segment's length are skipped
-    // everywhere (the same branch for the whole CTA), and groups that lie
-    // before the packed end take no test per score (the same for a warp): the
-    // kernel is bound by its instructions.
-    const int32_t plain = min(c, w_hi) - w_lo;   // this warp's scores before the packed end
-    float x[KPT], low = INFINITY, high = -INFINITY;
+    for (int32_t g0 = 0;;) {
 #pragma unroll
-    for (int u = 0; u < kGroups; ++u) {
-        if (128 * u >= seg) break;
-        float y[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        if (128 * u + 128 > plain) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int32_t j = w_lo + 128 * u + 4 * lane + e;
-                y[e] = j < w_hi ? (j < c ? y[e] : end_score[j - c]) : NAN;
+        for (int u = 0; u < BATCH; ++u) {
+            const int32_t g = g0 + NT * u + tid;
+            if (4 * g + 4 <= c) {
+                row4[g] = v[u];
+                low = fminf(fminf(low, fminf(v[u].x, v[u].y)), fminf(v[u].z, v[u].w));
+                high = fmaxf(fmaxf(high, fmaxf(v[u].x, v[u].y)), fmaxf(v[u].z, v[u].w));
+            } else if (4 * g < c) {                   // the group that the new scores follow in
+                const float y[3] = {v[u].x, v[u].y, v[u].z};
+                for (int x = 0; x < 3 && 4 * g + x < c; ++x) {
+                    row_s[4 * g + x] = y[x];
+                    low = fminf(low, y[x]);
+                    high = fmaxf(high, y[x]);
+                }
             }
         }
+        g0 += NT * BATCH;
+        if (g0 >= old4) break;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[4 * u + e] = y[e];
-            low = fminf(low, y[e]);
-            high = fmaxf(high, y[e]);
-        }
+        for (int u = 0; u < BATCH; ++u) v[u] = load(g0 + NT * u + tid);
     }
     low = -warp_max_f32(-low);
     high = warp_max_f32(high);
@@ -834,100 +856,134 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : KPT <= 8 ? 3 : 2)
     low = -warp_max_f32(lane < kWarps ? -__uint_as_float(S.wgt[lane]) : -INFINITY);
     high = warp_max_f32(lane < kWarps ? __uint_as_float(S.wmax[lane]) : -INFINITY);
 
-    // a little less than kBins intervals, so that `high` falls into the last
-    const float span = high - low, scale = ((float)kBins - 0.125f) / span;
-    const bool linear = span > 0.f && span < INFINITY && scale < INFINITY;   // false for NaN too
+    // interval of f: t = 4 + (f - low) * per, rounded to quarters, its floor;
+    // four spare ones at each end for the rounding of `off`
+    const float span = high - low, per = ((float)kBins - 8.f) / span, off = fmaf(-low, per, 2097152.f + 4.f);
+    const bool linear = span > 0.f && span < INFINITY && per < INFINITY;   // false for NaN too
+    const int32_t seg = ((n + kWarps - 1) / kWarps + 127) & ~127;
+    const int32_t w_lo = min(n, warp * seg), w_hi = min(n, w_lo + seg);
     float tf = 0.f;
-    uint32_t tau = 0u, need = 0u;
+    uint32_t need = 0u;
     bool ties = true, ranked = false;
-    auto bin = [&](float f) -> uint32_t { return (uint32_t)(int)((f - low) * scale); };
     if (linear) {
+#pragma unroll 2
+        for (int32_t g = tid; 4 * g < n; g += NT) {
+            const float4 x = row4[g];                 // at most 3 of -inf here: they add to interval 0
+            const float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int u = 0; u < kGroups; ++u) {
-            if (128 * u >= seg) break;
-            const bool all = 128 * u + 128 <= plain;
-#pragma unroll
-            for (int q = 4 * u; q < 4 * u + 4; ++q)
-                if (all || x[q] == x[q]) atomicAdd(&S.hist[min(bin(x[q]), (uint32_t)kBins - 1u)], 1u);
+            for (int q = 0; q < 4; ++q)
+                atomicAdd(&S.hist[(__float_as_uint(fmaf(y[q], per, off)) >> 2) & (uint32_t)(kBins - 1)], 1u);
         }
         __syncthreads();
         uint32_t cnt[kBinsPerThread], mine = 0u;
 #pragma unroll
-        for (int q = 0; q < kBinsPerThread; ++q) {
-            cnt[q] = S.hist[kBinsPerThread * tid + q];
-            S.hist[kBinsPerThread * tid + q] = 0u;
-            mine += cnt[q];
+        for (int q = 0; q < kBinsPerThread; q += 2) {
+            const uint2 two = *reinterpret_cast<const uint2*>(&S.hist[kBinsPerThread * tid + q]);
+            cnt[q] = two.x;
+            cnt[q + 1] = two.y;
+            mine += two.x + two.y;
         }
         const uint32_t incl = warp_inclusive_scan(mine);
         if (lane == 31) S.warp_sums[warp] = incl;
         __syncthreads();
-        const uint32_t sums = warp_inclusive_scan(lane < kWarps ? S.warp_sums[lane] : 0u);
-        const uint32_t before = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
-        // keys in higher bins
-        uint32_t above = __shfl_sync(0xffffffffu, sums, 31) - (incl + (warp ? before : 0u));
+        const uint32_t sums = lane < kWarps ? S.warp_sums[lane] : 0u;
+        // scores in higher intervals
+        uint32_t above = mine - incl + __reduce_add_sync(0xffffffffu, lane >= warp ? sums : 0u) - mine;
+        if (above < (uint32_t)k && (uint32_t)k <= above + mine) {
 #pragma unroll
-        for (int q = kBinsPerThread - 1; q >= 0; --q) {
-            if (above < (uint32_t)k && (uint32_t)k <= above + cnt[q]) {
-                S.sel_digit = (uint32_t)(kBinsPerThread * tid + q);
-                S.sel_above = above;
-                S.sel_count = cnt[q];
+            for (int q = kBinsPerThread - 1; q >= 0; --q) {
+                if (above < (uint32_t)k && (uint32_t)k <= above + cnt[q]) {
+                    S.sel_digit = (uint32_t)(kBinsPerThread * tid + q);
+                    S.sel_count = cnt[q];
+                }
+                above += cnt[q];
             }
-            above += cnt[q];
         }
         __syncthreads();
         if (S.sel_count <= 64u) {
-            const uint32_t digit = S.sel_digit;
+            const float at = (float)S.sel_digit, width = span / ((float)kBins - 8.f);
+            const float from = fmaf(at - 4.375f, width, low), to = fmaf(at - 2.875f, width, low);
+            uint32_t higher = 0u;
+#pragma unroll 2
+            for (int32_t j = w_lo; j < w_hi; j += 128) {
+                const float4 x = row4[(j >> 2) + lane];
+                const float y[4] = {x.x, x.y, x.z, x.w};
+                bool any = false;
 #pragma unroll
-            for (int u = 0; u < kGroups; ++u) {
-                if (128 * u >= seg) break;
-#pragma unroll
-                for (int q = 4 * u; q < 4 * u + 4; ++q)
-                    if (x[q] == x[q] && bin(x[q]) == digit)
-                        S.small[atomicAdd(&S.small_n, 1u) & 63u] = __float_as_uint(x[q]);
-            }
-            __syncthreads();
-            // eight threads rank a score against eight each
-            const uint32_t m = min(S.small_n, 64u), want = (uint32_t)k - S.sel_above;
-            if (tid < 512) {
-                const uint32_t q = (uint32_t)tid >> 3, sub = (uint32_t)tid & 7u;
-                const float f = q < m ? __uint_as_float(S.small[q]) : NAN;
-                uint32_t gt = 0u, eq = 0u;
-#pragma unroll
-                for (uint32_t o = 0; o < 8u; ++o) {
-                    const float y = sub * 8u + o < m ? __uint_as_float(S.small[sub * 8u + o]) : NAN;
-                    gt += y > f ? 1u : 0u;
-                    eq += y == f ? 1u : 0u;
+                for (int q = 0; q < 4; ++q) {
+                    higher += y[q] > to ? 1u : 0u;
+                    any |= y[q] >= from && y[q] <= to;
                 }
-#pragma unroll
-                for (int o = 1; o < 8; o <<= 1) {
-                    gt += __shfl_xor_sync(0xffffffffu, gt, o);
-                    eq += __shfl_xor_sync(0xffffffffu, eq, o);
-                }
-                if (sub == 0 && q < m && gt < want && want <= gt + eq) {
-                    // equal scores (both zeros) write the same values but this one
-                    S.small_tau = __float_as_uint(f);
-                    S.small_need = want - gt;
-                    S.total = eq;
+                if (any) {
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        const float f = row_s[j + 4 * lane + q];
+                        if (f >= from && f <= to) {
+                            const uint32_t s = atomicAdd(&S.small_n, 1u);
+                            if (s < 64u) {
+                                S.small[s] = __float_as_uint(f);
+                                S.small_all[s] = (uint32_t)warp;
+                            }
+                        }
+                    }
                 }
             }
+            higher = __reduce_add_sync(0xffffffffu, higher);
+            if (lane == 0) S.wcnt[warp] = higher;
             __syncthreads();
-            tf = __uint_as_float(S.small_tau);
-            need = S.small_need;
-            ties = S.total != need;
-            ranked = true;
+            const uint32_t m = S.small_n;
+            const uint32_t want = (uint32_t)k - __reduce_add_sync(0xffffffffu, lane < kWarps ? S.wcnt[lane] : 0u);
+            ranked = m <= 64u && want - 1u < m;       // 0 < want <= m
+            if (ranked) {
+                // eight threads rank a score against eight each
+                for (uint32_t ranker = (uint32_t)tid; ranker < 8u * m; ranker += NT) {
+                    const uint32_t q = ranker >> 3, sub = ranker & 7u;
+                    const float f = __uint_as_float(S.small[q]);
+                    uint32_t gt = 0u, eq = 0u;
+                    for (uint32_t o = sub; o < m; o += 8u) {
+                        const float y = __uint_as_float(S.small[o]);
+                        gt += y > f ? 1u : 0u;
+                        eq += y == f ? 1u : 0u;
+                    }
+                    const uint32_t group = 0xFFu << (lane & 24);
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) {
+                        gt += __shfl_xor_sync(group, gt, o);
+                        eq += __shfl_xor_sync(group, eq, o);
+                    }
+                    if (sub == 0 && gt < want && want <= gt + eq) {
+                        // equal scores (both zeros) write the same values but this one
+                        S.small_tau = __float_as_uint(f);
+                        S.small_need = want - gt;
+                        S.total = eq;
+                    }
+                }
+                __syncthreads();
+                tf = __uint_as_float(S.small_tau);
+                need = S.small_need;
+                ties = S.total != need;
+                if ((uint32_t)tid < m) {
+                    const float f = __uint_as_float(S.small[tid]);
+                    if (f > tf || (!ties && f == tf)) atomicAdd(&S.wcnt[S.small_all[tid]], 1u);
+                    else if (f == tf) atomicAdd(&S.weq[S.small_all[tid]], 1u);
+                }
+            }
         }
     }
+    uint32_t tau = 0u;
     if (!ranked) {
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kBinsPerThread; ++x) S.hist[NT * x + tid] = 0u;
         uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
 #pragma unroll 1
-        for (int32_t j = w_lo + lane; j < w_hi; j += 32) {
-            const uint32_t q = order_key(j < c ? __ldg(row + j) : end_score[j - c]);
+        for (int32_t j = tid; j < n; j += NT) {
+            const uint32_t q = order_key(row_s[j]);
             kmin = min(kmin, q);
             kmax = max(kmax, q);
         }
         kmin = __reduce_min_sync(0xffffffffu, kmin);
         kmax = __reduce_max_sync(0xffffffffu, kmax);
-        __syncthreads();
         if (lane == 0) {
             S.wgt[warp] = kmin;
             S.wmax[warp] = kmax;
@@ -938,100 +994,110 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : KPT <= 8 ? 3 : 2)
         tau = radix_select(cluster, 1, S, (uint32_t)k, varying_bits(kmin, kmax), kmin, 3,
                            [&](auto&& f) {
 #pragma unroll 1
-                               for (int32_t j = w_lo + lane; j < w_hi; j += 32)
-                                   f(order_key(j < c ? __ldg(row + j) : end_score[j - c]));
+                               for (int32_t j = tid; j < n; j += NT) f(order_key(row_s[j]));
                            },
                            need);
+        uint32_t gt = 0u, eq = 0u;
+#pragma unroll 1
+        for (int32_t j = w_lo + lane; j < w_hi; j += 32) {
+            const uint32_t q = order_key(row_s[j]);
+            gt += q > tau ? 1u : 0u;
+            eq += q == tau ? 1u : 0u;
+        }
+        gt = __reduce_add_sync(0xffffffffu, gt);
+        eq = __reduce_add_sync(0xffffffffu, eq);
+        if (lane == 0) {
+            S.wcnt[warp] = gt;
+            S.weq[warp] = eq;
+        }
     }
-
-    // scores above the k-th, and equal to it; without a cut among the equal
-    // ones they count as above.  A byte per 128-key group for the warp's scan.
-    uint32_t bg = 0u, be = 0u;
-    if (ranked) {
+    __syncthreads();
+    // the histogram's place takes the selected indices from here on
+    uint32_t* sel = S.hist;
+    const uint32_t sg = lane < kWarps ? S.wcnt[lane] : 0u;
+    uint32_t g0 = __reduce_add_sync(0xffffffffu, lane < warp ? sg : 0u);
+    if (__reduce_add_sync(0xffffffffu, sg) + (ties ? need : 0u) != (uint32_t)k) {   // would be a bug: no write past k
+        latch_status(status, DSA_ERR_INTERNAL);
+        return;
+    }
+    if (!ties) {
+        for (int32_t j0 = w_lo; j0 < w_hi; j0 += 128 * kBlock) {
+            // a byte per group for the warp's scan
+            float4 x[kBlock];
+            uint32_t own = 0u;
 #pragma unroll
-        for (int u = 0; u < kGroups; ++u) {
-            if (128 * u >= seg) break;
+            for (int u = 0; u < kBlock; ++u) {
+                if (j0 + 128 * u >= w_hi) break;
+                x[u] = row4[(j0 >> 2) + 32 * u + lane];
+                own += ((x[u].x >= tf ? 1u : 0u) + (x[u].y >= tf ? 1u : 0u) + (x[u].z >= tf ? 1u : 0u) +
+                        (x[u].w >= tf ? 1u : 0u)) << (8 * u);
+            }
+            const uint32_t incl = warp_inclusive_scan(own), all = __shfl_sync(0xffffffffu, incl, 31);
+            const uint32_t excl = incl - own;
 #pragma unroll
-            for (int q = 4 * u; q < 4 * u + 4; ++q) {
-                if (ties) {
-                    bg |= (x[q] > tf ? 1u : 0u) << q;
-                    be |= (x[q] == tf ? 1u : 0u) << q;
-                } else {
-                    bg |= (x[q] >= tf ? 1u : 0u) << q;
-                }
+            for (int u = 0; u < kBlock; ++u) {
+                if (j0 + 128 * u >= w_hi) break;
+                uint32_t* to = sel + g0 + ((excl >> (8 * u)) & 0xFFu);
+                const uint32_t j = (uint32_t)(j0 + 128 * u + 4 * lane);
+                if (x[u].x >= tf) *to++ = j;
+                if (x[u].y >= tf) *to++ = j + 1u;
+                if (x[u].z >= tf) *to++ = j + 2u;
+                if (x[u].w >= tf) *to++ = j + 3u;
+                g0 += (all >> (8 * u)) & 0xFFu;
             }
         }
     } else {
-#pragma unroll
-        for (int q = 0; q < KPT; ++q) {
-            const bool in = w_lo + 128 * (q >> 2) + 4 * lane + (q & 3) < w_hi;
-            const uint32_t key = in ? order_key(x[q]) : 0u;
-            bg |= (in && key > tau ? 1u : 0u) << q;
-            be |= (in && key == tau ? 1u : 0u) << q;
-        }
-    }
-    auto scan = [&](uint32_t bits, uint64_t& excl, uint64_t& total) -> uint32_t {
-        uint64_t p = 0u;
-#pragma unroll
-        for (int u = 0; u < kGroups; ++u) {
-            if (128 * u >= seg) break;
-            p |= (uint64_t)__popc((bits >> (4 * u)) & 0xFu) << (8 * u);
-        }
-        uint64_t incl = p;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += up;
-        }
-        total = __shfl_sync(0xffffffffu, incl, 31);
-        excl = incl - p;
-        // the bytes' sum
-        const uint64_t pairs = (total & 0x00FF00FF00FF00FFull) + ((total >> 8) & 0x00FF00FF00FF00FFull);
-        return (uint32_t)((pairs * 0x0001000100010001ull) >> 48);
-    };
-    uint64_t xg, tg, xe = 0u, te = 0u;
-    const uint32_t sg = scan(bg, xg, tg), se = ties ? scan(be, xe, te) : 0u;
-    __syncthreads();
-    if (lane == 0) {
-        S.wcnt[warp] = sg;
-        S.weq[warp] = se;
-    }
-    __syncthreads();
-    const uint32_t all_g = warp_inclusive_scan(lane < kWarps ? S.wcnt[lane] : 0u);
-    uint32_t g0 = __shfl_sync(0xffffffffu, all_g, warp) - sg;
-    if (!ties) {
-#pragma unroll
-        for (int u = 0; u < kGroups; ++u) {
-            if (128 * u >= seg) break;
-            uint32_t g = g0 + ((uint32_t)(xg >> (8 * u)) & 0xFFu);
-            const int32_t j = w_lo + 128 * u + 4 * lane;
-            const bool all = 128 * u + 128 <= plain;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if ((bg >> (4 * u + e)) & 1u) put(out, g++, k, all ? j + e : position(j + e), status);
-            g0 += (uint32_t)(tg >> (8 * u)) & 0xFFu;
-        }
-        return;
-    }
-    const uint32_t all_e = warp_inclusive_scan(lane < kWarps ? S.weq[lane] : 0u);
-    uint32_t e0 = __shfl_sync(0xffffffffu, all_e, warp) - se;
+        uint32_t e0 = __reduce_add_sync(0xffffffffu, lane < warp ? S.weq[lane] : 0u);
+        const uint32_t lower = (1u << lane) - 1u;
 #pragma unroll 1
-    for (int u = 0; u < kGroups; ++u) {
-        uint32_t g = g0 + ((uint32_t)(xg >> (8 * u)) & 0xFFu), e = e0 + ((uint32_t)(xe >> (8 * u)) & 0xFFu);
-        for (uint32_t both = ((bg | be) >> (4 * u)) & 0xFu; both; both &= both - 1u) {
-            const int q = __ffs(both) - 1;
-            const int32_t j = w_lo + 128 * u + 4 * lane + q;
-            if ((bg >> (4 * u + q)) & 1u) {
-                put(out, g + min(e, need), k, position(j), status);
-                ++g;
-            } else {
-                if (e < need) put(out, g + e, k, position(j), status);
-                ++e;
-            }
+        for (int32_t j0 = w_lo; j0 < w_hi; j0 += 32) {
+            const int32_t j = j0 + lane;
+            const float x = row_s[j];                 // at most 31 past w_hi, inside the padded row
+            const uint32_t key = order_key(x);
+            const bool gt = j < w_hi && (ranked ? x > tf : key > tau), eq = j < w_hi && (ranked ? x == tf : key == tau);
+            const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+            const uint32_t g = g0 + __popc(bg & lower), e = e0 + __popc(be & lower);
+            if (gt) sel[g + min(e, need)] = (uint32_t)j;
+            else if (eq && e < need) sel[g + e] = (uint32_t)j;
+            g0 += __popc(bg);
+            e0 += __popc(be);
         }
-        g0 += (uint32_t)(tg >> (8 * u)) & 0xFFu;
-        e0 += (uint32_t)(te >> (8 * u)) & 0xFFu;
     }
+    __syncthreads();
+    // late: a dependent's CTAs that come earlier take shared memory from rows
+    // that wait for it (256 rows over 8,192 in a loop: 9.5 us instead of 7.9)
+    pdl_launch_dependents();
+    auto position = [&](uint32_t j) -> int32_t { return (int32_t)j < c ? (int32_t)j : end_pos[(int32_t)j - c]; };
+    if (k % 4 == 0) {
+        for (int32_t g = tid; 4 * g < k; g += NT) {
+            const uint4 w = reinterpret_cast<const uint4*>(sel)[g];
+            reinterpret_cast<int4*>(out)[g] = make_int4(position(w.x), position(w.y), position(w.z), position(w.w));
+        }
+    } else {
+        for (int32_t g = tid; g < k; g += NT) out[g] = position(sel[g]);
+    }
+}
+
+template <int NT, int BATCH, int MINB>
+cudaError_t launch_short(const BatchDev& bd, const float* scores, int64_t ld, const uint64_t* mask, int k, int32_t* idx,
+                         int32_t* status, cudaStream_t stream) {
+    const size_t smem = ((size_t)bd.max_ctx + 127) / 128 * 128 * sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(topk_short_kernel<NT, BATCH, MINB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)bd.max_q, (unsigned)bd.B);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, topk_short_kernel<NT, BATCH, MINB>, bd, scores, ld, k, idx, status, mask);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
 }
 
 template <bool MASKED>
@@ -1062,22 +1128,22 @@ cudaError_t launch_topk(const BatchDev& bd, RowRange rr, const float* scores, in
 
 cudaError_t launch_tree_topk(const BatchDev& bd, const float* scores, int64_t ld, const uint64_t* mask, int k,
                              int32_t* idx, int32_t* status, cudaStream_t stream) {
-    // Rows that fit a CTA's registers.  With fewer rows than SMs a CTA has an
-    // SM to itself: 1024 threads; else 512 and two or three CTAs per SM.
-    const bool few = (int64_t)bd.B * bd.max_q < num_sms();
-    const int per = (bd.max_ctx + (few ? 1023 : 511)) / (few ? 1024 : 512);
-    if (per <= 32) {
-        auto kernel = few ? (per <= 8    ? topk_short_kernel<1024, 8>
-                             : per <= 16 ? topk_short_kernel<1024, 16>
-                                         : topk_short_kernel<1024, 32>)
-                          : (per <= 8    ? topk_short_kernel<512, 8>
-                             : per <= 16 ? topk_short_kernel<512, 16>
-                                         : topk_short_kernel<512, 32>);
-        kernel<<<dim3((unsigned)bd.max_q, (unsigned)bd.B), few ? 1024 : 512, 0, stream>>>(bd, scores, ld, k, idx, status,
-                                                                                      mask);
-        const cudaError_t e = cudaGetLastError();
-        if (e == cudaSuccess) count_launches(1);
-        return e;
+    // Rows that fit a CTA's shared memory.  Fewer rows than SMs: a CTA has an SM
+    // to itself and takes as many threads as its row feeds (8,192 positions: 5.7
+    // us with 512, 6.3 with 1024; 32,768: 11.8 and 10.9).  Else a smaller CTA
+    // pays for fewer warps' sums, as long as an SM's shared memory holds rows
+    // for enough of them (64 x 32 rows over 9,001: 41 us with 256 threads, 44
+    // with 512, 80 with 1024; 16 x 64 over 20,000: 51, 43, 54; over 32,768:
+    // 112, 91, 79).
+    // With fewer than two rows per SM the smaller CTA gains nothing (256 rows over
+    // 8,192: 8.7 us with 256 threads, 7.9 with 512).
+    const int64_t rows = (int64_t)bd.B * bd.max_q;
+    const bool few = rows < num_sms();
+    if (bd.max_ctx <= kShortRow) {
+        if (rows >= 2 * num_sms() && bd.max_ctx <= kRowOf256) return launch_short<256, 4, 5>(bd, scores, ld, mask, k, idx, status, stream);
+        return bd.max_ctx <= (few ? kFewRowOf512 : kRowOf512)
+                   ? launch_short<512, 4, 3>(bd, scores, ld, mask, k, idx, status, stream)
+                   : launch_short<1024, 8, 1>(bd, scores, ld, mask, k, idx, status, stream);
     }
     return launch_rows<true>(bd, RowRange{0, bd.max_q}, scores, ld, false, k, idx, false, status, stream, false, mask);
 }

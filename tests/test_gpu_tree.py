@@ -426,6 +426,31 @@ def test_tree_topk(c, m, k, kind):
     assert np.array_equal(idx.cpu().numpy(), _topk_ref(st, sc, k))
 
 
+_RANGES = {
+    "offset": lambda x: 1e4 + x, "far": lambda x: 1e7 + x, "outlier": lambda x: np.where(x == x[0, 3], 1e30, x),
+    "span": lambda x: np.clip(x, -3, 3) * 1.1e38, "tiny": lambda x: x * 1e-42,
+    "lowest": lambda x: -3.4e38 * (1 - 1e-3 * np.abs(x) / 8),
+}
+
+
+@pytest.mark.parametrize("c,m,k", [
+    ([700] * 5, [64] * 5, 333), ([11000] * 5, [64] * 5, 2047), ([26000] * 3, [60] * 3, 1001), ([900], [5], 30),
+    ([20000], [5], 2048), ([255, 256, 257, 64], [64, 1, 63, 64], 250), ([50000], [3], 2046),
+])
+@pytest.mark.parametrize("kind", list(_RANGES))
+def test_tree_topk_ranges(c, m, k, kind):
+    """Scores whose range an even division does not fit, at row lengths and counts of every kernel; exact."""
+    st = Step(c, m, 0, seed=k)
+    ld = (st.max_ctx + 3) // 4 * 4
+    x = np.random.default_rng(k).standard_normal((st.T, ld))
+    sc = _RANGES[kind](x).astype(np.float32)
+    assert np.isfinite(sc).all()
+    idx = torch.full((st.T, k), -7, dtype=I32, device="cuda")
+    dsa.tree_topk(st.b, torch.from_numpy(sc).cuda(), st.mask, k, idx, ws=st.ws)
+    assert st.status() == 0
+    assert np.array_equal(idx.cpu().numpy(), _topk_ref(st, sc, k))
+
+
 def test_tree_topk_of_a_chain_is_topk():
     st = Step([3000, 12], [7, 20], 0, masks=[[(2 << i) - 1 for i in range(n)] for n in (7, 20)])
     ld = (st.max_ctx + 3) // 4 * 4
