@@ -777,6 +777,8 @@ __global__ void __launch_bounds__(NT, MINB)
                       int32_t* __restrict__ idx, int32_t* status, const uint64_t* __restrict__ mask) {
     constexpr int kWarps = NT / 32, kBinsPerThread = kBins / NT, kBlock = 4;   // 128-score groups per scan
     static_assert(kMaxTopk <= kBins, "the selected indices take the histogram's place");
+    static_assert(kShortRow <= 32 * 128 * 32 && kRowOf512 <= 16 * 128 * 32 && kRowOf256 <= 8 * 128 * 32,
+                  "a warp's segment has at most 32 groups");
     static_assert(kWarps <= 32 && NT >= DSA_MAX_TREE * 2, "one lane per warp's sum; new scores and padding by one thread each");
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ TopkSmem<NT, 1> S;
@@ -903,9 +905,9 @@ __global__ void __launch_bounds__(NT, MINB)
         if (S.sel_count <= 64u) {
             const float at = (float)S.sel_digit, width = span / ((float)kBins - 8.f);
             const float from = fmaf(at - 4.375f, width, low), to = fmaf(at - 2.875f, width, low);
-            uint32_t higher = 0u;
+            uint32_t higher = 0u, hits = 0u;          // hits: the lane's groups with a score in the window
 #pragma unroll 2
-            for (int32_t j = w_lo; j < w_hi; j += 128) {
+            for (int32_t j = w_lo, u = 0; j < w_hi; j += 128, ++u) {
                 const float4 x = row4[(j >> 2) + lane];
                 const float y[4] = {x.x, x.y, x.z, x.w};
                 bool any = false;
@@ -914,19 +916,21 @@ __global__ void __launch_bounds__(NT, MINB)
                     higher += y[q] > to ? 1u : 0u;
                     any |= y[q] >= from && y[q] <= to;
                 }
-                if (any) {
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        const float f = row_s[j + 4 * lane + q];
-                        if (f >= from && f <= to) {
-                            const uint32_t s = atomicAdd(&S.small_n, 1u);
-                            if (s < 64u) {
-                                S.small[s] = __float_as_uint(f);
-                                S.small_all[s] = (uint32_t)warp;
-                            }
-                        }
+                hits |= (any ? 1u : 0u) << u;
+            }
+            for (; hits; hits &= hits - 1u) {
+                const float4 x = row4[(w_lo >> 2) + 32 * (__ffs(hits) - 1) + lane];
+                const float y[4] = {x.x, x.y, x.z, x.w};
+                uint32_t in = 0u;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) in += y[q] >= from && y[q] <= to ? 1u : 0u;
+                uint32_t s = atomicAdd(&S.small_n, in);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (y[q] >= from && y[q] <= to && s < 64u) {
+                        S.small[s] = __float_as_uint(y[q]);
+                        S.small_all[s++] = (uint32_t)warp;
                     }
-                }
             }
             higher = __reduce_add_sync(0xffffffffu, higher);
             if (lane == 0) S.wcnt[warp] = higher;
