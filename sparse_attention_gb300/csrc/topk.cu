@@ -65,7 +65,9 @@ constexpr int kKeysPerCta = 32768;
 constexpr int kShortRow = 49152;             // masked rows up to this stay in shared memory (192 KB)
 constexpr int kRowOf256 = 10240;             // and take a CTA of 256 threads up to this (four or five per SM),
 constexpr int kRowOf512 = 24576;             // of 512 up to this (two or three per SM),
-constexpr int kFewRowOf512 = 16384;          // or this when there are few (one per SM)
+constexpr int kFewRowOf512 = 16384;          // or this when there are few (one per SM);
+constexpr int kAloneRow = 24576;             // few rows above this are split over a cluster
+constexpr int kSlice = 12288;                // into slices of at most this
 
 __device__ __forceinline__ uint32_t order_key(float f) {
     uint32_t u = __float_as_uint(f);
@@ -766,16 +768,19 @@ cudaError_t launch_nt(const BatchDev& bd, RowRange rr, const float* scores, int6
 //   4. The selected indices, in order from packed warp scans, into shared
 //      memory, and from there to idx; ties at the k-th are told apart only if
 //      not all of them are taken.
+// CLUSTER: the CTAs of a cluster take a slice of the row each and exchange the
+// range, the sums of the intervals, the window's scores and the counts.
 // Bound by instructions (37 a score in 32, 4.7 K a row of 256 threads; a
 // scheduler issues in 60 % of the cycles).  k = 2048, 64 trees of up to 32 rows
-// over up to 9,001 positions: 18-21 us (topk_kernel 72, the row in registers
-// instead of shared memory 23-29); 64 x 32 over 2,500: 18 us; 8 x 8 over
-// 32,768: 10.7 us.
-template <int NT, int BATCH, int MINB>
+// over up to 9,001 positions: 17-19 us (topk_kernel 72, the row in registers
+// instead of shared memory 23-29); 64 x 32 over 2,500: 17 us; 8 x 8 over
+// 32,768: 9.6 us (CTA pairs); 1 x 8: 8.0 us (fours).
+template <int NT, int BATCH, int MINB, bool CLUSTER>
 __global__ void __launch_bounds__(NT, MINB)
     topk_short_kernel(const BatchDev bd, const float* __restrict__ scores, const int64_t ld, const int k,
                       int32_t* __restrict__ idx, int32_t* status, const uint64_t* __restrict__ mask) {
     constexpr int kWarps = NT / 32, kBinsPerThread = kBins / NT, kBlock = 4;   // 128-score groups per scan
+    constexpr int kBinGroups = kWarps, kBinsPerGroup = kBins / kWarps;
     static_assert(kMaxTopk <= kBins, "the selected indices take the histogram's place");
     static_assert(kShortRow <= 32 * 128 * 32 && kRowOf512 <= 16 * 128 * 32 && kRowOf256 <= 8 * 128 * 32,
                   "a warp's segment has at most 32 groups");
@@ -783,17 +788,25 @@ __global__ void __launch_bounds__(NT, MINB)
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ TopkSmem<NT, 1> S;
     __shared__ int32_t end_pos[DSA_MAX_TREE];
+    __shared__ uint32_t list[CLUSTER ? 64 : 1], owner[CLUSTER ? 64 : 1];
     float* row_s = reinterpret_cast<float*>(smem_raw);
     float4* row4 = reinterpret_cast<float4*>(smem_raw);
     cg::cluster_group cluster = cg::this_cluster();
-    const int b = blockIdx.y, i = blockIdx.x;
+    const int csize = CLUSTER ? (int)cluster.num_blocks() : 1, crank = CLUSTER ? (int)(blockIdx.x % (unsigned)csize) : 0;
+    const int b = blockIdx.y, i = blockIdx.x / (unsigned)csize;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();                  // the scores of the previous launch are complete
     SeqInfo sq;
     if (!load_seq(bd, b, status, sq) || i >= sq.nq) return;
     const float* row = scores + ((int64_t)sq.q0 + i) * ld;
     int32_t* out = idx + ((int64_t)sq.q0 + i) * k;
-    const int32_t c = sq.ctx - sq.nq, old4 = (c + 3) >> 2;
+    const int32_t c = sq.ctx - sq.nq;
+    // this CTA's slice of the row: positions [s_lo, s_lo + span), the first `cl`
+    // of them committed
+    const int32_t span = CLUSTER ? ((sq.ctx + csize - 1) / csize + 127) & ~127 : sq.ctx;
+    const int32_t s_lo = CLUSTER ? crank * span : 0;
+    const int32_t cl = CLUSTER ? min(max(c - s_lo, 0), span) : c, old4 = (cl + 3) >> 2;
+    row += s_lo;
     const unsigned long long word = __ldg(reinterpret_cast<const unsigned long long*>(mask) + sq.q0 + i);
     auto load = [&](int32_t g) -> float4 {
         return sq.ctx > k && g < old4 ? __ldg(reinterpret_cast<const float4*>(row) + g) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -807,6 +820,7 @@ __global__ void __launch_bounds__(NT, MINB)
     const bool seen = tid < DSA_MAX_TREE && (bits >> (tid & 63)) & 1u;
     const int32_t place = c + __popcll(bits & ((1ull << (tid & 63)) - 1u));
     if (n <= k) {
+        if (crank != 0) return;
         for (int j = tid; j < k; j += NT)
             if (j < c || j >= n) out[j] = j < c ? j : -1;
         if (seen) out[place] = c + tid;
@@ -814,29 +828,34 @@ __global__ void __launch_bounds__(NT, MINB)
     }
     float low = INFINITY, high = -INFINITY;
     if (seen) {
-        low = high = __ldg(row + c + tid);
-        row_s[place] = low;
         end_pos[place - c] = c + tid;
+        if (!CLUSTER || (place >= s_lo && place < s_lo + span)) {
+            low = high = __ldg(row - s_lo + c + tid);
+            row_s[place - s_lo] = low;
+        }
     }
-    if (n + tid < ((n + 127) & ~127)) row_s[n + tid] = -INFINITY;
+    const int32_t len = CLUSTER ? min(max(n - s_lo, 0), span) : n;   // the slice's scores
+    if (len + tid < ((len + 127) & ~127)) row_s[len + tid] = -INFINITY;
 #pragma unroll
     for (int x = 0; x < kBinsPerThread; ++x) S.hist[NT * x + tid] = 0u;
     if (tid < 32) S.weq[tid] = 0u;
     if (tid == 0) {
         S.small_n = 0u;
         S.sel_count = 0xFFFFFFFFu;
+        S.pre_gt = 0u;
+        S.pre_eq = 0u;
     }
     for (int32_t g0 = 0;;) {
 #pragma unroll
         for (int u = 0; u < BATCH; ++u) {
             const int32_t g = g0 + NT * u + tid;
-            if (4 * g + 4 <= c) {
+            if (4 * g + 4 <= cl) {
                 row4[g] = v[u];
                 low = fminf(fminf(low, fminf(v[u].x, v[u].y)), fminf(v[u].z, v[u].w));
                 high = fmaxf(fmaxf(high, fmaxf(v[u].x, v[u].y)), fmaxf(v[u].z, v[u].w));
-            } else if (4 * g < c) {                   // the group that the new scores follow in
+            } else if (4 * g < cl) {                  // the group that the new scores follow in
                 const float y[3] = {v[u].x, v[u].y, v[u].z};
-                for (int x = 0; x < 3 && 4 * g + x < c; ++x) {
+                for (int x = 0; x < 3 && 4 * g + x < cl; ++x) {
                     row_s[4 * g + x] = y[x];
                     low = fminf(low, y[x]);
                     high = fmaxf(high, y[x]);
@@ -857,19 +876,29 @@ __global__ void __launch_bounds__(NT, MINB)
     __syncthreads();
     low = -warp_max_f32(lane < kWarps ? -__uint_as_float(S.wgt[lane]) : -INFINITY);
     high = warp_max_f32(lane < kWarps ? __uint_as_float(S.wmax[lane]) : -INFINITY);
+    if constexpr (CLUSTER) {
+        if (tid == 0) {
+            S.cta_cand = __float_as_uint(low);
+            S.cta_max = __float_as_uint(high);
+        }
+        cluster.sync();
+        const auto* o = cluster.map_shared_rank(&S, (unsigned)min(lane, csize - 1));
+        low = -warp_max_f32(-__uint_as_float(o->cta_cand));
+        high = warp_max_f32(__uint_as_float(o->cta_max));
+    }
 
     // interval of f: t = 4 + (f - low) * per, rounded to quarters, its floor;
     // four spare ones at each end for the rounding of `off`
-    const float span = high - low, per = ((float)kBins - 8.f) / span, off = fmaf(-low, per, 2097152.f + 4.f);
-    const bool linear = span > 0.f && span < INFINITY && per < INFINITY;   // false for NaN too
-    const int32_t seg = ((n + kWarps - 1) / kWarps + 127) & ~127;
-    const int32_t w_lo = min(n, warp * seg), w_hi = min(n, w_lo + seg);
+    const float range = high - low, per = ((float)kBins - 8.f) / range, off = fmaf(-low, per, 2097152.f + 4.f);
+    const bool linear = range > 0.f && range < INFINITY && per < INFINITY;   // false for NaN too
+    const int32_t seg = ((len + kWarps - 1) / kWarps + 127) & ~127;
+    const int32_t w_lo = min(len, warp * seg), w_hi = min(len, w_lo + seg);
     float tf = 0.f;
-    uint32_t need = 0u;
+    uint32_t need = 0u, gt_pre = 0u;                  // gt_pre: in the lower ranks' slices
     bool ties = true, ranked = false;
     if (linear) {
 #pragma unroll 2
-        for (int32_t g = tid; 4 * g < n; g += NT) {
+        for (int32_t g = tid; 4 * g < len; g += NT) {
             const float4 x = row4[g];                 // at most 3 of -inf here: they add to interval 0
             const float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -885,38 +914,83 @@ __global__ void __launch_bounds__(NT, MINB)
             cnt[q + 1] = two.y;
             mine += two.x + two.y;
         }
-        const uint32_t incl = warp_inclusive_scan(mine);
-        if (lane == 31) S.warp_sums[warp] = incl;
-        __syncthreads();
-        const uint32_t sums = lane < kWarps ? S.warp_sums[lane] : 0u;
-        // scores in higher intervals
-        uint32_t above = mine - incl + __reduce_add_sync(0xffffffffu, lane >= warp ? sums : 0u) - mine;
-        if (above < (uint32_t)k && (uint32_t)k <= above + mine) {
+        if constexpr (CLUSTER) {
+            // the warp's bins that hold the k-th from every rank's sums of a
+            // warp's bins, then its bin from every rank's bins of that warp
+            mine = __reduce_add_sync(0xffffffffu, mine);
+            if (lane == 0) S.group[warp] = mine;
+            cluster.sync();
+            if (warp == 0) {
+                uint32_t sum = 0u;
 #pragma unroll
-            for (int q = kBinsPerThread - 1; q >= 0; --q) {
-                if (above < (uint32_t)k && (uint32_t)k <= above + cnt[q]) {
-                    S.sel_digit = (uint32_t)(kBinsPerThread * tid + q);
-                    S.sel_count = cnt[q];
+                for (int q = 0; q < kMaxCluster; ++q)
+                    if (q < csize && lane < kBinGroups) sum += cluster.map_shared_rank(S.group, (unsigned)q)[lane];
+                uint32_t incl = warp_inclusive_scan(sum);
+                uint32_t above = __shfl_sync(0xffffffffu, incl, 31) - incl;
+                const uint32_t has = __ballot_sync(0xffffffffu, above < (uint32_t)k && (uint32_t)k <= above + sum);
+                const int grp = has ? __ffs(has) - 1 : 0;
+                const uint32_t gabove = __shfl_sync(0xffffffffu, above, grp);
+                uint32_t bin[kBinsPerGroup / 32];
+#pragma unroll
+                for (int x = 0; x < kBinsPerGroup / 32; ++x) bin[x] = 0u;
+#pragma unroll
+                for (int q = 0; q < kMaxCluster; ++q)
+                    if (q < csize) {
+                        const uint32_t* from = cluster.map_shared_rank(S.hist, (unsigned)q) + kBinsPerGroup * grp;
+#pragma unroll
+                        for (int x = 0; x < kBinsPerGroup / 32; ++x) bin[x] += from[kBinsPerGroup / 32 * lane + x];
+                    }
+                sum = 0u;
+#pragma unroll
+                for (int x = 0; x < kBinsPerGroup / 32; ++x) sum += bin[x];
+                incl = warp_inclusive_scan(sum);
+                above = gabove + __shfl_sync(0xffffffffu, incl, 31) - incl;
+#pragma unroll
+                for (int x = kBinsPerGroup / 32 - 1; x >= 0; --x) {
+                    if (has && above < (uint32_t)k && (uint32_t)k <= above + bin[x]) {
+                        S.sel_digit = (uint32_t)(kBinsPerGroup * grp + kBinsPerGroup / 32 * lane + x);
+                        S.sel_count = bin[x];
+                    }
+                    above += bin[x];
                 }
-                above += cnt[q];
             }
+            __syncthreads();
+        } else {
+            const uint32_t incl = warp_inclusive_scan(mine);
+            if (lane == 31) S.warp_sums[warp] = incl;
+            __syncthreads();
+            const uint32_t sums = lane < kWarps ? S.warp_sums[lane] : 0u;
+            // scores in higher intervals
+            uint32_t above = mine - incl + __reduce_add_sync(0xffffffffu, lane >= warp ? sums : 0u) - mine;
+            if (above < (uint32_t)k && (uint32_t)k <= above + mine) {
+    #pragma unroll
+                for (int q = kBinsPerThread - 1; q >= 0; --q) {
+                    if (above < (uint32_t)k && (uint32_t)k <= above + cnt[q]) {
+                        S.sel_digit = (uint32_t)(kBinsPerThread * tid + q);
+                        S.sel_count = cnt[q];
+                    }
+                    above += cnt[q];
+                }
+            }
+            __syncthreads();
         }
-        __syncthreads();
         if (S.sel_count <= 64u) {
-            const float at = (float)S.sel_digit, width = span / ((float)kBins - 8.f);
+            const float at = (float)S.sel_digit, width = range / ((float)kBins - 8.f);
             const float from = fmaf(at - 4.375f, width, low), to = fmaf(at - 2.875f, width, low);
+            // subtraction is monotone: a score in the window is within `half` of mid
+            const float mid = 0.5f * from + 0.5f * to, half = fmaxf(to - mid, mid - from);
             uint32_t higher = 0u, hits = 0u;          // hits: the lane's groups with a score in the window
 #pragma unroll 2
             for (int32_t j = w_lo, u = 0; j < w_hi; j += 128, ++u) {
                 const float4 x = row4[(j >> 2) + lane];
                 const float y[4] = {x.x, x.y, x.z, x.w};
-                bool any = false;
+                float d = INFINITY;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     higher += y[q] > to ? 1u : 0u;
-                    any |= y[q] >= from && y[q] <= to;
+                    d = fminf(d, fabsf(y[q] - mid));
                 }
-                hits |= (any ? 1u : 0u) << u;
+                hits |= (d <= half ? 1u : 0u) << u;
             }
             for (; hits; hits &= hits - 1u) {
                 const float4 x = row4[(w_lo >> 2) + 32 * (__ffs(hits) - 1) + lane];
@@ -935,17 +1009,38 @@ __global__ void __launch_bounds__(NT, MINB)
             higher = __reduce_add_sync(0xffffffffu, higher);
             if (lane == 0) S.wcnt[warp] = higher;
             __syncthreads();
-            const uint32_t m = S.small_n;
-            const uint32_t want = (uint32_t)k - __reduce_add_sync(0xffffffffu, lane < kWarps ? S.wcnt[lane] : 0u);
+            uint32_t m = S.small_n, all_higher = __reduce_add_sync(0xffffffffu, lane < kWarps ? S.wcnt[lane] : 0u);
+            if constexpr (CLUSTER) {
+                // every rank's list behind the lower ranks', with its owner
+                if (tid == 0) S.cta_gt = all_higher;
+                cluster.sync();
+                const auto* o = cluster.map_shared_rank(&S, (unsigned)min(lane, csize - 1));
+                const uint32_t n_of = lane < csize ? o->small_n : 0u, higher_of = lane < csize ? o->cta_gt : 0u;
+                const uint32_t behind = warp_inclusive_scan(n_of);
+                m = __shfl_sync(0xffffffffu, behind, 31);
+                all_higher = __reduce_add_sync(0xffffffffu, higher_of);
+                gt_pre = __reduce_add_sync(0xffffffffu, lane < crank ? higher_of : 0u);
+                for (int q = warp; q < csize; q += kWarps) {
+                    const uint32_t from_q = __shfl_sync(0xffffffffu, behind - n_of, q), n_q = __shfl_sync(0xffffffffu, n_of, q);
+                    const auto* of = cluster.map_shared_rank(&S, (unsigned)q);
+                    for (uint32_t x = lane; m <= 64u && x < n_q; x += 32u) {
+                        list[from_q + x] = of->small[x];
+                        owner[from_q + x] = of->small_all[x] + ((uint32_t)q << 8);
+                    }
+                }
+                __syncthreads();
+            }
+            const uint32_t want = (uint32_t)k - all_higher;
+            const uint32_t* values = CLUSTER ? list : S.small;
             ranked = m <= 64u && want - 1u < m;       // 0 < want <= m
             if (ranked) {
                 // eight threads rank a score against eight each
                 for (uint32_t ranker = (uint32_t)tid; ranker < 8u * m; ranker += NT) {
                     const uint32_t q = ranker >> 3, sub = ranker & 7u;
-                    const float f = __uint_as_float(S.small[q]);
+                    const float f = __uint_as_float(values[q]);
                     uint32_t gt = 0u, eq = 0u;
                     for (uint32_t o = sub; o < m; o += 8u) {
-                        const float y = __uint_as_float(S.small[o]);
+                        const float y = __uint_as_float(values[o]);
                         gt += y > f ? 1u : 0u;
                         eq += y == f ? 1u : 0u;
                     }
@@ -967,21 +1062,26 @@ __global__ void __launch_bounds__(NT, MINB)
                 need = S.small_need;
                 ties = S.total != need;
                 if ((uint32_t)tid < m) {
-                    const float f = __uint_as_float(S.small[tid]);
-                    if (f > tf || (!ties && f == tf)) atomicAdd(&S.wcnt[S.small_all[tid]], 1u);
-                    else if (f == tf) atomicAdd(&S.weq[S.small_all[tid]], 1u);
+                    const float f = __uint_as_float(values[tid]);
+                    const uint32_t of = CLUSTER ? owner[tid] : S.small_all[tid], rank = of >> 8;
+                    const bool above = f > tf || (!ties && f == tf);
+                    if (above || f == tf) {
+                        if (rank == (uint32_t)crank) atomicAdd(above ? &S.wcnt[of & 0xFFu] : &S.weq[of & 0xFFu], 1u);
+                        else if (rank < (uint32_t)crank) atomicAdd(above ? &S.pre_gt : &S.pre_eq, 1u);
+                    }
                 }
             }
         }
     }
     uint32_t tau = 0u;
     if (!ranked) {
-        __syncthreads();
+        if constexpr (CLUSTER) cluster.sync();        // other ranks may still read this one's counts
+        else __syncthreads();
 #pragma unroll
         for (int x = 0; x < kBinsPerThread; ++x) S.hist[NT * x + tid] = 0u;
         uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
 #pragma unroll 1
-        for (int32_t j = tid; j < n; j += NT) {
+        for (int32_t j = tid; j < len; j += NT) {
             const uint32_t q = order_key(row_s[j]);
             kmin = min(kmin, q);
             kmax = max(kmax, q);
@@ -995,10 +1095,20 @@ __global__ void __launch_bounds__(NT, MINB)
         __syncthreads();
         kmin = __reduce_min_sync(0xffffffffu, lane < kWarps ? S.wgt[lane] : 0xFFFFFFFFu);
         kmax = __reduce_max_sync(0xffffffffu, lane < kWarps ? S.wmax[lane] : 0u);
-        tau = radix_select(cluster, 1, S, (uint32_t)k, varying_bits(kmin, kmax), kmin, 3,
+        if constexpr (CLUSTER) {
+            if (tid == 0) {
+                S.cta_overflow = kmin;
+                S.all_max = kmax;
+            }
+            cluster.sync();
+            const auto* o = cluster.map_shared_rank(&S, (unsigned)min(lane, csize - 1));
+            kmin = __reduce_min_sync(0xffffffffu, o->cta_overflow);
+            kmax = __reduce_max_sync(0xffffffffu, o->all_max);
+        }
+        tau = radix_select(cluster, csize, S, (uint32_t)k, varying_bits(kmin, kmax), kmin, 3,
                            [&](auto&& f) {
 #pragma unroll 1
-                               for (int32_t j = tid; j < n; j += NT) f(order_key(row_s[j]));
+                               for (int32_t j = tid; j < len; j += NT) f(order_key(row_s[j]));
                            },
                            need);
         uint32_t gt = 0u, eq = 0u;
@@ -1014,13 +1124,38 @@ __global__ void __launch_bounds__(NT, MINB)
             S.wcnt[warp] = gt;
             S.weq[warp] = eq;
         }
+        if constexpr (CLUSTER) {
+            __syncthreads();
+            gt = __reduce_add_sync(0xffffffffu, lane < kWarps ? S.wcnt[lane] : 0u);
+            eq = __reduce_add_sync(0xffffffffu, lane < kWarps ? S.weq[lane] : 0u);
+            if (tid == 0) {
+                S.cta_gt = gt;
+                S.cta_eq = eq;
+            }
+            cluster.sync();
+            const auto* o = cluster.map_shared_rank(&S, (unsigned)min(lane, csize - 1));
+            gt = __reduce_add_sync(0xffffffffu, lane < crank ? o->cta_gt : 0u);
+            eq = __reduce_add_sync(0xffffffffu, lane < crank ? o->cta_eq : 0u);
+            if (tid == 0) {
+                S.pre_gt = gt;
+                S.pre_eq = eq;
+            }
+            gt_pre = 0u;
+        }
     }
-    __syncthreads();
+    if constexpr (CLUSTER) cluster.sync();            // the last remote read is done
+    else __syncthreads();
     // the histogram's place takes the selected indices from here on
     uint32_t* sel = S.hist;
-    const uint32_t sg = lane < kWarps ? S.wcnt[lane] : 0u;
+    const uint32_t sg = lane < kWarps ? S.wcnt[lane] : 0u, se = ties && lane < kWarps ? S.weq[lane] : 0u;
     uint32_t g0 = __reduce_add_sync(0xffffffffu, lane < warp ? sg : 0u);
-    if (__reduce_add_sync(0xffffffffu, sg) + (ties ? need : 0u) != (uint32_t)k) {   // would be a bug: no write past k
+    uint32_t e0 = __reduce_add_sync(0xffffffffu, lane < warp ? se : 0u);
+    // taken in this slice, and where they go: scores above the k-th, and of the
+    // equal ones the first `need` of the row
+    const uint32_t e_pre = CLUSTER ? min(S.pre_eq, need) : 0u, first = CLUSTER ? gt_pre + S.pre_gt + e_pre : 0u;
+    const uint32_t left = need - e_pre;
+    const uint32_t taken = __reduce_add_sync(0xffffffffu, sg) + min(__reduce_add_sync(0xffffffffu, se), left);
+    if (first + taken > (uint32_t)k || (!CLUSTER && taken != (uint32_t)k)) {   // would be a bug: no write past k
         latch_status(status, DSA_ERR_INTERNAL);
         return;
     }
@@ -1051,7 +1186,6 @@ __global__ void __launch_bounds__(NT, MINB)
             }
         }
     } else {
-        uint32_t e0 = __reduce_add_sync(0xffffffffu, lane < warp ? S.weq[lane] : 0u);
         const uint32_t lower = (1u << lane) - 1u;
 #pragma unroll 1
         for (int32_t j0 = w_lo; j0 < w_hi; j0 += 32) {
@@ -1061,8 +1195,8 @@ __global__ void __launch_bounds__(NT, MINB)
             const bool gt = j < w_hi && (ranked ? x > tf : key > tau), eq = j < w_hi && (ranked ? x == tf : key == tau);
             const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
             const uint32_t g = g0 + __popc(bg & lower), e = e0 + __popc(be & lower);
-            if (gt) sel[g + min(e, need)] = (uint32_t)j;
-            else if (eq && e < need) sel[g + e] = (uint32_t)j;
+            if (gt) sel[g + min(e, left)] = (uint32_t)j;
+            else if (eq && e < left) sel[g + e] = (uint32_t)j;
             g0 += __popc(bg);
             e0 += __popc(be);
         }
@@ -1071,35 +1205,42 @@ __global__ void __launch_bounds__(NT, MINB)
     // late: a dependent's CTAs that come earlier take shared memory from rows
     // that wait for it (256 rows over 8,192 in a loop: 9.5 us instead of 7.9)
     pdl_launch_dependents();
-    auto position = [&](uint32_t j) -> int32_t { return (int32_t)j < c ? (int32_t)j : end_pos[(int32_t)j - c]; };
-    if (k % 4 == 0) {
+    auto position = [&](uint32_t at) -> int32_t {
+        const int32_t j = s_lo + (int32_t)at;
+        return j < c ? j : end_pos[j - c];
+    };
+    if (!CLUSTER && k % 4 == 0) {
         for (int32_t g = tid; 4 * g < k; g += NT) {
             const uint4 w = reinterpret_cast<const uint4*>(sel)[g];
             reinterpret_cast<int4*>(out)[g] = make_int4(position(w.x), position(w.y), position(w.z), position(w.w));
         }
     } else {
-        for (int32_t g = tid; g < k; g += NT) out[g] = position(sel[g]);
+        for (uint32_t g = tid; g < taken; g += NT) out[first + g] = position(sel[g]);
     }
 }
 
-template <int NT, int BATCH, int MINB>
+template <int NT, int BATCH, int MINB, bool CLUSTER = false>
 cudaError_t launch_short(const BatchDev& bd, const float* scores, int64_t ld, const uint64_t* mask, int k, int32_t* idx,
-                         int32_t* status, cudaStream_t stream) {
-    const size_t smem = ((size_t)bd.max_ctx + 127) / 128 * 128 * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(topk_short_kernel<NT, BATCH, MINB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         int32_t* status, cudaStream_t stream, int csize = 1) {
+    const size_t smem = (((size_t)bd.max_ctx + csize - 1) / csize + 127) / 128 * 128 * sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(topk_short_kernel<NT, BATCH, MINB, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)bd.max_q, (unsigned)bd.B);
+    cfg.gridDim = dim3((unsigned)(bd.max_q * csize), (unsigned)bd.B);
     cfg.blockDim = dim3(NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)csize;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, topk_short_kernel<NT, BATCH, MINB>, bd, scores, ld, k, idx, status, mask);
+    cfg.numAttrs = CLUSTER ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, topk_short_kernel<NT, BATCH, MINB, CLUSTER>, bd, scores, ld, k, idx, status, mask);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
@@ -1143,6 +1284,14 @@ cudaError_t launch_tree_topk(const BatchDev& bd, const float* scores, int64_t ld
     // 8,192: 8.7 us with 256 threads, 7.9 with 512).
     const int64_t rows = (int64_t)bd.B * bd.max_q;
     const bool few = rows < num_sms();
+    // Long rows and SMs to spare: a cluster shares a row (8 rows over 32,768: 9.8
+    // us with one CTA, 9.5, 8.0 and 8.5 with two, four and eight; over 100,000:
+    // 18 (topk_kernel) and 10.4 with eight; 16 rows over 16,384: 7.0, and 7.4 with four).
+    int csize = 1;
+    while (bd.max_ctx > kAloneRow && csize < kMaxCluster && rows * 2 * csize <= num_sms() && bd.max_ctx > kSlice * csize)
+        csize *= 2;
+    if (csize > 1 && bd.max_ctx <= (int64_t)kShortRow * csize)
+        return launch_short<512, 4, 1, true>(bd, scores, ld, mask, k, idx, status, stream, csize);
     if (bd.max_ctx <= kShortRow) {
         if (rows >= 2 * num_sms() && bd.max_ctx <= kRowOf256) return launch_short<256, 4, 5>(bd, scores, ld, mask, k, idx, status, stream);
         return bd.max_ctx <= (few ? kFewRowOf512 : kRowOf512)

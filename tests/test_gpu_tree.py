@@ -436,6 +436,7 @@ _RANGES = {
 @pytest.mark.parametrize("c,m,k", [
     ([700] * 5, [64] * 5, 333), ([11000] * 5, [64] * 5, 2047), ([26000] * 3, [60] * 3, 1001), ([900], [5], 30),
     ([20000], [5], 2048), ([255, 256, 257, 64], [64, 1, 63, 64], 250), ([50000], [3], 2046),
+    ([30000, 3000, 29000, 8191], [9, 9, 5, 1], 2047), ([25000] * 7, [10] * 7, 100),
 ])
 @pytest.mark.parametrize("kind", list(_RANGES))
 def test_tree_topk_ranges(c, m, k, kind):
