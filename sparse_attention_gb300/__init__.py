@@ -383,7 +383,7 @@ def _typed(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, numel: int,
 def _here(ws: torch.Tensor, stream) -> int:
     """The device of a call: the workspace's, which has to be the current one and the stream's."""
     dev = ws.get_device()
-    if dev < 0 or dev != torch.cuda.current_device() or (stream is not None and stream.device_index != dev):
+    if dev < 0 or dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
         raise ValueError(f"workspace on {ws.device}: expected on the current CUDA device, and the stream's")
     return dev
 
@@ -473,6 +473,14 @@ def tree_topk(batch: Batch, scores, mask, k: int, idx, ld: Optional[int] = None,
     return idx
 
 
+def _layered(name: str, t: torch.Tensor, width: int):
+    """(layers, rows) of a cache [layers, rows, width] or [rows, width]."""
+    s = t.shape
+    if len(s) not in (2, 3) or s[-1] != width:
+        raise ValueError(f"{name}: [layers, rows, {width}] expected, got {list(s)}")
+    return (s[0], s[1]) if len(s) == 3 else (1, s[0])
+
+
 def tree_commit(batch: Batch, mask, accepted, ctx_new, kv=None, k_idx=None, pages: Optional[Pages] = None, ws=None,
                 stream=None):
     """Moves the accepted paths' rows behind the committed ones in every layer
@@ -481,10 +489,12 @@ def tree_commit(batch: Batch, mask, accepted, ctx_new, kv=None, k_idx=None, page
     dev, bf16 = _here(ws, stream), torch.bfloat16
     c = batch.c
     pg, need = _paged(batch, pages, dev)
-    shapes = {(t.shape[0] if t.dim() == 3 else 1, t.shape[-2]) for t in (kv, k_idx) if t is not None}
-    if len(shapes) > 1:
-        raise ValueError("kv and k_idx: the same layers and rows expected")
-    layers, rows = shapes.pop() if shapes else (1, need)
+    layers, rows = _layered("kv", kv, D_QK) if kv is not None else (1, need)
+    if k_idx is not None:
+        other = _layered("k_idx", k_idx, D_IDX)
+        if kv is not None and other != (layers, rows):
+            raise ValueError("kv and k_idx: the same layers and rows expected")
+        layers, rows = other
     _check(load_library().dsa_tree_commit(
         ctypes.byref(c), pg, _typed("mask", mask, torch.int64, c.total_q, dev),
         _typed("accepted", accepted, torch.int32, c.batch, dev), layers, rows,

@@ -770,8 +770,8 @@ cudaError_t launch_nt(const BatchDev& bd, RowRange rr, const float* scores, int6
 //      not all of them are taken.
 // CLUSTER: the CTAs of a cluster take a slice of the row each and exchange the
 // range, the sums of the intervals, the window's scores and the counts.
-// Bound by instructions (37 a score in 32, 4.7 K a row of 256 threads; a
-// scheduler issues in 60 % of the cycles).  k = 2048, 64 trees of up to 32 rows
+// Bound by instructions (34 per 32 scores and 4.5 K a row of 256 threads; a
+// scheduler issues in 59-67 % of the cycles).  k = 2048, 64 trees of up to 32 rows
 // over up to 9,001 positions: 17-19 us (topk_kernel 72, the row in registers
 // instead of shared memory 23-29); 64 x 32 over 2,500: 17 us; 8 x 8 over
 // 32,768: 9.6 us (CTA pairs); 1 x 8: 8.0 us (fours).
@@ -1063,11 +1063,12 @@ __global__ void __launch_bounds__(NT, MINB)
                 ties = S.total != need;
                 if ((uint32_t)tid < m) {
                     const float f = __uint_as_float(values[tid]);
-                    const uint32_t of = CLUSTER ? owner[tid] : S.small_all[tid], rank = of >> 8;
+                    const uint32_t of = CLUSTER ? owner[tid] : S.small_all[tid];
+                    const int rank = (int)(of >> 8);
                     const bool above = f > tf || (!ties && f == tf);
                     if (above || f == tf) {
-                        if (rank == (uint32_t)crank) atomicAdd(above ? &S.wcnt[of & 0xFFu] : &S.weq[of & 0xFFu], 1u);
-                        else if (rank < (uint32_t)crank) atomicAdd(above ? &S.pre_gt : &S.pre_eq, 1u);
+                        if (rank == crank) atomicAdd(above ? &S.wcnt[of & 0xFFu] : &S.weq[of & 0xFFu], 1u);
+                        else if (rank < crank) atomicAdd(above ? &S.pre_gt : &S.pre_eq, 1u);
                     }
                 }
             }

@@ -520,6 +520,19 @@ def test_commit_refuses_a_sequence(inplace):
     assert int(new2[0]) == 21 and st2.status() == 0
 
 
+def test_commit_refuses_other_shapes():
+    st = Step([20], [3], 0, seed=1, masks=[[1, 2, 5]])
+    new = torch.zeros(1, dtype=I32, device="cuda")
+    kv, ki = (torch.zeros((2, st.rows, w), dtype=torch.bfloat16, device="cuda") for w in (D_QK, D_IDX))
+    for bad in (dict(kv=kv[None]), dict(kv=kv.view(-1)), dict(kv=ki), dict(k_idx=kv), dict(kv=kv, k_idx=ki[0]),
+                dict(kv=kv, k_idx=ki.view(1, -1, D_IDX)), dict(kv=kv[:, :, :D_IDX])):
+        with pytest.raises(ValueError):
+            dsa.tree_commit(st.b, st.mask, _dev([2]), new, ws=st.ws, **bad)
+    with pytest.raises(dsa.DsaError):                      # fewer cache rows than the batch spans
+        dsa.tree_commit(st.b, st.mask, _dev([2]), new, kv=kv[0, :-1], ws=st.ws)
+    assert st.status() == 0 and not kv.any() and int(new[0]) == 0
+
+
 # ------------------------------------------------- the step, as it is used --
 
 class Server:
