@@ -1291,6 +1291,13 @@ cudaError_t launch_tree_topk(const BatchDev& bd, const float* scores, int64_t ld
     int csize = 1;
     while (bd.max_ctx > kAloneRow && csize < kMaxCluster && rows * 2 * csize <= num_sms() && bd.max_ctx > kSlice * csize)
         csize *= 2;
+    // Rows that one CTA does not hold take as many as do, unless topk_kernel splits
+    // them itself and there are two of them per SM or nearly (512 rows over 131,000:
+    // 222 us, topk_kernel 904; 256 over 70,000: 55 and 71; 256 over 100,000: 105
+    // and 89).
+    int fit = 1;
+    while (fit < kMaxCluster && bd.max_ctx > (int64_t)kShortRow * fit) fit *= 2;
+    if (fit <= 2 || rows < num_sms() || rows >= 2 * num_sms()) csize = std::max(csize, fit);
     if (csize > 1 && bd.max_ctx <= (int64_t)kShortRow * csize)
         return launch_short<512, 4, 1, true>(bd, scores, ld, mask, k, idx, status, stream, csize);
     if (bd.max_ctx <= kShortRow) {

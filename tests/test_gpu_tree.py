@@ -452,6 +452,36 @@ def test_tree_topk_ranges(c, m, k, kind):
     assert np.array_equal(idx.cpu().numpy(), _topk_ref(st, sc, k))
 
 
+@pytest.mark.parametrize("c,m,k", [([100000, 5000, 70000], [64, 64, 64], 1000), ([400000], [2], 2048),
+                                   ([50000, 100], [64, 64], 7), ([99000] * 5, [62, 64, 1, 64, 64], 2048)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_tree_topk_long(c, m, k, ties):
+    """Rows longer than a CTA holds: clusters of every size, and the kernel that keeps candidates only."""
+    st = Step(c, m, 0, seed=k)
+    ld = (st.max_ctx + 3) // 4 * 4
+    g = torch.Generator().manual_seed(k)
+    sc = torch.randn((st.T, ld), generator=g)
+    sc = sc.mul_(30).round_().div_(30) if ties else sc
+    idx = torch.full((st.T, k), -7, dtype=I32, device="cuda")
+    dsa.tree_topk(st.b, sc.cuda(), st.mask, k, idx, ws=st.ws)
+    assert st.status() == 0
+    rows = [0, 1, st.T // 2, st.T - 1]
+    for r in rows:
+        b = int(np.searchsorted(st.off, r, side="right")) - 1
+        pos = st.seen(b, r - int(st.off[b]))
+        v = sc[r].numpy()[pos]
+        best = np.sort(pos[np.lexsort((pos, -(v + 0.0)))[:k]])
+        assert np.array_equal(idx[r].cpu().numpy(), np.pad(best, (0, k - len(best)), constant_values=-1))
+    # the others against a sort on the device
+    own = torch.tensor([b for b in range(st.B) for _ in range(st.m[b])])
+    for r in range(st.T):
+        b = int(own[r])
+        pos = torch.from_numpy(np.asarray(st.seen(b, r - int(st.off[b])))).cuda()
+        v = sc[r].cuda()[pos] + 0.0
+        best = pos[v.sort(descending=True, stable=True).indices[:k]].sort().values
+        assert torch.equal(idx[r, :len(best)].long(), best.long()) and (idx[r, len(best):] == -1).all()
+
+
 def test_tree_topk_of_a_chain_is_topk():
     st = Step([3000, 12], [7, 20], 0, masks=[[(2 << i) - 1 for i in range(n)] for n in (7, 20)])
     ld = (st.max_ctx + 3) // 4 * 4
