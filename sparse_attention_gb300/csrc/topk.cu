@@ -1224,8 +1224,9 @@ template <int NT, int BATCH, int MINB, bool CLUSTER = false>
 cudaError_t launch_short(const BatchDev& bd, const float* scores, int64_t ld, const uint64_t* mask, int k, int32_t* idx,
                          int32_t* status, cudaStream_t stream, int csize = 1) {
     const size_t smem = (((size_t)bd.max_ctx + csize - 1) / csize + 127) / 128 * 128 * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(topk_short_kernel<NT, BATCH, MINB, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    // the same limit in every call: another thread's may come between this and the launch
+    cudaError_t e = cudaFuncSetAttribute(topk_short_kernel<NT, BATCH, MINB, CLUSTER>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kShortRow * (int)sizeof(float));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(bd.max_q * csize), (unsigned)bd.B);
@@ -1301,7 +1302,8 @@ cudaError_t launch_tree_topk(const BatchDev& bd, const float* scores, int64_t ld
     if (csize > 1 && bd.max_ctx <= (int64_t)kShortRow * csize)
         return launch_short<512, 4, 1, true>(bd, scores, ld, mask, k, idx, status, stream, csize);
     if (bd.max_ctx <= kShortRow) {
-        if (rows >= 2 * num_sms() && bd.max_ctx <= kRowOf256) return launch_short<256, 4, 5>(bd, scores, ld, mask, k, idx, status, stream);
+        if (rows >= 2 * num_sms() && bd.max_ctx <= kRowOf256)
+            return launch_short<256, 4, 5>(bd, scores, ld, mask, k, idx, status, stream);
         return bd.max_ctx <= (few ? kFewRowOf512 : kRowOf512)
                    ? launch_short<512, 4, 3>(bd, scores, ld, mask, k, idx, status, stream)
                    : launch_short<1024, 8, 1>(bd, scores, ld, mask, k, idx, status, stream);

@@ -482,6 +482,38 @@ def test_tree_topk_long(c, m, k, ties):
         assert torch.equal(idx[r, :len(best)].long(), best.long()) and (idx[r, len(best):] == -1).all()
 
 
+def test_tree_topk_from_two_threads():
+    """Calls of two host threads, each with a stream and a workspace: long rows beside short ones."""
+    import threading
+    steps = [Step([20000], [2], 0, seed=1), Step([24000], [2], 0, seed=2)]
+    wanted, jobs, wrong = [], [], []
+    for st in steps:
+        sc = torch.randn((st.T, (st.max_ctx + 3) // 4 * 4), generator=torch.Generator().manual_seed(st.max_ctx)).cuda()
+        idx = torch.empty((st.T, 500), dtype=I32, device="cuda")
+        dsa.tree_topk(st.b, sc, st.mask, 500, idx, ws=st.ws)
+        wanted.append(idx.clone())
+        jobs.append((st, sc, idx))
+    torch.cuda.synchronize()
+
+    def work(n):
+        st, sc, idx = jobs[n]
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(2000):
+                dsa.tree_topk(st.b, sc, st.mask, 500, idx, ws=st.ws, stream=stream)
+            stream.synchronize()
+        except Exception as e:
+            wrong.append(e)
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    for (st, _, idx), w in zip(jobs, wanted):
+        assert st.status() == 0 and torch.equal(idx, w)
+
+
 def test_tree_topk_of_a_chain_is_topk():
     st = Step([3000, 12], [7, 20], 0, masks=[[(2 << i) - 1 for i in range(n)] for n in (7, 20)])
     ld = (st.max_ctx + 3) // 4 * 4
