@@ -372,6 +372,7 @@ cudaError_t launch_step_tables(const BatchDev& bd, const PagesDev& pg, const int
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     count_launches(1);
     cudaLaunchConfig_t cfg = {};
+    if (items == 0) return e;                        // no rows and no pages
     cfg.gridDim = dim3((unsigned)std::min<int64_t>((items + 255) / 256, 8 * num_sms()));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;

@@ -167,6 +167,25 @@ def test_tables_bad_parents_and_pages():
     assert t.slots[:2].tolist() == [-1, -1] and (t.slots[2:] >= 0).all()
 
 
+@pytest.mark.parametrize("B", [3, 300])
+@pytest.mark.parametrize("page", [0, 16])
+def test_tables_of_a_step_without_tokens(B, page):
+    q_off, ctx = torch.full((B + 1,), 9, dtype=I32, device="cuda"), torch.zeros(B, dtype=I32, device="cuda")
+    old, zero = torch.arange(B, dtype=I32, device="cuda") % 7, torch.zeros(B, dtype=I32, device="cuda")
+    b = dsa.make_batch(q_off, ctx, 4, 16, 16, total_q=0)
+    none = torch.empty(0, dtype=I32, device="cuda")
+    kw = {}
+    if page:
+        held, span = torch.ones(B, dtype=I32, device="cuda"), _dev([0, B])
+        kw = dict(pages=dsa.make_pages(torch.arange(B, dtype=I32, device="cuda").view(B, 1), page, B), n_pages_old=held,
+                  n_pages=held.clone(), free_pages=torch.arange(B, dtype=I32, device="cuda"), free_range=span,
+                  free_range_out=span.clone())
+    ws = dsa.tree_workspace(b)
+    dsa.step_tables(b, zero, old, none, none, ws=ws, **kw)
+    assert dsa.read_device_status(ws) == 0
+    assert not q_off.any() and torch.equal(ctx, old)
+
+
 # ------------------------------------------------------------------ append --
 
 @pytest.mark.parametrize("T,wide", [(1, 0), (7, 8), (129, 2048), (4001, 24)])
