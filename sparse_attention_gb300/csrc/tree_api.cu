@@ -144,7 +144,8 @@ dsa_status dsa_tree_commit(const dsa_batch* batch, const dsa_pages* pages, const
     if (layers < 1 || layers > 65535 || cache_rows < 0) return DSA_ERR_INVALID_ARG;
     const int64_t rows = pages ? (int64_t)pages->pool_pages * pages->page_size : batch->batch * batch->cache_stride;
     if (pages ? cache_rows != rows : cache_rows < rows) return DSA_ERR_INVALID_ARG;
-    if (!given(mask, 8) || !given(accepted, 4) || !given(ctx_new, 4)) return DSA_ERR_INVALID_ARG;
+    if (!given(accepted, 4) || !given(ctx_new, 4)) return DSA_ERR_INVALID_ARG;
+    if (batch->total_q > 0 && !given(mask, 8)) return DSA_ERR_INVALID_ARG;      // no row: no node to accept
     if (!aligned(kv, 16) || !aligned(k_idx, 16)) return DSA_ERR_INVALID_ARG;
     return cuda_status(launch_tree_commit(to_dev(batch), to_dev(pages), mask, accepted, layers, cache_rows, kv, k_idx,
                                           ctx_new, static_cast<int32_t*>(scratch_of(ws)), static_cast<int32_t*>(ws),

@@ -614,6 +614,28 @@ def test_commit_refuses_other_shapes():
     assert st.status() == 0 and not kv.any() and int(new[0]) == 0
 
 
+@pytest.mark.parametrize("inplace", [False, True])
+def test_calls_of_a_step_without_tokens(inplace):
+    """No new token in any sequence: every call returns, and the lengths stay."""
+    ctx = _dev([5, 0, 30])
+    b = dsa.make_batch(torch.zeros(4, dtype=I32, device="cuda"), ctx, 4, 40, 40, total_q=0)
+    ws = dsa.tree_workspace(b)
+    kv = torch.randn((120, D_QK), device="cuda").to(torch.bfloat16)
+    was = kv.clone()
+
+    def none(*shape, dtype=torch.bfloat16):
+        return torch.empty((0,) + shape, dtype=dtype, device="cuda")
+    mask = none(dtype=torch.int64)
+    dsa.latent_append(none(D_QK), torch.ones(D_V, device="cuda"), 1e-5, torch.ones((40, 64), device="cuda"),
+                      torch.ones((40, 64), device="cuda"), none(dtype=I32), none(dtype=I32), kv, ws)
+    dsa.tree_mla_fwd(b, none(64, D_QK), kv, mask, 0.06, none(64, D_V), none(64, dtype=torch.float32), ws=ws)
+    dsa.tree_topk(b, none(40, dtype=torch.float32), mask, 8, none(8, dtype=I32), ws=ws)
+    new = ctx if inplace else torch.zeros(3, dtype=I32, device="cuda")
+    dsa.tree_commit(b, mask, _dev([-1, -1, -1]), new, kv=kv, ws=ws)
+    assert dsa.read_device_status(ws) == 0
+    assert new.tolist() == [5, 0, 30] and torch.equal(kv, was)
+
+
 # ------------------------------------------------- the step, as it is used --
 
 class Server:
