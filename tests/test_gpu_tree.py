@@ -501,6 +501,50 @@ def test_tree_topk_long(c, m, k, ties):
         assert torch.equal(idx[r, :len(best)].long(), best.long()) and (idx[r, len(best):] == -1).all()
 
 
+@pytest.mark.parametrize("B,longest", [(3, 2500), (40, 2500), (3, 30000)])
+def test_tree_topk_right_behind_the_tables(B, longest):
+    """Lengths and masks that the launch just before writes, changing from call to call."""
+    rng = np.random.default_rng(B)
+    m, T, k = 8, 8 * B, 100
+    q_off, ctx = torch.zeros(B + 1, dtype=I32, device="cuda"), torch.zeros(B, dtype=I32, device="cuda")
+    b = dsa.make_batch(q_off, ctx, m, longest + m, longest + m, total_q=T)
+    ws = dsa.tree_workspace(b)
+    slots, pos = (torch.zeros(T, dtype=I32, device="cuda") for _ in range(2))
+    mask = torch.zeros(T, dtype=torch.int64, device="cuda")
+    sc = torch.randn((T, (longest + m + 3) // 4 * 4), device="cuda")
+    steps = []
+    for _ in range(6):
+        n = rng.integers(0, m + 1, B)
+        par = np.full(T, -1, np.int32)
+        at = 0
+        for x in n:
+            for i in range(x):
+                par[at + i] = rng.integers(-1, i) if i else -1
+            at += x
+        steps.append((_dev(n.tolist()), _dev(rng.integers(0, longest + 1, B).tolist()), _dev(par.tolist())))
+
+    def run(s, idx):
+        dsa.step_tables(b, s[0], s[1], slots, pos, mask, parent=s[2], ws=ws)
+        dsa.tree_topk(b, sc, mask, k, idx, ws=ws)
+    want = []
+    for s in steps:
+        idx = torch.full((T, k), -7, dtype=I32, device="cuda")
+        torch.cuda.synchronize()
+        dsa.step_tables(b, s[0], s[1], slots, pos, mask, parent=s[2], ws=ws)
+        torch.cuda.synchronize()
+        dsa.tree_topk(b, sc, mask, k, idx, ws=ws)
+        torch.cuda.synchronize()
+        want.append(idx)
+    order = rng.integers(0, len(steps), 300)
+    got = torch.full((len(order), T, k), -7, dtype=I32, device="cuda")
+    torch.cuda.synchronize()
+    for x, s in enumerate(order):
+        run(steps[s], got[x])
+    assert dsa.read_device_status(ws) == 0
+    for x, s in enumerate(order):
+        assert torch.equal(got[x], want[s]), x
+
+
 def test_tree_topk_from_two_threads():
     """Calls of two host threads, each with a stream and a workspace: long rows beside short ones."""
     import threading
