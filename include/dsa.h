@@ -429,8 +429,10 @@ DSA_API dsa_status dsa_latent_append(int32_t total_q, const uint16_t* x, int64_t
  *   q, kv, out, lse, sm_scale as dsa_sparse_mla_fwd (kv paged or contiguous)
  * A row that sees nothing gets out = 0 and lse = -inf.  Cache rows past
  * ctx_len and new rows that a row does not see do not reach its results,
- * whatever they hold; a row that sees a new row with a NaN or infinity gets
- * NaN.  A block-table entry outside [0, pool_pages) among the sequence's
+ * whatever they hold; a row that sees a new row with a NaN or infinity in any
+ * of its 576 values gets NaN throughout, out and lse.  (Those of a committed
+ * row follow the arithmetic: a weight of 0 times an infinity is NaN.)
+ * A block-table entry outside [0, pool_pages) among the sequence's
  * pages latches DSA_ERR_BAD_INDEX and leaves the sequence's rows unwritten.
  * max_q > 64 or total_q >= 2^25 -> DSA_ERR_UNSUPPORTED.
  * fp32 scores, softmax statistics and sums; the softmax weights are rounded

@@ -31,8 +31,10 @@
 // pair's share of the work and publishes its segments.  Tiles that reach
 // past the committed rows go through the fix-up warp, which zeroes V rows past
 // the sequence (a page's leftovers may hold anything, and 0 * NaN is NaN) and
-// values of drafted rows that are not finite: a row that sees such a row gets
-// NaN through its score, the others nothing.
+// values of drafted rows that are not finite.  A row that does not see such a
+// row gets nothing of it; one that does gets NaN through its score, which is
+// NaN or infinite: +inf by the subtraction of the maximum, -inf (an infinity
+// against the query's sign) by a look at the row itself.
 //
 // Work: the items' tiles, plus kItemCost tiles per item for its start and
 // end, laid end to end and cut into equal shares, one per pair (after whole
@@ -101,6 +103,7 @@ struct Smem {
     int32_t longest[kThreads / 32];
     float xch[2][128];
     int32_t bad[4];
+    uint32_t lost[4];            // softmax warps: 1 + the last segment with a score of -inf past the committed rows
     uint32_t tmem;
 };
 static_assert(sizeof(Smem) <= 232448, "one CTA's shared memory");
@@ -413,6 +416,32 @@ __device__ __forceinline__ int32_t box_row(const Args& a, const Seg& s, int32_t 
 
 __device__ __forceinline__ bool past_committed(const Seg& s, int32_t t) { return (t + 1) * kTile > s.c; }
 
+// Whether one of the new rows `rows` in the segment's tiles holds a NaN or an
+// infinity; all lanes.  Called when a row past the committed ones scored -inf,
+// which is seldom; a call, since the code of it inside the softmax role costs
+// long calls 1-2 %, out of the way 0.5 % (16 trees of 64 over 8,192 rows).
+__device__ __noinline__ bool any_not_finite(const Args& a, const Seg& s, uint64_t rows) {
+#pragma unroll 1
+    for (; rows; rows &= rows - 1u) {
+        const int32_t pos = s.c + __ffsll((long long)rows) - 1;
+        if (pos < s.t0 * kTile || pos >= s.t1 * kTile) continue;
+        const int32_t at = cache_row(a.bd, a.pg, s.b, pos);
+        if (at < 0) continue;                    // a bad page: latched, and nothing is written
+        const uint4* row = reinterpret_cast<const uint4*>(a.kv + (int64_t)at * kDQK);
+        bool hit = false;
+#pragma unroll 1
+        for (int k = (int)lane_id(); k < kDQK / 8; k += 32) {
+            const uint4 v = row[k];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                hit = hit || (w[q] & 0x7F80u) == 0x7F80u || (w[q] & 0x7F800000u) == 0x7F800000u;
+        }
+        if (__any_sync(0xffffffffu, hit)) return true;
+    }
+    return false;
+}
+
 // kKRows, kVRows: positions of a K box (of one chunk, or of a stage's three)
 // and of a V box (of two).  Pages of 64 rows and more, and contiguous caches:
 // boxes of 64; pages of 32: of 32; pages of 16: K boxes of 8 rows x 3 chunks,
@@ -458,6 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         fence_mbar_init();
     }
+    if (tid < 4) S.lost[tid] = 0u;
     if (warp == 1) tmem_alloc_pair(smem_u32(&S.tmem), 512);
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&tm_q);
@@ -763,6 +793,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int32_t d = s.c - (t * kTile + 64 * half);     // committed columns of this thread's 64
                     uint64_t vis = d >= 64 ? ~0ull : d > 0 ? (1ull << d) - 1u : 0u;
                     vis |= d >= 64 ? 0u : d >= 0 ? bits << d : d > -64 ? bits >> -d : 0u;
+                    float least = INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) least = fminf(least, __uint_as_float(r[k >> 5][k & 31]));
+                    if (least == -INFINITY) *reinterpret_cast<volatile uint32_t*>(&S.lost[warp - 4]) = seg + 1;
 #pragma unroll
                     for (int k = 0; k < 64; ++k)
                         if (!((vis >> k) & 1u)) r[k >> 5][k & 31] = 0xFF800000u;
@@ -816,6 +850,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const bool bad = *reinterpret_cast<volatile int32_t*>(&S.bad[seg & 3]) != 0;
             if (mine) {
+                __syncwarp();
+                if (*reinterpret_cast<volatile uint32_t*>(&S.lost[warp - 4]) == seg + 1 && any_not_finite(a, s, bits))
+                    l = NAN;
                 l += exchange(l);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const float ls = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
