@@ -277,29 +277,35 @@ __device__ bool plan_rounds(const Args& a, Smem& S, const SeqInfo& q, int64_t un
     per[tid] = (q.ctx + kTile - 1) / kTile + kItemCost;
     if (tid == 0) first[kThreads] = total;
     __syncthreads();
-    // thread k: what the rounds give pair k; one round less if some pair gets
-    // a quarter more than its part of all (up to there the saved reads are worth
-    // more: 24 ragged trees of up to 13 over 7,001 rows 119 -> 113 us)
-    int rounds = total / pairs;
-    int64_t load = 0, last = 0;
-    if (tid < pairs) {
+    // thread k: what the rounds give pair k, which takes as many of them as
+    // leave it no more than a quarter above its part of all (up to there the
+    // saved reads are worth more: 24 ragged trees of up to 13 over 7,001 rows
+    // 119 -> 113 us); all pairs take as many as the one that takes fewest
+    const int64_t most = part + part / 4;
+    auto given_by = [&](int n, int64_t& load) -> int {     // the rounds of n that fit, and their load
+        load = 0;
         int b = 0, top = a.bd.B;
         while (b + 1 < top) {                    // the sequence of item tid
             const int mid = (b + top) >> 1;
             if (first[mid] <= tid) b = mid;
             else top = mid;
         }
-        for (int r = 0; r < rounds; ++r) {
+        for (int r = 0; r < n; ++r) {
             const int32_t item = r * pairs + tid;
             while (first[b + 1] <= item) ++b;
-            last = per[b];
-            load += last;
+            if (load + per[b] > most) return r;
+            load += per[b];
         }
-    }
-    if (__syncthreads_or(tid < pairs && load > part + part / 4)) {
-        if (--rounds == 0) return false;
-        load -= last;
-    }
+        return n;
+    };
+    int64_t load = 0;
+    int rounds = total / pairs;
+    const int fit = __reduce_min_sync(0xffffffffu, tid < pairs ? given_by(rounds, load) : rounds);
+    if (lane == 0) sums[32 + warp] = fit;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) rounds = min(rounds, sums[32 + w]);
+    if (rounds == 0) return false;
+    if (rounds < total / pairs && tid < pairs) given_by(rounds, load);
     // shares of the rest, one behind the other
     if (tid < kMaxPairs) {
         // one unit at least, so that no pair inside a cut item is without a piece

@@ -1,0 +1,143 @@
+"""Tree attention over caches beyond what L2 keeps, where whole items (a pair
+of new rows of a sequence) go round the CTA pairs before the rest is cut into
+shares.  That takes more than 48 MiB of rows in sequences of several items, as
+many items as pairs, and 48 units (tiles and 3 an item) a pair."""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_gb300 as dsa
+from tree_case import D_QK, D_V, H, SCALE, Step, check_attention
+
+pytestmark = pytest.mark.gpu
+I16 = torch.int16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from sparse_attention_gb300 import build as B
+    B.build()
+    dsa.load_library()
+
+
+def _pairs():
+    return torch.cuda.get_device_properties(0).multi_processor_count // 2
+
+
+def _inputs(st, seed):
+    """q and caches made on the device; rows of no sequence hold NaN."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randn((st.T, H, D_QK), generator=g, device="cuda").to(torch.bfloat16)
+    kv = torch.randn((st.rows, D_QK), generator=g, device="cuda").to(torch.bfloat16)
+    used = np.zeros(st.rows, bool)
+    for b in range(st.B):
+        used[st.row(b, np.arange(st.L[b]))] = True
+    kv[torch.from_numpy(~used).cuda()] = float("nan")
+    return q, kv
+
+
+def _sample(st, rng, n=12):
+    return set(rng.choice(st.T, min(n, st.T), replace=False).tolist()) | {0, st.T - 1}
+
+
+def _equal(seqs, n, ctx):
+    return [ctx] * seqs, [n] * seqs
+
+
+def _ragged(seqs, rng):
+    c, m = rng.integers(1000, 7000, seqs), rng.integers(0, 14, seqs)
+    m[::7] = 0
+    return c.tolist(), m.tolist()
+
+
+def _steps():
+    """19 x 4 items of 35 units, then 10 x 4 of 19 and 9 x 4 of 97: on 76 pairs the second round would
+    leave some pairs with 132 units of 91 on average, so the first is the last."""
+    return [4000] * 19 + [2000] * 10 + [12000] * 9, [8] * 38
+
+
+CASES = {
+    "equal": lambda rng: _equal(20, 16, 4000),              # 160 items: two rounds on 76 pairs, 8 left over
+    "no_rest": lambda rng: _equal(19, 16, 4000),            # 152 items: two rounds and nothing left
+    "odd": lambda rng: _equal(31, 5, 5003),                 # 93 items, each third one with a single row
+    "ragged": lambda rng: _ragged(60, rng),
+    "fewer": lambda rng: _steps(),
+    "long_first": lambda rng: ([60000] + [4000] * 20, [2] + [16] * 20),
+    "long_last": lambda rng: ([4000] * 20 + [60000], [16] * 20 + [3]),
+    "b256": lambda rng: (rng.integers(1500, 2500, 256).tolist(), [4] * 256),     # the most sequences that take rounds
+    "b257": lambda rng: (rng.integers(1500, 2500, 257).tolist(), [4] * 257),     # and one more
+}
+
+
+@pytest.mark.parametrize("page", [0, 16, 64])
+@pytest.mark.parametrize("name", list(CASES))
+def test_results(name, page):
+    rng = np.random.default_rng(len(name) + page)
+    c, m = CASES[name](rng)
+    st = Step(c, m, page, seed=page)
+    q, kv = _inputs(st, 3)
+    out, lse = st.attention(q, kv)
+    assert st.status() == 0
+    # nothing is left out: every row was written, and every head of it
+    assert not (out == 7).all(-1).any() and not (lse == 7).any() and not torch.isnan(out).any()
+    again = st.attention(q, kv)
+    assert torch.equal(out.view(I16), again[0].view(I16)) and torch.equal(lse, again[1])
+    check_attention(st, q.cpu(), kv.cpu(), out, lse, _sample(st, rng))
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_bad_page_in_a_whole_item(page):
+    """The rows of its sequence stay as they were, the others get their results."""
+    rng = np.random.default_rng(page)
+    st = Step(*_equal(20, 16, 4000), page, seed=1)
+    q, kv = _inputs(st, 4)
+    st.pages.block_table[3, 40] = st.pool
+    out, lse = st.attention(q, kv)
+    assert st.status() == 7
+    hurt = slice(3 * 16, 4 * 16)
+    assert (out[hurt] == 7).all() and (lse[hurt] == 7).all()
+    check_attention(st, q.cpu(), kv.cpu(), out, lse, _sample(st, rng) - set(range(48, 64)))
+
+
+def test_masks_and_unwritten_rows():
+    """Rows that see nothing new, and packed rows behind the last sequence."""
+    masks = [[0] * 16 if b % 3 else [(2 << i) - 1 for i in range(16)] for b in range(20)]
+    st = Step(*_equal(20, 16, 4000), 64, seed=2, masks=masks)
+    q, kv = _inputs(st, 5)
+    st.b.q_off[20] = st.T - 16                       # the last sequence has no new row
+    out, lse = st.attention(q, kv)
+    assert st.status() == 0
+    assert (out[-16:] == 7).all() and (lse[-16:] == 7).all()
+    check_attention(st, q.cpu(), kv.cpu(), out, lse, {0, 15, 16, 31, 200, st.T - 17})
+
+
+def _time(st, q, kv):
+    out = torch.empty((st.T, H, D_V), dtype=torch.bfloat16, device="cuda")
+    best = 1e9
+    for _ in range(8):
+        e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        torch.cuda.synchronize()
+        e[0].record()
+        dsa.tree_mla_fwd(st.b, q, kv, st.mask, SCALE, out, pages=st.pages, ws=st.ws)
+        e[1].record()
+        torch.cuda.synchronize()
+        best = min(best, e[0].elapsed_time(e[1]))
+    return best
+
+
+@pytest.mark.parametrize("long,n,seqs,tree,ctx", [(100000, 2, 24, 16, 4000), (32768, 2, 24, 16, 4000),
+                                                  (100000, 16, 24, 16, 4000), (65536, 2, 40, 8, 8192)])
+def test_a_long_sequence_ahead_of_the_others(long, n, seqs, tree, ctx):
+    """Sequences in another order are the same work: a long one ahead of the others does not stay whole on
+    one pair (2.8 to 7.9 times the even share of these) and takes no more than half as long again."""
+    took = []
+    for ahead in (True, False):
+        c, m = [ctx] * seqs, [tree] * seqs
+        c.insert(0 if ahead else seqs, long)
+        m.insert(0 if ahead else seqs, n)
+        st = Step(c, m, 64, seed=1)
+        q, kv = _inputs(st, 6)
+        took.append(_time(st, q, kv))
+        assert st.status() == 0
+    assert took[0] <= 1.5 * took[1], took
