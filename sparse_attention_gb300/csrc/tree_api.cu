@@ -14,13 +14,19 @@ namespace {
 inline bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline bool given(const void* p, unsigned n = 16) { return p && aligned(p, n); }
 
-// The batch with its caches: contiguous, or paged (then the cache stride only
-// bounds max_ctx).
-dsa_status check(const dsa_batch* b, const dsa_pages* p) {
+// The batch alone, for a call that touches no cache.
+dsa_status check(const dsa_batch* b) {
     if (!b || b->batch < 1 || b->batch > 65535 || b->total_q < 0 || b->max_q < 0 || b->max_ctx < 0)
         return DSA_ERR_INVALID_ARG;
     if (b->cache_stride < b->max_ctx || !given(b->q_off, 4) || !given(b->ctx_len, 4)) return DSA_ERR_INVALID_ARG;
-    if (b->max_q > (1 << 19) || b->total_q >= (1 << 26)) return DSA_ERR_UNSUPPORTED;
+    return b->max_q > (1 << 19) || b->total_q >= (1 << 26) ? DSA_ERR_UNSUPPORTED : DSA_OK;
+}
+
+// The batch with its caches: contiguous, or paged (then the cache stride only
+// bounds max_ctx).
+dsa_status check(const dsa_batch* b, const dsa_pages* p) {
+    const dsa_status st = check(b);
+    if (st != DSA_OK) return st;
     if (!p) return b->cache_stride < (int64_t(1) << 31) / b->batch ? DSA_OK : DSA_ERR_UNSUPPORTED;
     if (p->page_size < 16 || p->page_size > 1024 || (p->page_size & (p->page_size - 1)) != 0) return DSA_ERR_INVALID_ARG;
     if (p->pool_pages < 1 || p->max_pages < 1 || (int64_t)p->max_pages * p->page_size < b->max_ctx ||
@@ -124,7 +130,7 @@ dsa_status dsa_tree_mla_fwd(const dsa_batch* batch, const dsa_pages* pages, cons
 
 dsa_status dsa_tree_topk(const dsa_batch* batch, const float* scores, int64_t ld, const uint64_t* mask, int k,
                          int32_t* idx, void* ws, size_t ws_bytes, void* stream) {
-    dsa_status st = check(batch, nullptr);
+    const dsa_status st = check(batch);
     if (st != DSA_OK) return st;
     if (k < 1 || k > kMaxTopk) return DSA_ERR_INVALID_ARG;
     if (batch->max_q > DSA_MAX_TREE) return DSA_ERR_UNSUPPORTED;

@@ -127,3 +127,18 @@ def test_binding_refuses_tensors(lib):
     with pytest.raises(ValueError):
         dsa._typed("t", t[::2], torch.int32, 2, cpu)
     assert dsa._typed("t", None, torch.int32, 5, cpu) is None
+
+
+def test_topk_of_batches_whose_contiguous_cache_would_be_too_large(lib):
+    """The call reads no cache: sequences times stride has no limit there, as in paged calls."""
+    def topk(scores=P, **kw):
+        b = _batch(B=16384, max_ctx=131072, stride=131072, **kw)
+        return lib.dsa_tree_topk(ctypes.byref(b), scores, 131072, P, 8, P, WS, 256, None)
+    g = _pages(width=8192)
+    b = _batch(B=16384, max_ctx=131072, stride=131072, total_q=0)
+    assert lib.dsa_tree_mla_fwd(ctypes.byref(b), ctypes.byref(g), P, P, P, ctypes.c_float(0.1), P, None, WS,
+                                _ws(lib, b), None) == 0
+    assert topk(total_q=0) == 0 and topk(scores=None) == 1
+    assert topk(max_q=65) == 2 and topk(total_q=1 << 26) == 2
+    # attention over contiguous caches of that size stays refused
+    assert _attn(lib, b) == 2
