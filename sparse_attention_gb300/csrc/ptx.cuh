@@ -79,7 +79,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
 // The same in few instructions, for kernels with many waits: unrolled 64
 // times, the polling loop takes 4 KB at every call, and a short launch fetches
 // its code from L2 as it goes (four polls in a row: a call's 1-3 % over one).
-__device__ __forceinline__ bool mbar_wait_rolled(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_rolled(uint32_t bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
 #pragma unroll 1
@@ -87,7 +87,7 @@ __device__ __forceinline__ bool mbar_wait_rolled(uint32_t bar, uint32_t parity) 
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 15u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) return false;
+        if ((i & 15u) == 0 && globaltimer_ns() - t0 > limit_ns) return false;
     }
 }
 

@@ -1,5 +1,6 @@
 // selftest.cu -- exercises the bounded-wait path of the kernels without a
-// fault: one thread waits on an mbarrier phase that nothing completes.
+// fault: one thread waits on an mbarrier phase that nothing completes, with
+// each of the two forms of the wait that the kernels use.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -11,8 +12,10 @@ __global__ void wait_timeout_kernel(uint64_t limit_ns, int32_t* status) {
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&bar), 1);
         fence_mbar_init();
-        // nobody arrives: the wait gives up after limit_ns
-        if (!mbar_wait_for(smem_u32(&bar), 0, limit_ns)) latch_status(status, DSA_ERR_TIMEOUT);
+        // nobody arrives: either wait gives up after limit_ns
+        const bool unrolled = mbar_wait_for(smem_u32(&bar), 0, limit_ns);
+        const bool rolled = mbar_wait_rolled(smem_u32(&bar), 0, limit_ns);
+        latch_status(status, !unrolled && !rolled ? DSA_ERR_TIMEOUT : DSA_ERR_INTERNAL);
     }
 }
 
