@@ -380,8 +380,10 @@ def _typed(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, numel: int,
     raise ValueError(f"{name}: {numel} elements expected, got {t.numel()}")
 
 
-def _here(ws: torch.Tensor, stream) -> int:
+def _here(where: str, ws: Optional[torch.Tensor], stream) -> int:
     """The device of a call: the workspace's, which has to be the current one and the stream's."""
+    if ws is None:
+        raise DsaError(3, where)
     dev = ws.get_device()
     if dev < 0 or dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
         raise ValueError(f"workspace on {ws.device}: expected on the current CUDA device, and the stream's")
@@ -409,7 +411,7 @@ def step_tables(batch: Batch, n_new, ctx_old, slots, positions, mask=None, paren
     """q_off and ctx_len of `batch`, block table, slot map, positions and
     masks of a step from its lengths (see dsa_step_tables).  mask: int64
     tensor holding the 64 bits."""
-    dev, i32 = _here(ws, stream), torch.int32
+    dev, i32 = _here("dsa_step_tables", ws, stream), torch.int32
     c = batch.c
     pg, _ = _paged(batch, pages, dev)
     _check(load_library().dsa_step_tables(
@@ -427,7 +429,7 @@ def step_tables(batch: Batch, n_new, ctx_old, slots, positions, mask=None, paren
 def latent_append(x, gamma, eps: float, cos, sin, positions, slots, kv, ws, stream=None):
     """RMSNorm | RoPE of the new tokens' compressed rows x [total_q, >= 576]
     (rows may be strided), written to kv at slots (see dsa_latent_append)."""
-    dev, f32, i32 = _here(ws, stream), torch.float32, torch.int32
+    dev, f32, i32 = _here("dsa_latent_append", ws, stream), torch.float32, torch.int32
     if x.dtype is not torch.bfloat16 or x.get_device() != dev:
         raise TypeError(f"x: bf16 tensor on cuda:{dev} expected")
     if x.dim() != 2 or x.shape[1] != D_QK or x.stride(1) != 1:
@@ -448,7 +450,7 @@ def tree_mla_fwd(batch: Batch, q, kv, mask, sm_scale: float, out, lse=None, page
                  stream=None):
     """Attention of every new row over the committed rows and the new rows of
     its mask (see dsa_tree_mla_fwd)."""
-    dev, bf16 = _here(ws, stream), torch.bfloat16
+    dev, bf16 = _here("dsa_tree_mla_fwd", ws, stream), torch.bfloat16
     c = batch.c
     pg, rows = _paged(batch, pages, dev)
     _check(load_library().dsa_tree_mla_fwd(
@@ -461,7 +463,7 @@ def tree_mla_fwd(batch: Batch, q, kv, mask, sm_scale: float, out, lse=None, page
 
 def tree_topk(batch: Batch, scores, mask, k: int, idx, ld: Optional[int] = None, ws=None, stream=None):
     """Causal top-k among what every new row sees (see dsa_tree_topk)."""
-    dev = _here(ws, stream)
+    dev = _here("dsa_tree_topk", ws, stream)
     c = batch.c
     ld = int(ld if ld is not None else scores.shape[-1])
     _paged(batch, None, dev)
@@ -486,7 +488,7 @@ def tree_commit(batch: Batch, mask, accepted, ctx_new, kv=None, k_idx=None, page
     """Moves the accepted paths' rows behind the committed ones in every layer
     of kv [layers, rows, 576] and k_idx [layers, rows, 128] (one layer without
     the first dimension; see dsa_tree_commit)."""
-    dev, bf16 = _here(ws, stream), torch.bfloat16
+    dev, bf16 = _here("dsa_tree_commit", ws, stream), torch.bfloat16
     c = batch.c
     pg, need = _paged(batch, pages, dev)
     layers, rows = _layered("kv", kv, D_QK) if kv is not None else (1, need)

@@ -142,3 +142,14 @@ def test_topk_of_batches_whose_contiguous_cache_would_be_too_large(lib):
     assert topk(max_q=65) == 2 and topk(total_q=1 << 26) == 2
     # attention over contiguous caches of that size stays refused
     assert _attn(lib, b) == 2
+
+
+def test_binding_without_a_workspace(lib):
+    """DSA_ERR_WORKSPACE, as from the calls of the path."""
+    import sparse_attention_gb300 as dsa
+    calls = dict(step_tables=[None] * 5, latent_append=[None, None, 1e-5] + [None] * 5,
+                 tree_mla_fwd=[None] * 4 + [0.1, None], tree_topk=[None, None, None, 8, None], tree_commit=[None] * 4)
+    for name, args in calls.items():
+        with pytest.raises(dsa.DsaError, match=f"dsa_{name}: DSA_ERR_WORKSPACE") as e:
+            getattr(dsa, name)(*args, ws=None)
+        assert e.value.code == 3
