@@ -366,7 +366,11 @@ typedef struct dsa_pages {
 } dsa_pages;
 
 /* Bytes of workspace that the calls of this section need for `batch` (the
- * largest of them); NULL: dsa_latent_append alone (256).  Host only. */
+ * largest of them, dsa_tree_mla_fwd's); NULL: dsa_latent_append alone (256).
+ * Host only.  Less will do without that call: dsa_step_tables and
+ * dsa_tree_commit need 264 + 8 * batch bytes, dsa_latent_append and
+ * dsa_tree_topk 256, so a workspace of dsa_workspace_size serves a tree that
+ * is verified by the indexer and the sparse attention. */
 DSA_API dsa_status dsa_tree_workspace_size(const dsa_batch* batch, size_t* bytes);
 
 /* The tables of a step, on the device, from the sequences' lengths:

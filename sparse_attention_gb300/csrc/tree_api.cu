@@ -50,14 +50,13 @@ PagesDev to_dev(const dsa_pages* p) {
 }
 
 // The calls of a step run one after another in their stream, so their scratch
-// overlaps behind the status header.
-size_t ws_bytes_needed(const dsa_batch* b) {
-    const size_t scratch = std::max(step_tables_bytes(b->batch), tree_mla_scratch_bytes(to_dev(b)));
-    return (kWsHeaderBytes + scratch + 255) / 256 * 256;
-}
+// overlaps behind the status header; each asks for its own.
+size_t with_header(size_t scratch) { return kWsHeaderBytes + scratch; }
+size_t tables_ws(const dsa_batch* b) { return with_header(step_tables_bytes(b->batch)); }
+size_t attention_ws(const dsa_batch* b) { return with_header(tree_mla_scratch_bytes(to_dev(b))); }
 
-dsa_status check_ws(const dsa_batch* b, const void* ws, size_t bytes) {
-    return given(ws) && bytes >= ws_bytes_needed(b) ? DSA_OK : DSA_ERR_WORKSPACE;
+dsa_status check_ws(const void* ws, size_t bytes, size_t needed) {
+    return given(ws) && bytes >= needed ? DSA_OK : DSA_ERR_WORKSPACE;
 }
 
 void* scratch_of(void* ws) { return static_cast<uint8_t*>(ws) + kWsHeaderBytes; }
@@ -69,12 +68,12 @@ extern "C" {
 dsa_status dsa_tree_workspace_size(const dsa_batch* batch, size_t* bytes) {
     if (!bytes) return DSA_ERR_INVALID_ARG;
     if (!batch) {
-        *bytes = kWsHeaderBytes;
+        *bytes = with_header(0);
         return DSA_OK;
     }
     if (batch->batch < 1 || batch->batch > 65535 || batch->total_q < 0 || batch->max_q < 0 || batch->max_ctx < 0)
         return DSA_ERR_INVALID_ARG;
-    *bytes = ws_bytes_needed(batch);
+    *bytes = (std::max(tables_ws(batch), attention_ws(batch)) + 255) / 256 * 256;
     return DSA_OK;
 }
 
@@ -84,7 +83,7 @@ dsa_status dsa_step_tables(const dsa_batch* batch, const dsa_pages* pages, const
                            int32_t* free_range_out, int32_t* slots, int32_t* positions, uint64_t* mask, void* ws,
                            size_t ws_bytes, void* stream) {
     dsa_status st = check(batch, pages);
-    if (st != DSA_OK || (st = check_ws(batch, ws, ws_bytes)) != DSA_OK) return st;
+    if (st != DSA_OK || (st = check_ws(ws, ws_bytes, tables_ws(batch))) != DSA_OK) return st;
     if (!given(n_new, 4) || !given(ctx_old, 4) || !aligned(parent, 4) || !aligned(mask, 8)) return DSA_ERR_INVALID_ARG;
     if (batch->total_q > 0 && (!given(slots, 4) || !given(positions, 4))) return DSA_ERR_INVALID_ARG;
     if (pages && (!given(n_pages_old, 4) || !given(n_pages, 4) || !given(free_pages, 4) || !given(free_range, 4) ||
@@ -101,7 +100,7 @@ dsa_status dsa_latent_append(int32_t total_q, const uint16_t* x, int64_t x_strid
                              const int32_t* slots, int64_t cache_rows, uint16_t* kv, void* ws, size_t ws_bytes,
                              void* stream) {
     if (total_q < 0 || total_q >= (1 << 26)) return DSA_ERR_INVALID_ARG;
-    if (!given(ws) || ws_bytes < kWsHeaderBytes) return DSA_ERR_WORKSPACE;
+    if (check_ws(ws, ws_bytes, with_header(0)) != DSA_OK) return DSA_ERR_WORKSPACE;
     if (total_q == 0) return DSA_OK;
     if (x_stride < kDQK || x_stride % 8 != 0 || table_rows < 0 || cache_rows < 0) return DSA_ERR_INVALID_ARG;
     if (!given(x) || !given(gamma) || !given(cos_t) || !given(sin_t) || !given(positions, 4) || !given(slots, 4) ||
@@ -120,7 +119,7 @@ dsa_status dsa_tree_mla_fwd(const dsa_batch* batch, const dsa_pages* pages, cons
     if (st != DSA_OK) return st;
     if (batch->max_q > DSA_MAX_TREE) return DSA_ERR_UNSUPPORTED;
     if (batch->total_q >= (1 << 25)) return DSA_ERR_UNSUPPORTED;     // 64 query rows each, in int32 TMA coordinates
-    if ((st = check_ws(batch, ws, ws_bytes)) != DSA_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, attention_ws(batch))) != DSA_OK) return st;
     if (batch->total_q == 0 || batch->max_q == 0) return DSA_OK;
     if (!given(q) || !given(kv) || !given(mask, 8) || !given(out) || !aligned(lse, 16)) return DSA_ERR_INVALID_ARG;
     if (!(sm_scale > 0.f) || sm_scale == INFINITY) return DSA_ERR_INVALID_ARG;
@@ -134,7 +133,7 @@ dsa_status dsa_tree_topk(const dsa_batch* batch, const float* scores, int64_t ld
     if (st != DSA_OK) return st;
     if (k < 1 || k > kMaxTopk) return DSA_ERR_INVALID_ARG;
     if (batch->max_q > DSA_MAX_TREE) return DSA_ERR_UNSUPPORTED;
-    if (!given(ws) || ws_bytes < kWsHeaderBytes) return DSA_ERR_WORKSPACE;
+    if (check_ws(ws, ws_bytes, with_header(0)) != DSA_OK) return DSA_ERR_WORKSPACE;
     if (batch->total_q == 0 || batch->max_q == 0) return DSA_OK;
     if (!given(scores) || !given(mask, 8) || !given(idx)) return DSA_ERR_INVALID_ARG;
     if (ld < batch->max_ctx || ld % 4 != 0) return DSA_ERR_INVALID_ARG;
@@ -146,7 +145,7 @@ dsa_status dsa_tree_commit(const dsa_batch* batch, const dsa_pages* pages, const
                            const int32_t* accepted, int32_t layers, int64_t cache_rows, uint16_t* kv, uint16_t* k_idx,
                            int32_t* ctx_new, void* ws, size_t ws_bytes, void* stream) {
     dsa_status st = check(batch, pages);
-    if (st != DSA_OK || (st = check_ws(batch, ws, ws_bytes)) != DSA_OK) return st;
+    if (st != DSA_OK || (st = check_ws(ws, ws_bytes, tables_ws(batch))) != DSA_OK) return st;
     if (layers < 1 || layers > 65535 || cache_rows < 0) return DSA_ERR_INVALID_ARG;
     const int64_t rows = pages ? (int64_t)pages->pool_pages * pages->page_size : batch->batch * batch->cache_stride;
     if (pages ? cache_rows != rows : cache_rows < rows) return DSA_ERR_INVALID_ARG;

@@ -153,3 +153,21 @@ def test_binding_without_a_workspace(lib):
         with pytest.raises(dsa.DsaError, match=f"dsa_{name}: DSA_ERR_WORKSPACE") as e:
             getattr(dsa, name)(*args, ws=None)
         assert e.value.code == 3
+
+
+@pytest.mark.parametrize("B", [1, 2, 300])
+def test_each_call_asks_for_its_own_workspace(lib, B):
+    b, g = _batch(B=B), _pages()
+    n = 264 + 8 * B
+    assert n < _ws(lib, b)
+
+    def tables(bytes_):
+        return lib.dsa_step_tables(ctypes.byref(b), ctypes.byref(g), None, P, None, P, P, P, P, P, P, P, P, WS, bytes_, None)
+
+    def commit(bytes_):
+        return lib.dsa_tree_commit(ctypes.byref(b), ctypes.byref(g), P, None, 1, 320, P, None, P, WS, bytes_, None)
+    for call in (tables, commit):
+        assert call(n - 1) == 3 and call(n) == 1               # then refused for a missing array
+    assert _attn(lib, b, g, q=None, n=n) == 3 and _attn(lib, b, g, q=None, n=_ws(lib, b)) == 1
+    size = ctypes.c_size_t(0)
+    assert lib.dsa_workspace_size(ctypes.byref(b), 1, ctypes.byref(size)) == 0 and size.value >= n
