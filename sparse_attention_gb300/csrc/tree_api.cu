@@ -120,7 +120,7 @@ dsa_status dsa_tree_mla_fwd(const dsa_batch* batch, const dsa_pages* pages, cons
     if (batch->max_q > DSA_MAX_TREE) return DSA_ERR_UNSUPPORTED;
     if (batch->total_q >= (1 << 25)) return DSA_ERR_UNSUPPORTED;     // 64 query rows each, in int32 TMA coordinates
     if ((st = check_ws(ws, ws_bytes, attention_ws(batch))) != DSA_OK) return st;
-    if (batch->total_q == 0 || batch->max_q == 0) return DSA_OK;
+    if (batch->total_q == 0 || batch->max_q == 0 || batch->max_ctx == 0) return DSA_OK;      // no row can be
     if (!given(q) || !given(kv) || !given(mask, 8) || !given(out) || !aligned(lse, 16)) return DSA_ERR_INVALID_ARG;
     if (!(sm_scale > 0.f) || sm_scale == INFINITY) return DSA_ERR_INVALID_ARG;
     return cuda_status(launch_tree_mla(to_dev(batch), to_dev(pages), q, kv, mask, sm_scale, out, lse, scratch_of(ws),

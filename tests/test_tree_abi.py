@@ -171,3 +171,10 @@ def test_each_call_asks_for_its_own_workspace(lib, B):
     assert _attn(lib, b, g, q=None, n=n) == 3 and _attn(lib, b, g, q=None, n=_ws(lib, b)) == 1
     size = ctypes.c_size_t(0)
     assert lib.dsa_workspace_size(ctypes.byref(b), 1, ctypes.byref(size)) == 0 and size.value >= n
+
+
+def test_attention_of_a_batch_without_context(lib):
+    """No sequence can hold a row: nothing to do, as for max_q = 0, whatever the caches' size."""
+    for g in (None, _pages()):
+        assert _attn(lib, _batch(max_ctx=0, stride=0), g) == 0
+    assert _attn(lib, _batch(max_ctx=0, stride=0), ws=None) == 3
