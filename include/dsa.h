@@ -341,7 +341,8 @@ DSA_API dsa_status dsa_forward_fp8(const dsa_batch* batch, const uint8_t* q8, co
  *                      table, slot map, positions, masks
  *   dsa_latent_append  the new tokens' latent rows into their slots
  *   dsa_tree_mla_fwd   attention over everything a row sees (contexts of at
- *                      most index_topk rows, layers without an indexer)
+ *                      most index_topk rows; any length in layers without an
+ *                      indexer)
  *   dsa_tree_topk      the DSA selection of a row among what it sees, between
  *                      dsa_indexer_scores and dsa_sparse_mla_fwd
  *   dsa_tree_commit    the accepted path's rows moved behind the committed
@@ -349,7 +350,9 @@ DSA_API dsa_status dsa_forward_fp8(const dsa_batch* batch, const uint8_t* q8, co
  * Paged caches: with a dsa_pages, position s of sequence b is cache row
  * block_table[b * max_pages + s / page_size] * page_size + s % page_size of a
  * cache of pool_pages * page_size rows, and cache_stride plays no part (it
- * must still be >= max_ctx).  Without one (NULL) it is row
+ * must still be >= max_ctx).  The calls of steps 1 to 3 take contiguous caches
+ * only, so dsa_tree_mla_fwd is the one attention over pages, for up to 64 new
+ * rows a sequence; prompt rows over pages are the caller's own.  Without one (NULL) it is row
  * b * cache_stride + s, as in every other call.
  * Every launch is sized from the host arguments alone.  Calls that may run at
  * the same time (two streams, or two captured graphs) need a workspace each.

@@ -12,6 +12,12 @@
 //                                 when a score exceeds it by 2^8 (then O is
 //                                 rescaled), so sums and weights stay far from
 //                                 both ends of fp32
+//                                 P is rounded to bf16 for the product, the
+//                                 MMA's type, and its sum taken before, in
+//                                 fp32: an error of half a bf16 step of a
+//                                 weight, like the result's own rounding (fp32
+//                                 weights would need TF32 MMAs of half the rate
+//                                 and twice the shared memory)
 //   O[128 q, 512] += P V          two N = 256 halves; each CTA stages, for all
 //                                 128 positions, the 128 dims of each half
 //                                 whose columns it supplies
@@ -45,10 +51,11 @@
 // Bounds.  A row pair's tile is 36 MMAs of N = 128 (37 cycles each) and 16 of
 // N = 256 (65): 2,372 cycles for 35.7 MFLOP, 92 % of the tensor rate; a single
 // row leaves rank 1's half empty and is bound by HBM (121 flop a byte).
-// Measured: 16 trees of 64 over 8,192 rows 0.64-0.66 ms = 1,770-1,820 TFLOP/s
-// (1,907 measured peak; the power cap holds the clock at 1.8 GHz); 64 single
-// rows over 32,768 each 0.396 ms = 6.1 TB/s (6.78 measured copy); one tree of
-// 8 over 1,500 rows 17 us with the merge.
+// Measured, in single calls and in a loop that the power cap slows: 16 trees
+// of 64 over 8,192 rows 0.64-0.66 ms = 1,770-1,820 TFLOP/s (1,907 measured
+// peak) and 0.73-0.75 ms = 1,560-1,600 (1,698 sustained); 64 single rows over
+// 32,768 each 0.37-0.38 ms = 6.4-6.6 TB/s (6.78 measured copy) and 0.41-0.43
+// ms; one tree of 8 over 1,500 rows 17 us with the merge.
 #include <algorithm>
 #include <atomic>
 
