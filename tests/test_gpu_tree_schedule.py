@@ -21,10 +21,6 @@ def _lib():
     dsa.load_library()
 
 
-def _pairs():
-    return torch.cuda.get_device_properties(0).multi_processor_count // 2
-
-
 def _inputs(st, seed):
     """q and caches made on the device; rows of no sequence hold NaN."""
     g = torch.Generator(device="cuda").manual_seed(seed)
@@ -63,6 +59,7 @@ CASES = {
     "odd": lambda rng: _equal(31, 5, 5003),                 # 93 items, each third one with a single row
     "ragged": lambda rng: _ragged(60, rng),
     "fewer": lambda rng: _steps(),
+    "two_fewer": lambda rng: ([4000] * 19 + [1000] * 10 + [20000] * 9 + [4000] * 19, [8] * 57),   # one round of three
     "long_first": lambda rng: ([60000] + [4000] * 20, [2] + [16] * 20),
     "long_last": lambda rng: ([4000] * 20 + [60000], [16] * 20 + [3]),
     "b256": lambda rng: (rng.integers(1500, 2500, 256).tolist(), [4] * 256),     # the most sequences that take rounds
