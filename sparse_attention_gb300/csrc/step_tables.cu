@@ -11,10 +11,10 @@
 // for itself and then writes its part of the rows (one launch, bound by latency:
 // a step reads and writes some 20 KB), more are summed by one CTA, with the
 // rows in a second launch, and so are the tables of more than 1,024 rows (32
-// a tree at least) whose outputs take their inputs' place: the first CTA would advance what the
-// others still have to read.  64 trees of 16: 3.7 us, in place 5.8; 256 of them
-// 4.3 and 6.1; 257 to 512 of them 7.4-7.6 either way; 256 prompts of up to 256
-// tokens 4.1; 512 prompts of 128 9.3 and 9.9.
+// a tree at least) whose outputs take their inputs' place: the first CTA would
+// advance what the others still have to read.  64 trees of 16: 3.7 us, in place
+// 5.8; 256 of them 4.3 and 6.1; 257 to 512 of them 7.4-7.7 either way; 256
+// prompts of up to 256 tokens 4.1; 512 prompts of 128 9.3 and 9.9.
 // A row's page is looked up in the held part of the block table or, behind
 // it, in the free list itself, so rows do not wait for the new entries.
 //

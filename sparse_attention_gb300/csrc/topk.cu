@@ -773,7 +773,7 @@ cudaError_t launch_nt(const BatchDev& bd, RowRange rr, const float* scores, int6
 // Limited by instructions (34 per 32 scores and 4.5 K a row of 256 threads) and
 // by the barriers between the passes (a scheduler issues in 59-67 % of the
 // cycles).  Scores that an even division does not fit take the fallback of
-// step 3, three times as long: with one score of 50 standard deviations in a
+// step 3, about three times as long: with one score of 50 standard deviations in a
 // row, or many equal ones, 8 x 8 over 32,768 27-29 us (9.7), 64 full trees of 32
 // over 9,001 125 (38), 1 x 8 over 32,768 19-20 (8.0); from about 20 standard
 // deviations some rows do.  k = 2048, 64 trees of up to 32 rows
