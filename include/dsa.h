@@ -476,6 +476,64 @@ DSA_API dsa_status dsa_tree_commit(const dsa_batch* batch, const dsa_pages* page
                                    const int32_t* accepted, int32_t layers, int64_t cache_rows, uint16_t* kv,
                                    uint16_t* k_idx, int32_t* ctx_new, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- Rotary positions.
+ *
+ *   dsa_rope_table       rotary tables of a range of positions
+ *   dsa_rope             a part of every head rotated (queries, index queries) */
+
+#define DSA_MAX_ROPE_DIM 256
+#define DSA_ROPE_NEIGHBOUR 1     /* pairs (2i, 2i + 1); without: (i, i + dim / 2) */
+#define DSA_ROPE_INVERSE 2       /* by the negative angle: undoes a rotation; also its gradient */
+
+/* Scaling of rotary frequencies for long contexts.  original_ctx = 0: every
+ * frequency is divided by `factor` (linear interpolation).  Else by parts
+ * (YaRN, Peng et al. 2023, section 3.2): pair i of the dim / 2 is divided by
+ * `factor` to the part
+ *   ramp(i) = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *   lo = max(floor(e(beta_fast)), 0), hi = min(ceil(e(beta_slow)), dim - 1),
+ *   e(n) = dim ln(original_ctx / (2 pi n)) / (2 ln base)
+ * (the pair that turns n times in the original context), and kept to the rest.
+ * cos and sin are multiplied by mscale. */
+typedef struct dsa_rope_scaling {
+    double factor;           /* >= 1 */
+    int32_t original_ctx;    /* >= 0 */
+    float beta_fast;         /* turns above which a pair is kept (32); > 0 */
+    float beta_slow;         /* turns below which it is interpolated (1); > 0 */
+    float mscale;            /* > 0 */
+} dsa_rope_scaling;
+
+/* cos[r, i] = cos[r, i + dim/2] = mscale cos((first + r) f_i), sin the same,
+ * f_i = base^(-2i / dim) or as scaled: the tables of dsa_rope,
+ * dsa_latent_append and (its rows gathered) dsa_index_key_producer.
+ *   cos, sin fp32 [rows, dim] (DEVICE)
+ * Angles are formed in 64-bit fixed point: far positions are as exact as near
+ * ones (about 2 units of the last fp32 place).  dim a multiple of 16, 16 ..
+ * 256; rows, first >= 0, first + rows <= 2^31; base >= 1, above 1 with
+ * original_ctx > 0; scaling NULL: none.  cos and sin may not overlap. */
+DSA_API dsa_status dsa_rope_table(int32_t rows, int32_t first, int32_t dim, double base,
+                                  const dsa_rope_scaling* scaling, float* cos, float* sin, void* stream);
+
+/* Rotates `dim` columns of every head of every token:
+ *   out[t, h, a] = x[t, h, a] cos[p, i] - x[t, h, b] sin[p, i]
+ *   out[t, h, b] = x[t, h, b] cos[p, i] + x[t, h, a] sin[p, i],  p = positions[t]
+ * for i < dim/2 and (a, b) = (i, i + dim/2) or, with DSA_ROPE_NEIGHBOUR,
+ * (2i, 2i + 1).  fp32 arithmetic, one rounding to bf16.
+ *   x, out   bf16 (DEVICE), element (t, h, i) at t * token + h * head + i;
+ *            strides >= 0 and multiples of 8; point at the first rotated column.
+ *            out = x with the same strides rotates in place; otherwise the
+ *            two may not overlap (from first to last element), and no two
+ *            elements of out may share a place.
+ *   cos, sin fp32 [table_rows, dim], of which the first dim/2 columns are read
+ *   positions int32 [total_q]: -1 leaves the token's out as it was; another
+ *            value outside [0, table_rows) does too and latches DSA_ERR_BAD_INDEX
+ *   flags    DSA_ROPE_*
+ * ws: at least 256 bytes.  dim a multiple of 16, 16 .. 256; total_q < 2^26;
+ * heads >= 1. */
+DSA_API dsa_status dsa_rope(int32_t total_q, int32_t heads, int32_t dim, const uint16_t* x, int64_t x_token,
+                            int64_t x_head, const float* cos, const float* sin, int32_t table_rows,
+                            const int32_t* positions, int32_t flags, uint16_t* out, int64_t out_token,
+                            int64_t out_head, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -36,7 +36,7 @@ EXPORTS = ("dsa_status_string", "dsa_last_cuda_error", "dsa_kernel_launch_count"
            "dsa_sparse_mla_fwd_noalloc", "dsa_forward", "dsa_mla_absorb_q", "dsa_mla_workspace_size", "dsa_mla_output", "dsa_index_key_workspace_size",
            "dsa_index_key_producer", "dsa_quantize_fp8", "dsa_indexer_scores_fp8", "dsa_forward_fp8",
            "dsa_tree_workspace_size", "dsa_step_tables", "dsa_latent_append", "dsa_tree_mla_fwd", "dsa_tree_topk",
-           "dsa_tree_commit")
+           "dsa_tree_commit", "dsa_rope_table", "dsa_rope")
 
 
 class DsaError(RuntimeError):
@@ -57,6 +57,11 @@ class DsaBatch(ctypes.Structure):
 class DsaPages(ctypes.Structure):
     _fields_ = [("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("pool_pages", ctypes.c_int32),
                 ("block_table", ctypes.c_void_p)]
+
+
+class DsaRopeScaling(ctypes.Structure):
+    _fields_ = [("factor", ctypes.c_double), ("original_ctx", ctypes.c_int32), ("beta_fast", ctypes.c_float),
+                ("beta_slow", ctypes.c_float), ("mscale", ctypes.c_float)]
 
 
 _lib = None
@@ -103,6 +108,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dsa_tree_mla_fwd.argtypes = [BP, GP, P, P, P, f32, P, P, P, sz, P]
     lib.dsa_tree_topk.argtypes = [BP, P, i64, P, i32, P, P, sz, P]
     lib.dsa_tree_commit.argtypes = [BP, GP, P, P, i32, i64, P, P, P, P, sz, P]
+    lib.dsa_rope_table.argtypes = [i32, i32, i32, ctypes.c_double, ctypes.POINTER(DsaRopeScaling), P, P, P]
+    lib.dsa_rope.argtypes = [i32, i32, i32, P, i64, i64, P, P, i32, P, i32, P, i64, i64, P, sz, P]
     for name in EXPORTS:
         if name not in ("dsa_status_string", "dsa_last_cuda_error", "dsa_kernel_launch_count"):
             getattr(lib, name).restype = ctypes.c_int
@@ -504,3 +511,58 @@ def tree_commit(batch: Batch, mask, accepted, ctx_new, kv=None, k_idx=None, page
         _typed("ctx_new", ctx_new, torch.int32, c.batch, dev), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)),
         "dsa_tree_commit")
     return ctx_new
+
+
+# ---- Rotary positions -------------------------------------------------------
+
+class RopeScaling:
+    """Host handle of a dsa_rope_scaling: frequencies divided by `factor`, all
+    of them (original_ctx 0) or by parts (YaRN), and cos and sin times mscale."""
+
+    def __init__(self, factor: float, original_ctx: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 mscale: float = 1.0):
+        self.c = DsaRopeScaling(float(factor), int(original_ctx), float(beta_fast), float(beta_slow), float(mscale))
+
+
+def rope_table(cos, sin, base: float, first: int = 0, scaling: Optional[RopeScaling] = None, stream=None):
+    """Fills cos and sin fp32 [rows, dim] with the rotary rows of positions
+    first, first + 1, .. (see dsa_rope_table)."""
+    dev = cos.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
+        raise ValueError(f"cos on {cos.device}: expected on the current CUDA device, and the stream's")
+    if cos.dim() != 2 or sin.shape != cos.shape:
+        raise ValueError("cos, sin: [rows, dim] of one shape expected")
+    rows, dim = cos.shape
+    _check(load_library().dsa_rope_table(
+        rows, int(first), dim, float(base), ctypes.byref(scaling.c) if scaling is not None else None,
+        _typed("cos", cos, torch.float32, rows * dim, dev), _typed("sin", sin, torch.float32, rows * dim, dev),
+        _raw_stream(stream, dev)), "dsa_rope_table")
+    return cos, sin
+
+
+def rope(x, cos, sin, positions, out=None, interleaved: bool = False, inverse: bool = False, ws=None, stream=None):
+    """Rotates x [total_q, heads, dim] (any strides, unit in the last
+    dimension: a slice of wider heads) into out, or in place (see dsa_rope).
+    interleaved: neighbours as pairs instead of the halves."""
+    dev, f32 = _here("dsa_rope", ws, stream), torch.float32
+    out = x if out is None else out
+    for name, t in (("x", x), ("out", out)):
+        if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+            raise TypeError(f"{name}: bf16 tensor on cuda:{dev} expected")
+        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+            raise ValueError(f"{name}: [total_q, heads, dim] with unit stride in the last dimension expected")
+    if out.shape != x.shape:
+        raise ValueError("x, out: one shape expected")
+    total_q, heads, dim = x.shape
+    if cos.dim() != 2 or cos.shape[1] != dim or sin.shape != cos.shape:
+        raise ValueError(f"cos, sin: [table_rows, {dim}] expected")
+    rows = cos.shape[0]
+    if heads == 0:
+        return out
+    st = [t.stride(d) if t.shape[d] > 1 else 0 for t in (x, out) for d in (0, 1)]
+    _check(load_library().dsa_rope(
+        total_q, heads, dim, x.data_ptr(), st[0], st[1], _typed("cos", cos, f32, rows * dim, dev),
+        _typed("sin", sin, f32, rows * dim, dev), rows, _typed("positions", positions, torch.int32, total_q, dev),
+        (1 if interleaved else 0) | (2 if inverse else 0), out.data_ptr(), st[2], st[3], ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, dev)), "dsa_rope")
+    return out

@@ -1,0 +1,75 @@
+// prompt_api.cu -- the extern "C" entry points of rotary positions (declared
+// and documented in include/dsa.h): host-side argument checks.
+#include <algorithm>
+#include <cmath>
+
+#include "api_checks.h"
+#include "prompt.h"
+
+using namespace dsa;
+
+namespace {
+
+bool good_dim(int32_t dim) { return dim >= 16 && dim <= DSA_MAX_ROPE_DIM && dim % 16 == 0; }
+
+// Bytes from a tensor's first element to behind its last.
+int64_t extent(int32_t tokens, int64_t token, int32_t heads, int64_t head, int32_t dim) {
+    return 2 * ((tokens - 1) * token + (heads - 1) * head + dim);
+}
+
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
+}  // namespace
+
+extern "C" {
+
+dsa_status dsa_rope_table(int32_t rows, int32_t first, int32_t dim, double base, const dsa_rope_scaling* scaling,
+                          float* cos_t, float* sin_t, void* stream) {
+    if (rows < 0 || first < 0 || (int64_t)rows + first > (int64_t(1) << 31) || !good_dim(dim)) return DSA_ERR_INVALID_ARG;
+    if (!(base >= 1.0) || !std::isfinite(base)) return DSA_ERR_INVALID_ARG;
+    if (scaling) {
+        if (!(scaling->factor >= 1.0) || !std::isfinite(scaling->factor) || scaling->original_ctx < 0 ||
+            !positive(scaling->mscale))
+            return DSA_ERR_INVALID_ARG;
+        if (scaling->original_ctx > 0 &&
+            (base == 1.0 || !positive(scaling->beta_fast) || !positive(scaling->beta_slow)))
+            return DSA_ERR_INVALID_ARG;
+    }
+    if (rows == 0) return DSA_OK;
+    if (!given(cos_t) || !given(sin_t)) return DSA_ERR_INVALID_ARG;
+    const int64_t bytes = (int64_t)rows * dim * 4;
+    if (overlap(cos_t, bytes, sin_t, bytes)) return DSA_ERR_INVALID_ARG;
+    return cuda_status(launch_rope_table(rows, first, dim, base, scaling, cos_t, sin_t,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_rope(int32_t total_q, int32_t heads, int32_t dim, const uint16_t* x, int64_t x_token, int64_t x_head,
+                    const float* cos_t, const float* sin_t, int32_t table_rows, const int32_t* positions,
+                    int32_t flags, uint16_t* out, int64_t out_token, int64_t out_head, void* ws, size_t ws_bytes,
+                    void* stream) {
+    if (total_q < 0 || total_q >= (1 << 26) || heads < 1 || heads > (1 << 16) || !good_dim(dim)) return DSA_ERR_INVALID_ARG;
+    if (table_rows < 0 || (flags & ~(DSA_ROPE_NEIGHBOUR | DSA_ROPE_INVERSE))) return DSA_ERR_INVALID_ARG;
+    if (check_ws(ws, ws_bytes, with_header(0)) != DSA_OK) return DSA_ERR_WORKSPACE;
+    if (total_q == 0) return DSA_OK;
+    if (!given(x) || !given(out) || !given(cos_t) || !given(sin_t) || !given(positions, 4)) return DSA_ERR_INVALID_ARG;
+    for (int64_t s : {x_token, x_head, out_token, out_head})
+        if (s < 0 || s % 8 != 0 || s > (int64_t(1) << 36)) return DSA_ERR_INVALID_ARG;
+    // tokens of whole heads, or heads of whole tokens
+    const bool by_token = (heads == 1 || out_head >= dim) &&
+                          (total_q == 1 || out_token >= (heads - 1) * out_head + dim);
+    const bool by_head = (total_q == 1 || out_token >= dim) &&
+                         (heads == 1 || out_head >= (total_q - 1) * out_token + dim);
+    if (!by_token && !by_head) return DSA_ERR_INVALID_ARG;
+    const bool place = x == out && (total_q == 1 || x_token == out_token) && (heads == 1 || x_head == out_head);
+    if (!place && overlap(x, extent(total_q, x_token, heads, x_head, dim), out,
+                          extent(total_q, out_token, heads, out_head, dim)))
+        return DSA_ERR_INVALID_ARG;
+    return cuda_status(launch_rope(total_q, heads, dim, x, x_token, x_head, cos_t, sin_t, table_rows, positions,
+                                   (flags & DSA_ROPE_NEIGHBOUR) != 0, (flags & DSA_ROPE_INVERSE) != 0, out, out_token,
+                                   out_head, static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
