@@ -6,11 +6,11 @@
 // Tables.  Pair i of position p turns by p f_i, f_i = base^(-2i/dim).  In 64-bit
 // fixed point an angle is a fraction of a turn: F_i = 2^64 f_i / (2 pi) is formed
 // on the host, p F_i mod 2^64 drops whole turns for nothing, its upper bits are
-// the nearest quarter turn, and the signed rest is a float and the remainder of
-// that rounding, whose first-order term is added.  So far positions are as exact as near ones
-// (error of the angle p 2^-56 turns, from F_i's 53 bits) without 64-bit floating
-// point, which this GPU has little of.  Bound by the writes and the launch: 202,752
-// x 64 x 2 floats are 104 MB.
+// the nearest quarter turn, and the signed rest is rounded to a float (relative
+// to its own size, so small angles lose nothing).  Far positions are as exact
+// as near ones (error of the angle p 2^-56 turns, from F_i's 53 bits) without
+// 64-bit floating point, which this GPU has little of.  Bound by the writes and the
+// launch: 202,752 x 64 x 2 floats are 104 MB.
 //
 // Rotation.  A thread holds 8 pairs of up to 4 heads of a token, so that a
 // token's table row is read once for them, all loads in flight before the
@@ -32,16 +32,23 @@ struct Turns {
     uint64_t f[kMaxPairs];       // 2^64 turns per position
 };
 
-// cos and sin of phase / 2^64 turns.
+// cos and sin of phase / 2^64 turns: within an eighth of a turn of a quarter,
+// so the first six terms of the Taylor series leave 2e-9 of a sine and 1e-10
+// of a cosine.
 __device__ __forceinline__ void turn(uint64_t phase, float& c, float& s) {
     const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
     const int64_t rest = (int64_t)(phase - ((uint64_t)quarter << 62));
-    const float hi = __ll2float_rn(rest);
-    const float lo = __ll2float_rn(rest - __float2ll_rn(hi));
-    float c0, s0;
-    sincospif(hi * 0x1p-63f, &s0, &c0);
-    const float d = lo * (float)(M_PI * 0x1p-63);
-    const float c1 = fmaf(-s0, d, c0), s1 = fmaf(c0, d, s0);
+    const float x = __ll2float_rn(rest) * (float)(2 * M_PI * 0x1p-64), z = x * x;
+    float c1 = -1.f / 3628800, s1 = 1.f / 362880;
+    c1 = fmaf(c1, z, 1.f / 40320);
+    s1 = fmaf(s1, z, -1.f / 5040);
+    c1 = fmaf(c1, z, -1.f / 720);
+    s1 = fmaf(s1, z, 1.f / 120);
+    c1 = fmaf(c1, z, 1.f / 24);
+    s1 = fmaf(s1, z, -1.f / 6);
+    c1 = fmaf(c1, z, -0.5f);
+    s1 = fmaf(s1 * z, x, x);
+    c1 = fmaf(c1, z, 1.f);
     const bool odd = quarter & 1;
     c = odd ? s1 : c1;
     s = odd ? c1 : s1;
