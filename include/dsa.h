@@ -476,10 +476,21 @@ DSA_API dsa_status dsa_tree_commit(const dsa_batch* batch, const dsa_pages* page
                                    const int32_t* accepted, int32_t layers, int64_t cache_rows, uint16_t* kv,
                                    uint16_t* k_idx, int32_t* ctx_new, void* ws, size_t ws_bytes, void* stream);
 
-/* ---- Rotary positions.
+/* ---- Prompts over the latent cache.
  *
  *   dsa_rope_table       rotary tables of a range of positions
- *   dsa_rope             a part of every head rotated (queries, index queries) */
+ *   dsa_rope             a part of every head rotated (queries, index queries)
+ *   dsa_mla_expand       latent cache rows -> each head's keys and values
+ *   dsa_prompt_mla_fwd   causal attention of new rows over expanded rows
+ *   dsa_mla_o_proj       o_proj on its result
+ *
+ * Expanded or absorbed.  A (query, key) pair of one layer takes 65,536 flop in
+ * expanded form and 139,264 in absorbed form (dsa_sparse_mla_fwd,
+ * dsa_tree_mla_fwd), but each cached row has to be expanded
+ * first (29.4 MFLOP) and is 57,472 bytes wide then instead of 1,152.  So prompts and
+ * chunks of some 400 and more new tokens are cheaper expanded, decode steps
+ * absorbed.  Both forms are exact: without an indexer, or for contexts of at
+ * most index_topk rows, where the selection keeps everything. */
 
 #define DSA_MAX_ROPE_DIM 256
 #define DSA_ROPE_NEIGHBOUR 1     /* pairs (2i, 2i + 1); without: (i, i + dim / 2) */
@@ -533,6 +544,69 @@ DSA_API dsa_status dsa_rope(int32_t total_q, int32_t heads, int32_t dim, const u
                             int64_t x_head, const float* cos, const float* sin, int32_t table_rows,
                             const int32_t* positions, int32_t flags, uint16_t* out, int64_t out_token,
                             int64_t out_head, void* ws, size_t ws_bytes, void* stream);
+
+#define DSA_EXPANDED_ROOM 128
+
+/* Expanded rows.  Position s of sequence b is row off[b] + s of
+ *   kv    bf16 [rows, 64, 448]   per head [192 key columns | 256 value columns]
+ *   k_pe  bf16 [rows, 64]        the rotary key that all heads share
+ * off (DEVICE int32 [batch + 1]) is ascending, each sequence's begin a
+ * multiple of 128 and its room off[b+1] - off[b] at least ctx_len[b] rounded up
+ * to a multiple of 128, off[batch] <= rows; a sequence that breaks this is skipped and
+ * DSA_ERR_BAD_BATCH latched. */
+typedef struct dsa_expanded {
+    int32_t rows;
+    const int32_t* off;
+    uint16_t* kv;
+    uint16_t* k_pe;
+} dsa_expanded;
+
+/* Bytes of workspace that dsa_mla_expand and dsa_prompt_mla_fwd need for
+ * `batch`.  Host only. */
+DSA_API dsa_status dsa_prompt_workspace_size(const dsa_batch* batch, size_t* bytes);
+
+/* Expands latent cache rows ("GLM-5.1 架构深度拆解", section 4.5 Step 2:
+ * kv_b_proj, split 192 | 256 per head): for every sequence b and position s in
+ * [first[b], ctx_len[b]), with c | pe its cache row,
+ *   expanded.kv[off[b] + s, h, :] = w_kv_b[448 h : 448 h + 448, :] c
+ *   expanded.k_pe[off[b] + s, :]  = pe
+ * fp32 accumulation, one rounding to bf16, values past bf16's largest kept at
+ * it.  The rows behind a sequence's last, up to the next multiple of 128, are
+ * zeroed wherever first[b] did not already lie in the same 128, so a
+ * sequence that grows by chunks keeps what was expanded and passes its old length.
+ * A cache row with a NaN or infinity among its 576 values gets finite kv and
+ * NaN throughout k_pe: queries that see it get NaN, others nothing of it.
+ *   kv     bf16 latent cache, contiguous or paged, as dsa_tree_mla_fwd
+ *   w_kv_b bf16 [64 * 448, 512]
+ *   first  int32 [batch] (DEVICE) or NULL (0 throughout); outside [0,
+ *          ctx_len[b]]: the sequence is skipped, DSA_ERR_BAD_BATCH
+ * Positions on a page outside the pool are not written, DSA_ERR_BAD_INDEX.
+ * The batch's q_off is checked but plays no other part. */
+DSA_API dsa_status dsa_mla_expand(const dsa_batch* batch, const dsa_pages* pages, const uint16_t* kv,
+                                  const uint16_t* w_kv_b, const int32_t* first, const dsa_expanded* expanded,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/* Causal attention of the batch's new rows over expanded rows:
+ *   q    bf16 [total_q, 64, 256]  [192 | 64 rotated] per head
+ *   out  bf16 [total_q, 64, 256]  softmax(sm_scale q k^T) v over positions s <= t,
+ *                                 head-major: o_mid of dsa_mla_output
+ *   lse  fp32 [total_q, 64] or NULL
+ * The row at position t (as in every call) sees expanded rows off[b] .. off[b] + t.  The
+ * rows of a sequence's room up to the next multiple of 128 behind ctx_len have to hold
+ * finite kv, as dsa_mla_expand leaves them; what else the buffers hold is not
+ * read.  fp32 scores, softmax statistics and sums; the softmax weights are
+ * rounded to bf16 for the product with the values and the result once more.
+ * The same inputs give the same bits.  Calls that may run at the same time need
+ * a workspace each. */
+DSA_API dsa_status dsa_prompt_mla_fwd(const dsa_batch* batch, const uint16_t* q, const dsa_expanded* expanded,
+                                      float sm_scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                                      void* stream);
+
+/* y[t, n] = sum_c w_o[n, c] o_mid[t, c]: the second product of dsa_mla_output
+ * alone, for attention results that are already 64 x 256 wide.  Arguments,
+ * workspace and errors as there. */
+DSA_API dsa_status dsa_mla_o_proj(int32_t total_q, const uint16_t* o_mid, const uint16_t* w_o, uint16_t* y, void* ws,
+                                  size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

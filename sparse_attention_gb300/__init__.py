@@ -24,6 +24,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdsa.so")
 
 H_IDX, D_IDX, H, D_QK, D_V, MAX_TOPK = 32, 128, 64, 576, 512, 2048
+D_HEAD, D_EXP, D_HIDDEN, EXPANDED_ROOM = 256, 448, 6144, 128
 
 STATUS = {
     0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED", 3: "DSA_ERR_WORKSPACE",
@@ -36,7 +37,8 @@ EXPORTS = ("dsa_status_string", "dsa_last_cuda_error", "dsa_kernel_launch_count"
            "dsa_sparse_mla_fwd_noalloc", "dsa_forward", "dsa_mla_absorb_q", "dsa_mla_workspace_size", "dsa_mla_output", "dsa_index_key_workspace_size",
            "dsa_index_key_producer", "dsa_quantize_fp8", "dsa_indexer_scores_fp8", "dsa_forward_fp8",
            "dsa_tree_workspace_size", "dsa_step_tables", "dsa_latent_append", "dsa_tree_mla_fwd", "dsa_tree_topk",
-           "dsa_tree_commit", "dsa_rope_table", "dsa_rope")
+           "dsa_tree_commit", "dsa_rope_table", "dsa_rope", "dsa_prompt_workspace_size", "dsa_mla_expand",
+           "dsa_prompt_mla_fwd", "dsa_mla_o_proj")
 
 
 class DsaError(RuntimeError):
@@ -57,6 +59,11 @@ class DsaBatch(ctypes.Structure):
 class DsaPages(ctypes.Structure):
     _fields_ = [("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("pool_pages", ctypes.c_int32),
                 ("block_table", ctypes.c_void_p)]
+
+
+class DsaExpanded(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("off", ctypes.c_void_p), ("kv", ctypes.c_void_p),
+                ("k_pe", ctypes.c_void_p)]
 
 
 class DsaRopeScaling(ctypes.Structure):
@@ -110,6 +117,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dsa_tree_commit.argtypes = [BP, GP, P, P, i32, i64, P, P, P, P, sz, P]
     lib.dsa_rope_table.argtypes = [i32, i32, i32, ctypes.c_double, ctypes.POINTER(DsaRopeScaling), P, P, P]
     lib.dsa_rope.argtypes = [i32, i32, i32, P, i64, i64, P, P, i32, P, i32, P, i64, i64, P, sz, P]
+    XP = ctypes.POINTER(DsaExpanded)
+    lib.dsa_prompt_workspace_size.argtypes = [BP, ctypes.POINTER(sz)]
+    lib.dsa_mla_expand.argtypes = [BP, GP, P, P, P, XP, P, sz, P]
+    lib.dsa_prompt_mla_fwd.argtypes = [BP, P, XP, f32, P, P, P, sz, P]
+    lib.dsa_mla_o_proj.argtypes = [i32, P, P, P, P, sz, P]
     for name in EXPORTS:
         if name not in ("dsa_status_string", "dsa_last_cuda_error", "dsa_kernel_launch_count"):
             getattr(lib, name).restype = ctypes.c_int
@@ -513,7 +525,7 @@ def tree_commit(batch: Batch, mask, accepted, ctx_new, kv=None, k_idx=None, page
     return ctx_new
 
 
-# ---- Rotary positions -------------------------------------------------------
+# ---- Prompts over the latent cache, and sequences behind a shared prefix ----
 
 class RopeScaling:
     """Host handle of a dsa_rope_scaling: frequencies divided by `factor`, all
@@ -540,29 +552,116 @@ def rope_table(cos, sin, base: float, first: int = 0, scaling: Optional[RopeScal
     return cos, sin
 
 
+def _heads(name: str, t: torch.Tensor, dtype: torch.dtype, dev: int):
+    """The shape of a tensor [total_q, heads, dim] of any strides but a unit one in its last dimension."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name}: {dtype} tensor on cuda:{dev} expected")
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{name}: [total_q, heads, dim] with unit stride in the last dimension expected")
+    return t.shape
+
+
 def rope(x, cos, sin, positions, out=None, interleaved: bool = False, inverse: bool = False, ws=None, stream=None):
     """Rotates x [total_q, heads, dim] (any strides, unit in the last
     dimension: a slice of wider heads) into out, or in place (see dsa_rope).
     interleaved: neighbours as pairs instead of the halves."""
-    dev, f32 = _here("dsa_rope", ws, stream), torch.float32
-    out = x if out is None else out
-    for name, t in (("x", x), ("out", out)):
-        if t.dtype is not torch.bfloat16 or t.get_device() != dev:
-            raise TypeError(f"{name}: bf16 tensor on cuda:{dev} expected")
-        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-            raise ValueError(f"{name}: [total_q, heads, dim] with unit stride in the last dimension expected")
-    if out.shape != x.shape:
+    dev, f32, bf16 = _here("dsa_rope", ws, stream), torch.float32, torch.bfloat16
+    if out is None:
+        out = x
+    total_q, heads, dim = shape = _heads("x", x, bf16, dev)
+    if out is not x and _heads("out", out, bf16, dev) != shape:
         raise ValueError("x, out: one shape expected")
-    total_q, heads, dim = x.shape
-    if cos.dim() != 2 or cos.shape[1] != dim or sin.shape != cos.shape:
-        raise ValueError(f"cos, sin: [table_rows, {dim}] expected")
     rows = cos.shape[0]
+    if cos.shape != (rows, dim) or sin.shape != (rows, dim):
+        raise ValueError(f"cos, sin: [table_rows, {dim}] expected")
     if heads == 0:
         return out
-    st = [t.stride(d) if t.shape[d] > 1 else 0 for t in (x, out) for d in (0, 1)]
+    # the stride of a dimension of one element means nothing
+    xt, xh, _ = x.stride()
+    ot, oh, _ = out.stride()
+    if total_q <= 1:
+        xt = ot = 0
+    if heads == 1:
+        xh = oh = 0
     _check(load_library().dsa_rope(
-        total_q, heads, dim, x.data_ptr(), st[0], st[1], _typed("cos", cos, f32, rows * dim, dev),
+        total_q, heads, dim, x.data_ptr(), xt, xh, _typed("cos", cos, f32, rows * dim, dev),
         _typed("sin", sin, f32, rows * dim, dev), rows, _typed("positions", positions, torch.int32, total_q, dev),
-        (1 if interleaved else 0) | (2 if inverse else 0), out.data_ptr(), st[2], st[3], ws.data_ptr(), ws.numel(),
+        (1 if interleaved else 0) | (2 if inverse else 0), out.data_ptr(), ot, oh, ws.data_ptr(), ws.numel(),
         _raw_stream(stream, dev)), "dsa_rope")
     return out
+
+
+class Expanded:
+    """Host handle of a dsa_expanded.  Keeps its buffers alive."""
+
+    def __init__(self, off: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor):
+        dev = kv.get_device()
+        rows = kv.shape[0] if kv.dim() >= 1 else 0
+        if kv.numel() != rows * H * D_EXP or k_pe.numel() != rows * 64:
+            raise ValueError("kv [rows, 64, 448] and k_pe [rows, 64] expected")
+        if dev < 0:
+            raise ValueError("device tensor expected")
+        self.off, self.kv, self.k_pe = off, kv, k_pe
+        self.c = DsaExpanded(rows, _typed("off", off, torch.int32, 1, dev), _typed("kv", kv, torch.bfloat16, 0, dev),
+                             _typed("k_pe", k_pe, torch.bfloat16, 0, dev))
+
+
+def make_expanded(off: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor) -> Expanded:
+    """Expanded rows: sequence b's begin at row off[b] (a multiple of 128) of kv [rows, 64, 448] and k_pe [rows, 64]."""
+    return Expanded(off, kv, k_pe)
+
+
+def prompt_workspace(batch: Batch, device="cuda") -> torch.Tensor:
+    """A workspace of mla_expand and prompt_mla_fwd with a cleared status word."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().dsa_prompt_workspace_size(ctypes.byref(batch.c), ctypes.byref(n)),
+           "dsa_prompt_workspace_size")
+    ws = torch.empty(int(n.value), dtype=torch.uint8, device=device)
+    reset_device_status(ws)
+    return ws
+
+
+def _expanded(batch: Batch, x: Expanded, dev: int):
+    if x.off.get_device() != dev:
+        raise ValueError(f"expanded rows: expected on cuda:{dev}")
+    if x.off.numel() <= batch.c.batch:
+        raise ValueError("expanded rows: an offset for each sequence and one behind them expected")
+    return ctypes.byref(x.c)
+
+
+def mla_expand(batch: Batch, kv, w_kv_b, expanded: Expanded, first=None, pages: Optional[Pages] = None, ws=None,
+               stream=None):
+    """Expands cache rows first[b] .. ctx_len[b] - 1 of every sequence into
+    each head's keys and values (see dsa_mla_expand)."""
+    dev, bf16 = _here("dsa_mla_expand", ws, stream), torch.bfloat16
+    pg, rows = _paged(batch, pages, dev)
+    _check(load_library().dsa_mla_expand(
+        ctypes.byref(batch.c), pg, _typed("kv", kv, bf16, rows * D_QK, dev),
+        _typed("w_kv_b", w_kv_b, bf16, H * D_EXP * D_V, dev), _typed("first", first, torch.int32, batch.c.batch, dev),
+        _expanded(batch, expanded, dev), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "dsa_mla_expand")
+    return expanded
+
+
+def prompt_mla_fwd(batch: Batch, q, expanded: Expanded, sm_scale: float, out, lse=None, ws=None, stream=None):
+    """Causal attention of the new rows q [total_q, 64, 256] over expanded
+    rows (see dsa_prompt_mla_fwd)."""
+    dev, bf16 = _here("dsa_prompt_mla_fwd", ws, stream), torch.bfloat16
+    c = batch.c
+    _paged(batch, None, dev)
+    _check(load_library().dsa_prompt_mla_fwd(
+        ctypes.byref(c), _typed("q", q, bf16, c.total_q * H * D_HEAD, dev), _expanded(batch, expanded, dev),
+        float(sm_scale), _typed("out", out, bf16, c.total_q * H * D_HEAD, dev),
+        _typed("lse", lse, torch.float32, c.total_q * H, dev), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)),
+        "dsa_prompt_mla_fwd")
+    return out
+
+
+def mla_o_proj(o_mid, w_o, y, ws, stream=None):
+    """y[t] = w_o o_mid[t] for attention results [total_q, 64, 256] (see dsa_mla_o_proj; ws: mla_workspace)."""
+    dev, bf16 = _here("dsa_mla_o_proj", ws, stream), torch.bfloat16
+    total_q = o_mid.shape[0]
+    _check(load_library().dsa_mla_o_proj(
+        int(total_q), _typed("o_mid", o_mid, bf16, total_q * H * D_HEAD, dev),
+        _typed("w_o", w_o, bf16, D_HIDDEN * H * D_HEAD, dev), _typed("y", y, bf16, total_q * D_HIDDEN, dev),
+        ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "dsa_mla_o_proj")
+    return y

@@ -355,6 +355,17 @@ dsa_status dsa_mla_output(int32_t total_q, const uint16_t* o_lat, const uint16_t
                                          static_cast<cudaStream_t>(stream)));
 }
 
+dsa_status dsa_mla_o_proj(int32_t total_q, const uint16_t* o_mid, const uint16_t* w_o, uint16_t* y, void* ws,
+                          size_t ws_bytes, void* stream) {
+    if (total_q < 0 || total_q >= (1 << 26)) return DSA_ERR_INVALID_ARG;
+    if (!ws || !aligned16(ws) || ws_bytes < kWsHeaderBytes + mla_partial_bytes(total_q)) return DSA_ERR_WORKSPACE;
+    if (total_q == 0) return DSA_OK;
+    if (!w_o || !o_mid || !y || !aligned16(w_o) || !aligned16(o_mid) || !aligned16(y)) return DSA_ERR_INVALID_ARG;
+    float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsHeaderBytes);
+    return cuda_status(launch_mla_o_proj(total_q, o_mid, w_o, y, part, static_cast<int32_t*>(ws),
+                                         static_cast<cudaStream_t>(stream)));
+}
+
 dsa_status dsa_index_key_workspace_size(int32_t total_q, size_t* bytes) {
     if (!bytes || total_q < 0 || total_q >= (1 << 26)) return DSA_ERR_INVALID_ARG;
     *bytes = round_up(kWsHeaderBytes + index_key_partial_bytes(total_q), 256);

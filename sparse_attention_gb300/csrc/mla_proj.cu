@@ -422,22 +422,28 @@ cudaError_t launch_mla_output(int32_t total_q, const uint16_t* o_lat, const uint
     g.c_col_step = kDVh;
     g.splits = choose_k_splits(g.M, g.N, g.K, g.batches);    // partials cover all of o_mid
     g.part = part;
-    cudaError_t e = launch_gemm<false>(tm_a, tm_b, g, status, stream);
-    if (e != cudaSuccess) return e;
-    // y = o_mid . W_o^T
+    const cudaError_t e = launch_gemm<false>(tm_a, tm_b, g, status, stream);
+    return e != cudaSuccess ? e : launch_mla_o_proj(total_q, o_mid, w_o, y, part, status, stream);
+}
+
+// y = o_mid . W_o^T
+cudaError_t launch_mla_o_proj(int32_t total_q, const uint16_t* o_mid, const uint16_t* w_o, uint16_t* y, float* part,
+                              int32_t* status, cudaStream_t stream) {
+    if (total_q <= 0) return cudaSuccess;
+    CUtensorMap tm_a, tm_b;
     if (!make_tmap_bf16_2d(&tm_a, o_mid, (uint64_t)kH * kDVh, (uint64_t)total_q, kBK, kBM) ||
         !make_tmap_bf16_2d(&tm_b, w_o, (uint64_t)kH * kDVh, kHidden, kBK, kBN))
         return cudaErrorInvalidValue;
-    GemmArgs g2{};
-    g2.M = total_q;
-    g2.N = kHidden;
-    g2.K = kH * kDVh;
-    g2.batches = 1;
-    g2.C = y;
-    g2.ldc = kHidden;
-    g2.splits = choose_k_splits(g2.M, g2.N, g2.K, 1);
-    g2.part = part;
-    return launch_gemm<false>(tm_a, tm_b, g2, status, stream);
+    GemmArgs g{};
+    g.M = total_q;
+    g.N = kHidden;
+    g.K = kH * kDVh;
+    g.batches = 1;
+    g.C = y;
+    g.ldc = kHidden;
+    g.splits = choose_k_splits(g.M, g.N, g.K, 1);
+    g.part = part;
+    return launch_gemm<false>(tm_a, tm_b, g, status, stream);
 }
 
 }  // namespace dsa

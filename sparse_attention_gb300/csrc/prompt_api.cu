@@ -1,5 +1,6 @@
-// prompt_api.cu -- the extern "C" entry points of rotary positions (declared
-// and documented in include/dsa.h): host-side argument checks.
+// prompt_api.cu -- the extern "C" entry points of rotary positions, of the
+// expanded form of the latent attention and of shared prefixes (declared and
+// documented in include/dsa.h): host-side argument checks and workspace sizes.
 #include <algorithm>
 #include <cmath>
 
@@ -21,6 +22,19 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
 }
+
+// The two calls of the expanded form run one after another in their stream, so
+// their scratch overlaps behind the status header.
+size_t prompt_ws(const dsa_batch* b) {
+    return with_header(std::max(prompt_mla_scratch_bytes(to_dev(b)), mla_expand_scratch_bytes(to_dev(b))));
+}
+
+dsa_status check(const dsa_expanded* x) {
+    if (!x || x->rows < 0 || !given(x->off, 4)) return DSA_ERR_INVALID_ARG;
+    return x->rows == 0 || (given(x->kv) && given(x->k_pe)) ? DSA_OK : DSA_ERR_INVALID_ARG;
+}
+
+ExpandedDev to_dev(const dsa_expanded* x) { return ExpandedDev{x->rows, x->off, x->kv, x->k_pe}; }
 
 }  // namespace
 
@@ -70,6 +84,39 @@ dsa_status dsa_rope(int32_t total_q, int32_t heads, int32_t dim, const uint16_t*
     return cuda_status(launch_rope(total_q, heads, dim, x, x_token, x_head, cos_t, sin_t, table_rows, positions,
                                    (flags & DSA_ROPE_NEIGHBOUR) != 0, (flags & DSA_ROPE_INVERSE) != 0, out, out_token,
                                    out_head, static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_prompt_workspace_size(const dsa_batch* batch, size_t* bytes) {
+    if (!bytes || !batch || batch->batch < 1 || batch->batch > 65535 || batch->total_q < 0 || batch->max_q < 0 ||
+        batch->max_ctx < 0)
+        return DSA_ERR_INVALID_ARG;
+    *bytes = (prompt_ws(batch) + 255) / 256 * 256;
+    return DSA_OK;
+}
+
+dsa_status dsa_mla_expand(const dsa_batch* batch, const dsa_pages* pages, const uint16_t* kv, const uint16_t* w_kv_b,
+                          const int32_t* first, const dsa_expanded* expanded, void* ws, size_t ws_bytes,
+                          void* stream) {
+    dsa_status st = check(batch, pages);
+    if (st != DSA_OK || (st = check(expanded)) != DSA_OK) return st;
+    if (check_ws(ws, ws_bytes, prompt_ws(batch)) != DSA_OK) return DSA_ERR_WORKSPACE;
+    if (batch->max_ctx == 0 || expanded->rows == 0) return DSA_OK;      // no row can be
+    if (!given(kv) || !given(w_kv_b) || !aligned(first, 4)) return DSA_ERR_INVALID_ARG;
+    return cuda_status(launch_mla_expand(to_dev(batch), to_dev(pages), kv, w_kv_b, first, to_dev(expanded),
+                                         scratch_of(ws), static_cast<int32_t*>(ws),
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_prompt_mla_fwd(const dsa_batch* batch, const uint16_t* q, const dsa_expanded* expanded, float sm_scale,
+                              uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    dsa_status st = check(batch);
+    if (st != DSA_OK || (st = check(expanded)) != DSA_OK) return st;
+    if (check_ws(ws, ws_bytes, prompt_ws(batch)) != DSA_OK) return DSA_ERR_WORKSPACE;
+    if (!positive(sm_scale)) return DSA_ERR_INVALID_ARG;
+    if (batch->total_q == 0 || batch->max_q == 0 || batch->max_ctx == 0 || expanded->rows == 0) return DSA_OK;
+    if (!given(q) || !given(out) || !aligned(lse, 16)) return DSA_ERR_INVALID_ARG;
+    return cuda_status(launch_prompt_mla(to_dev(batch), q, to_dev(expanded), sm_scale, out, lse, scratch_of(ws),
+                                         static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,617 @@
+// prompt_mla.cu -- causal attention of prompts over expanded rows: 64 heads,
+// keys of 192 + 64 columns (the 64 shared by all heads), values of 256.
+//
+// A CTA pair takes an item: a head, and 256 consecutive new rows of a sequence
+// (128 of them each CTA).  It walks the rows' keys in tiles of 128 positions:
+//   S[256 q, 128 pos] = Q K^T     each CTA stages its 128 query rows (64 KiB,
+//                                 resident) and 64 of the tile's keys
+//   P = 2^(S c - m)               the running maximum m of a row moves only when
+//                                 a score exceeds it by 2^8 (then O is
+//                                 rescaled); P is rounded to bf16 for the
+//                                 product, the MMA's type, its sum taken before
+//                                 in fp32: an error of half a bf16 step of a
+//                                 weight, like the result's own rounding
+//   O[256 q, 256] += P V          each CTA stages 128 of the value columns of
+//                                 all 128 positions
+// O (256 TMEM columns) and two S tiles (128 each) fill a CTA's TMEM, a lane per
+// query row; nothing but barriers and item numbers crosses between the CTAs.  S of
+// tile g + 1 is issued before PV of tile g, so the softmax of a tile runs under the
+// tensor work of the next.
+//
+// What is masked cannot leak: expanded values are finite (a row that is not
+// carries NaN in its key instead), rows behind a sequence up to the next multiple
+// of 128 are zero, and a tile ends at such a multiple.  A masked score is replaced by
+// -inf before anything is formed of it, its weight is 0, and 0 times a finite
+// value is 0.
+//
+// The new rows of a sequence are cut into 256s from their end, so that a
+// remainder has the fewest keys (12 prompts of 839 to 2,012 rows: 420 tiles a pair
+// cut from the front, 401 from the end).
+//
+// Items are taken from a counter, all query tiles of a head before the next
+// head's, longest first: pairs that run together then read the same keys (a
+// pair alone reads 128 KB a tile, 9 TB/s over the GPU; in step they come from
+// L2), and short items fill the end.  The order decides which pair computes an item,
+// never what it computes.
+//
+// Roles of a CTA's 12 warps: Q and K loads, MMA (rank 0 only), V loads, items,
+// eight softmax / epilogue warps (two threads share a query row, 64 positions
+// each).
+//
+// Bounds.  A tile is 16 MMAs of N = 128 and 8 of N = 256: 2,048 cycles for
+// 33.6 MFLOP at M = 256.
+#include <algorithm>
+#include <atomic>
+
+#include "internal.h"
+#include "prompt.h"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kTile = 128;                   // positions per tile
+constexpr int kRows = 256;                   // query rows of an item, half of them each CTA's
+constexpr int kThreads = 384;
+constexpr int kSoftWarps = 8;
+constexpr int kQBytes = 128 * 128;           // 128 rows x 64 columns
+constexpr int kKBytes = 64 * 128;            // 64 rows x 64 columns
+constexpr int kQChunks = kHeadQK / 64;       // 4
+constexpr int kStages = 2;                   // whole tiles of K and of V
+constexpr uint32_t kOCol = 0, kSCol = 256;   // TMEM columns
+constexpr int kSlots = 2;                    // items published ahead
+constexpr int kMaxPairs = 96;
+constexpr float kRescale = 8.f;              // log2
+static_assert(kTile == kExpRoom, "a tile ends where a sequence's zeroed rows do");
+
+struct Item {
+    int32_t row;                 // packed row of the first of its query rows
+    int32_t rows;                // how many there are
+    int32_t pos;                 // position of the first
+    int32_t at;                  // expanded row of position 0
+    int32_t head, tiles;         // no tiles: nothing left
+};
+
+struct Smem {
+    alignas(1024) uint8_t q[kQChunks * kQBytes];
+    alignas(1024) uint8_t k[kStages * kQChunks * kKBytes];
+    alignas(1024) uint8_t v[kStages * 2 * kQBytes];      // two blocks of 64 columns x 128 positions
+    alignas(1024) uint8_t p[2 * kQBytes];
+    alignas(8) uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
+    uint64_t qfull[kQChunks], qempty[kQChunks], sfull[2], sempty[2], pfull, pvdone, ofree, itemfull[kSlots], itemempty[kSlots];
+    uint64_t numfull[kSlots], numempty[kSlots];          // item numbers on their way to rank 1
+    Item item[kSlots];
+    uint32_t number[kSlots];
+    float xch[2][32 * kSoftWarps];
+    uint32_t tmem;
+};
+static_assert(sizeof(Smem) <= 232448, "one CTA's shared memory");
+
+struct Args {
+    BatchDev bd;
+    ExpandedDev x;
+    float scale_log2;
+    uint16_t* out;
+    float* lse;
+    const int32_t* start;        // [B + 1] query tiles before a sequence
+    uint32_t* next;              // number of the next item that nobody has taken
+    int32_t* status;
+};
+
+// Query tiles before each sequence, and the counter behind the items that the
+// pairs begin with.  A sequence that breaks the bounds has none.
+__global__ void __launch_bounds__(1024)
+    prompt_plan_kernel(const BatchDev bd, const ExpandedDev x, int32_t* start, uint32_t* next, uint32_t pairs,
+                       int32_t* status) {
+    __shared__ int32_t sums[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (tid == 0) {
+        *next = pairs;
+        start[0] = 0;
+    }
+    int32_t carry = 0;
+    for (int b0 = 0; b0 < bd.B; b0 += 1024) {
+        const int b = b0 + tid;
+        SeqInfo s{0, 0, 0};
+        int32_t n = 0;
+        if (b < bd.B && load_seq(bd, b, status, s) && s.nq > 0 && expanded_at(x, b, s.ctx, status) >= 0)
+            n = (s.nq + kRows - 1) / kRows;
+        int32_t incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sums[warp] = incl;
+        __syncthreads();
+        if (warp == 0) {
+            int32_t v = sums[lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            sums[lane] = v;
+        }
+        __syncthreads();
+        if (b < bd.B) start[b + 1] = carry + incl + (warp > 0 ? sums[warp - 1] : 0);
+        carry += sums[31];
+        __syncthreads();
+    }
+}
+
+__device__ __forceinline__ Item item_of(const Args& a, uint32_t number) {
+    Item it{0, 0, 0, 0, 0, 0};
+    if (number >= (uint32_t)a.start[a.bd.B] * kH) return it;
+    const int b = last_at_or_below(a.start, a.bd.B, (int32_t)(number / kH));
+    const uint32_t tiles = (uint32_t)(a.start[b + 1] - a.start[b]), in = number - (uint32_t)a.start[b] * kH;
+    SeqInfo s;
+    if (!load_seq(a.bd, b, nullptr, s)) return it;       // lengths that change under the call
+    const int32_t end = s.nq - kRows * (int32_t)(in % tiles), i0 = max(0, end - kRows);
+    if (end <= 0) return it;
+    it.head = (int32_t)(in / tiles);
+    it.row = s.q0 + i0;
+    it.rows = end - i0;
+    it.pos = s.ctx - s.nq + i0;
+    it.at = __ldg(a.x.off + b);
+    it.tiles = (it.pos + it.rows - 1) / kTile + 1;
+    return it;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    prompt_mla_kernel(const Args a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_pe) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Smem& S = *reinterpret_cast<Smem*>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank();
+    pdl_launch_dependents();
+    if (smem_u32(smem_raw) & 1023u) {            // the swizzle goes by address bits
+        if (tid == 0) latch_status(a.status, DSA_ERR_INTERNAL);
+        return;                                  // both CTAs: the same launch, the same offset
+    }
+    if (tid == kThreads - 32) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&S.kfull[i]), 2);
+            mbar_init(smem_u32(&S.kempty[i]), 1);
+            mbar_init(smem_u32(&S.vfull[i]), 2);
+            mbar_init(smem_u32(&S.vempty[i]), 1);
+        }
+        for (int i = 0; i < kQChunks; ++i) {
+            mbar_init(smem_u32(&S.qfull[i]), 2);
+            mbar_init(smem_u32(&S.qempty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&S.sfull[i]), 1);
+            mbar_init(smem_u32(&S.sempty[i]), 2 * kSoftWarps);
+        }
+        mbar_init(smem_u32(&S.pfull), 2 * kSoftWarps);
+        mbar_init(smem_u32(&S.pvdone), 1);
+        mbar_init(smem_u32(&S.ofree), 2 * kSoftWarps);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(smem_u32(&S.itemfull[i]), 1);
+            mbar_init(smem_u32(&S.itemempty[i]), kSoftWarps + (rank == 0 ? 3 : 2));   // the warps that read items
+            mbar_init(smem_u32(&S.numfull[i]), 1);
+            mbar_init(smem_u32(&S.numempty[i]), 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(&S.tmem), 512);
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+        prefetch_tmap(&tm_pe);
+    }
+    __syncwarp();
+    cluster_arrive();                            // the peer may use this CTA's barriers and TMEM ..
+    pdl_wait();                                  // inputs, and the scratch of an earlier call
+    tc_fence_before();
+    __syncthreads();
+    cluster_wait();                              // .. and this CTA the peer's
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    Item it;
+    bool ok = true;
+    // the barrier at `b`'s offset in the CTA of rank 0
+    auto lead = [&](uint64_t& b) -> uint32_t { return map_to_cluster_rank(smem_u32(&b), 0); };
+    // bounded; a thread whose wait expired waits for nothing any more
+    auto wait = [&](uint64_t& b, uint32_t parity) -> bool {
+        if (ok && !mbar_wait_rolled(smem_u32(&b), parity)) {
+            ok = false;
+            latch_status(a.status, DSA_ERR_TIMEOUT);
+        }
+        return ok;
+    };
+    // the next item that warp 3 published; false behind the last
+    uint32_t items_read = 0;
+    auto next_item = [&](Item& to) -> bool {
+        const uint32_t slot = items_read % kSlots;
+        wait(S.itemfull[slot], (items_read / kSlots) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        to = S.item[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&S.itemempty[slot]));
+        ++items_read;
+        return ok && to.tiles > 0;
+    };
+
+    if (warp == 0) {
+        // Q and K loads: lane 0 waits, then each lane issues a box.  Rows behind
+        // the last new row are another sequence's or zeros: nobody reads what
+        // comes of them.
+        uint32_t g = 0, seg = 0;
+        Item n;
+        bool more = next_item(it);
+        for (; more; ++seg) {
+            for (int32_t t = 0; ok && t < it.tiles; ++t, ++g) {
+                if (t == 0) {
+#pragma unroll 1
+                    for (int c = 0; ok && c < kQChunks; ++c) {
+                        if (lane == 0 && (seg == 0 || wait(S.qempty[c], (seg - 1) & 1))) {
+                            mbar_arrive_expect_tx_pair(lead(S.qfull[c]), kQBytes);
+                            tma_load_2d_pair(smem_u32(S.q + c * kQBytes), &tm_q, lead(S.qfull[c]),
+                                             it.head * kHeadQK + 64 * c, it.row + 128 * (int)rank);
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                    }
+                }
+                const uint32_t st = g % kStages;
+                const uint32_t bar = lead(S.kfull[st]);
+                if (lane == 0 && (g < kStages || wait(S.kempty[st], (g / kStages - 1) & 1)))
+                    mbar_arrive_expect_tx_pair(bar, kQChunks * kKBytes);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                const int32_t r = it.at + t * kTile + 64 * (int)rank;
+                uint8_t* to = S.k + (st * kQChunks + lane) * kKBytes;
+                if (ok && lane < kQChunks - 1)
+                    tma_load_2d_pair(smem_u32(to), &tm_k, bar, it.head * kExpRow + 64 * lane, r);
+                else if (ok && lane == kQChunks - 1)
+                    tma_load_2d_pair(smem_u32(to), &tm_pe, bar, 0, r);
+            }
+            // the queries of the next item, whose place in shared memory is
+            // not free before this one's last S
+            more = next_item(n);
+            if (more && lane < kQChunks) tma_prefetch_2d(&tm_q, n.head * kHeadQK + 64 * lane, n.row + 128 * (int)rank);
+            it = n;
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // MMA: S of tile g + 1, then PV of tile g, issued by one elected
+            // lane, which also waits; an item's first S behind the last PV before
+            // it, under which its queries are loaded
+            constexpr uint32_t kIdS = idesc_bf16_f32(kRows, kTile), kIdO = idesc_bf16_f32(kRows, kHeadV, false, true);
+            // S of tile g; first / last of its item (number seg)
+            auto issue_s = [&](uint32_t g, bool first, bool last, uint32_t seg) {
+                const uint32_t buf = g & 1, st = g % kStages;
+                if (g >= 2 && !wait(S.sempty[buf], ((g >> 1) - 1) & 1)) return;
+                if (!wait(S.kfull[st], (g / kStages) & 1)) return;
+                tc_fence_after();
+                const uint64_t dq = sdesc_sw128(smem_u32(S.q), 0, 1024);
+                const uint64_t dk = sdesc_sw128(smem_u32(S.k + st * kQChunks * kKBytes), 0, 1024);
+#pragma unroll
+                for (int c = 0; c < kQChunks; ++c) {
+                    if (first) {
+                        if (!wait(S.qfull[c], seg & 1)) return;
+                        tc_fence_after();
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16_ss_pair(tmem + kSCol + kTile * buf, dq + c * (kQBytes >> 4) + 2 * k,
+                                         dk + c * (kKBytes >> 4) + 2 * k, kIdS, (c | k) != 0);
+                    if (last) mma_commit_pair(smem_u32(&S.qempty[c]));
+                }
+                mma_commit_pair(smem_u32(&S.kempty[st]));
+                mma_commit_pair(smem_u32(&S.sfull[buf]));
+            };
+            // PV of tile g, of whose positions `keys` are seen by some row
+            auto issue_pv = [&](uint32_t g, bool first, int32_t keys, uint32_t seg) {
+                if (first && seg > 0 && !wait(S.ofree, (seg - 1) & 1)) return;
+                const uint32_t st = g % kStages;
+                if (!wait(S.vfull[st], (g / kStages) & 1)) return;
+                if (!wait(S.pfull, g & 1)) return;
+                tc_fence_after();
+                const uint64_t dp = sdesc_sw128(smem_u32(S.p), 0, 1024);
+                const uint64_t dv = sdesc_sw128(smem_u32(S.v + st * 2 * kQBytes), kQBytes, 1024);
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                    if (16 * k < keys)
+                        mma_bf16_ss_pair(tmem + kOCol, dp + (k >> 2) * (kQBytes >> 4) + 2 * (k & 3), dv + 128 * k, kIdO,
+                                         !first || k != 0);
+                mma_commit_pair(smem_u32(&S.vempty[st]));
+                mma_commit_pair(smem_u32(&S.pvdone));
+            };
+            uint32_t g = 0;
+            for (uint32_t seg = 0; next_item(it); ++seg) {
+                if (elect_one()) {
+                    issue_s(g, true, it.tiles == 1, seg);
+                    for (int32_t t = 0; ok && t < it.tiles; ++t) {
+                        if (t + 1 < it.tiles) issue_s(g + t + 1, false, t + 2 == it.tiles, seg);
+                        if (ok) issue_pv(g + t, t == 0, it.pos + it.rows - t * kTile, seg);
+                    }
+                }
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, ok);
+                g += it.tiles;
+            }
+        }
+    } else if (warp == 2) {
+        // V loads
+        uint32_t g = 0;
+        while (next_item(it)) {
+            for (int32_t t = 0; ok && t < it.tiles; ++t, ++g) {
+                const uint32_t st = g % kStages;
+                const uint32_t bar = lead(S.vfull[st]);
+                if (lane == 0 && (g < kStages || wait(S.vempty[st], (g / kStages - 1) & 1)))
+                    mbar_arrive_expect_tx_pair(bar, 2 * kQBytes);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (ok && lane < 2)
+                    tma_load_2d_pair(smem_u32(S.v + (st * 2 + lane) * kQBytes), &tm_v, bar,
+                                     it.head * kExpRow + kNope + 128 * (int)rank + 64 * lane, it.at + t * kTile);
+            }
+        }
+    } else if (warp == 3) {
+        // items: rank 0 takes their numbers and passes them on
+        for (uint32_t n = 0; ok; ++n) {
+            const uint32_t slot = n % kSlots, turn = n / kSlots;
+            uint32_t number = 0;
+            auto wait_peer = [&](uint64_t& b, uint32_t parity) {
+                if (ok && !mbar_wait_peer(smem_u32(&b), parity)) {
+                    ok = false;
+                    latch_status(a.status, DSA_ERR_TIMEOUT);
+                }
+            };
+            if (n >= kSlots) wait(S.itemempty[slot], (turn - 1) & 1);
+            if (lane == 0 && ok) {
+                if (rank == 0) {
+                    number = n == 0 ? blockIdx.x >> 1 : atomicAdd(a.next, 1u);
+                    if (n >= kSlots) wait_peer(S.numempty[slot], (turn - 1) & 1);
+                    if (ok) {
+                        st_peer_u32(map_to_cluster_rank(smem_u32(&S.number[slot]), 1), number);
+                        mbar_arrive_peer(map_to_cluster_rank(smem_u32(&S.numfull[slot]), 1));
+                    }
+                } else {
+                    wait_peer(S.numfull[slot], turn & 1);
+                    number = *reinterpret_cast<volatile uint32_t*>(&S.number[slot]);
+                    if (ok) mbar_arrive_peer(lead(S.numempty[slot]));
+                }
+            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            it = item_of(a, __shfl_sync(0xffffffffu, number, 0));
+            if (lane == 0) {
+                S.item[slot] = it;
+                mbar_arrive(smem_u32(&S.itemfull[slot]));
+            }
+            __syncwarp();
+            if (it.tiles == 0) break;
+        }
+    } else {
+        // softmax and epilogue: TMEM lane = query row of this CTA
+        const int ln = tid - 128, x = ln & 127, half = ln >> 7;
+        const uint32_t tl = tmem + ((uint32_t)(x & ~31) << 16);
+        uint32_t g = 0, xb = 0;
+        auto exchange = [&](float v) -> float {
+            xb ^= 1;
+            S.xch[xb][ln] = v;
+            named_bar_sync(1, 32 * kSoftWarps);
+            return S.xch[xb][ln ^ 128];
+        };
+        // the warps agree on each item, since they meet at barriers
+        while (!named_bar_or(1, 32 * kSoftWarps, !next_item(it))) {
+            const int32_t first = it.pos + 128 * (int)rank;      // position of the CTA's first row
+            float m = -INFINITY, l = 0.f;
+            for (int32_t t = 0; t < it.tiles; ++t, ++g) {
+                const uint32_t buf = g & 1;
+                wait(S.sfull[buf], (g >> 1) & 1);
+                __syncwarp();
+                tc_fence_after();
+                uint32_t r[2][32];
+                tmem_ld_32x32b_x32(tl + kSCol + kTile * buf + 64 * half, r[0]);
+                tmem_ld_32x32b_x32(tl + kSCol + kTile * buf + 64 * half + 32, r[1]);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(lead(S.sempty[buf]));
+                if ((t + 1) * kTile - 1 > first) {
+                    const int32_t d = first + x - (t * kTile + 64 * half);       // the last column that the row sees
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        if (k > d) r[k >> 5][k & 31] = 0xFF800000u;
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 64; ++k) mx = fmaxf(mx, __uint_as_float(r[k >> 5][k & 31]));
+                mx = fmaxf(mx, exchange(mx)) * a.scale_log2;
+                const bool move = mx > m + kRescale || (m == -INFINITY && mx > m);
+                const float m_new = move ? mx : m;
+                const float f = move ? ex2_approx(m - m_new) : 1.f;
+                const float off = m_new == -INFINITY ? 0.f : m_new;
+                m = m_new;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t pk[32];
+#pragma unroll
+                for (int k = 0; k < 64; k += 2) {
+                    const float p0 = ex2_approx(fmaf(__uint_as_float(r[k >> 5][k & 31]), a.scale_log2, -off));
+                    const float p1 = ex2_approx(fmaf(__uint_as_float(r[k >> 5][(k & 31) + 1]), a.scale_log2, -off));
+                    sum[(k >> 1) & 3] += p0 + p1;
+                    pk[k >> 1] = pack_bf16x2(p0, p1);
+                }
+                l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                if (g > 0) wait(S.pvdone, (g - 1) & 1);
+                __syncwarp();
+                tc_fence_after();
+                if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+                    for (uint32_t c = 0; c < 128; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld_32x32b_x16(tl + kOCol + 128 * half + c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st_32x32b_x16(tl + kOCol + 128 * half + c, o);
+                    }
+                    tmem_st_wait();
+                }
+                uint8_t* pr = S.p + half * kQBytes + x * 128;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<uint4*>(pr + ((k ^ (x & 7)) << 4)) =
+                        make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(lead(S.pfull));
+            }
+            wait(S.pvdone, (g - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            // Every row sees itself, so l > 0 but where every score is -inf: NaN, as of the formula.
+            l += exchange(l);
+            const float inv = 1.f / l;
+            const int32_t mine = it.row + 128 * (int)rank, live = it.rows - 128 * (int)rank;      // rows of this CTA
+            if (ok && a.lse && half == 0 && x < live)
+                a.lse[(int64_t)(mine + x) * kH + it.head] = (m + log2f(l)) * kLn2;
+            // O through this warp's 4 KiB of P's buffer, so that a store covers
+            // whole 128-byte lines of 4 rows
+            uint8_t* stage = S.p + (warp - 4) * 4096;
+            const int32_t r0 = x & ~31;
+            if (ok && r0 < live) {
+#pragma unroll 1
+                for (uint32_t c = 0; c < 128; c += 64) {
+                    uint32_t o[2][32];
+                    tmem_ld_32x32b_x32(tl + kOCol + 128 * half + c, o[0]);
+                    tmem_ld_32x32b_x32(tl + kOCol + 128 * half + c + 32, o[1]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = pack_bf16x2(__uint_as_float(o[v >> 2][8 * (v & 3) + 2 * k]) * inv,
+                                               __uint_as_float(o[v >> 2][8 * (v & 3) + 2 * k + 1]) * inv);
+                        *reinterpret_cast<uint4*>(stage + lane * 128 + ((v ^ (lane & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int row = 4 * k + (lane >> 3), at = lane & 7;
+                        if (r0 + row < live)
+                            *reinterpret_cast<uint4*>(a.out + ((int64_t)(mine + r0 + row) * kH + it.head) * kHeadV +
+                                                      128 * half + c + 8 * at) =
+                                *reinterpret_cast<const uint4*>(stage + row * 128 + ((at ^ (row & 7)) << 4));
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(lead(S.ofree));
+        }
+    }
+    if (!ok) {
+        // let copies in flight land before the CTA's shared memory goes
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000u) __nanosleep(1000);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// Query tiles that the batch's bounds allow, over all heads.
+int64_t most_items(const BatchDev& bd) {
+    return ((int64_t)bd.total_q / kRows + std::min<int64_t>(bd.B, bd.total_q)) * kH;
+}
+
+}  // namespace
+
+int resident_pairs(const void* f, int threads, size_t smem, int most) {
+    constexpr int kMaxDevices = 64, kMaxKernels = 8;
+    static std::atomic<uintptr_t> key[kMaxKernels];
+    static std::atomic<int> cache[kMaxKernels][kMaxDevices];
+    int dev = 0, n = 0, slot = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return std::min(kDefaultSMs / 2, most);
+    }
+    for (; slot < kMaxKernels; ++slot) {
+        uintptr_t none = 0, mine = reinterpret_cast<uintptr_t>(f);
+        if (key[slot].compare_exchange_strong(none, mine) || none == mine) break;
+    }
+    if (slot < kMaxKernels && (n = cache[slot][dev].load(std::memory_order_relaxed)) > 0) return std::min(n, most);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * num_sms());
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, f, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        return std::min(num_sms() / 2, most);
+    }
+    n = std::min(n, num_sms() / 2);
+    if (slot < kMaxKernels) cache[slot][dev].store(n, std::memory_order_relaxed);
+    return std::min(n, most);
+}
+
+size_t prompt_mla_scratch_bytes(const BatchDev& bd) { return ((size_t)bd.B + 1) * sizeof(int32_t) + sizeof(uint32_t); }
+
+cudaError_t launch_prompt_mla(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, float sm_scale,
+                              uint16_t* out, float* lse, void* scratch, int32_t* status, cudaStream_t stream) {
+    const int pairs = (int)std::min<int64_t>(
+        resident_pairs(reinterpret_cast<const void*>(prompt_mla_kernel), kThreads, sizeof(Smem), kMaxPairs), most_items(bd));
+    Args a{};
+    a.bd = bd;
+    a.x = x;
+    a.scale_log2 = sm_scale * kLog2e;
+    a.out = out;
+    a.lse = lse;
+    a.next = static_cast<uint32_t*>(scratch);
+    int32_t* start = static_cast<int32_t*>(scratch) + 1;
+    a.start = start;
+    a.status = status;
+    CUtensorMap tm_q, tm_k, tm_v, tm_pe;
+    if (!make_tmap_bf16_2d(&tm_q, q, (uint64_t)kH * kHeadQK, (uint64_t)bd.total_q, 64, 128) ||
+        !make_tmap_bf16_2d(&tm_k, x.kv, (uint64_t)kH * kExpRow, (uint64_t)x.rows, 64, 64) ||
+        !make_tmap_bf16_2d(&tm_v, x.kv, (uint64_t)kH * kExpRow, (uint64_t)x.rows, 64, kTile) ||
+        !make_tmap_bf16_2d(&tm_pe, x.k_pe, DSA_ROPE_DIM, (uint64_t)x.rows, 64, 64))
+        return cudaErrorInvalidValue;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, prompt_plan_kernel, bd, x, start, a.next, (uint32_t)pairs, status);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+    if ((e = cudaFuncSetAttribute(prompt_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem))) !=
+        cudaSuccess)
+        return e;
+    cfg.gridDim = dim3(2 * (unsigned)pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Smem);
+    e = cudaLaunchKernelEx(&cfg, prompt_mla_kernel, a, tm_q, tm_k, tm_v, tm_pe);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+}  // namespace dsa

@@ -385,6 +385,11 @@ __device__ __forceinline__ bool mbar_wait_peer(uint32_t bar, uint32_t parity) {
     }
 }
 
+// A box of the tensor of `tmap` brought to L2.
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(tmap), "r"(c0), "r"(c1) : "memory");
+}
+
 // A box of this CTA's shared memory to the tensor of `tmap`, in this thread's
 // current bulk group; groups that may still be reading shared memory, and those
 // whose writes may still be under way.

@@ -63,3 +63,81 @@ def test_rope_refusals(lib, bad, code):
 
 def test_rope_without_tokens(lib):
     assert _rope(lib, t=0, x=0, out=0, cos=0, sin=0, pos=0) == 0
+
+
+def _batch(B=2, total_q=8, max_q=4, max_ctx=100, stride=100, q_off=0x10000, ctx=0x20000):
+    import sparse_attention_gb300 as dsa
+    return dsa.DsaBatch(B, total_q, max_q, max_ctx, stride, q_off, ctx)
+
+
+def _pages(size=16, width=7, pool=20, table=0x30000):
+    import sparse_attention_gb300 as dsa
+    return dsa.DsaPages(size, width, pool, table)
+
+
+def _expanded(rows=256, off=0x40000, kv=P, k_pe=P):
+    import sparse_attention_gb300 as dsa
+    return dsa.DsaExpanded(rows, off, kv, k_pe)
+
+
+def _ws(lib, b):
+    n = ctypes.c_size_t(0)
+    assert lib.dsa_prompt_workspace_size(ctypes.byref(b), ctypes.byref(n)) == 0
+    return n.value
+
+
+def test_prompt_workspace(lib):
+    n = ctypes.c_size_t(0)
+    assert lib.dsa_prompt_workspace_size(None, ctypes.byref(n)) == 1
+    assert lib.dsa_prompt_workspace_size(ctypes.byref(_batch()), None) == 1
+    assert lib.dsa_prompt_workspace_size(ctypes.byref(_batch(B=0)), ctypes.byref(n)) == 1
+    assert _ws(lib, _batch()) % 256 == 0 and _ws(lib, _batch(B=65535)) >= 256 + 4 * 65537
+
+
+def _call(lib, which, b, g, x, q=P, out=P, lse=None, scale=0.0625, first=None, w=P, ws=WS, n=None):
+    n = _ws(lib, _batch()) if n is None else n
+    b, x = (ctypes.byref(t) if t is not None else None for t in (b, x))
+    if which == "prompt":
+        return lib.dsa_prompt_mla_fwd(b, q, x, ctypes.c_float(scale), out, lse, ws, n, None)
+    return lib.dsa_mla_expand(b, ctypes.byref(g) if g is not None else None, q, w, first, x, ws, n, None)
+
+
+@pytest.mark.parametrize("which", ["prompt", "expand"])
+@pytest.mark.parametrize("b,x,kw,code", [
+    (None, {}, {}, 1), (dict(B=0), {}, {}, 1), (dict(B=65536), {}, {}, 1), (dict(total_q=-1), {}, {}, 1),
+    (dict(stride=99), {}, {}, 1), (dict(q_off=0), {}, {}, 1), (dict(ctx=0x20002), {}, {}, 1),
+    (dict(total_q=1 << 26), {}, {}, 2), (dict(max_q=(1 << 19) + 1), {}, {}, 2),
+    ({}, None, {}, 1), ({}, dict(rows=-1), {}, 1), ({}, dict(off=0), {}, 1), ({}, dict(off=0x40002), {}, 1),
+    ({}, dict(kv=0), {}, 1), ({}, dict(k_pe=P + 8), {}, 1), ({}, {}, dict(q=0), 1), ({}, {}, dict(q=P + 2), 1),
+    ({}, {}, dict(ws=0), 3), ({}, {}, dict(ws=WS + 4), 3), ({}, {}, dict(n=256), 3),
+])
+def test_expanded_form_refusals(lib, which, b, x, kw, code):
+    got = _call(lib, which, _batch(**b) if b is not None else None, None, _expanded(**x) if x is not None else None, **kw)
+    assert got == code
+
+
+@pytest.mark.parametrize("g,kw,code", [
+    (dict(size=8), {}, 1), (dict(size=48), {}, 1), (dict(width=6), {}, 1), (dict(pool=0), {}, 1), (dict(table=0), {}, 1),
+    (dict(pool=1 << 27), {}, 2), (None, dict(w=0), 1), (None, dict(first=0x50002), 1),
+])
+def test_expand_refusals(lib, g, kw, code):
+    assert _call(lib, "expand", _batch(), _pages(**g) if g is not None else None, _expanded(), **kw) == code
+
+
+@pytest.mark.parametrize("kw", [dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan), dict(out=0),
+                                dict(out=P + 4), dict(lse=P + 4)])
+def test_prompt_refusals(lib, kw):
+    assert _call(lib, "prompt", _batch(), None, _expanded(), **kw) == 1
+
+
+def test_calls_without_rows(lib):
+    assert _call(lib, "prompt", _batch(total_q=0), None, _expanded(), q=0, out=0) == 0
+    assert _call(lib, "expand", _batch(max_ctx=0), None, _expanded(), q=0, w=0) == 0
+    assert _call(lib, "expand", _batch(), None, _expanded(rows=0, kv=0, k_pe=0), q=0, w=0) == 0
+
+
+@pytest.mark.parametrize("kw,code", [(dict(t=-1), 1), (dict(o=0), 1), (dict(w=P + 2), 1), (dict(y=0), 1), (dict(ws=0), 3),
+                                     (dict(n=256), 3), (dict(t=0, o=0, w=0, y=0), 0)])
+def test_o_proj_refusals(lib, kw, code):
+    a = dict(dict(t=8, o=P, w=P, y=P, ws=WS, n=1 << 30), **kw)
+    assert lib.dsa_mla_o_proj(a["t"], a["o"], a["w"], a["y"], a["ws"], a["n"], None) == code
