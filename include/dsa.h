@@ -476,17 +476,18 @@ DSA_API dsa_status dsa_tree_commit(const dsa_batch* batch, const dsa_pages* page
                                    const int32_t* accepted, int32_t layers, int64_t cache_rows, uint16_t* kv,
                                    uint16_t* k_idx, int32_t* ctx_new, void* ws, size_t ws_bytes, void* stream);
 
-/* ---- Prompts over the latent cache.
+/* ---- Prompts over the latent cache, and sequences behind a shared prefix.
  *
  *   dsa_rope_table       rotary tables of a range of positions
  *   dsa_rope             a part of every head rotated (queries, index queries)
  *   dsa_mla_expand       latent cache rows -> each head's keys and values
  *   dsa_prompt_mla_fwd   causal attention of new rows over expanded rows
  *   dsa_mla_o_proj       o_proj on its result
+ *   dsa_prefix_mla_fwd   latent attention of sequences whose first rows are shared
  *
  * Expanded or absorbed.  A (query, key) pair of one layer takes 65,536 flop in
  * expanded form and 139,264 in absorbed form (dsa_sparse_mla_fwd,
- * dsa_tree_mla_fwd), but each cached row has to be expanded
+ * dsa_tree_mla_fwd, dsa_prefix_mla_fwd), but each cached row has to be expanded
  * first (29.4 MFLOP) and is 57,472 bytes wide then instead of 1,152.  So prompts and
  * chunks of some 400 and more new tokens are cheaper expanded, decode steps
  * absorbed.  Both forms are exact: without an indexer, or for contexts of at
@@ -607,6 +608,38 @@ DSA_API dsa_status dsa_prompt_mla_fwd(const dsa_batch* batch, const uint16_t* q,
  * workspace and errors as there. */
 DSA_API dsa_status dsa_mla_o_proj(int32_t total_q, const uint16_t* o_mid, const uint16_t* w_o, uint16_t* y, void* ws,
                                   size_t ws_bytes, void* stream);
+
+/* Groups of consecutive sequences that share their first rows.  off (DEVICE
+ * int32 [groups + 1]): group g is sequences off[g] .. off[g+1] - 1; off[0] = 0,
+ * ascending, off[groups] = batch.  shared (DEVICE int32 [groups]): the first
+ * shared[g] positions of every sequence of group g that has new rows hold the same
+ * rows, and at most its ctx_len[b] - n_b.  A sequence without a common prefix is a
+ * group of its own, or one of a group with shared = 0. */
+typedef struct dsa_groups {
+    int32_t groups;
+    const int32_t* off;
+    const int32_t* shared;
+} dsa_groups;
+
+/* Bytes of workspace that dsa_prefix_mla_fwd needs for `batch` in `groups`
+ * groups (its arrays are not read): some 263 KB a new row and sequence (fp32
+ * results over the shared and over the own part before they are joined).  Host
+ * only. */
+DSA_API dsa_status dsa_prefix_workspace_size(const dsa_batch* batch, const dsa_groups* groups, size_t* bytes);
+
+/* dsa_tree_mla_fwd for sequences behind shared prefixes: the same arguments,
+ * results and errors, but the shared rows (rounded down to a multiple of 128)
+ * are read once for each two new rows of the whole group, from the cache of its first
+ * sequence with new rows, instead of once for each two of every sequence.  With pages the
+ * sequences' block tables name the same pages there; contiguous caches hold the
+ * rows once per sequence.
+ *   mask  as there, or NULL: each new row sees itself and those before it
+ * Groups that are not the whole batch in order, or a shared length that is
+ * negative or beyond a sequence's committed rows, latch DSA_ERR_BAD_BATCH, and every sequence
+ * (of the group with that length) is computed by itself.  Three launches. */
+DSA_API dsa_status dsa_prefix_mla_fwd(const dsa_batch* batch, const dsa_groups* groups, const dsa_pages* pages,
+                                      const uint16_t* q, const uint16_t* kv, const uint64_t* mask, float sm_scale,
+                                      uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -38,7 +38,7 @@ EXPORTS = ("dsa_status_string", "dsa_last_cuda_error", "dsa_kernel_launch_count"
            "dsa_index_key_producer", "dsa_quantize_fp8", "dsa_indexer_scores_fp8", "dsa_forward_fp8",
            "dsa_tree_workspace_size", "dsa_step_tables", "dsa_latent_append", "dsa_tree_mla_fwd", "dsa_tree_topk",
            "dsa_tree_commit", "dsa_rope_table", "dsa_rope", "dsa_prompt_workspace_size", "dsa_mla_expand",
-           "dsa_prompt_mla_fwd", "dsa_mla_o_proj")
+           "dsa_prompt_mla_fwd", "dsa_mla_o_proj", "dsa_prefix_workspace_size", "dsa_prefix_mla_fwd")
 
 
 class DsaError(RuntimeError):
@@ -59,6 +59,10 @@ class DsaBatch(ctypes.Structure):
 class DsaPages(ctypes.Structure):
     _fields_ = [("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("pool_pages", ctypes.c_int32),
                 ("block_table", ctypes.c_void_p)]
+
+
+class DsaGroups(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("off", ctypes.c_void_p), ("shared", ctypes.c_void_p)]
 
 
 class DsaExpanded(ctypes.Structure):
@@ -122,6 +126,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dsa_mla_expand.argtypes = [BP, GP, P, P, P, XP, P, sz, P]
     lib.dsa_prompt_mla_fwd.argtypes = [BP, P, XP, f32, P, P, P, sz, P]
     lib.dsa_mla_o_proj.argtypes = [i32, P, P, P, P, sz, P]
+    RP = ctypes.POINTER(DsaGroups)
+    lib.dsa_prefix_workspace_size.argtypes = [BP, RP, ctypes.POINTER(sz)]
+    lib.dsa_prefix_mla_fwd.argtypes = [BP, RP, GP, P, P, P, f32, P, P, P, sz, P]
     for name in EXPORTS:
         if name not in ("dsa_status_string", "dsa_last_cuda_error", "dsa_kernel_launch_count"):
             getattr(lib, name).restype = ctypes.c_int
@@ -665,3 +672,46 @@ def mla_o_proj(o_mid, w_o, y, ws, stream=None):
         _typed("w_o", w_o, bf16, D_HIDDEN * H * D_HEAD, dev), _typed("y", y, bf16, total_q * D_HIDDEN, dev),
         ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "dsa_mla_o_proj")
     return y
+
+
+class Groups:
+    """Host handle of a dsa_groups.  Keeps its device arrays alive."""
+
+    def __init__(self, off: torch.Tensor, shared: torch.Tensor):
+        dev, n = off.get_device(), shared.numel()
+        if dev < 0:
+            raise ValueError("device tensor expected")
+        self.off, self.shared = off, shared
+        self.c = DsaGroups(n, _typed("off", off, torch.int32, n + 1, dev), _typed("shared", shared, torch.int32, 0, dev))
+
+
+def make_groups(off: torch.Tensor, shared: torch.Tensor) -> Groups:
+    """Groups of consecutive sequences off[g] .. off[g + 1] - 1 whose first shared[g] cache rows are the same."""
+    return Groups(off, shared)
+
+
+def prefix_workspace(batch: Batch, groups: Groups, device="cuda") -> torch.Tensor:
+    """A workspace of prefix_mla_fwd with a cleared status word."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().dsa_prefix_workspace_size(ctypes.byref(batch.c), ctypes.byref(groups.c), ctypes.byref(n)),
+           "dsa_prefix_workspace_size")
+    ws = torch.empty(int(n.value), dtype=torch.uint8, device=device)
+    reset_device_status(ws)
+    return ws
+
+
+def prefix_mla_fwd(batch: Batch, groups: Groups, q, kv, mask, sm_scale: float, out, lse=None,
+                   pages: Optional[Pages] = None, ws=None, stream=None):
+    """tree_mla_fwd for groups of sequences that share their first rows, which
+    are read once a group (see dsa_prefix_mla_fwd).  mask None: a chain."""
+    dev, bf16 = _here("dsa_prefix_mla_fwd", ws, stream), torch.bfloat16
+    c = batch.c
+    pg, rows = _paged(batch, pages, dev)
+    if groups.off.get_device() != dev:
+        raise ValueError(f"groups: expected on cuda:{dev}")
+    _check(load_library().dsa_prefix_mla_fwd(
+        ctypes.byref(c), ctypes.byref(groups.c), pg, _typed("q", q, bf16, c.total_q * H * D_QK, dev),
+        _typed("kv", kv, bf16, rows * D_QK, dev), _typed("mask", mask, torch.int64, c.total_q, dev), float(sm_scale),
+        _typed("out", out, bf16, c.total_q * H * D_V, dev), _typed("lse", lse, torch.float32, c.total_q * H, dev),
+        ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "dsa_prefix_mla_fwd")
+    return out

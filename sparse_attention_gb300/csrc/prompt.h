@@ -43,6 +43,12 @@ __device__ __forceinline__ int last_at_or_below(const int32_t* start, int n, int
     return lo;
 }
 
+// Device view of dsa_groups.
+struct GroupsDev {
+    int32_t n;
+    const int32_t *off, *shared;
+};
+
 // CTA pairs of kernel `f` that can be resident at once on the current device,
 // at most `most`.
 int resident_pairs(const void* f, int threads, size_t smem, int most);
@@ -62,5 +68,10 @@ cudaError_t launch_mla_expand(const BatchDev& bd, const PagesDev& pg, const uint
 size_t prompt_mla_scratch_bytes(const BatchDev& bd);
 cudaError_t launch_prompt_mla(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, float sm_scale,
                               uint16_t* out, float* lse, void* scratch, int32_t* status, cudaStream_t stream);
+
+size_t prefix_mla_scratch_bytes(const BatchDev& bd, int32_t groups);
+cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const PagesDev& pg, const uint16_t* q,
+                              const uint16_t* kv, const uint64_t* mask, float sm_scale, uint16_t* out, float* lse,
+                              void* scratch, int32_t* status, cudaStream_t stream);
 
 }  // namespace dsa

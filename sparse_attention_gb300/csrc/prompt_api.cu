@@ -29,6 +29,10 @@ size_t prompt_ws(const dsa_batch* b) {
     return with_header(std::max(prompt_mla_scratch_bytes(to_dev(b)), mla_expand_scratch_bytes(to_dev(b))));
 }
 
+size_t prefix_ws(const dsa_batch* b, const dsa_groups* g) {
+    return with_header(prefix_mla_scratch_bytes(to_dev(b), g->groups));
+}
+
 dsa_status check(const dsa_expanded* x) {
     if (!x || x->rows < 0 || !given(x->off, 4)) return DSA_ERR_INVALID_ARG;
     return x->rows == 0 || (given(x->kv) && given(x->k_pe)) ? DSA_OK : DSA_ERR_INVALID_ARG;
@@ -116,6 +120,33 @@ dsa_status dsa_prompt_mla_fwd(const dsa_batch* batch, const uint16_t* q, const d
     if (batch->total_q == 0 || batch->max_q == 0 || batch->max_ctx == 0 || expanded->rows == 0) return DSA_OK;
     if (!given(q) || !given(out) || !aligned(lse, 16)) return DSA_ERR_INVALID_ARG;
     return cuda_status(launch_prompt_mla(to_dev(batch), q, to_dev(expanded), sm_scale, out, lse, scratch_of(ws),
+                                         static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_prefix_workspace_size(const dsa_batch* batch, const dsa_groups* groups, size_t* bytes) {
+    if (!bytes || !batch || batch->batch < 1 || batch->batch > 65535 || batch->total_q < 0 || batch->max_q < 0 ||
+        batch->max_ctx < 0 || !groups || groups->groups < 1 || groups->groups > batch->batch)
+        return DSA_ERR_INVALID_ARG;
+    *bytes = (prefix_ws(batch, groups) + 255) / 256 * 256;
+    return DSA_OK;
+}
+
+dsa_status dsa_prefix_mla_fwd(const dsa_batch* batch, const dsa_groups* groups, const dsa_pages* pages,
+                              const uint16_t* q, const uint16_t* kv, const uint64_t* mask, float sm_scale,
+                              uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    const dsa_status st = check(batch, pages);
+    if (st != DSA_OK) return st;
+    if (!groups || groups->groups < 1 || groups->groups > batch->batch || !given(groups->off, 4) ||
+        !given(groups->shared, 4))
+        return DSA_ERR_INVALID_ARG;
+    if (batch->max_q > DSA_MAX_TREE) return DSA_ERR_UNSUPPORTED;
+    if (batch->total_q >= (1 << 25)) return DSA_ERR_UNSUPPORTED;     // 64 query rows each, in int32 TMA coordinates
+    if (check_ws(ws, ws_bytes, prefix_ws(batch, groups)) != DSA_OK) return DSA_ERR_WORKSPACE;
+    if (!positive(sm_scale)) return DSA_ERR_INVALID_ARG;
+    if (batch->total_q == 0 || batch->max_q == 0 || batch->max_ctx == 0) return DSA_OK;      // no row can be
+    if (!given(q) || !given(kv) || !aligned(mask, 8) || !given(out) || !aligned(lse, 16)) return DSA_ERR_INVALID_ARG;
+    return cuda_status(launch_prefix_mla(to_dev(batch), GroupsDev{groups->groups, groups->off, groups->shared},
+                                         to_dev(pages), q, kv, mask, sm_scale, out, lse, scratch_of(ws),
                                          static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)));
 }
 

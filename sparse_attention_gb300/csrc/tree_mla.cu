@@ -58,8 +58,10 @@
 // ms; one tree of 8 over 1,500 rows 17 us with the merge.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
+#include "prompt.h"
 #include "ptx.cuh"
 #include "tree.h"
 
@@ -95,9 +97,41 @@ struct Seg {
     int32_t b, row, c, len, i0, rows, t0, t1, tiles;
     int64_t u0;                  // the unit of tile 0, for a piece of a cut item
     __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
+    __device__ int32_t first_pos(int32_t t) const { return t * kTile; }
 };
 
-struct Smem {
+// Behind shared prefixes an item may begin further into its sequence.
+struct SharedSeg : Seg {
+    int32_t base;                // tiles before the item's first
+    int32_t slot;                // where the piece goes
+    bool ahead;                  // no other item reads its rows
+    __device__ int32_t first_pos(int32_t t) const { return (base + t) * kTile; }
+};
+
+// Behind shared prefixes the work is a list of runs: first every group's new
+// rows over its shared tiles (whole ones only, from its first sequence's
+// cache), then every sequence's over its own.
+struct Run {
+    int32_t q0, nq, len, base;   // new rows, length of the cache, tiles before the run's first
+    int32_t b, item0;            // the sequence whose cache it reads, items before it
+    int64_t u;                   // units before it
+};
+static_assert(sizeof(Run) == 32, "two 16-byte loads");
+
+struct RunPlan {
+    int64_t all, chunk;          // units, and those of a pair
+    int32_t runs, shared;        // all runs, and those over shared tiles
+};
+
+// The pieces of a row's shared or own part: those of one item, in order of the
+// pairs that computed them.
+struct RowPieces {
+    int32_t slot;                // the first one's
+    int32_t count;               // twice their number, and which of the item's two rows this is
+};
+
+template <class S>
+struct SmemOf {
     alignas(1024) uint8_t q[kQChunks * kChunkBytes];
     alignas(1024) uint8_t k[kKStages * kKBytes];
     alignas(1024) uint8_t v[kVStages * kVBytes];
@@ -105,7 +139,7 @@ struct Smem {
     alignas(8) uint64_t kfull[kKStages], kempty[kKStages], vfull[kVStages], vempty[kVStages], vloc[kVStages];
     uint64_t qfull, qempty, sfull[2], sempty[2], pfull, pvdone, ofree, segfull[kSegs], segempty[kSegs];
     Plan plan;
-    Seg seg[kSegs];
+    S seg[kSegs];
     int64_t scan[kThreads / 32];
     int32_t longest[kThreads / 32];
     float xch[2][128];
@@ -113,7 +147,8 @@ struct Smem {
     uint32_t lost[4];            // softmax warps: 1 + the last segment with a score of -inf past the committed rows
     uint32_t tmem;
 };
-static_assert(sizeof(Smem) <= 232448, "one CTA's shared memory");
+using Smem = SmemOf<Seg>;
+static_assert(sizeof(SmemOf<SharedSeg>) <= 232448, "one CTA's shared memory");
 
 struct Args {
     BatchDev bd;
@@ -130,6 +165,10 @@ struct Args {
     int32_t rows_total;  // cache rows
     bool may_round;      // the bounds allow plan_rounds
     bool ahead;          // a sequence's rows are read by one pair only
+    // behind shared prefixes only
+    const RunPlan* rplan;
+    const Run* runs;
+    RowPieces* pieces;   // [2][total_q]: shared, own
 };
 
 __device__ __forceinline__ int64_t seq_units(const SeqInfo& s) {
@@ -221,6 +260,66 @@ struct SegIter {
                 }
             }
             u += (int64_t)items * per;
+        }
+        return false;
+    }
+};
+
+// The same over runs, by one warp: a pair has an equal share of their units.
+struct RunIter {
+    const Args& a;
+    const int32_t pair;
+    int64_t lo, hi, chunk;
+    int32_t r = 0, p = -1, n_runs, n_shared;
+    __device__ RunIter(const Args& args, int32_t pair_) : a(args), pair(pair_) {
+        const RunPlan pl = *a.rplan;
+        chunk = pl.chunk;
+        lo = min(pl.all, pair * chunk);
+        hi = min(pl.all, lo + chunk);
+        n_runs = pl.runs;
+        n_shared = pl.shared;
+        // the last run that begins at or before lo
+        int top = n_runs;
+        while (r + 1 < top) {
+            const int mid = (r + top) >> 1;
+            if (a.runs[mid].u <= lo) r = mid;
+            else top = mid;
+        }
+    }
+    __device__ int32_t holder(int64_t u) const { return (int32_t)(u / chunk); }
+
+    __device__ bool next(SharedSeg& s) {
+        if (lo >= hi) return false;
+        for (; r < n_runs; ++r, p = 0) {
+            const Run q = a.runs[r];
+            const int32_t tiles = (q.len + kTile - 1) / kTile - q.base, per = tiles + kItemCost, items = (q.nq + 1) >> 1;
+            if (p < 0) p = (int32_t)min((int64_t)items, (lo - q.u) / per);
+            while (p < items) {
+                const int64_t u0 = q.u + (int64_t)p * per + kItemCost;
+                if (u0 - kItemCost >= hi) return false;
+                s.t0 = (int32_t)max((int64_t)0, min((int64_t)tiles, lo - u0));
+                s.t1 = (int32_t)max((int64_t)0, min((int64_t)tiles, hi - u0));
+                const int32_t item = p++;
+                if (s.t1 <= s.t0) continue;
+                const bool shared = r < n_shared;
+                s.b = q.b;
+                s.i0 = shared ? 0 : 2 * item;
+                s.row = q.q0 + 2 * item;
+                s.rows = min(2, q.nq - 2 * item);
+                s.c = shared ? q.len : q.len - q.nq;
+                s.len = q.len;
+                s.tiles = tiles;
+                s.base = q.base;
+                s.ahead = q.nq <= 2;
+                s.u0 = u0;
+                s.slot = q.item0 + item + pair;
+                if (s.t0 == 0 && cluster_rank() == 0 && (int)lane_id() < s.rows) {
+                    const int32_t last = holder(u0 + tiles - 1);
+                    a.pieces[(shared ? 0 : a.bd.total_q) + s.row + lane_id()] =
+                        RowPieces{s.slot, 2 * (last - pair + 1) + (int)lane_id()};
+                }
+                return true;
+            }
         }
         return false;
     }
@@ -419,7 +518,8 @@ __device__ void make_plan(const Args& a, Smem& S, int pair, int pairs) {
 
 // First cache row of a box of positions at pos; past the sequence, or on a
 // page outside the pool, the rows behind the cache (TMA fills zeros).
-__device__ __forceinline__ int32_t box_row(const Args& a, const Seg& s, int32_t pos, bool& bad) {
+template <class S>
+__device__ __forceinline__ int32_t box_row(const Args& a, const S& s, int32_t pos, bool& bad) {
     if (pos >= s.len) return a.rows_total;
     const int32_t r = cache_row(a.bd, a.pg, s.b, pos);
     if (r >= 0) return r;
@@ -427,17 +527,19 @@ __device__ __forceinline__ int32_t box_row(const Args& a, const Seg& s, int32_t 
     return a.rows_total;
 }
 
-__device__ __forceinline__ bool past_committed(const Seg& s, int32_t t) { return (t + 1) * kTile > s.c; }
+template <class S>
+__device__ __forceinline__ bool past_committed(const S& s, int32_t t) { return s.first_pos(t + 1) > s.c; }
 
 // Whether one of the new rows `rows` in the segment's tiles holds a NaN or an
 // infinity; all lanes.  Called when a row past the committed ones scored -inf,
 // which is seldom; a call, since the code of it inside the softmax role costs
 // long calls 1-2 %, out of the way 0.5 % (16 trees of 64 over 8,192 rows).
-__device__ __noinline__ bool any_not_finite(const Args& a, const Seg& s, uint64_t rows) {
+template <class S>
+__device__ __noinline__ bool any_not_finite(const Args& a, const S& s, uint64_t rows) {
 #pragma unroll 1
     for (; rows; rows &= rows - 1u) {
         const int32_t pos = s.c + __ffsll((long long)rows) - 1;
-        if (pos < s.t0 * kTile || pos >= s.t1 * kTile) continue;
+        if (pos < s.first_pos(s.t0) || pos >= s.first_pos(s.t1)) continue;
         const int32_t at = cache_row(a.bd, a.pg, s.b, pos);
         if (at < 0) continue;                    // a bad page: latched, and nothing is written
         const uint4* row = reinterpret_cast<const uint4*>(a.kv + (int64_t)at * kDQK);
@@ -461,12 +563,16 @@ __device__ __noinline__ bool any_not_finite(const Args& a, const Seg& s, uint64_
 // whose 8-row groups stay evenly spaced in a stage as a descriptor needs them
 // (24 K and 16 V boxes a tile; boxes of one chunk of 16 rows, 36 and 32: 0.94
 // instead of 0.89 ms for 16 trees of 64 over 8,192 rows).
-template <int kKRows, int kVRows>
+//
+// kShared: behind shared prefixes.  The work is the runs that prefix_plan_kernel
+// wrote, and every piece goes out in fp32 for prefix_merge_kernel to join.
+template <int kKRows, int kVRows, bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_mla_kernel(const Args a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    Smem& S = *reinterpret_cast<Smem*>(smem_raw);
+    using Segment = std::conditional_t<kShared, SharedSeg, Seg>;
+    SmemOf<Segment>& S = *reinterpret_cast<SmemOf<Segment>*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -510,14 +616,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_arrive();                            // the peer may use this CTA's barriers and TMEM ..
     pdl_wait();                                  // lengths, tables and inputs, and the scratch of an earlier call
-    make_plan(a, S, pair, pairs);
-    if (a.may_round) fence_proxy_async_smem();   // plan_rounds used the V ring
+    if constexpr (!kShared) {
+        make_plan(a, S, pair, pairs);
+        if (a.may_round) fence_proxy_async_smem();   // plan_rounds used the V ring
+    }
     tc_fence_before();
     __syncthreads();
     cluster_wait();                              // .. and this CTA the peer's
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    Seg s;
+    Segment s;
     bool ok = true;
     // the barrier at `b`'s offset in the CTA of rank 0
     auto lead = [&](uint64_t& b) -> uint32_t { return map_to_cluster_rank(smem_u32(&b), 0); };
@@ -531,7 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     // the next segment that warp 8 published; false behind the last
     uint32_t segs_read = 0;
-    auto next_seg = [&](Seg& to) -> bool {
+    auto next_seg = [&](Segment& to) -> bool {
         const uint32_t slot = segs_read & (kSegs - 1);
         wait(S.segfull[slot], (segs_read / kSegs) & 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -559,7 +667,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 bool bad = false;
                 const int32_t x = x0 + lane;
                 const int32_t row =
-                    box_row(a, s, (s.t0 + x / kboxes) * kTile + 64 * (int)rank + (x % kboxes) * kKRows, bad);
+                    box_row(a, s, s.first_pos(s.t0 + x / kboxes) + 64 * (int)rank + (x % kboxes) * kKRows, bad);
                 for (int32_t y = 0; ok && y < 32 && x0 + y < n; y += kboxes) {
                     if (x0 + y == 0) {
                         // No row for this CTA: zeros, from behind the queries.
@@ -591,7 +699,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     // tile's are brought to L2 while this one's are loaded
                     // (64 x 1 row over 32,768: 416 -> 399 us; with rows that
                     // several pairs share the same costs 4-7 %).
-                    if (a.ahead) {
+                    bool ahead = a.ahead;
+                    if constexpr (kShared) ahead = s.ahead;
+                    if (ahead) {
                         const int32_t next = y + kboxes + lane;
                         const int32_t r2 = __shfl_sync(0xffffffffu, row, next & 31);
                         if (lane < kboxes && next < 32 && x0 + next < n && r2 < a.rows_total)
@@ -651,7 +761,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 mma_commit_pair(smem_u32(&S.pvdone));
             };
-            Seg n;
+            Segment n;
             bool more = next_seg(n);
             uint32_t g = 0;
             if (more && elect_one()) issue_s(0, true, n.t1 - n.t0 == 1, 0);
@@ -681,7 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool bad = false;
             for (int32_t x0 = 0; ok && x0 < n; x0 += 32) {
                 const int32_t x = x0 + lane;
-                const int32_t row = box_row(a, s, s.t0 * kTile + x * kVRows, bad);
+                const int32_t row = box_row(a, s, s.first_pos(s.t0) + x * kVRows, bad);
                 const bool any_bad = __any_sync(0xffffffffu, bad);
                 if (lane == 0) {
                     S.bad[seg & 3] = any_bad;
@@ -713,7 +823,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (next_seg(s)) {
             for (int32_t t = s.t0; t < s.t1; ++t) {
                 if (!past_committed(s, t)) continue;
-                const int32_t pos0 = t * kTile;
+                const int32_t pos0 = s.first_pos(t);
                 for (int j = 0; j < kVStages; ++j) {
                     wait(S.vloc[j], fixed & 1);
                     __syncwarp();
@@ -771,7 +881,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (!named_bar_or(1, 128, !next_seg(s))) {
             const bool mine = (int)rank < s.rows;
             const uint64_t bits =
-                mine ? visible_bits(__ldg(reinterpret_cast<const unsigned long long*>(a.mask) + s.row + rank),
+                mine ? visible_bits(kShared && !a.mask
+                                        ? ~0ull
+                                        : __ldg(reinterpret_cast<const unsigned long long*>(a.mask) + s.row + rank),
                                     s.i0 + (int)rank)
                      : 0u;
             if (!mine) {
@@ -803,7 +915,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(lead(S.sempty[buf]));
                 if (past_committed(s, t)) {
-                    const int32_t d = s.c - (t * kTile + 64 * half);     // committed columns of this thread's 64
+                    const int32_t d = s.c - (s.first_pos(t) + 64 * half);     // committed columns of this thread's 64
                     uint64_t vis = d >= 64 ? ~0ull : d > 0 ? (1ull << d) - 1u : 0u;
                     vis |= d >= 64 ? 0u : d >= 0 ? bits << d : d > -64 ? bits >> -d : 0u;
                     float least = INFINITY;
@@ -870,8 +982,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const float ls = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                 const int64_t head = (int64_t)(s.row + (int)rank) * kH;
-                const bool whole = s.whole();
-                const int64_t slot = 2 * (int64_t)pair + (s.t0 == 0 ? 1 : 0);
+                const bool whole = !kShared && s.whole();
+                int64_t slot = 2 * (int64_t)pair + (s.t0 == 0 ? 1 : 0);
+                if constexpr (kShared) slot = s.slot;
                 if (half == 0 && ok) {
                     if (!whole) a.part_lse[slot * 128 + 64 * (int)rank + x] = bad ? INFINITY : ls;
                     else if (a.lse && !bad) a.lse[head + x] = ls;
@@ -938,18 +1051,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         // the segments, and what tree_merge_kernel has to know of a cut item
-        SegIter it(a, S.plan, pair, pairs);
-        // the pair whose share holds unit u: the last with lo <= u
-        auto holder = [&](int64_t u) -> int {
-            int k = 0;
-            for (int x = 0; x < pairs; x += 32)
-                k += __popc(__ballot_sync(0xffffffffu, x + lane < pairs && S.plan.lo[x + lane] <= u));
-            return k - 1;
-        };
-        int4 meta = make_int4(0, 0, 0, 0);
-        bool more = true;
-        for (uint32_t n = 0; ok && more; ++n) {
-            more = it.next(s);
+        auto publish = [&](uint32_t n, bool more) {
             const uint32_t slot = n & (kSegs - 1);
             if (n >= kSegs) wait(S.segempty[slot], (n / kSegs - 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
@@ -959,9 +1061,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mbar_arrive(smem_u32(&S.segfull[slot]));
             }
             __syncwarp();
-            if (more && !s.whole()) meta = make_int4(s.row, s.rows, holder(s.u0 + s.tiles - 1), holder(s.u0));
+        };
+        bool more = true;
+        if constexpr (kShared) {
+            RunIter it(a, pair);
+            for (uint32_t n = 0; ok && more; ++n) {
+                more = it.next(s);
+                publish(n, more);
+            }
+        } else {
+            SegIter it(a, S.plan, pair, pairs);
+            // the pair whose share holds unit u: the last with lo <= u
+            auto holder = [&](int64_t u) -> int {
+                int k = 0;
+                for (int x = 0; x < pairs; x += 32)
+                    k += __popc(__ballot_sync(0xffffffffu, x + lane < pairs && S.plan.lo[x + lane] <= u));
+                return k - 1;
+            };
+            int4 meta = make_int4(0, 0, 0, 0);
+            for (uint32_t n = 0; ok && more; ++n) {
+                more = it.next(s);
+                publish(n, more);
+                if (more && !s.whole()) meta = make_int4(s.row, s.rows, holder(s.u0 + s.tiles - 1), holder(s.u0));
+            }
+            if (rank == 0 && lane == 0) a.meta[pair] = meta;
         }
-        if (rank == 0 && lane == 0) a.meta[pair] = meta;
     }
     if (!ok) {
         // let copies in flight land before the CTA's shared memory goes
@@ -977,19 +1101,114 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
+constexpr int kMergeBlocks = 16, kMergeWarps = 8;
+
+// Joins one unit's pieces: 16 TMEM columns (from c, of warp w's quarter) of 32
+// lanes, a lane per query row, whose head is at row `head` of out.  at(e): twice
+// the slot of piece e, and which of the item's two rows this is.  A warp alone, or
+// (wide, all warps of the block) every 8th piece a warp.
+template <class At>
+__device__ __forceinline__ void join_unit(const At& at, int pieces, bool wide, int w, int c, int64_t head,
+                                          const float* __restrict__ part_lse, const float4* __restrict__ part_o,
+                                          uint16_t* __restrict__ out, float* __restrict__ lse,
+                                          float (*acc_s)[18][32]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e0 = wide ? warp : 0, step = wide ? kMergeWarps : 1;
+    const int x = 32 * (w & 1) + lane;           // the lane's head
+    auto piece_lse = [&](int e) -> float { return part_lse[at(e) * 64 + x]; };
+    // eight pieces' sums at a time, with a running maximum
+    float acc[16], sum = 0.f, top = -INFINITY;
+    bool bad = false, nan = false;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+#pragma unroll 1
+    for (int e1 = e0; e1 < pieces; e1 += 8 * step) {
+        float ls[8], mx = top;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) ls[q] = e1 + q * step < pieces ? piece_lse(e1 + q * step) : -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            bad = bad || ls[q] == INFINITY;
+            nan = nan || ls[q] != ls[q];
+            mx = fmaxf(mx, ls[q]);
+        }
+        const float base = mx == -INFINITY ? 0.f : mx, down = ex2_approx((top - base) * kLog2e);
+        top = mx;
+        sum *= down;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[k] *= down;
+#pragma unroll 2
+        for (int q = 0; q < 8; ++q) {
+            if (e1 + q * step >= pieces) break;
+            const float f = ex2_approx((ls[q] - base) * kLog2e);
+            const float4* o = part_o + ((at(e1 + q * step) * 4 + w) * 64 + c / 4) * 32 + lane;
+            sum += f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 v = o[32 * k];
+                acc[4 * k] += f * v.x;
+                acc[4 * k + 1] += f * v.y;
+                acc[4 * k + 2] += f * v.z;
+                acc[4 * k + 3] += f * v.w;
+            }
+        }
+    }
+    if (bad) top = INFINITY;
+    else if (nan) top = NAN;
+    if (wide) {
+        // the warps' sums, in order
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc_s[warp][k][lane] = acc[k];
+        acc_s[warp][16][lane] = sum;
+        acc_s[warp][17][lane] = top;
+        __syncthreads();
+        if (warp == 0) {
+            float mx = top;
+#pragma unroll
+            for (int v = 1; v < kMergeWarps; ++v) {
+                const float m = acc_s[v][17][lane];
+                if (mx != INFINITY) mx = m == INFINITY || m != m ? m : mx != mx ? mx : fmaxf(mx, m);
+            }
+            const float base = mx == -INFINITY ? 0.f : mx;
+            const float own = ex2_approx((top - base) * kLog2e);
+            sum *= own;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) acc[k] *= own;
+#pragma unroll
+            for (int v = 1; v < kMergeWarps; ++v) {
+                const float f = ex2_approx((acc_s[v][17][lane] - base) * kLog2e);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) acc[k] += f * acc_s[v][k][lane];
+                sum += f * acc_s[v][16][lane];
+            }
+            top = mx;
+        }
+        __syncthreads();
+        if (warp != 0) return;
+    }
+    if (top == INFINITY) return;                 // a bad page in one of the pieces
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint4* to = reinterpret_cast<uint4*>(out + (head + x) * kDV + 128 * (w >> 1) + (c & 127) + 2 * (c & 128));
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        to[k] = make_uint4(pack_bf16x2(acc[8 * k] * inv, acc[8 * k + 1] * inv),
+                           pack_bf16x2(acc[8 * k + 2] * inv, acc[8 * k + 3] * inv),
+                           pack_bf16x2(acc[8 * k + 4] * inv, acc[8 * k + 5] * inv),
+                           pack_bf16x2(acc[8 * k + 6] * inv, acc[8 * k + 7] * inv));
+    if (lse && (w >> 1) == 0 && c == 0) lse[head + x] = sum == 0.f ? -INFINITY : top + log2f(sum) * kLn2;
+}
+
 // Joins the partial results of the items that chunks cut.  A unit is 16 TMEM
 // columns of a CTA's 32 lanes, a lane per query row.  Items of few pieces: the
 // 16 blocks of the pair that begins the item take a unit per warp.  Items of
 // many (one long sequence over the whole GPU: 10 MB of pieces): the blocks of
 // the pairs inside it, which begin nothing, help; a block takes a unit, its
 // warps every 8th piece (1 x 100,000 rows: 83 -> 30 us, merge included).
-constexpr int kMergeBlocks = 16, kMergeWarps = 8;
-
 __global__ void __launch_bounds__(32 * kMergeWarps)
     tree_merge_kernel(const int4* __restrict__ meta, const float* __restrict__ part_lse,
                       const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
     __shared__ float acc_s[kMergeWarps][18][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5;
     pdl_launch_dependents();
     pdl_wait();
     const int4 it = meta[blockIdx.x];
@@ -1001,95 +1220,141 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     const bool wide = pieces > kMergeWarps;
     if (!wide && helper > 0) return;
     const int helpers = wide ? it.z - pair + (meta[it.z].w == pair ? 1 : 0) : 1;
-    const int e0 = wide ? warp : 0, step = wide ? kMergeWarps : 1;
     const int units = 64 * it.y, stride = wide ? kMergeBlocks * helpers : units;
-    auto slot = [&](int e) -> int64_t { return e == 0 ? 2 * (int64_t)pair + 1 : 2 * ((int64_t)pair + e); };
     for (int unit = wide ? kMergeBlocks * helper + (int)blockIdx.y : kMergeWarps * (int)blockIdx.y + warp; unit < units;
          unit += stride) {
-        const int rank = unit >> 6, w = (unit >> 4) & 3, c = 16 * (unit & 15);
-        const int x = 32 * (w & 1) + lane;           // the lane's head
-        auto piece_lse = [&](int e) -> float { return part_lse[slot(e) * 128 + 64 * rank + x]; };
-        // eight pieces' sums at a time, with a running maximum
-        float acc[16], sum = 0.f, top = -INFINITY;
-        bool bad = false, nan = false;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-#pragma unroll 1
-        for (int e1 = e0; e1 < pieces; e1 += 8 * step) {
-            float ls[8], mx = top;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) ls[q] = e1 + q * step < pieces ? piece_lse(e1 + q * step) : -INFINITY;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                bad = bad || ls[q] == INFINITY;
-                nan = nan || ls[q] != ls[q];
-                mx = fmaxf(mx, ls[q]);
+        const int rank = unit >> 6;
+        auto at = [&](int e) -> int64_t {
+            return 2 * (e == 0 ? 2 * (int64_t)pair + 1 : 2 * ((int64_t)pair + e)) + rank;
+        };
+        join_unit(at, pieces, wide, (unit >> 4) & 3, 16 * (unit & 15), (int64_t)(it.x + rank) * kH, part_lse, part_o, out,
+                  lse, acc_s);
+    }
+}
+
+// Joins a row's pieces, those over the group's shared tiles and then its own.
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    prefix_merge_kernel(const RowPieces* __restrict__ pieces, int32_t total_q, const float* __restrict__ part_lse,
+                        const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
+    __shared__ float acc_s[kMergeWarps][18][32];
+    const int warp = threadIdx.x >> 5;
+    pdl_launch_dependents();
+    pdl_wait();
+    const RowPieces shared = pieces[blockIdx.x], own = pieces[total_q + blockIdx.x];
+    if (own.count == 0) return;                  // no row, or a sequence outside the bounds
+    const int first = shared.count >> 1, all = first + (own.count >> 1);
+    const bool wide = all > kMergeWarps;
+    auto at = [&](int e) -> int64_t {
+        return e < first ? 2 * ((int64_t)shared.slot + e) + (shared.count & 1)
+                         : 2 * ((int64_t)own.slot + e - first) + (own.count & 1);
+    };
+    const int step = (int)gridDim.y * (wide ? 1 : kMergeWarps);
+    for (int unit = wide ? (int)blockIdx.y : kMergeWarps * (int)blockIdx.y + warp; unit < 64; unit += step)
+        join_unit(at, all, wide, unit >> 4, 16 * (unit & 15), (int64_t)blockIdx.x * kH, part_lse, part_o, out, lse, acc_s);
+}
+
+// The runs of a call behind shared prefixes, by the first block; the others
+// clear the rows' pieces.  A group counts if all groups together are the
+// batch in order and each of its sequences with new rows keeps the shared ones; else
+// its sequences are computed each by itself.
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads)
+    prefix_plan_kernel(const BatchDev bd, const GroupsDev gr, RunPlan* plan, Run* runs, int32_t* tiles_of,
+                       int32_t* lead, RowPieces* pieces, int pairs, int32_t* status) {
+    __shared__ int64_t s_units[kPlanThreads / 32];
+    __shared__ int32_t s_items[kPlanThreads / 32], s_longest[kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (blockIdx.x > 0) {
+        for (int64_t i = (int64_t)(blockIdx.x - 1) * kPlanThreads + tid; i < 2 * (int64_t)bd.total_q;
+             i += (int64_t)(gridDim.x - 1) * kPlanThreads)
+            pieces[i] = RowPieces{0, 0};
+        return;
+    }
+    bool wrong = false;
+    for (int g = tid; g < gr.n; g += kPlanThreads) {
+        const int32_t lo = __ldg(gr.off + g), hi = __ldg(gr.off + g + 1), rows = __ldg(gr.shared + g);
+        wrong = wrong || lo < 0 || lo > hi || hi > bd.B || (g == 0 && lo != 0) || (g == gr.n - 1 && hi != bd.B) || rows < 0;
+        tiles_of[g] = max(rows, 0) / kTile;
+        lead[g] = bd.B;
+    }
+    if (wrong) latch_status(status, DSA_ERR_BAD_BATCH);
+    wrong = __syncthreads_or(wrong);
+    for (int b = tid; b < bd.B && !wrong; b += kPlanThreads) {
+        const int g = last_at_or_below(gr.off, gr.n, b);
+        SeqInfo q;
+        const bool good = load_seq(bd, b, status, q);
+        if (good && q.nq == 0) continue;
+        if (good && __ldg(gr.shared + g) <= q.ctx - q.nq) {
+            atomicMin(lead + g, b);
+        } else {
+            latch_status(status, DSA_ERR_BAD_BATCH);
+            tiles_of[g] = 0;
+        }
+    }
+    __syncthreads();
+    int64_t units = 0;
+    int32_t items = 0, longest = 0;
+    const int32_t n = gr.n + bd.B;
+    for (int32_t i0 = 0; i0 < n; i0 += kPlanThreads) {
+        const int32_t i = i0 + tid;
+        Run r{0, 0, 0, 0, 0, 0, 0};
+        if (i < gr.n) {
+            if (!wrong && tiles_of[i] > 0 && lead[i] < bd.B) {
+                r.q0 = __ldg(bd.q_off + __ldg(gr.off + i));
+                r.nq = __ldg(bd.q_off + __ldg(gr.off + i + 1)) - r.q0;
+                r.len = tiles_of[i] * kTile;
+                r.b = lead[i];
             }
-            const float base = mx == -INFINITY ? 0.f : mx, down = ex2_approx((top - base) * kLog2e);
-            top = mx;
-            sum *= down;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) acc[k] *= down;
-#pragma unroll 2
-            for (int q = 0; q < 8; ++q) {
-                if (e1 + q * step >= pieces) break;
-                const float f = ex2_approx((ls[q] - base) * kLog2e);
-                const float4* o = part_o + (((slot(e1 + q * step) * 2 + rank) * 4 + w) * 64 + c / 4) * 32 + lane;
-                sum += f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 v = o[32 * k];
-                    acc[4 * k] += f * v.x;
-                    acc[4 * k + 1] += f * v.y;
-                    acc[4 * k + 2] += f * v.z;
-                    acc[4 * k + 3] += f * v.w;
-                }
+        } else if (i < n) {
+            SeqInfo q;
+            r.b = i - gr.n;
+            if (load_seq(bd, r.b, status, q) && q.nq > 0) {
+                r.q0 = q.q0;
+                r.nq = q.nq;
+                r.len = q.ctx;
+                r.base = wrong ? 0 : tiles_of[last_at_or_below(gr.off, gr.n, r.b)];
             }
         }
-        if (bad) top = INFINITY;
-        else if (nan) top = NAN;
-        if (wide) {
-            // the warps' sums, in order
+        const int32_t mine = (r.nq + 1) >> 1, tiles = (r.len + kTile - 1) / kTile - r.base;
+        const int64_t cost = (int64_t)mine * (tiles + kItemCost);
+        longest = max(longest, mine > 0 ? tiles : 0);
+        int64_t iu = cost;
+        int32_t ii = mine;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) acc_s[warp][k][lane] = acc[k];
-            acc_s[warp][16][lane] = sum;
-            acc_s[warp][17][lane] = top;
-            __syncthreads();
-            if (warp == 0) {
-                float mx = top;
-#pragma unroll
-                for (int v = 1; v < kMergeWarps; ++v) {
-                    const float m = acc_s[v][17][lane];
-                    if (mx != INFINITY) mx = m == INFINITY || m != m ? m : mx != mx ? mx : fmaxf(mx, m);
-                }
-                const float base = mx == -INFINITY ? 0.f : mx;
-                const float own = ex2_approx((top - base) * kLog2e);
-                sum *= own;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) acc[k] *= own;
-#pragma unroll
-                for (int v = 1; v < kMergeWarps; ++v) {
-                    const float f = ex2_approx((acc_s[v][17][lane] - base) * kLog2e);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) acc[k] += f * acc_s[v][k][lane];
-                    sum += f * acc_s[v][16][lane];
-                }
-                top = mx;
-            }
-            __syncthreads();
-            if (warp != 0) continue;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, iu, o);
+            const int32_t v = __shfl_up_sync(0xffffffffu, ii, o);
+            if (lane >= o) iu += u, ii += v;
         }
-        if (top == INFINITY) continue;           // a bad page in one of the pieces
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t head = (int64_t)(it.x + rank) * kH + x;
-        uint4* to = reinterpret_cast<uint4*>(out + head * kDV + 128 * (w >> 1) + (c & 127) + 2 * (c & 128));
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            to[k] = make_uint4(pack_bf16x2(acc[8 * k] * inv, acc[8 * k + 1] * inv),
-                               pack_bf16x2(acc[8 * k + 2] * inv, acc[8 * k + 3] * inv),
-                               pack_bf16x2(acc[8 * k + 4] * inv, acc[8 * k + 5] * inv),
-                               pack_bf16x2(acc[8 * k + 6] * inv, acc[8 * k + 7] * inv));
-        if (lse && (w >> 1) == 0 && c == 0) lse[head] = sum == 0.f ? -INFINITY : top + log2f(sum) * kLn2;
+        if (lane == 31) {
+            s_units[warp] = iu;
+            s_items[warp] = ii;
+        }
+        __syncthreads();
+        int64_t bu = units;
+        int32_t bi = items;
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            if (w < warp) bu += s_units[w], bi += s_items[w];
+            units += s_units[w];
+            items += s_items[w];
+        }
+        if (i < n) {
+            r.u = bu + iu - cost;
+            r.item0 = bi + ii - mine;
+            runs[i] = r;
+        }
+        __syncthreads();
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) s_longest[warp] = longest;
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < kPlanThreads / 32; ++w) longest = max(longest, s_longest[w]);
+        const int64_t even = (units + pairs - 1) / pairs;
+        *plan = RunPlan{units, max(even, (int64_t)least_chunk(longest)), n, gr.n};
     }
 }
 
@@ -1115,9 +1380,9 @@ int max_pairs() {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(tree_mla_kernel<64, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem)) !=
+    if (cudaFuncSetAttribute(tree_mla_kernel<64, 64, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem)) !=
             cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, tree_mla_kernel<64, 64>, &cfg) != cudaSuccess || n <= 0) {
+        cudaOccupancyMaxActiveClusters(&n, tree_mla_kernel<64, 64, false>, &cfg) != cudaSuccess || n <= 0) {
         cudaGetLastError();
         return num_sms() / 2;
     }
@@ -1125,6 +1390,21 @@ int max_pairs() {
     cache[dev].store(n, std::memory_order_relaxed);
     return n;
 }
+
+// Tensor maps of the queries and of the cache, whose boxes go by its pages.
+struct TreeMaps {
+    CUtensorMap q, k, v;
+    uint32_t krows;
+    bool ok;
+    TreeMaps(const Args& a, const uint16_t* queries) {
+        const int page = a.pg.table ? 1 << a.pg.shift : kTile;
+        krows = page >= 64 ? 64 : page == 32 ? 32 : 8;
+        const uint32_t kchunks = krows == 32 ? 1 : kGroup, vrows = (uint32_t)std::min(page, 64);
+        ok = make_tmap_bf16_2d(&q, queries, kDQK, (uint64_t)a.bd.total_q * kH, 64, 64) &&
+             make_tmap_bf16_chunks(&k, a.kv, kQChunks, (uint64_t)a.rows_total, krows, kchunks) &&
+             make_tmap_bf16_chunks(&v, a.kv, kQChunks, (uint64_t)a.rows_total, vrows, 2);
+    }
+};
 
 // Pairs that a call launches: no more than its bounds give work to.
 int pairs_for(const BatchDev& bd) {
@@ -1161,17 +1441,11 @@ cudaError_t launch_tree_mla(const BatchDev& bd, const PagesDev& pg, const uint16
     a.may_round = bd.B <= kPlanSeqs && bd.max_q > 2 && pairs <= kMaxPairs &&
                   (int64_t)bd.B * bd.max_ctx * 2 * kDQK > kSharedBytes;
     a.rows_total = pg.table ? pg.pool_pages << pg.shift : (int32_t)(bd.B * bd.stride);
-    const int page = pg.table ? 1 << pg.shift : kTile;
-    const uint32_t krows = page >= 64 ? 64 : page == 32 ? 32 : 8, kchunks = krows == 32 ? 1 : kGroup;
-    const uint32_t vrows = (uint32_t)std::min(page, 64);
-    CUtensorMap tm_q, tm_k, tm_v;
-    if (!make_tmap_bf16_2d(&tm_q, q, kDQK, (uint64_t)bd.total_q * kH, 64, 64) ||
-        !make_tmap_bf16_chunks(&tm_k, kv, kQChunks, (uint64_t)a.rows_total, krows, kchunks) ||
-        !make_tmap_bf16_chunks(&tm_v, kv, kQChunks, (uint64_t)a.rows_total, vrows, 2))
-        return cudaErrorInvalidValue;
-    auto kernel = krows == 64   ? tree_mla_kernel<64, 64>
-                  : krows == 32 ? tree_mla_kernel<32, 32>
-                                : tree_mla_kernel<8, 16>;
+    const TreeMaps maps(a, q);
+    if (!maps.ok) return cudaErrorInvalidValue;
+    auto kernel = maps.krows == 64   ? tree_mla_kernel<64, 64, false>
+                  : maps.krows == 32 ? tree_mla_kernel<32, 32, false>
+                                     : tree_mla_kernel<8, 16, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
     if (e != cudaSuccess) return e;
     // Both are programmatic dependents of the launch before them: they set up
@@ -1186,12 +1460,104 @@ cudaError_t launch_tree_mla(const BatchDev& bd, const PagesDev& pg, const uint16
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, kernel, a, tm_q, tm_k, tm_v)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, a, maps.q, maps.k, maps.v)) != cudaSuccess) return e;
     count_launches(1);
     cfg.gridDim = dim3((unsigned)pairs, kMergeBlocks);
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, (const int4*)a.meta, (const float*)a.part_lse,
+                           (const float4*)a.part_o, out, lse);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+namespace {
+
+// Pieces that a call behind shared prefixes can have: two items' worth of rows
+// each, one more for an odd one of every group and sequence, and the pairs' cuts.
+size_t prefix_slots(const BatchDev& bd, int32_t groups, int pairs) {
+    const size_t rows = (size_t)bd.total_q;
+    return (rows + std::min<size_t>(rows, groups)) / 2 + (rows + std::min<size_t>(rows, bd.B)) / 2 + 2 + pairs;
+}
+
+struct PrefixScratch {
+    size_t plan, tiles, lead, runs, pieces, lse, o, bytes;
+    PrefixScratch(const BatchDev& bd, int32_t groups, int pairs) {
+        const size_t slots = prefix_slots(bd, groups, pairs);
+        size_t at = 0;
+        auto take = [&](size_t n) {
+            const size_t mine = at;
+            at += (n + 255) / 256 * 256;
+            return mine;
+        };
+        plan = take(sizeof(RunPlan));
+        tiles = take(sizeof(int32_t) * (size_t)groups);
+        lead = take(sizeof(int32_t) * (size_t)groups);
+        runs = take(sizeof(Run) * ((size_t)groups + bd.B));
+        pieces = take(sizeof(RowPieces) * 2 * (size_t)bd.total_q);
+        lse = take(sizeof(float) * 128 * slots);
+        o = take(sizeof(float) * 128 * kDV * slots);
+        bytes = at;
+    }
+};
+
+}  // namespace
+
+size_t prefix_mla_scratch_bytes(const BatchDev& bd, int32_t groups) {
+    return PrefixScratch(bd, groups, std::min(num_sms() / 2, kMaxPairs)).bytes;
+}
+
+cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const PagesDev& pg, const uint16_t* q,
+                              const uint16_t* kv, const uint64_t* mask, float sm_scale, uint16_t* out, float* lse,
+                              void* scratch, int32_t* status, cudaStream_t stream) {
+    const int pairs = max_pairs();
+    const PrefixScratch at(bd, gr.n, std::min(num_sms() / 2, kMaxPairs));
+    uint8_t* const mem = static_cast<uint8_t*>(scratch);
+    Args a{};
+    a.bd = bd;
+    a.pg = pg;
+    a.mask = mask;
+    a.kv = kv;
+    a.scale_log2 = sm_scale * kLog2e;
+    a.status = status;
+    a.part_o = reinterpret_cast<float*>(mem + at.o);
+    a.part_lse = reinterpret_cast<float*>(mem + at.lse);
+    RunPlan* plan = reinterpret_cast<RunPlan*>(mem + at.plan);
+    Run* runs = reinterpret_cast<Run*>(mem + at.runs);
+    a.rplan = plan;
+    a.runs = runs;
+    a.pieces = reinterpret_cast<RowPieces*>(mem + at.pieces);
+    a.rows_total = pg.table ? pg.pool_pages << pg.shift : (int32_t)(bd.B * bd.stride);
+    const TreeMaps maps(a, q);
+    if (!maps.ok) return cudaErrorInvalidValue;
+    auto kernel = maps.krows == 64   ? tree_mla_kernel<64, 64, true>
+                  : maps.krows == 32 ? tree_mla_kernel<32, 32, true>
+                                     : tree_mla_kernel<8, 16, true>;
+    constexpr size_t kSmem = sizeof(SmemOf<SharedSeg>);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1 + (unsigned)std::min<int64_t>(64, (2 * (int64_t)bd.total_q + kPlanThreads - 1) / kPlanThreads));
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, prefix_plan_kernel, bd, gr, plan, runs, reinterpret_cast<int32_t*>(mem + at.tiles),
+                           reinterpret_cast<int32_t*>(mem + at.lead), a.pieces, pairs, status);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+    cfg.gridDim = dim3(2 * (unsigned)pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, a, maps.q, maps.k, maps.v)) != cudaSuccess) return e;
+    count_launches(1);
+    cfg.gridDim = dim3((unsigned)bd.total_q, bd.total_q <= 16 ? 64 : 64 / kMergeWarps);
+    cfg.blockDim = dim3(32 * kMergeWarps);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, prefix_merge_kernel, (const RowPieces*)a.pieces, bd.total_q, (const float*)a.part_lse,
                            (const float4*)a.part_o, out, lse);
     if (e == cudaSuccess) count_launches(1);
     return e;

@@ -141,3 +141,41 @@ def test_calls_without_rows(lib):
 def test_o_proj_refusals(lib, kw, code):
     a = dict(dict(t=8, o=P, w=P, y=P, ws=WS, n=1 << 30), **kw)
     assert lib.dsa_mla_o_proj(a["t"], a["o"], a["w"], a["y"], a["ws"], a["n"], None) == code
+
+
+def _groups(n=1, off=0x60000, shared=0x70000):
+    import sparse_attention_gb300 as dsa
+    return dsa.DsaGroups(n, off, shared)
+
+
+def _prefix(lib, b, r, g=None, q=P, kv=P, mask=P, scale=0.0625, out=P, lse=None, ws=WS, n=1 << 40):
+    b, r, g = (ctypes.byref(t) if t is not None else None for t in (b, r, g))
+    return lib.dsa_prefix_mla_fwd(b, r, g, q, kv, mask, ctypes.c_float(scale), out, lse, ws, n, None)
+
+
+def test_prefix_workspace(lib):
+    n = ctypes.c_size_t(0)
+    size = lambda b, r: lib.dsa_prefix_workspace_size(ctypes.byref(_batch(**b)), ctypes.byref(_groups(**r)),  # noqa: E731
+                                                      ctypes.byref(n))
+    assert size({}, {}) == 0 and n.value % 256 == 0
+    assert [size(dict(B=0), {}), size({}, dict(n=0)), size({}, dict(n=3))] == [1, 1, 1]
+    assert lib.dsa_prefix_workspace_size(ctypes.byref(_batch()), None, ctypes.byref(n)) == 1
+    assert lib.dsa_prefix_workspace_size(ctypes.byref(_batch()), ctypes.byref(_groups()), None) == 1
+    # every piece of 64 sequences of one row has its place: 32 pairs of shared rows, 64 own, and the cuts
+    assert size(dict(B=64, total_q=64, max_q=1), {}) == 0 and n.value >= (32 + 64 + 76) * 4 * 128 * 513
+
+
+@pytest.mark.parametrize("b,r,g,kw,code", [
+    (None, {}, None, {}, 1), ({}, None, None, {}, 1), (dict(B=0), {}, None, {}, 1), (dict(max_q=65), {}, None, {}, 2),
+    (dict(total_q=1 << 25), {}, None, {}, 2), (dict(stride=99), {}, None, {}, 1), (dict(stride=1 << 30), {}, None, {}, 2),
+    ({}, dict(n=0), None, {}, 1), ({}, dict(n=3), None, {}, 1), ({}, dict(off=0), None, {}, 1),
+    ({}, dict(shared=0x70002), None, {}, 1), ({}, {}, dict(size=24), {}, 1), ({}, {}, dict(width=6), {}, 1),
+    ({}, {}, None, dict(q=0), 1), ({}, {}, None, dict(kv=P + 8), 1), ({}, {}, None, dict(mask=P + 4), 1),
+    ({}, {}, None, dict(out=0), 1), ({}, {}, None, dict(lse=P + 4), 1), ({}, {}, None, dict(scale=0.0), 1),
+    ({}, {}, None, dict(scale=math.nan), 1), ({}, {}, None, dict(ws=0), 3), ({}, {}, None, dict(n=4096), 3),
+    (dict(total_q=0), {}, None, dict(q=0, kv=0, out=0), 0), (dict(max_ctx=0), {}, None, dict(q=0), 0),
+])
+def test_prefix_refusals(lib, b, r, g, kw, code):
+    got = _prefix(lib, _batch(**b) if b is not None else None, _groups(**r) if r is not None else None,
+                  _pages(**g) if g is not None else None, **kw)
+    assert got == code
