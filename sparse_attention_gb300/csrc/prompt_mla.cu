@@ -14,9 +14,13 @@
 //   O[256 q, 256] += P V          each CTA stages 128 of the value columns of
 //                                 all 128 positions
 // O (256 TMEM columns) and two S tiles (128 each) fill a CTA's TMEM, a lane per
-// query row; nothing but barriers and item numbers crosses between the CTAs.  S of
-// tile g + 1 is issued before PV of tile g, so the softmax of a tile runs under the
-// tensor work of the next.
+// query row; nothing but barriers and item numbers crosses between the CTAs.  P
+// takes the place of its S, half the columns of each of the two threads of a
+// row: from shared memory it would cost 64 KB a tile of a bandwidth that Q, K
+// and V already use for 192 (128 bytes a cycle; a tile took 2,680 cycles, 2,090
+// so).
+// S of tile g + 1 is issued before PV of tile g, so the softmax of a tile runs
+// under the tensor work of the next.
 //
 // What is masked cannot leak: expanded values are finite (a row that is not
 // carries NaN in its key instead), rows behind a sequence up to the next multiple
@@ -34,12 +38,19 @@
 // L2), and short items fill the end.  The order decides which pair computes an item,
 // never what it computes.
 //
-// Roles of a CTA's 12 warps: Q and K loads, MMA (rank 0 only), V loads, items,
-// eight softmax / epilogue warps (two threads share a query row, 64 positions
-// each).
+// Roles of a CTA's 16 warps: K loads, MMA (rank 0 only), Q and V loads, items,
+// eight softmax warps (two threads share a query row, 64 positions each),
+// four that write results (an item's O is read out under the first S and softmax of
+// the next).
 //
 // Bounds.  A tile is 16 MMAs of N = 128 and 8 of N = 256: 2,048 cycles for
-// 33.6 MFLOP at M = 256.
+// 33.6 MFLOP at M = 256.  An item costs 3,000 cycles more: its first S waits for its
+// queries, which take the place of those of the item before, and its first PV for the
+// softmax of that.  Measured, in single calls and in a loop that the power cap
+// slows: 16,384 tokens 4.35-4.40 ms = 2,000-2,020 TFLOP/s (cuBLAS 1,921) and
+// 5.0-5.05 ms = 1,740-1,760 (1,730 sustained); 12 prompts of 839 to 2,012 tokens
+// 0.60 ms and 0.68-0.72, 401 tiles a pair for the 319 that the mask leaves;
+// 100 tokens 12 us.
 #include <algorithm>
 #include <atomic>
 
@@ -53,8 +64,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTile = 128;                   // positions per tile
 constexpr int kRows = 256;                   // query rows of an item, half of them each CTA's
-constexpr int kThreads = 384;
-constexpr int kSoftWarps = 8;
+constexpr int kThreads = 512;
+constexpr int kSoftWarps = 8, kOutWarps = 4;
 constexpr int kQBytes = 128 * 128;           // 128 rows x 64 columns
 constexpr int kKBytes = 64 * 128;            // 64 rows x 64 columns
 constexpr int kQChunks = kHeadQK / 64;       // 4
@@ -77,13 +88,14 @@ struct Smem {
     alignas(1024) uint8_t q[kQChunks * kQBytes];
     alignas(1024) uint8_t k[kStages * kQChunks * kKBytes];
     alignas(1024) uint8_t v[kStages * 2 * kQBytes];      // two blocks of 64 columns x 128 positions
-    alignas(1024) uint8_t p[2 * kQBytes];
+    alignas(1024) uint8_t out[kOutWarps * 4096];
     alignas(8) uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
-    uint64_t qfull[kQChunks], qempty[kQChunks], sfull[2], sempty[2], pfull, pvdone, ofree, itemfull[kSlots], itemempty[kSlots];
+    uint64_t qfull[kQChunks], qempty[kQChunks], sfull[2], pfull[2], pvdone, odone, lfull, invfree, ofree, itemfull[kSlots], itemempty[kSlots];
     uint64_t numfull[kSlots], numempty[kSlots];          // item numbers on their way to rank 1
     Item item[kSlots];
     uint32_t number[kSlots];
     float xch[2][32 * kSoftWarps];
+    float inv[128];                                      // 1 / the sum of a finished item's row
     uint32_t tmem;
 };
 static_assert(sizeof(Smem) <= 232448, "one CTA's shared memory");
@@ -173,7 +185,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (tid == 0) latch_status(a.status, DSA_ERR_INTERNAL);
         return;                                  // both CTAs: the same launch, the same offset
     }
-    if (tid == kThreads - 32) {
+    if (tid == 128) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&S.kfull[i]), 2);
             mbar_init(smem_u32(&S.kempty[i]), 1);
@@ -186,14 +198,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&S.sfull[i]), 1);
-            mbar_init(smem_u32(&S.sempty[i]), 2 * kSoftWarps);
+            mbar_init(smem_u32(&S.pfull[i]), 2 * kSoftWarps);
         }
-        mbar_init(smem_u32(&S.pfull), 2 * kSoftWarps);
         mbar_init(smem_u32(&S.pvdone), 1);
-        mbar_init(smem_u32(&S.ofree), 2 * kSoftWarps);
+        mbar_init(smem_u32(&S.odone), 1);
+        mbar_init(smem_u32(&S.lfull), kSoftWarps / 2);
+        mbar_init(smem_u32(&S.invfree), kOutWarps);
+        mbar_init(smem_u32(&S.ofree), 2 * kOutWarps);
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_u32(&S.itemfull[i]), 1);
-            mbar_init(smem_u32(&S.itemempty[i]), kSoftWarps + (rank == 0 ? 3 : 2));   // the warps that read items
+            mbar_init(smem_u32(&S.itemempty[i]), kSoftWarps + kOutWarps + (rank == 0 ? 3 : 2));   // the warps that read items
             mbar_init(smem_u32(&S.numfull[i]), 1);
             mbar_init(smem_u32(&S.numempty[i]), 1);
         }
@@ -220,10 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto lead = [&](uint64_t& b) -> uint32_t { return map_to_cluster_rank(smem_u32(&b), 0); };
     // bounded; a thread whose wait expired waits for nothing any more
     auto wait = [&](uint64_t& b, uint32_t parity) -> bool {
-        if (ok && !mbar_wait_rolled(smem_u32(&b), parity)) {
-            ok = false;
-            latch_status(a.status, DSA_ERR_TIMEOUT);
-        }
+        ok = ok && mbar_wait_small(smem_u32(&b), parity, a.status);
         return ok;
     };
     // the next item that warp 3 published; false behind the last
@@ -239,121 +250,118 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return ok && to.tiles > 0;
     };
 
-    if (warp == 0) {
-        // Q and K loads: lane 0 waits, then each lane issues a box.  Rows behind
-        // the last new row are another sequence's or zeros: nobody reads what
-        // comes of them.
+    if (warp == 0 || warp == 2) {
+        // K or V loads: lane 0 waits, then each lane issues a box.  Before an
+        // item's V its Q, a chunk as soon as the last S before is through with
+        // it: not before its K, which need not wait for that.  Rows behind the
+        // last new row are another sequence's or zeros: nobody reads what comes
+        // of them.
+        const bool k = warp == 0;
+        uint64_t* const full = k ? S.kfull : S.vfull;
+        uint64_t* const empty = k ? S.kempty : S.vempty;
+        const int boxes = k ? kQChunks : 2;
+        const uint32_t box = k ? kKBytes : kQBytes;
+        const bool pe = k && lane == kQChunks - 1;
+        const CUtensorMap* const map = pe ? &tm_pe : k ? &tm_k : &tm_v;
+        const uint32_t to = smem_u32(k ? S.k : S.v) + lane * box;
+        const int32_t col = k ? 64 * lane : kNope + 128 * (int)rank + 64 * lane, row = k ? 64 * (int)rank : 0;
         uint32_t g = 0, seg = 0;
-        Item n;
-        bool more = next_item(it);
-        for (; more; ++seg) {
-            for (int32_t t = 0; ok && t < it.tiles; ++t, ++g) {
-                if (t == 0) {
-#pragma unroll 1
-                    for (int c = 0; ok && c < kQChunks; ++c) {
-                        if (lane == 0 && (seg == 0 || wait(S.qempty[c], (seg - 1) & 1))) {
-                            mbar_arrive_expect_tx_pair(lead(S.qfull[c]), kQBytes);
-                            tma_load_2d_pair(smem_u32(S.q + c * kQBytes), &tm_q, lead(S.qfull[c]),
-                                             it.head * kHeadQK + 64 * c, it.row + 128 * (int)rank);
-                        }
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
+        for (; next_item(it); ++seg) {
+            if (!k) {
+                for (int q = 0; ok && q < kQChunks; ++q) {
+                    if (lane == 0 && (seg == 0 || wait(S.qempty[q], (seg - 1) & 1))) {
+                        mbar_arrive_expect_tx_pair(lead(S.qfull[q]), kQBytes);
+                        tma_load_2d_pair(smem_u32(S.q + q * kQBytes), &tm_q, lead(S.qfull[q]), it.head * kHeadQK + 64 * q,
+                                         it.row + 128 * (int)rank);
                     }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
                 }
-                const uint32_t st = g % kStages;
-                const uint32_t bar = lead(S.kfull[st]);
-                if (lane == 0 && (g < kStages || wait(S.kempty[st], (g / kStages - 1) & 1)))
-                    mbar_arrive_expect_tx_pair(bar, kQChunks * kKBytes);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                const int32_t r = it.at + t * kTile + 64 * (int)rank;
-                uint8_t* to = S.k + (st * kQChunks + lane) * kKBytes;
-                if (ok && lane < kQChunks - 1)
-                    tma_load_2d_pair(smem_u32(to), &tm_k, bar, it.head * kExpRow + 64 * lane, r);
-                else if (ok && lane == kQChunks - 1)
-                    tma_load_2d_pair(smem_u32(to), &tm_pe, bar, 0, r);
             }
-            // the queries of the next item, whose place in shared memory is
-            // not free before this one's last S
-            more = next_item(n);
-            if (more && lane < kQChunks) tma_prefetch_2d(&tm_q, n.head * kHeadQK + 64 * lane, n.row + 128 * (int)rank);
-            it = n;
+            const int32_t c = pe ? 0 : it.head * kExpRow + col;
+            for (int32_t t = 0; ok && t < it.tiles; ++t, ++g) {
+                const uint32_t st = g % kStages, bar = lead(full[st]);
+                if (lane == 0 && (g < kStages || wait(empty[st], (g / kStages - 1) & 1)))
+                    mbar_arrive_expect_tx_pair(bar, boxes * box);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (ok && lane < boxes) tma_load_2d_pair(to + st * boxes * box, map, bar, c, it.at + t * kTile + row);
+            }
         }
     } else if (warp == 1) {
-        if (rank == 0) {
-            // MMA: S of tile g + 1, then PV of tile g, issued by one elected
-            // lane, which also waits; an item's first S behind the last PV before
-            // it, under which its queries are loaded
+        if (rank == 0 && elect_one()) {
+            // MMA, by one lane that also waits: S of tile t, then PV of tile t - 1;
+            // an item's first S behind the last PV before it, under which its
+            // queries are loaded.  One loop over all tiles, with the next
+            // item read before that last PV: what is met once an item is
+            // fetched as it goes (15 cycles an instruction), and nothing
+            // else runs meanwhile.
             constexpr uint32_t kIdS = idesc_bf16_f32(kRows, kTile), kIdO = idesc_bf16_f32(kRows, kHeadV, false, true);
-            // S of tile g; first / last of its item (number seg)
-            auto issue_s = [&](uint32_t g, bool first, bool last, uint32_t seg) {
-                const uint32_t buf = g & 1, st = g % kStages;
-                if (g >= 2 && !wait(S.sempty[buf], ((g >> 1) - 1) & 1)) return;
-                if (!wait(S.kfull[st], (g / kStages) & 1)) return;
-                tc_fence_after();
-                const uint64_t dq = sdesc_sw128(smem_u32(S.q), 0, 1024);
-                const uint64_t dk = sdesc_sw128(smem_u32(S.k + st * kQChunks * kKBytes), 0, 1024);
-#pragma unroll
-                for (int c = 0; c < kQChunks; ++c) {
-                    if (first) {
-                        if (!wait(S.qfull[c], seg & 1)) return;
-                        tc_fence_after();
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16_ss_pair(tmem + kSCol + kTile * buf, dq + c * (kQBytes >> 4) + 2 * k,
-                                         dk + c * (kKBytes >> 4) + 2 * k, kIdS, (c | k) != 0);
-                    if (last) mma_commit_pair(smem_u32(&S.qempty[c]));
-                }
-                mma_commit_pair(smem_u32(&S.kempty[st]));
-                mma_commit_pair(smem_u32(&S.sfull[buf]));
+            const uint64_t dq = sdesc_sw128(smem_u32(S.q), 0, 1024), dk = sdesc_sw128(smem_u32(S.k), 0, 1024);
+            const uint64_t dv = sdesc_sw128(smem_u32(S.v), kQBytes, 1024);
+            // tiles of item `seg`, and its keys
+            auto read = [&](uint32_t seg, int32_t& tiles, int32_t& keys) {
+                const uint32_t slot = seg % kSlots;
+                tiles = keys = 0;
+                if (!wait(S.itemfull[slot], (seg / kSlots) & 1)) return;
+                tiles = S.item[slot].tiles;
+                keys = S.item[slot].pos + S.item[slot].rows;
+                mbar_arrive(smem_u32(&S.itemempty[slot]));
             };
-            // PV of tile g, of whose positions `keys` are seen by some row
-            auto issue_pv = [&](uint32_t g, bool first, int32_t keys, uint32_t seg) {
-                if (first && seg > 0 && !wait(S.ofree, (seg - 1) & 1)) return;
-                const uint32_t st = g % kStages;
-                if (!wait(S.vfull[st], (g / kStages) & 1)) return;
-                if (!wait(S.pfull, g & 1)) return;
-                tc_fence_after();
-                const uint64_t dp = sdesc_sw128(smem_u32(S.p), 0, 1024);
-                const uint64_t dv = sdesc_sw128(smem_u32(S.v + st * 2 * kQBytes), kQBytes, 1024);
+            int32_t tiles, keys, tiles_next = 0, keys_next = 0;
+            read(0, tiles, keys);
+            uint32_t seg = 0, n = 0;             // n: tiles whose S is issued
+#pragma unroll 1
+            for (int32_t t = 0; tiles > 0; ++t) {
+                if (t < tiles) {
+                    const uint32_t buf = n & 1, st = n % kStages;
+                    if (!wait(S.kfull[st], (n / kStages) & 1)) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < kQChunks; ++c) {
+                        if (t == 0) {
+                            if (!wait(S.qfull[c], seg & 1)) break;
+                            tc_fence_after();
+                        }
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    if (16 * k < keys)
-                        mma_bf16_ss_pair(tmem + kOCol, dp + (k >> 2) * (kQBytes >> 4) + 2 * (k & 3), dv + 128 * k, kIdO,
-                                         !first || k != 0);
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_ss_pair(tmem + kSCol + kTile * buf, dq + c * (kQBytes >> 4) + 2 * k,
+                                             dk + (st * kQChunks + c) * (kKBytes >> 4) + 2 * k, kIdS, (c | k) != 0);
+                        if (t + 1 == tiles) mma_commit_pair(smem_u32(&S.qempty[c]));
+                    }
+                    if (!ok) break;
+                    mma_commit_pair(smem_u32(&S.kempty[st]));
+                    mma_commit_pair(smem_u32(&S.sfull[buf]));
+                    ++n;
+                    if (t == 0) continue;
+                } else {
+                    read(seg + 1, tiles_next, keys_next);
+                    if (!ok) break;
+                }
+                const uint32_t m = n - (t < tiles ? 2 : 1), st = m % kStages;
+                if (t == 1 && seg > 0 && !wait(S.ofree, (seg - 1) & 1)) break;
+                if (!wait(S.vfull[st], (m / kStages) & 1)) break;
+                if (!wait(S.pfull[m & 1], (m >> 1) & 1)) break;
+                tc_fence_after();
+                // positions behind the last that a row sees have no weight
+                const int32_t steps = min(kTile, keys - (t - 1) * kTile + 15) / 16;
+#pragma unroll 1
+                for (int k = 0; k < steps; ++k)
+                    mma_bf16_ts_pair(tmem + kOCol, tmem + kSCol + kTile * (m & 1) + 64 * (k >> 2) + 8 * (k & 3),
+                                     dv + st * (2 * kQBytes >> 4) + 128 * k, kIdO, t > 1 || k != 0);
                 mma_commit_pair(smem_u32(&S.vempty[st]));
                 mma_commit_pair(smem_u32(&S.pvdone));
-            };
-            uint32_t g = 0;
-            for (uint32_t seg = 0; next_item(it); ++seg) {
-                if (elect_one()) {
-                    issue_s(g, true, it.tiles == 1, seg);
-                    for (int32_t t = 0; ok && t < it.tiles; ++t) {
-                        if (t + 1 < it.tiles) issue_s(g + t + 1, false, t + 2 == it.tiles, seg);
-                        if (ok) issue_pv(g + t, t == 0, it.pos + it.rows - t * kTile, seg);
-                    }
+                if (t == tiles) {
+                    mma_commit_pair(smem_u32(&S.odone));
+                    tiles = tiles_next;
+                    keys = keys_next;
+                    ++seg;
+                    t = -1;
                 }
-                __syncwarp();
-                ok = __all_sync(0xffffffffu, ok);
-                g += it.tiles;
             }
         }
-    } else if (warp == 2) {
-        // V loads
-        uint32_t g = 0;
-        while (next_item(it)) {
-            for (int32_t t = 0; ok && t < it.tiles; ++t, ++g) {
-                const uint32_t st = g % kStages;
-                const uint32_t bar = lead(S.vfull[st]);
-                if (lane == 0 && (g < kStages || wait(S.vempty[st], (g / kStages - 1) & 1)))
-                    mbar_arrive_expect_tx_pair(bar, 2 * kQBytes);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (ok && lane < 2)
-                    tma_load_2d_pair(smem_u32(S.v + (st * 2 + lane) * kQBytes), &tm_v, bar,
-                                     it.head * kExpRow + kNope + 128 * (int)rank + 64 * lane, it.at + t * kTile);
-            }
-        }
+        __syncwarp();
     } else if (warp == 3) {
-        // items: rank 0 takes their numbers and passes them on
+        // items: rank 0 takes their numbers and passes them on; their queries
+        // are brought to L2 ahead
         for (uint32_t n = 0; ok; ++n) {
             const uint32_t slot = n % kSlots, turn = n / kSlots;
             uint32_t number = 0;
@@ -363,16 +371,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     latch_status(a.status, DSA_ERR_TIMEOUT);
                 }
             };
-            if (n >= kSlots) wait(S.itemempty[slot], (turn - 1) & 1);
-            if (lane == 0 && ok) {
-                if (rank == 0) {
+            if (lane == 0) {
+                if (n >= kSlots) wait(S.itemempty[slot], (turn - 1) & 1);
+                if (ok && rank == 0) {
                     number = n == 0 ? blockIdx.x >> 1 : atomicAdd(a.next, 1u);
                     if (n >= kSlots) wait_peer(S.numempty[slot], (turn - 1) & 1);
                     if (ok) {
                         st_peer_u32(map_to_cluster_rank(smem_u32(&S.number[slot]), 1), number);
                         mbar_arrive_peer(map_to_cluster_rank(smem_u32(&S.numfull[slot]), 1));
                     }
-                } else {
+                } else if (ok) {
                     wait_peer(S.numfull[slot], turn & 1);
                     number = *reinterpret_cast<volatile uint32_t*>(&S.number[slot]);
                     if (ok) mbar_arrive_peer(lead(S.numempty[slot]));
@@ -387,13 +395,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mbar_arrive(smem_u32(&S.itemfull[slot]));
             }
             __syncwarp();
+            if (it.tiles > 0 && lane < kQChunks)
+                tma_prefetch_2d(&tm_q, it.head * kHeadQK + 64 * lane, it.row + 128 * (int)rank);
+            __syncwarp();
             if (it.tiles == 0) break;
         }
-    } else {
-        // softmax and epilogue: TMEM lane = query row of this CTA
+    } else if (warp < 4 + kSoftWarps) {
+        // softmax: TMEM lane = query row of this CTA
         const int ln = tid - 128, x = ln & 127, half = ln >> 7;
         const uint32_t tl = tmem + ((uint32_t)(x & ~31) << 16);
-        uint32_t g = 0, xb = 0;
+        uint32_t g = 0, seg = 0, xb = 0;
         auto exchange = [&](float v) -> float {
             xb ^= 1;
             S.xch[xb][ln] = v;
@@ -413,9 +424,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tmem_ld_32x32b_x32(tl + kSCol + kTile * buf + 64 * half, r[0]);
                 tmem_ld_32x32b_x32(tl + kSCol + kTile * buf + 64 * half + 32, r[1]);
                 tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(lead(S.sempty[buf]));
                 if ((t + 1) * kTile - 1 > first) {
                     const int32_t d = first + x - (t * kTile + 64 * half);       // the last column that the row sees
 #pragma unroll
@@ -441,10 +449,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     pk[k >> 1] = pack_bf16x2(p0, p1);
                 }
                 l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
-                if (g > 0) wait(S.pvdone, (g - 1) & 1);
-                __syncwarp();
-                tc_fence_after();
                 if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                    wait(S.pvdone, (g - 1) & 1);
+                    __syncwarp();
+                    tc_fence_after();
 #pragma unroll 1
                     for (uint32_t c = 0; c < 128; c += 16) {
                         uint32_t o[16];
@@ -454,37 +462,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                         tmem_st_32x32b_x16(tl + kOCol + 128 * half + c, o);
                     }
-                    tmem_st_wait();
                 }
-                uint8_t* pr = S.p + half * kQBytes + x * 128;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    *reinterpret_cast<uint4*>(pr + ((k ^ (x & 7)) << 4)) =
-                        make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
-                fence_proxy_async_smem();
+                // P over the first half of the columns that this warp's part of S had
+                tmem_st_32x32b_x32(tl + kSCol + kTile * buf + 64 * half, pk);
+                tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_pair(lead(S.pfull));
+                if (lane == 0) mbar_arrive_pair(lead(S.pfull[buf]));
             }
-            wait(S.pvdone, (g - 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
             // Every row sees itself, so l > 0 but where every score is -inf: NaN, as of the formula.
             l += exchange(l);
-            const float inv = 1.f / l;
-            const int32_t mine = it.row + 128 * (int)rank, live = it.rows - 128 * (int)rank;      // rows of this CTA
-            if (ok && a.lse && half == 0 && x < live)
-                a.lse[(int64_t)(mine + x) * kH + it.head] = (m + log2f(l)) * kLn2;
-            // O through this warp's 4 KiB of P's buffer, so that a store covers
-            // whole 128-byte lines of 4 rows
-            uint8_t* stage = S.p + (warp - 4) * 4096;
-            const int32_t r0 = x & ~31;
-            if (ok && r0 < live) {
+            if (half == 0) {
+                if (seg > 0) wait(S.invfree, (seg - 1) & 1);
+                S.inv[x] = rcp_approx(l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&S.lfull));
+                if (a.lse && x < it.rows - 128 * (int)rank)
+                    a.lse[(int64_t)(it.row + 128 * (int)rank + x) * kH + it.head] = (m + lg2_approx(l)) * kLn2;
+            }
+            ++seg;
+        }
+    } else {
+        // results: TMEM lane = query row of this CTA
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const int r0 = 32 * (warp & 3);
+        // through shared memory, so that a store covers whole lines of 4 rows
+        uint8_t* const stage = S.out + (warp & 3) * 4096;
+        uint32_t seg = 0;
+        while (next_item(it)) {
+            wait(S.lfull, seg & 1);
+            wait(S.odone, seg & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            const float inv = S.inv[r0 + lane];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.invfree));
+            const int32_t mine = it.row + 128 * (int)rank + r0, live = it.rows - 128 * (int)rank - r0;
+            if (ok && live > 0) {
+                uint16_t* const to = a.out + ((int64_t)mine * kH + it.head) * kHeadV + 8 * (lane & 7);
 #pragma unroll 1
-                for (uint32_t c = 0; c < 128; c += 64) {
+                for (uint32_t c = 0; c < 256; c += 64) {
                     uint32_t o[2][32];
-                    tmem_ld_32x32b_x32(tl + kOCol + 128 * half + c, o[0]);
-                    tmem_ld_32x32b_x32(tl + kOCol + 128 * half + c + 32, o[1]);
+                    tmem_ld_32x32b_x32(tl + kOCol + c, o[0]);
+                    tmem_ld_32x32b_x32(tl + kOCol + c + 32, o[1]);
                     tmem_ld_wait();
 #pragma unroll
                     for (int v = 0; v < 8; ++v) {
@@ -499,18 +519,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     __syncwarp();
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const int row = 4 * k + (lane >> 3), at = lane & 7;
-                        if (r0 + row < live)
-                            *reinterpret_cast<uint4*>(a.out + ((int64_t)(mine + r0 + row) * kH + it.head) * kHeadV +
-                                                      128 * half + c + 8 * at) =
-                                *reinterpret_cast<const uint4*>(stage + row * 128 + ((at ^ (row & 7)) << 4));
+                        const int row = 4 * k + (lane >> 3);
+                        if (row < live)
+                            *reinterpret_cast<uint4*>(to + (int64_t)row * kH * kHeadV + c) =
+                                *reinterpret_cast<const uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
                     }
                     __syncwarp();
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair(lead(S.ofree));
+            if (lane == 0) {
+                mbar_arrive_pair(lead(S.ofree));
+            }
+            ++seg;
         }
     }
     if (!ok) {
