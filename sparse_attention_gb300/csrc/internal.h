@@ -25,6 +25,11 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // The first 256 bytes of every workspace: the device status word.
 constexpr size_t kWsHeaderBytes = 256;
 
+// 32-bit words of the header behind the status word in which kernels of the
+// expanded form count what their CTAs have taken.  They are 0 between launches: cleared
+// with the status word, and by each launch behind itself.
+constexpr int kCounterWord = 16;
+
 // Device view of dsa_batch.
 struct BatchDev {
     int32_t B, total_q, max_q, max_ctx;

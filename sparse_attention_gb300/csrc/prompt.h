@@ -49,6 +49,27 @@ struct GroupsDev {
     const int32_t *off, *shared;
 };
 
+// The sum of v over the threads before this one of a block of `warps` warps, and
+// over all of it in `all`; `sums` has a place for each warp.
+__device__ __forceinline__ int32_t block_sum_before(int32_t v, int warps, int32_t* sums, int32_t& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t n = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += n;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int32_t before = incl - v;
+    all = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) before += sums[w];
+        all += sums[w];
+    }
+    return before;
+}
+
 // CTA pairs of kernel `f` that can be resident at once on the current device,
 // at most `most`.
 int resident_pairs(const void* f, int threads, size_t smem, int most);

@@ -95,6 +95,8 @@ struct Smem {
     Item item[kSlots];
     uint32_t number[kSlots];
     float xch[2][32 * kSoftWarps];
+    alignas(16) int4 seq[kThreads];                      // the plan of a batch of few sequences: first new row, how many,
+    int32_t start[kThreads + 1], sums[kThreads / 32];    // .. length, first expanded row; query tiles before it
     float inv[128];                                      // 1 / the sum of a finished item's row
     uint32_t tmem;
 };
@@ -106,69 +108,55 @@ struct Args {
     float scale_log2;
     uint16_t* out;
     float* lse;
-    const int32_t* start;        // [B + 1] query tiles before a sequence
-    uint32_t* next;              // number of the next item that nobody has taken
+    const int32_t* start;        // [B + 1] query tiles before a sequence; nullptr: each CTA sums them up itself
+    uint32_t* next;              // items that pairs have taken behind their first ones, and pairs that are done; 0 between launches
     int32_t* status;
 };
 
-// Query tiles before each sequence, and the counter behind the items that the
-// pairs begin with.  A sequence that breaks the bounds has none.
+// Sequence b: its first new row, how many there are, its length, and where its
+// expanded rows begin; no new rows for one that breaks the bounds.
+__device__ __forceinline__ int4 sequence(const BatchDev& bd, const ExpandedDev& x, int b, int32_t* status) {
+    SeqInfo s;
+    if (b >= bd.B || !load_seq(bd, b, status, s) || s.nq == 0) return make_int4(0, 0, 0, 0);
+    const int32_t at = expanded_at(x, b, s.ctx, status);
+    return at < 0 ? make_int4(0, 0, 0, 0) : make_int4(s.q0, s.nq, s.ctx, at);
+}
+__device__ __forceinline__ int32_t tiles_of(int32_t rows) { return (rows + kRows - 1) / kRows; }
+
+// Query tiles before each sequence, for batches of more than kThreads (a launch
+// more: 4 us).
 __global__ void __launch_bounds__(1024)
-    prompt_plan_kernel(const BatchDev bd, const ExpandedDev x, int32_t* start, uint32_t* next, uint32_t pairs,
-                       int32_t* status) {
+    prompt_plan_kernel(const BatchDev bd, const ExpandedDev x, int32_t* start, int32_t* status) {
     __shared__ int32_t sums[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     pdl_launch_dependents();
     pdl_wait();
-    if (tid == 0) {
-        *next = pairs;
-        start[0] = 0;
-    }
+    if (tid == 0) start[0] = 0;
     int32_t carry = 0;
     for (int b0 = 0; b0 < bd.B; b0 += 1024) {
-        const int b = b0 + tid;
-        SeqInfo s{0, 0, 0};
-        int32_t n = 0;
-        if (b < bd.B && load_seq(bd, b, status, s) && s.nq > 0 && expanded_at(x, b, s.ctx, status) >= 0)
-            n = (s.nq + kRows - 1) / kRows;
-        int32_t incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) sums[warp] = incl;
-        __syncthreads();
-        if (warp == 0) {
-            int32_t v = sums[lane];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
-            sums[lane] = v;
-        }
-        __syncthreads();
-        if (b < bd.B) start[b + 1] = carry + incl + (warp > 0 ? sums[warp - 1] : 0);
-        carry += sums[31];
+        const int32_t n = tiles_of(sequence(bd, x, b0 + tid, status).y);
+        int32_t all;
+        const int32_t before = block_sum_before(n, 32, sums, all);
+        if (b0 + tid < bd.B) start[b0 + tid + 1] = carry + before + n;
+        carry += all;
         __syncthreads();
     }
 }
 
-__device__ __forceinline__ Item item_of(const Args& a, uint32_t number) {
+__device__ __forceinline__ Item item_of(const Args& a, const Smem& S, uint32_t number) {
     Item it{0, 0, 0, 0, 0, 0};
-    if (number >= (uint32_t)a.start[a.bd.B] * kH) return it;
-    const int b = last_at_or_below(a.start, a.bd.B, (int32_t)(number / kH));
-    const uint32_t tiles = (uint32_t)(a.start[b + 1] - a.start[b]), in = number - (uint32_t)a.start[b] * kH;
-    SeqInfo s;
-    if (!load_seq(a.bd, b, nullptr, s)) return it;       // lengths that change under the call
-    const int32_t end = s.nq - kRows * (int32_t)(in % tiles), i0 = max(0, end - kRows);
-    if (end <= 0) return it;
+    const int32_t* const start = a.start ? a.start : S.start;
+    if (number >= (uint32_t)start[a.bd.B] * kH) return it;
+    const int b = last_at_or_below(start, a.bd.B, (int32_t)(number / kH));
+    const uint32_t tiles = (uint32_t)(start[b + 1] - start[b]), in = number - (uint32_t)start[b] * kH;
+    const int4 s = a.start ? sequence(a.bd, a.x, b, nullptr) : S.seq[b];
+    const int32_t end = s.y - kRows * (int32_t)(in % tiles), i0 = max(0, end - kRows);
+    if (end <= 0) return it;                     // lengths that change under the call
     it.head = (int32_t)(in / tiles);
-    it.row = s.q0 + i0;
+    it.row = s.x + i0;
     it.rows = end - i0;
-    it.pos = s.ctx - s.nq + i0;
-    it.at = __ldg(a.x.off + b);
+    it.pos = s.z - s.y + i0;
+    it.at = s.w;
     it.tiles = (it.pos + it.rows - 1) / kTile + 1;
     return it;
 }
@@ -223,6 +211,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_arrive();                            // the peer may use this CTA's barriers and TMEM ..
     pdl_wait();                                  // inputs, and the scratch of an earlier call
+    if (!a.start) {
+        S.seq[tid] = sequence(a.bd, a.x, tid, a.status);
+        const int32_t n = tiles_of(S.seq[tid].y);
+        int32_t all;
+        S.start[tid + 1] = block_sum_before(n, kThreads / 32, S.sums, all) + n;
+        if (tid == 0) S.start[0] = 0;
+    }
     tc_fence_before();
     __syncthreads();
     cluster_wait();                              // .. and this CTA the peer's
@@ -259,12 +254,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool k = warp == 0;
         uint64_t* const full = k ? S.kfull : S.vfull;
         uint64_t* const empty = k ? S.kempty : S.vempty;
-        const int boxes = k ? kQChunks : 2;
-        const uint32_t box = k ? kKBytes : kQBytes;
-        const bool pe = k && lane == kQChunks - 1;
-        const CUtensorMap* const map = pe ? &tm_pe : k ? &tm_k : &tm_v;
-        const uint32_t to = smem_u32(k ? S.k : S.v) + lane * box;
-        const int32_t col = k ? 64 * lane : kNope + 128 * (int)rank + 64 * lane, row = k ? 64 * (int)rank : 0;
+        // K: the head's three chunks, and by lane 1 the shared one; V: two
+        const int boxes = k ? 2 : 1;
+        const bool pe = k && lane == 1;
+        const uint32_t bytes = k ? kQChunks * kKBytes : 2 * kQBytes;
+        const uint32_t to = smem_u32(k ? S.k : S.v) + (pe ? (kQChunks - 1) * kKBytes : 0);
+        const int32_t chunk = k ? 0 : kNope / 64 + 2 * (int)rank, row = k ? 64 * (int)rank : 0;
         uint32_t g = 0, seg = 0;
         for (; next_item(it); ++seg) {
             if (!k) {
@@ -277,13 +272,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                 }
             }
-            const int32_t c = pe ? 0 : it.head * kExpRow + col;
             for (int32_t t = 0; ok && t < it.tiles; ++t, ++g) {
                 const uint32_t st = g % kStages, bar = lead(full[st]);
                 if (lane == 0 && (g < kStages || wait(empty[st], (g / kStages - 1) & 1)))
-                    mbar_arrive_expect_tx_pair(bar, boxes * box);
+                    mbar_arrive_expect_tx_pair(bar, bytes);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (ok && lane < boxes) tma_load_2d_pair(to + st * boxes * box, map, bar, c, it.at + t * kTile + row);
+                const int32_t r = it.at + t * kTile + row;
+                if (ok && pe) tma_load_2d_pair(to + st * bytes, &tm_pe, bar, 0, r);
+                else if (ok && lane < boxes) tma_load_3d_pair(to + st * bytes, k ? &tm_k : &tm_v, bar, 0, r, it.head * (kExpRow / 64) + chunk);
             }
         }
     } else if (warp == 1) {
@@ -374,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 if (n >= kSlots) wait(S.itemempty[slot], (turn - 1) & 1);
                 if (ok && rank == 0) {
-                    number = n == 0 ? blockIdx.x >> 1 : atomicAdd(a.next, 1u);
+                    number = n == 0 ? blockIdx.x >> 1 : (gridDim.x >> 1) + atomicAdd(a.next, 1u);
                     if (n >= kSlots) wait_peer(S.numempty[slot], (turn - 1) & 1);
                     if (ok) {
                         st_peer_u32(map_to_cluster_rank(smem_u32(&S.number[slot]), 1), number);
@@ -389,7 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            it = item_of(a, __shfl_sync(0xffffffffu, number, 0));
+            it = item_of(a, S, __shfl_sync(0xffffffffu, number, 0));
             if (lane == 0) {
                 S.item[slot] = it;
                 mbar_arrive(smem_u32(&S.itemfull[slot]));
@@ -547,6 +543,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_wait();
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
+    // the last pair leaves the counters as it found them
+    if (tid == 0 && rank == 0) {
+        const uint32_t last = (gridDim.x >> 1) - 1;
+        __threadfence();
+        if (atomicInc(a.next + 1, last) == last) *a.next = 0u;
+    }
 }
 
 // Query tiles that the batch's bounds allow, over all heads.
@@ -591,7 +593,7 @@ int resident_pairs(const void* f, int threads, size_t smem, int most) {
     return std::min(n, most);
 }
 
-size_t prompt_mla_scratch_bytes(const BatchDev& bd) { return ((size_t)bd.B + 1) * sizeof(int32_t) + sizeof(uint32_t); }
+size_t prompt_mla_scratch_bytes(const BatchDev& bd) { return ((size_t)bd.B + 1) * sizeof(int32_t); }
 
 cudaError_t launch_prompt_mla(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, float sm_scale,
                               uint16_t* out, float* lse, void* scratch, int32_t* status, cudaStream_t stream) {
@@ -603,28 +605,30 @@ cudaError_t launch_prompt_mla(const BatchDev& bd, const uint16_t* q, const Expan
     a.scale_log2 = sm_scale * kLog2e;
     a.out = out;
     a.lse = lse;
-    a.next = static_cast<uint32_t*>(scratch);
-    int32_t* start = static_cast<int32_t*>(scratch) + 1;
-    a.start = start;
+    a.next = reinterpret_cast<uint32_t*>(status) + kCounterWord;
     a.status = status;
     CUtensorMap tm_q, tm_k, tm_v, tm_pe;
     if (!make_tmap_bf16_2d(&tm_q, q, (uint64_t)kH * kHeadQK, (uint64_t)bd.total_q, 64, 128) ||
-        !make_tmap_bf16_2d(&tm_k, x.kv, (uint64_t)kH * kExpRow, (uint64_t)x.rows, 64, 64) ||
-        !make_tmap_bf16_2d(&tm_v, x.kv, (uint64_t)kH * kExpRow, (uint64_t)x.rows, 64, kTile) ||
+        !make_tmap_bf16_chunks(&tm_k, x.kv, (uint64_t)kH * kExpRow / 64, (uint64_t)x.rows, 64, kNope / 64) ||
+        !make_tmap_bf16_chunks(&tm_v, x.kv, (uint64_t)kH * kExpRow / 64, (uint64_t)x.rows, kTile, 2) ||
         !make_tmap_bf16_2d(&tm_pe, x.k_pe, DSA_ROPE_DIM, (uint64_t)x.rows, 64, 64))
         return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(1024);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, prompt_plan_kernel, bd, x, start, a.next, (uint32_t)pairs, status);
-    if (e != cudaSuccess) return e;
-    count_launches(1);
+    cudaError_t e;
+    if (bd.B > kThreads) {
+        int32_t* start = static_cast<int32_t*>(scratch);
+        a.start = start;
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(1024);
+        if ((e = cudaLaunchKernelEx(&cfg, prompt_plan_kernel, bd, x, start, status)) != cudaSuccess) return e;
+        count_launches(1);
+    }
     if ((e = cudaFuncSetAttribute(prompt_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem))) !=
         cudaSuccess)
         return e;
