@@ -120,7 +120,6 @@ static_assert(sizeof(Run) == 32, "two 16-byte loads");
 
 struct RunPlan {
     int64_t all, chunk;          // units, and those of a pair
-    int32_t runs, shared;        // all runs, and those over shared tiles
 };
 
 // The pieces of a row's shared or own part: those of one item, in order of the
@@ -168,6 +167,7 @@ struct Args {
     // behind shared prefixes only
     const RunPlan* rplan;
     const Run* runs;
+    int32_t runs_total, runs_shared;     // all runs, and those over shared tiles
     RowPieces* pieces;   // [2][total_q]: shared, own
 };
 
@@ -270,28 +270,33 @@ struct RunIter {
     const Args& a;
     const int32_t pair;
     int64_t lo, hi, chunk;
-    int32_t r = 0, p = -1, n_runs, n_shared;
+    int32_t r = 0, p = -1;
+    Run q{};
     __device__ RunIter(const Args& args, int32_t pair_) : a(args), pair(pair_) {
-        const RunPlan pl = *a.rplan;
-        chunk = pl.chunk;
-        lo = min(pl.all, pair * chunk);
-        hi = min(pl.all, lo + chunk);
-        n_runs = pl.runs;
-        n_shared = pl.shared;
-        // the last run that begins at or before lo
-        int top = n_runs;
-        while (r + 1 < top) {
-            const int mid = (r + top) >> 1;
-            if (a.runs[mid].u <= lo) r = mid;
-            else top = mid;
+        // The last run that begins at or before lo: 32 probes at a time, the
+        // first on their way with the plan itself.
+        const int lane = (int)lane_id();
+        int32_t span = a.runs_total;             // it is one of runs r .. r + span - 1
+        for (bool first = true; first || span > 1; first = false) {
+            const int32_t step = (span + 31) / 32, at = r + lane * step;
+            const int64_t u = lane * step < span ? a.runs[at].u : INT64_MAX;
+            if (first) {
+                const RunPlan pl = *a.rplan;
+                chunk = pl.chunk;
+                lo = min(pl.all, pair * chunk);
+                hi = min(pl.all, lo + chunk);
+            }
+            const int last = __popc(__ballot_sync(0xffffffffu, u <= lo)) - 1;
+            r += last * step;
+            span = min(step, span - last * step);
         }
+        if (lo < hi) q = a.runs[r];
     }
     __device__ int32_t holder(int64_t u) const { return (int32_t)(u / chunk); }
 
     __device__ bool next(SharedSeg& s) {
         if (lo >= hi) return false;
-        for (; r < n_runs; ++r, p = 0) {
-            const Run q = a.runs[r];
+        while (r < a.runs_total) {
             const int32_t tiles = (q.len + kTile - 1) / kTile - q.base, per = tiles + kItemCost, items = (q.nq + 1) >> 1;
             if (p < 0) p = (int32_t)min((int64_t)items, (lo - q.u) / per);
             while (p < items) {
@@ -301,7 +306,7 @@ struct RunIter {
                 s.t1 = (int32_t)max((int64_t)0, min((int64_t)tiles, hi - u0));
                 const int32_t item = p++;
                 if (s.t1 <= s.t0) continue;
-                const bool shared = r < n_shared;
+                const bool shared = r < a.runs_shared;
                 s.b = q.b;
                 s.i0 = shared ? 0 : 2 * item;
                 s.row = q.q0 + 2 * item;
@@ -320,6 +325,8 @@ struct RunIter {
                 }
                 return true;
             }
+            p = 0;
+            if (++r < a.runs_total) q = a.runs[r];
         }
         return false;
     }
@@ -1256,39 +1263,67 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 // The runs of a call behind shared prefixes, by the first block; the others
 // clear the rows' pieces.  A group counts if all groups together are the
 // batch in order and each of its sequences with new rows keeps the shared ones; else
-// its sequences are computed each by itself.
+// its sequences are computed each by itself.  kFew: a thread for each run at most, so
+// that everything is loaded at once and the rest is shared memory's.
 constexpr int kPlanThreads = 1024;
 
+template <bool kFew>
 __global__ void __launch_bounds__(kPlanThreads)
-    prefix_plan_kernel(const BatchDev bd, const GroupsDev gr, RunPlan* plan, Run* runs, int32_t* tiles_of,
-                       int32_t* lead, RowPieces* pieces, int pairs, int32_t* status) {
+    prefix_plan_kernel(const BatchDev bd, const GroupsDev gr, RunPlan* plan, Run* runs, int32_t* tiles_all,
+                       int32_t* lead_all, RowPieces* pieces, int pairs, int32_t* status) {
     __shared__ int64_t s_units[kPlanThreads / 32];
     __shared__ int32_t s_items[kPlanThreads / 32], s_longest[kPlanThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int32_t s_off[kFew ? kPlanThreads + 1 : 1], s_rows[kFew ? kPlanThreads : 1], s_q[kFew ? kPlanThreads + 1 : 1],
+        s_tiles[kFew ? kPlanThreads : 1], s_lead[kFew ? kPlanThreads : 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = (int)blockDim.x;
     pdl_launch_dependents();
     pdl_wait();
     if (blockIdx.x > 0) {
-        for (int64_t i = (int64_t)(blockIdx.x - 1) * kPlanThreads + tid; i < 2 * (int64_t)bd.total_q;
-             i += (int64_t)(gridDim.x - 1) * kPlanThreads)
+        for (int64_t i = (int64_t)(blockIdx.x - 1) * threads + tid; i < 2 * (int64_t)bd.total_q;
+             i += (int64_t)(gridDim.x - 1) * threads)
             pieces[i] = RowPieces{0, 0};
         return;
     }
-    bool wrong = false;
-    for (int g = tid; g < gr.n; g += kPlanThreads) {
-        const int32_t lo = __ldg(gr.off + g), hi = __ldg(gr.off + g + 1), rows = __ldg(gr.shared + g);
-        wrong = wrong || lo < 0 || lo > hi || hi > bd.B || (g == 0 && lo != 0) || (g == gr.n - 1 && hi != bd.B) || rows < 0;
-        tiles_of[g] = max(rows, 0) / kTile;
+    // tiles that a group shares, and the sequence that they are read from
+    int32_t* const tiles_of = kFew ? s_tiles : tiles_all;
+    int32_t* const lead = kFew ? s_lead : lead_all;
+    const int32_t* const off = kFew ? s_off : gr.off;
+    const int32_t* const rows_of = kFew ? s_rows : gr.shared;
+    const int32_t* const q_off = kFew ? s_q : bd.q_off;
+    const int32_t n = gr.n + bd.B;
+    // the sequence of run i >= gr.n
+    auto sequence = [&](int32_t i, SeqInfo& q) -> bool { return load_seq(bd, i - gr.n, status, q); };
+    SeqInfo mine{0, 0, 0};
+    bool good = false, wrong = false;
+    if (kFew) {
+        if (tid >= gr.n && tid < n) {
+            good = sequence(tid, mine);
+            s_q[tid - gr.n] = mine.q0;
+            if (tid == n - 1) s_q[bd.B] = mine.q0 + mine.nq;
+        }
+        if (tid < gr.n) {
+            s_off[tid] = __ldg(gr.off + tid);
+            s_rows[tid] = __ldg(gr.shared + tid);
+            if (tid == gr.n - 1) s_off[gr.n] = __ldg(gr.off + gr.n);
+        }
+        __syncthreads();
+    }
+    for (int g = tid; g < gr.n; g += threads) {
+        const int32_t lo = off[g], hi = off[g + 1];
+        wrong = wrong || lo < 0 || lo > hi || hi > bd.B || (g == 0 && lo != 0) || (g == gr.n - 1 && hi != bd.B) ||
+                rows_of[g] < 0;
+        tiles_of[g] = max(rows_of[g], 0) / kTile;
         lead[g] = bd.B;
     }
     if (wrong) latch_status(status, DSA_ERR_BAD_BATCH);
     wrong = __syncthreads_or(wrong);
-    for (int b = tid; b < bd.B && !wrong; b += kPlanThreads) {
-        const int g = last_at_or_below(gr.off, gr.n, b);
-        SeqInfo q;
-        const bool good = load_seq(bd, b, status, q);
-        if (good && q.nq == 0) continue;
-        if (good && __ldg(gr.shared + g) <= q.ctx - q.nq) {
-            atomicMin(lead + g, b);
+    for (int32_t i = kFew ? tid : gr.n + tid; i < n && !wrong; i += threads) {
+        if (i < gr.n) continue;
+        if (!kFew) good = sequence(i, mine);
+        if (good && mine.nq == 0) continue;
+        const int g = last_at_or_below(off, gr.n, i - gr.n);
+        if (good && rows_of[g] <= mine.ctx - mine.nq) {
+            atomicMin(lead + g, i - gr.n);
         } else {
             latch_status(status, DSA_ERR_BAD_BATCH);
             tiles_of[g] = 0;
@@ -1297,32 +1332,31 @@ __global__ void __launch_bounds__(kPlanThreads)
     __syncthreads();
     int64_t units = 0;
     int32_t items = 0, longest = 0;
-    const int32_t n = gr.n + bd.B;
-    for (int32_t i0 = 0; i0 < n; i0 += kPlanThreads) {
+    for (int32_t i0 = 0; i0 < n; i0 += threads) {
         const int32_t i = i0 + tid;
         Run r{0, 0, 0, 0, 0, 0, 0};
         if (i < gr.n) {
             if (!wrong && tiles_of[i] > 0 && lead[i] < bd.B) {
-                r.q0 = __ldg(bd.q_off + __ldg(gr.off + i));
-                r.nq = __ldg(bd.q_off + __ldg(gr.off + i + 1)) - r.q0;
+                r.q0 = q_off[off[i]];
+                r.nq = q_off[off[i + 1]] - r.q0;
                 r.len = tiles_of[i] * kTile;
                 r.b = lead[i];
             }
         } else if (i < n) {
-            SeqInfo q;
+            if (!kFew) good = sequence(i, mine);
             r.b = i - gr.n;
-            if (load_seq(bd, r.b, status, q) && q.nq > 0) {
-                r.q0 = q.q0;
-                r.nq = q.nq;
-                r.len = q.ctx;
-                r.base = wrong ? 0 : tiles_of[last_at_or_below(gr.off, gr.n, r.b)];
+            if (good && mine.nq > 0) {
+                r.q0 = mine.q0;
+                r.nq = mine.nq;
+                r.len = mine.ctx;
+                r.base = wrong ? 0 : tiles_of[last_at_or_below(off, gr.n, r.b)];
             }
         }
-        const int32_t mine = (r.nq + 1) >> 1, tiles = (r.len + kTile - 1) / kTile - r.base;
-        const int64_t cost = (int64_t)mine * (tiles + kItemCost);
-        longest = max(longest, mine > 0 ? tiles : 0);
+        const int32_t its = (r.nq + 1) >> 1, tiles = (r.len + kTile - 1) / kTile - r.base;
+        const int64_t cost = (int64_t)its * (tiles + kItemCost);
+        longest = max(longest, its > 0 ? tiles : 0);
         int64_t iu = cost;
-        int32_t ii = mine;
+        int32_t ii = its;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t u = __shfl_up_sync(0xffffffffu, iu, o);
@@ -1336,25 +1370,25 @@ __global__ void __launch_bounds__(kPlanThreads)
         __syncthreads();
         int64_t bu = units;
         int32_t bi = items;
-        for (int w = 0; w < kPlanThreads / 32; ++w) {
+        for (int w = 0; w < threads / 32; ++w) {
             if (w < warp) bu += s_units[w], bi += s_items[w];
             units += s_units[w];
             items += s_items[w];
         }
         if (i < n) {
             r.u = bu + iu - cost;
-            r.item0 = bi + ii - mine;
+            r.item0 = bi + ii - its;
             runs[i] = r;
         }
-        __syncthreads();
+        if (!kFew) __syncthreads();
     }
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) s_longest[warp] = longest;
     __syncthreads();
     if (tid == 0) {
-        for (int w = 1; w < kPlanThreads / 32; ++w) longest = max(longest, s_longest[w]);
+        for (int w = 1; w < threads / 32; ++w) longest = max(longest, s_longest[w]);
         const int64_t even = (units + pairs - 1) / pairs;
-        *plan = RunPlan{units, max(even, (int64_t)least_chunk(longest)), n, gr.n};
+        *plan = RunPlan{units, max(even, (int64_t)least_chunk(longest))};
     }
 }
 
@@ -1526,6 +1560,8 @@ cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const Pag
     Run* runs = reinterpret_cast<Run*>(mem + at.runs);
     a.rplan = plan;
     a.runs = runs;
+    a.runs_total = gr.n + bd.B;
+    a.runs_shared = gr.n;
     a.pieces = reinterpret_cast<RowPieces*>(mem + at.pieces);
     a.rows_total = pg.table ? pg.pool_pages << pg.shift : (int32_t)(bd.B * bd.stride);
     const TreeMaps maps(a, q);
@@ -1540,12 +1576,15 @@ cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const Pag
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1 + (unsigned)std::min<int64_t>(64, (2 * (int64_t)bd.total_q + kPlanThreads - 1) / kPlanThreads));
-    cfg.blockDim = dim3(kPlanThreads);
+    const int64_t n = (int64_t)gr.n + bd.B;
+    const bool few = n <= kPlanThreads;
+    const int threads = few ? (int)((n + 31) / 32 * 32) : kPlanThreads;
+    cfg.gridDim = dim3(1 + (unsigned)std::min<int64_t>(64, (2 * (int64_t)bd.total_q + threads - 1) / threads));
+    cfg.blockDim = dim3(threads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, prefix_plan_kernel, bd, gr, plan, runs, reinterpret_cast<int32_t*>(mem + at.tiles),
+    e = cudaLaunchKernelEx(&cfg, few ? prefix_plan_kernel<true> : prefix_plan_kernel<false>, bd, gr, plan, runs, reinterpret_cast<int32_t*>(mem + at.tiles),
                            reinterpret_cast<int32_t*>(mem + at.lead), a.pieces, pairs, status);
     if (e != cudaSuccess) return e;
     count_launches(1);
