@@ -63,7 +63,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTile = 128;                   // positions per tile
-constexpr int kRows = 256;                   // query rows of an item, half of them each CTA's
+constexpr int kMmaRows = 256;                // M of a pair's MMA; rows of an item, but where all have at most ..
+constexpr int kFewRows = 128;                // .. these
 constexpr int kThreads = 512;
 constexpr int kSoftWarps = 8, kOutWarps = 4;
 constexpr int kQBytes = 128 * 128;           // 128 rows x 64 columns
@@ -121,10 +122,14 @@ __device__ __forceinline__ int4 sequence(const BatchDev& bd, const ExpandedDev& 
     const int32_t at = expanded_at(x, b, s.ctx, status);
     return at < 0 ? make_int4(0, 0, 0, 0) : make_int4(s.q0, s.nq, s.ctx, at);
 }
-__device__ __forceinline__ int32_t tiles_of(int32_t rows) { return (rows + kRows - 1) / kRows; }
+template <int R>
+__device__ __forceinline__ int32_t tiles_of(int32_t rows) {
+    return (rows + R - 1) / R;
+}
 
 // Query tiles before each sequence, for batches of more than kThreads (a launch
 // more: 4 us).
+template <int R>
 __global__ void __launch_bounds__(1024)
     prompt_plan_kernel(const BatchDev bd, const ExpandedDev x, int32_t* start, int32_t* status) {
     __shared__ int32_t sums[32];
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(1024)
     if (tid == 0) start[0] = 0;
     int32_t carry = 0;
     for (int b0 = 0; b0 < bd.B; b0 += 1024) {
-        const int32_t n = tiles_of(sequence(bd, x, b0 + tid, status).y);
+        const int32_t n = tiles_of<R>(sequence(bd, x, b0 + tid, status).y);
         int32_t all;
         const int32_t before = block_sum_before(n, 32, sums, all);
         if (b0 + tid < bd.B) start[b0 + tid + 1] = carry + before + n;
@@ -143,6 +148,7 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
+template <int R>
 __device__ __forceinline__ Item item_of(const Args& a, const Smem& S, uint32_t number) {
     Item it{0, 0, 0, 0, 0, 0};
     const int32_t* const start = a.start ? a.start : S.start;
@@ -150,7 +156,7 @@ __device__ __forceinline__ Item item_of(const Args& a, const Smem& S, uint32_t n
     const int b = last_at_or_below(start, a.bd.B, (int32_t)(number / kH));
     const uint32_t tiles = (uint32_t)(start[b + 1] - start[b]), in = number - (uint32_t)start[b] * kH;
     const int4 s = a.start ? sequence(a.bd, a.x, b, nullptr) : S.seq[b];
-    const int32_t end = s.y - kRows * (int32_t)(in % tiles), i0 = max(0, end - kRows);
+    const int32_t end = s.y - R * (int32_t)(in % tiles), i0 = max(0, end - R);
     if (end <= 0) return it;                     // lengths that change under the call
     it.head = (int32_t)(in / tiles);
     it.row = s.x + i0;
@@ -161,9 +167,21 @@ __device__ __forceinline__ Item item_of(const Args& a, const Smem& S, uint32_t n
     return it;
 }
 
+// kFew: items have 128 rows at most, 64 each CTA's.  Queries then take half the
+// shared memory and are loaded an item ahead, an item's first S goes before the
+// last PV of the item before, and pairs take every pairs-th item instead of
+// asking (an answer takes 2 us, a short item 3).  Taken where the bound on new rows
+// is 128 and below (30 prompts of 8 to 23 tokens 70 us, 79 without; 32 of 128 96,
+// 102 without; one of 100 10.5, 12.4; 32 of 33 to 100 behind up to 1,000 255, 247
+// without: HBM).  The MMAs read 128 rows all the same: what follows the queries,
+// whose products are nobody's.
+template <bool kFew>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prompt_mla_kernel(const Args a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_pe) {
+    constexpr int R = kFew ? kFewRows : kMmaRows, kMine = R / 2;     // rows of an item, and of a CTA
+    constexpr int kQRows = kMine * 128;                              // bytes of a chunk of them
+    constexpr int kQBufs = kFew ? 2 : 1;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem& S = *reinterpret_cast<Smem*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -213,7 +231,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_wait();                                  // inputs, and the scratch of an earlier call
     if (!a.start) {
         S.seq[tid] = sequence(a.bd, a.x, tid, a.status);
-        const int32_t n = tiles_of(S.seq[tid].y);
+        const int32_t n = tiles_of<R>(S.seq[tid].y);
         int32_t all;
         S.start[tid + 1] = block_sum_before(n, kThreads / 32, S.sums, all) + n;
         if (tid == 0) S.start[0] = 0;
@@ -247,10 +265,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp == 0 || warp == 2) {
         // K or V loads: lane 0 waits, then each lane issues a box.  Before an
-        // item's V its Q, a chunk as soon as the last S before is through with
-        // it: not before its K, which need not wait for that.  Rows behind the
-        // last new row are another sequence's or zeros: nobody reads what comes
-        // of them.
+        // item's V its Q, a chunk as soon as the last S of the item before (kFew:
+        // of the one before that) is through with it: not before its K, which
+        // need not wait for that.  Rows behind the last new row are another
+        // sequence's or zeros: nobody reads what comes of them.
         const bool k = warp == 0;
         uint64_t* const full = k ? S.kfull : S.vfull;
         uint64_t* const empty = k ? S.kempty : S.vempty;
@@ -263,11 +281,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t g = 0, seg = 0;
         for (; next_item(it); ++seg) {
             if (!k) {
+                // the barriers of chunk q, or (kFew) of buffer seg % 2
                 for (int q = 0; ok && q < kQChunks; ++q) {
-                    if (lane == 0 && (seg == 0 || wait(S.qempty[q], (seg - 1) & 1))) {
-                        mbar_arrive_expect_tx_pair(lead(S.qfull[q]), kQBytes);
-                        tma_load_2d_pair(smem_u32(S.q + q * kQBytes), &tm_q, lead(S.qfull[q]), it.head * kHeadQK + 64 * q,
-                                         it.row + 128 * (int)rank);
+                    const uint32_t b = kFew ? seg % kQBufs : q, use = seg / kQBufs;
+                    if (lane == 0 && (use == 0 || (kFew && q > 0) || wait(S.qempty[b], (use - 1) & 1))) {
+                        if (!kFew || q == 0) mbar_arrive_expect_tx_pair(lead(S.qfull[b]), kFew ? kQChunks * kQRows : kQRows);
+                        tma_load_2d_pair(smem_u32(S.q + (kFew ? b * kQChunks + q : q) * kQRows), &tm_q, lead(S.qfull[b]),
+                                         it.head * kHeadQK + 64 * q, it.row + kMine * (int)rank);
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                 }
@@ -284,74 +304,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
-            // MMA, by one lane that also waits: S of tile t, then PV of tile t - 1;
-            // an item's first S behind the last PV before it, under which its
-            // queries are loaded.  One loop over all tiles, with the next
-            // item read before that last PV: what is met once an item is
-            // fetched as it goes (15 cycles an instruction), and nothing
-            // else runs meanwhile.
-            constexpr uint32_t kIdS = idesc_bf16_f32(kRows, kTile), kIdO = idesc_bf16_f32(kRows, kHeadV, false, true);
+            // MMA, by one lane that also waits: S of a tile, then PV of the one
+            // before; an item's first S behind the last PV before it, under which
+            // its queries are loaded (but kFew).  One loop over all tiles of all
+            // items, and the next item is read behind the last S of one: what is
+            // met once an item is fetched as it goes (15 cycles an instruction),
+            // and nothing else runs meanwhile.
+            constexpr uint32_t kIdS = idesc_bf16_f32(kMmaRows, kTile);
+            constexpr uint32_t kIdO = idesc_bf16_f32(kMmaRows, kHeadV, false, true);
             const uint64_t dq = sdesc_sw128(smem_u32(S.q), 0, 1024), dk = sdesc_sw128(smem_u32(S.k), 0, 1024);
             const uint64_t dv = sdesc_sw128(smem_u32(S.v), kQBytes, 1024);
-            // tiles of item `seg`, and its keys
-            auto read = [&](uint32_t seg, int32_t& tiles, int32_t& keys) {
+            int32_t tiles = 0, keys = 0;         // of item `seg`
+            uint32_t seg = 0, n = 0;             // n: tiles whose S is issued
+            auto read = [&]() {
                 const uint32_t slot = seg % kSlots;
-                tiles = keys = 0;
+                tiles = 0;
                 if (!wait(S.itemfull[slot], (seg / kSlots) & 1)) return;
                 tiles = S.item[slot].tiles;
                 keys = S.item[slot].pos + S.item[slot].rows;
                 mbar_arrive(smem_u32(&S.itemempty[slot]));
             };
-            int32_t tiles, keys, tiles_next = 0, keys_next = 0;
-            read(0, tiles, keys);
-            uint32_t seg = 0, n = 0;             // n: tiles whose S is issued
+            read();
+            // the tile whose PV is next: its number, steps of 16 positions that some row sees, place in its item
+            uint32_t m = 0, m_seg = 0;
+            int32_t steps = 0;
+            bool pending = false, m_first = false, m_last = false;
 #pragma unroll 1
-            for (int32_t t = 0; tiles > 0; ++t) {
-                if (t < tiles) {
+            for (int32_t t = 0; ok;) {
+                const bool s_now = tiles > 0 && (kFew || t > 0 || !pending);
+                if (!s_now && !pending) break;
+                const bool first = t == 0, last = t + 1 == tiles;
+                const uint32_t mine = seg;
+                int32_t seen = 0;
+                if (s_now) {
                     const uint32_t buf = n & 1, st = n % kStages;
                     if (!wait(S.kfull[st], (n / kStages) & 1)) break;
+                    if (kFew && first && !wait(S.qfull[seg % kQBufs], (seg / kQBufs) & 1)) break;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < kQChunks; ++c) {
-                        if (t == 0) {
+                        if (!kFew && first) {
                             if (!wait(S.qfull[c], seg & 1)) break;
                             tc_fence_after();
                         }
+                        const uint64_t da = dq + ((kFew ? seg % kQBufs * kQChunks + c : c) * kQRows >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_bf16_ss_pair(tmem + kSCol + kTile * buf, dq + c * (kQBytes >> 4) + 2 * k,
+                            mma_bf16_ss_pair(tmem + kSCol + kTile * buf, da + 2 * k,
                                              dk + (st * kQChunks + c) * (kKBytes >> 4) + 2 * k, kIdS, (c | k) != 0);
-                        if (t + 1 == tiles) mma_commit_pair(smem_u32(&S.qempty[c]));
+                        if (!kFew && last) mma_commit_pair(smem_u32(&S.qempty[c]));
                     }
                     if (!ok) break;
+                    if (kFew && last) mma_commit_pair(smem_u32(&S.qempty[seg % kQBufs]));
                     mma_commit_pair(smem_u32(&S.kempty[st]));
                     mma_commit_pair(smem_u32(&S.sfull[buf]));
                     ++n;
-                    if (t == 0) continue;
-                } else {
-                    read(seg + 1, tiles_next, keys_next);
-                    if (!ok) break;
+                    seen = min(kTile, keys - t * kTile + 15) / 16;
+                    ++t;
                 }
-                const uint32_t m = n - (t < tiles ? 2 : 1), st = m % kStages;
-                if (t == 1 && seg > 0 && !wait(S.ofree, (seg - 1) & 1)) break;
-                if (!wait(S.vfull[st], (m / kStages) & 1)) break;
-                if (!wait(S.pfull[m & 1], (m >> 1) & 1)) break;
-                tc_fence_after();
-                // positions behind the last that a row sees have no weight
-                const int32_t steps = min(kTile, keys - (t - 1) * kTile + 15) / 16;
+                if (pending) {
+                    const uint32_t st = m % kStages;
+                    if (m_first && m_seg > 0 && !wait(S.ofree, (m_seg - 1) & 1)) break;
+                    if (!wait(S.vfull[st], (m / kStages) & 1)) break;
+                    if (!wait(S.pfull[m & 1], (m >> 1) & 1)) break;
+                    tc_fence_after();
 #pragma unroll 1
-                for (int k = 0; k < steps; ++k)
-                    mma_bf16_ts_pair(tmem + kOCol, tmem + kSCol + kTile * (m & 1) + 64 * (k >> 2) + 8 * (k & 3),
-                                     dv + st * (2 * kQBytes >> 4) + 128 * k, kIdO, t > 1 || k != 0);
-                mma_commit_pair(smem_u32(&S.vempty[st]));
-                mma_commit_pair(smem_u32(&S.pvdone));
-                if (t == tiles) {
-                    mma_commit_pair(smem_u32(&S.odone));
-                    tiles = tiles_next;
-                    keys = keys_next;
-                    ++seg;
-                    t = -1;
+                    for (int k = 0; k < steps; ++k)
+                        mma_bf16_ts_pair(tmem + kOCol, tmem + kSCol + kTile * (m & 1) + 64 * (k >> 2) + 8 * (k & 3),
+                                         dv + st * (2 * kQBytes >> 4) + 128 * k, kIdO, !m_first || k != 0);
+                    mma_commit_pair(smem_u32(&S.vempty[st]));
+                    mma_commit_pair(smem_u32(&S.pvdone));
+                    if (m_last) mma_commit_pair(smem_u32(&S.odone));
                 }
+                if (s_now && last) {
+                    t = 0;
+                    ++seg;
+                    read();
+                }
+                pending = s_now;
+                m = n - 1;
+                m_seg = mine;
+                m_first = first;
+                m_last = last;
+                steps = seen;
             }
         }
         __syncwarp();
@@ -369,7 +404,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             };
             if (lane == 0) {
                 if (n >= kSlots) wait(S.itemempty[slot], (turn - 1) & 1);
-                if (ok && rank == 0) {
+                if (kFew) {
+                    number = (blockIdx.x >> 1) + n * (gridDim.x >> 1);
+                } else if (ok && rank == 0) {
                     number = n == 0 ? blockIdx.x >> 1 : (gridDim.x >> 1) + atomicAdd(a.next, 1u);
                     if (n >= kSlots) wait_peer(S.numempty[slot], (turn - 1) & 1);
                     if (ok) {
@@ -385,14 +422,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            it = item_of(a, S, __shfl_sync(0xffffffffu, number, 0));
+            it = item_of<R>(a, S, __shfl_sync(0xffffffffu, number, 0));
             if (lane == 0) {
                 S.item[slot] = it;
                 mbar_arrive(smem_u32(&S.itemfull[slot]));
             }
             __syncwarp();
             if (it.tiles > 0 && lane < kQChunks)
-                tma_prefetch_2d(&tm_q, it.head * kHeadQK + 64 * lane, it.row + 128 * (int)rank);
+                tma_prefetch_2d(&tm_q, it.head * kHeadQK + 64 * lane, it.row + kMine * (int)rank);
             __syncwarp();
             if (it.tiles == 0) break;
         }
@@ -409,13 +446,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         // the warps agree on each item, since they meet at barriers
         while (!named_bar_or(1, 32 * kSoftWarps, !next_item(it))) {
-            const int32_t first = it.pos + 128 * (int)rank;      // position of the CTA's first row
+            const int32_t first = it.pos + kMine * (int)rank;    // position of the CTA's first row
+            // rows of this CTA; a warp without one keeps in step with the others
+            const int32_t live = min(kMine, it.rows - kMine * (int)rank);
+            const bool idle = (x & ~31) >= live;
             float m = -INFINITY, l = 0.f;
             for (int32_t t = 0; t < it.tiles; ++t, ++g) {
                 const uint32_t buf = g & 1;
                 wait(S.sfull[buf], (g >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
+                if (idle) {
+                    exchange(0.f);
+                    if (lane == 0) mbar_arrive_pair(lead(S.pfull[buf]));
+                    continue;
+                }
                 uint32_t r[2][32];
                 tmem_ld_32x32b_x32(tl + kSCol + kTile * buf + 64 * half, r[0]);
                 tmem_ld_32x32b_x32(tl + kSCol + kTile * buf + 64 * half + 32, r[1]);
@@ -473,8 +518,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 S.inv[x] = rcp_approx(l);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&S.lfull));
-                if (a.lse && x < it.rows - 128 * (int)rank)
-                    a.lse[(int64_t)(it.row + 128 * (int)rank + x) * kH + it.head] = (m + lg2_approx(l)) * kLn2;
+                if (a.lse && x < live)
+                    a.lse[(int64_t)(it.row + kMine * (int)rank + x) * kH + it.head] = (m + lg2_approx(l)) * kLn2;
             }
             ++seg;
         }
@@ -493,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float inv = S.inv[r0 + lane];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.invfree));
-            const int32_t mine = it.row + 128 * (int)rank + r0, live = it.rows - 128 * (int)rank - r0;
+            const int32_t mine = it.row + kMine * (int)rank + r0, live = min(kMine, it.rows - kMine * (int)rank) - r0;
             if (ok && live > 0) {
                 uint16_t* const to = a.out + ((int64_t)mine * kH + it.head) * kHeadV + 8 * (lane & 7);
 #pragma unroll 1
@@ -551,11 +596,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-// Query tiles that the batch's bounds allow, over all heads.
-int64_t most_items(const BatchDev& bd) {
-    return ((int64_t)bd.total_q / kRows + std::min<int64_t>(bd.B, bd.total_q)) * kH;
-}
-
 }  // namespace
 
 int resident_pairs(const void* f, int threads, size_t smem, int most) {
@@ -595,10 +635,17 @@ int resident_pairs(const void* f, int threads, size_t smem, int most) {
 
 size_t prompt_mla_scratch_bytes(const BatchDev& bd) { return ((size_t)bd.B + 1) * sizeof(int32_t); }
 
-cudaError_t launch_prompt_mla(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, float sm_scale,
-                              uint16_t* out, float* lse, void* scratch, int32_t* status, cudaStream_t stream) {
+namespace {
+
+template <bool kFew>
+cudaError_t launch(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, float sm_scale, uint16_t* out,
+                   float* lse, void* scratch, int32_t* status, cudaStream_t stream) {
+    constexpr int R = kFew ? kFewRows : kMmaRows;
+    const auto kernel = prompt_mla_kernel<kFew>;
+    // no more pairs than the batch's bounds allow items
+    const int64_t items = ((int64_t)bd.total_q / R + std::min<int64_t>(bd.B, bd.total_q)) * kH;
     const int pairs = (int)std::min<int64_t>(
-        resident_pairs(reinterpret_cast<const void*>(prompt_mla_kernel), kThreads, sizeof(Smem), kMaxPairs), most_items(bd));
+        resident_pairs(reinterpret_cast<const void*>(kernel), kThreads, sizeof(Smem), kMaxPairs), items);
     Args a{};
     a.bd = bd;
     a.x = x;
@@ -608,7 +655,7 @@ cudaError_t launch_prompt_mla(const BatchDev& bd, const uint16_t* q, const Expan
     a.next = reinterpret_cast<uint32_t*>(status) + kCounterWord;
     a.status = status;
     CUtensorMap tm_q, tm_k, tm_v, tm_pe;
-    if (!make_tmap_bf16_2d(&tm_q, q, (uint64_t)kH * kHeadQK, (uint64_t)bd.total_q, 64, 128) ||
+    if (!make_tmap_bf16_2d(&tm_q, q, (uint64_t)kH * kHeadQK, (uint64_t)bd.total_q, 64, R / 2) ||
         !make_tmap_bf16_chunks(&tm_k, x.kv, (uint64_t)kH * kExpRow / 64, (uint64_t)x.rows, 64, kNope / 64) ||
         !make_tmap_bf16_chunks(&tm_v, x.kv, (uint64_t)kH * kExpRow / 64, (uint64_t)x.rows, kTile, 2) ||
         !make_tmap_bf16_2d(&tm_pe, x.k_pe, DSA_ROPE_DIM, (uint64_t)x.rows, 64, 64))
@@ -626,18 +673,26 @@ cudaError_t launch_prompt_mla(const BatchDev& bd, const uint16_t* q, const Expan
         a.start = start;
         cfg.gridDim = dim3(1);
         cfg.blockDim = dim3(1024);
-        if ((e = cudaLaunchKernelEx(&cfg, prompt_plan_kernel, bd, x, start, status)) != cudaSuccess) return e;
+        if ((e = cudaLaunchKernelEx(&cfg, prompt_plan_kernel<R>, bd, x, start, status)) != cudaSuccess) return e;
         count_launches(1);
     }
-    if ((e = cudaFuncSetAttribute(prompt_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem))) !=
-        cudaSuccess)
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem))) != cudaSuccess)
         return e;
     cfg.gridDim = dim3(2 * (unsigned)pairs);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(Smem);
-    e = cudaLaunchKernelEx(&cfg, prompt_mla_kernel, a, tm_q, tm_k, tm_v, tm_pe);
+    e = cudaLaunchKernelEx(&cfg, kernel, a, tm_q, tm_k, tm_v, tm_pe);
     if (e == cudaSuccess) count_launches(1);
     return e;
+}
+
+}  // namespace
+
+// By the bound on new rows alone, so that a captured call serves other lengths.
+cudaError_t launch_prompt_mla(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, float sm_scale,
+                              uint16_t* out, float* lse, void* scratch, int32_t* status, cudaStream_t stream) {
+    return bd.max_q <= kFewRows ? launch<true>(bd, q, x, sm_scale, out, lse, scratch, status, stream)
+                                : launch<false>(bd, q, x, sm_scale, out, lse, scratch, status, stream);
 }
 
 }  // namespace dsa
