@@ -572,9 +572,9 @@ DSA_API dsa_status dsa_prompt_workspace_size(const dsa_batch* batch, size_t* byt
  *   expanded.kv[off[b] + s, h, :] = w_kv_b[448 h : 448 h + 448, :] c
  *   expanded.k_pe[off[b] + s, :]  = pe
  * fp32 accumulation, one rounding to bf16, values past bf16's largest kept at
- * it.  The rows behind a sequence's last, up to the next multiple of 128, are
- * zeroed wherever first[b] did not already lie in the same 128, so a
- * sequence that grows by chunks keeps what was expanded and passes its old length.
+ * it.  The rows behind a sequence's last, up to the next multiple of 16, are
+ * zeroed, the rest of its room is left as it was.  A sequence that grows by
+ * chunks keeps what was expanded and passes its old length as first[b].
  * A cache row with a NaN or infinity among its 576 values gets finite kv and
  * NaN throughout k_pe: queries that see it get NaN, others nothing of it.
  *   kv     bf16 latent cache, contiguous or paged, as dsa_tree_mla_fwd
@@ -592,10 +592,10 @@ DSA_API dsa_status dsa_mla_expand(const dsa_batch* batch, const dsa_pages* pages
  *   out  bf16 [total_q, 64, 256]  softmax(sm_scale q k^T) v over positions s <= t,
  *                                 head-major: o_mid of dsa_mla_output
  *   lse  fp32 [total_q, 64] or NULL
- * The row at position t (as in every call) sees expanded rows off[b] .. off[b] + t.  The
- * rows of a sequence's room up to the next multiple of 128 behind ctx_len have to hold
- * finite kv, as dsa_mla_expand leaves them; what else the buffers hold is not
- * read.  fp32 scores, softmax statistics and sums; the softmax weights are
+ * The row at position t (as in every call) sees expanded rows off[b] .. off[b] + t.  Whatever
+ * the buffers hold elsewhere does not reach the results, but kv of a sequence's own
+ * rows, and of those behind its last up to the next multiple of 16, has to be
+ * finite, as dsa_mla_expand leaves it.  fp32 scores, softmax statistics and sums; the softmax weights are
  * rounded to bf16 for the product with the values and the result once more.
  * The same inputs give the same bits.  Calls that may run at the same time need
  * a workspace each. */

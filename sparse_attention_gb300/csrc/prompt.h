@@ -90,6 +90,11 @@ size_t prompt_mla_scratch_bytes(const BatchDev& bd);
 cudaError_t launch_prompt_mla(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, float sm_scale,
                               uint16_t* out, float* lse, void* scratch, int32_t* status, cudaStream_t stream);
 
+// Few new rows over short contexts (prompt_rows.cu).
+bool prompt_rows_suit(const BatchDev& bd);
+cudaError_t launch_prompt_rows(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, float sm_scale,
+                               uint16_t* out, float* lse, int32_t* status, cudaStream_t stream);
+
 size_t prefix_mla_scratch_bytes(const BatchDev& bd, int32_t groups);
 cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const PagesDev& pg, const uint16_t* q,
                               const uint16_t* kv, const uint64_t* mask, float sm_scale, uint16_t* out, float* lse,

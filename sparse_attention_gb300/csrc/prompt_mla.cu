@@ -24,9 +24,11 @@
 //
 // What is masked cannot leak: expanded values are finite (a row that is not
 // carries NaN in its key instead), rows behind a sequence up to the next multiple
-// of 128 are zero, and a tile ends at such a multiple.  A masked score is replaced by
-// -inf before anything is formed of it, its weight is 0, and 0 times a finite
-// value is 0.
+// of 16 are zero, and the product with the values ends at such a multiple
+// behind the last position that a row of the item sees.  A masked score is
+// replaced by -inf before anything is formed of it, its weight is 0, and 0 times a
+// finite value is 0.  (Tiles of keys go on to multiples of 128, which a
+// sequence's room holds.)
 //
 // The new rows of a sequence are cut into 256s from their end, so that a
 // remainder has the fewest keys (12 prompts of 839 to 2,012 rows: 420 tiles a pair
@@ -75,7 +77,7 @@ constexpr uint32_t kOCol = 0, kSCol = 256;   // TMEM columns
 constexpr int kSlots = 2;                    // items published ahead
 constexpr int kMaxPairs = 96;
 constexpr float kRescale = 8.f;              // log2
-static_assert(kTile == kExpRoom, "a tile ends where a sequence's zeroed rows do");
+static_assert(kTile == kExpRoom, "a sequence's room holds whole tiles");
 
 struct Item {
     int32_t row;                 // packed row of the first of its query rows
@@ -688,9 +690,10 @@ cudaError_t launch(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, 
 
 }  // namespace
 
-// By the bound on new rows alone, so that a captured call serves other lengths.
+// By the bounds on new rows and lengths alone, so that a captured call serves others.
 cudaError_t launch_prompt_mla(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, float sm_scale,
                               uint16_t* out, float* lse, void* scratch, int32_t* status, cudaStream_t stream) {
+    if (prompt_rows_suit(bd)) return launch_prompt_rows(bd, q, x, sm_scale, out, lse, status, stream);
     return bd.max_q <= kFewRows ? launch<true>(bd, q, x, sm_scale, out, lse, scratch, status, stream)
                                 : launch<false>(bd, q, x, sm_scale, out, lse, scratch, status, stream);
 }

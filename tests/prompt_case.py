@@ -71,13 +71,12 @@ class Prompts:
 
     def filled(self):
         """Random expanded rows, zeros behind each sequence, NaN in the rest."""
-        x = self.buffers()
+        x = self.buffers()                       # NaN
         for b in range(self.B):
             lo, n = int(self.at[b]), self.L[b]
             x.kv[lo:lo + n] = self.normal(n, H, D_EXP).to(self.dev)
             x.k_pe[lo:lo + n] = self.normal(n, D_ROPE).to(self.dev)
-            x.kv[lo + n:lo + up(n)] = 0
-            x.k_pe[lo + n:lo + up(n)] = 0
+            x.kv[lo + n:lo + up(n, 16)] = 0
         return x
 
 

@@ -41,13 +41,8 @@ def _check_expansion(P, x, kv, w, first, before=None):
             # an fp32 sum of 512 exact products, and the rounding to bf16
             assert (err <= HALF * ref.abs() + 512 * F32 * (1 + HALF) * size).all(), b
             assert torch.equal(pe[lo + f:lo + n], rows[:, D_LAT:])
-            want_nan[lo + f:lo + n] = False
-            if up(f) < up(n):
-                assert (got[lo + n:lo + up(n)] == 0).all() and (pe[lo + n:lo + up(n)] == 0).all()
-                want_nan[lo + n:lo + up(n)] = False
-            elif up(n, 16) > n:
-                # rows of the last 16 that this call may zero again
-                want_nan[lo + n:min(lo + up(n, 16), lo + up(n))] = False
+            want_nan[lo + f:lo + up(n, 16)] = False
+            assert (got[lo + n:lo + up(n, 16)] == 0).all() and (pe[lo + n:lo + up(n, 16)] == 0).all()
     if before is None:
         assert got[want_nan].isnan().all() and pe[want_nan].isnan().all()
     else:
@@ -84,7 +79,8 @@ def test_expansion_by_chunks(weight):
         b = dsa.make_batch(P.i32(np.zeros(4)), P.i32(new), 0, P.max_ctx, P.stride, total_q=0)
         dsa.mla_expand(b, kv, w, many, first=P.i32(old), pages=P.pages, ws=P.ws)
         old = new
-    assert torch.equal(one.kv, many.kv) and torch.equal(one.k_pe, many.k_pe)
+    for a, b in ((one.kv, many.kv), (one.k_pe, many.k_pe)):
+        assert torch.equal(a.nan_to_num(-7), b.nan_to_num(-7))
     assert dsa.read_device_status(P.ws) == 0
 
 
@@ -109,8 +105,10 @@ def test_expansion_keeps_values_finite(weight):
     for pos, (b, _, _) in bad.items():
         hit[int(P.at[b]) + pos] = True
     hit = hit.cuda()
-    assert x.k_pe[hit].isnan().all() and torch.equal(x.k_pe[~hit], ref.k_pe[~hit])
-    assert x.kv.isfinite().all() and torch.equal(x.kv[~hit], ref.kv[~hit])
+    same = lambda a, b: torch.equal(a[~hit].nan_to_num(-7), b[~hit].nan_to_num(-7))  # noqa: E731
+    assert x.k_pe[hit].isnan().all() and same(x.k_pe, ref.k_pe) and same(x.kv, ref.kv)
+    for b in range(2):
+        assert x.kv[int(P.at[b]):int(P.at[b]) + up(P.L[b], 16)].isfinite().all()
     # overflow: kept at the largest value
     kv = torch.full((P.cache_rows, D_QK), 3e38, dtype=torch.bfloat16, device="cuda")
     dsa.mla_expand(P.batch, kv, w.abs() * 100, x, pages=P.pages, ws=P.ws)
@@ -160,9 +158,11 @@ def test_expansion_skips_what_is_wrong(weight):
 @pytest.mark.parametrize("c,m", [
     ([0], [1]), ([0], [2]), ([127], [1]), ([128], [1]), ([0], [128]), ([0], [129]), ([0], [256]), ([0], [257]),
     ([300], [5]), ([1], [255]), ([0, 0, 7, 513], [3, 0, 130, 260]), ([100] * 9, [1] * 9), ([2000], [300]),
+    ([0, 31, 28, 0, 3], [32, 1, 4, 0, 29]), ([1020], [1]), ([500, 3, 0], [2, 1, 2]), ([5, 6, 7, 8], [5, 6, 7, 8]),
 ])
-def test_attention(c, m):
-    P = Prompts(c, m, seed=sum(c) + sum(m), gap=128, pad=7)
+@pytest.mark.parametrize("max_ctx", [None, 20000])       # the bound on lengths, with that on new rows, chooses the kernel
+def test_attention(c, m, max_ctx):
+    P = Prompts(c, m, seed=sum(c) + sum(m), gap=128, pad=7, max_ctx=max_ctx)
     x = P.filled()
     q = P.normal(P.T + 7, H, D_HEAD).cuda()
     out = torch.full((P.T + 7, H, D_HEAD), 9.0, dtype=torch.bfloat16, device="cuda")
@@ -210,6 +210,32 @@ def test_moving_maxima():
         got, tol = out[at][:, [0, 5, 63]].cpu().double(), HALF * ref.abs() + (HALF * (1 + HALF) + 2 * e + 64 * F32) * big
         assert ((got - ref).abs() <= tol).all()
         assert ((lse[at][:, [0, 5, 63]].cpu().double() - z).abs() <= e + 16 * F32 * (1 + z.abs())).all()
+
+
+def test_masked_rows_do_not_leak_in_few_rows():
+    """The same for the kernel of few rows over short contexts."""
+    P = Prompts([5, 0, 0], [20, 9, 1], seed=16, gap=128, max_q=20, max_ctx=25)
+    x = P.filled()
+    q = P.normal(P.T, H, D_HEAD).cuda()
+    out, out2 = (torch.empty((P.T, H, D_HEAD), dtype=torch.bfloat16, device="cuda") for _ in (0, 1))
+    lse, lse2 = (torch.empty((P.T, H), device="cuda") for _ in (0, 1))
+    dsa.prompt_mla_fwd(P.batch, q, x, SCALE, out, lse, ws=P.ws)
+    x.k_pe[12] = float("nan")                # position 12: new row 7 of sequence 0 and later see it
+    x.kv[15, 4, 192:] = float("inf")
+    x.kv[int(P.at[1]) + 8] = float("nan")    # the last row of sequence 1
+    q[3, 9] = float("-inf")
+    dsa.prompt_mla_fwd(P.batch, q, x, SCALE, out2, lse2, ws=P.ws)
+    assert dsa.read_device_status(P.ws) == 0
+    hurt = torch.zeros(P.T, dtype=torch.bool)
+    hurt[7:20] = True
+    hurt[28] = True
+    assert out2[hurt.cuda()].isnan().all() and lse2[hurt.cuda()].isnan().all()
+    keep = ~hurt
+    keep[3] = False
+    keep = keep.cuda()
+    assert torch.equal(out[keep], out2[keep]) and torch.equal(lse[keep], lse2[keep])
+    heads = torch.arange(H, device="cuda") != 9
+    assert torch.equal(out[3][heads], out2[3][heads]) and out2[3, 9].isnan().all()
 
 
 def test_masked_rows_do_not_leak():

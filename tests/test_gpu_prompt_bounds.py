@@ -41,9 +41,10 @@ class Guarded:
 
 @pytest.mark.parametrize("c,m", [([0], [70]), ([5] * 600, [1] * 600), ([0] * 384, [3] * 384), ([0] * 385, [3] * 385),
                                  ([0] * 512, [2] * 512), ([2] * 513, [2] * 513), ([130] * 3, [400] * 3)])
-def test_expanded_form(weight, c, m):
-    """Up to 384 and 512 sequences the kernels plan by themselves, above them a launch before."""
-    P = Prompts(c, m, 16, seed=len(c))
+@pytest.mark.parametrize("max_ctx", [None, 3000])
+def test_expanded_form(weight, c, m, max_ctx):
+    """Up to 384 and 512 sequences the tensor kernels plan by themselves, above them a launch before."""
+    P = Prompts(c, m, 16, seed=len(c), max_ctx=max_ctx)
     P.ws = (g := Guarded(P.ws.numel())).ws
     kv = P.normal(P.cache_rows, D_QK)
     x = P.buffers()
