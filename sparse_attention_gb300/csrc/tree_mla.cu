@@ -71,6 +71,10 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTile = 128;                   // positions per tile
 constexpr int kItemCost = 3;                 // an item's start and end, in tiles
+// .. behind shared prefixes, where every item writes its results in fp32 (64 rows
+// behind 32,768, their own parts 64 short items: 206, 171, 148, 137, 139 and 142 us at 1, 2, 3,
+// 4, 5 and 7)
+constexpr int kRunItemCost = 4;
 constexpr int kThreads = 288;
 constexpr int kChunkBytes = 64 * 128;        // 64 rows x 64 dims
 constexpr int kQChunks = kDQK / 64;          // 9
@@ -105,6 +109,7 @@ struct SharedSeg : Seg {
     int32_t base;                // tiles before the item's first
     int32_t slot;                // where the piece goes
     bool ahead;                  // no other item reads its rows
+    bool all;                    // everything that its rows see: the result itself, no piece
     __device__ int32_t first_pos(int32_t t) const { return (base + t) * kTile; }
 };
 
@@ -297,11 +302,11 @@ struct RunIter {
     __device__ bool next(SharedSeg& s) {
         if (lo >= hi) return false;
         while (r < a.runs_total) {
-            const int32_t tiles = (q.len + kTile - 1) / kTile - q.base, per = tiles + kItemCost, items = (q.nq + 1) >> 1;
+            const int32_t tiles = (q.len + kTile - 1) / kTile - q.base, per = tiles + kRunItemCost, items = (q.nq + 1) >> 1;
             if (p < 0) p = (int32_t)min((int64_t)items, (lo - q.u) / per);
             while (p < items) {
-                const int64_t u0 = q.u + (int64_t)p * per + kItemCost;
-                if (u0 - kItemCost >= hi) return false;
+                const int64_t u0 = q.u + (int64_t)p * per + kRunItemCost;
+                if (u0 - kRunItemCost >= hi) return false;
                 s.t0 = (int32_t)max((int64_t)0, min((int64_t)tiles, lo - u0));
                 s.t1 = (int32_t)max((int64_t)0, min((int64_t)tiles, hi - u0));
                 const int32_t item = p++;
@@ -318,7 +323,8 @@ struct RunIter {
                 s.ahead = q.nq <= 2;
                 s.u0 = u0;
                 s.slot = q.item0 + item + pair;
-                if (s.t0 == 0 && cluster_rank() == 0 && (int)lane_id() < s.rows) {
+                s.all = !shared && q.base == 0 && s.whole();
+                if (!s.all && s.t0 == 0 && cluster_rank() == 0 && (int)lane_id() < s.rows) {
                     const int32_t last = holder(u0 + tiles - 1);
                     a.pieces[(shared ? 0 : a.bd.total_q) + s.row + lane_id()] =
                         RowPieces{s.slot, 2 * (last - pair + 1) + (int)lane_id()};
@@ -572,7 +578,8 @@ __device__ __noinline__ bool any_not_finite(const Args& a, const S& s, uint64_t 
 // instead of 0.89 ms for 16 trees of 64 over 8,192 rows).
 //
 // kShared: behind shared prefixes.  The work is the runs that prefix_plan_kernel
-// wrote, and every piece goes out in fp32 for prefix_merge_kernel to join.
+// wrote, and every piece goes out in fp32 for prefix_merge_kernel to join (but
+// whole items of sequences that share no tile).
 template <int kKRows, int kVRows, bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_mla_kernel(const Args a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -989,7 +996,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const float ls = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                 const int64_t head = (int64_t)(s.row + (int)rank) * kH;
-                const bool whole = !kShared && s.whole();
+                bool whole = s.whole();
+                if constexpr (kShared) whole = s.all;
                 int64_t slot = 2 * (int64_t)pair + (s.t0 == 0 ? 1 : 0);
                 if constexpr (kShared) slot = s.slot;
                 if (half == 0 && ok) {
@@ -1110,6 +1118,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 constexpr int kMergeBlocks = 16, kMergeWarps = 8;
 
+// 16 joined columns of a lane's query row, `head` in out and lse.
+__device__ __forceinline__ void store_joined(const float (&acc)[16], float sum, float top, int w, int c, int64_t head,
+                                             uint16_t* __restrict__ out, float* __restrict__ lse) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint4* to = reinterpret_cast<uint4*>(out + head * kDV + 128 * (w >> 1) + (c & 127) + 2 * (c & 128));
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        to[k] = make_uint4(pack_bf16x2(acc[8 * k] * inv, acc[8 * k + 1] * inv),
+                           pack_bf16x2(acc[8 * k + 2] * inv, acc[8 * k + 3] * inv),
+                           pack_bf16x2(acc[8 * k + 4] * inv, acc[8 * k + 5] * inv),
+                           pack_bf16x2(acc[8 * k + 6] * inv, acc[8 * k + 7] * inv));
+    if (lse && (w >> 1) == 0 && c == 0) lse[head] = sum == 0.f ? -INFINITY : top + log2f(sum) * kLn2;
+}
+
 // Joins one unit's pieces: 16 TMEM columns (from c, of warp w's quarter) of 32
 // lanes, a lane per query row, whose head is at row `head` of out.  at(e): twice
 // the slot of piece e, and which of the item's two rows this is.  A warp alone, or
@@ -1194,15 +1216,7 @@ __device__ __forceinline__ void join_unit(const At& at, int pieces, bool wide, i
         if (warp != 0) return;
     }
     if (top == INFINITY) return;                 // a bad page in one of the pieces
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint4* to = reinterpret_cast<uint4*>(out + (head + x) * kDV + 128 * (w >> 1) + (c & 127) + 2 * (c & 128));
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        to[k] = make_uint4(pack_bf16x2(acc[8 * k] * inv, acc[8 * k + 1] * inv),
-                           pack_bf16x2(acc[8 * k + 2] * inv, acc[8 * k + 3] * inv),
-                           pack_bf16x2(acc[8 * k + 4] * inv, acc[8 * k + 5] * inv),
-                           pack_bf16x2(acc[8 * k + 6] * inv, acc[8 * k + 7] * inv));
-    if (lse && (w >> 1) == 0 && c == 0) lse[head + x] = sum == 0.f ? -INFINITY : top + log2f(sum) * kLn2;
+    store_joined(acc, sum, top, w, c, head + x, out, lse);
 }
 
 // Joins the partial results of the items that chunks cut.  A unit is 16 TMEM
@@ -1239,7 +1253,59 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     }
 }
 
+// The same for at most 8 pieces, by a warp alone, with half of all loads on their
+// way at once: for calls of few rows, which wait for each in turn (4 rows behind
+// 2,000 20.5 -> 18.6 us; 610 rows, whose warps fill the SMs, 242 -> 254).
+template <class At>
+__device__ __forceinline__ void join_few(const At& at, int pieces, int w, int c, int64_t head,
+                                         const float* __restrict__ part_lse, const float4* __restrict__ part_o,
+                                         uint16_t* __restrict__ out, float* __restrict__ lse) {
+    const int lane = threadIdx.x & 31, x = 32 * (w & 1) + lane;
+    float ls[8], top = -INFINITY, acc[16], sum = 0.f;
+    bool bad = false, nan = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ls[e] = e < pieces ? part_lse[at(e) * 64 + x] : -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+#pragma unroll 1
+    for (int e0 = 0; e0 < pieces; e0 += 4) {
+        float4 v[4][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4* o = part_o + ((at(min(e0 + e, pieces - 1)) * 4 + w) * 64 + c / 4) * 32 + lane;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[e][k] = o[32 * k];
+        }
+        if (e0 == 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                bad = bad || ls[e] == INFINITY;
+                nan = nan || ls[e] != ls[e];
+                top = fmaxf(top, ls[e]);
+            }
+        }
+        const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (e0 + e >= pieces) break;
+            const float f = ex2_approx(((e0 == 0 ? ls[e] : ls[e + 4]) - base) * kLog2e);
+            sum += f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[4 * k] += f * v[e][k].x;
+                acc[4 * k + 1] += f * v[e][k].y;
+                acc[4 * k + 2] += f * v[e][k].z;
+                acc[4 * k + 3] += f * v[e][k].w;
+            }
+        }
+    }
+    if (bad) return;                             // a bad page in one of the pieces
+    if (nan) top = NAN;
+    store_joined(acc, sum, top, w, c, head + x, out, lse);
+}
+
 // Joins a row's pieces, those over the group's shared tiles and then its own.
+template <bool kFewRows>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     prefix_merge_kernel(const RowPieces* __restrict__ pieces, int32_t total_q, const float* __restrict__ part_lse,
                         const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
@@ -1255,9 +1321,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
         return e < first ? 2 * ((int64_t)shared.slot + e) + (shared.count & 1)
                          : 2 * ((int64_t)own.slot + e - first) + (own.count & 1);
     };
-    const int step = (int)gridDim.y * (wide ? 1 : kMergeWarps);
-    for (int unit = wide ? (int)blockIdx.y : kMergeWarps * (int)blockIdx.y + warp; unit < 64; unit += step)
-        join_unit(at, all, wide, unit >> 4, 16 * (unit & 15), (int64_t)blockIdx.x * kH, part_lse, part_o, out, lse, acc_s);
+    const int64_t head = (int64_t)blockIdx.x * kH;
+    if (wide) {
+        for (int unit = (int)blockIdx.y; unit < 64; unit += (int)gridDim.y)
+            join_unit(at, all, true, unit >> 4, 16 * (unit & 15), head, part_lse, part_o, out, lse, acc_s);
+    } else {
+        for (int unit = kMergeWarps * (int)blockIdx.y + warp; unit < 64; unit += kMergeWarps * (int)gridDim.y)
+            if constexpr (kFewRows) join_few(at, all, unit >> 4, 16 * (unit & 15), head, part_lse, part_o, out, lse);
+            else join_unit(at, all, false, unit >> 4, 16 * (unit & 15), head, part_lse, part_o, out, lse, acc_s);
+    }
 }
 
 // The runs of a call behind shared prefixes, by the first block; the others
@@ -1353,7 +1425,7 @@ __global__ void __launch_bounds__(kPlanThreads)
             }
         }
         const int32_t its = (r.nq + 1) >> 1, tiles = (r.len + kTile - 1) / kTile - r.base;
-        const int64_t cost = (int64_t)its * (tiles + kItemCost);
+        const int64_t cost = (int64_t)its * (tiles + kRunItemCost);
         longest = max(longest, its > 0 ? tiles : 0);
         int64_t iu = cost;
         int32_t ii = its;
@@ -1553,6 +1625,8 @@ cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const Pag
     a.mask = mask;
     a.kv = kv;
     a.scale_log2 = sm_scale * kLog2e;
+    a.out = out;
+    a.lse = lse;
     a.status = status;
     a.part_o = reinterpret_cast<float*>(mem + at.o);
     a.part_lse = reinterpret_cast<float*>(mem + at.lse);
@@ -1596,8 +1670,9 @@ cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const Pag
     cfg.gridDim = dim3((unsigned)bd.total_q, bd.total_q <= 16 ? 64 : 64 / kMergeWarps);
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, prefix_merge_kernel, (const RowPieces*)a.pieces, bd.total_q, (const float*)a.part_lse,
-                           (const float4*)a.part_o, out, lse);
+    e = cudaLaunchKernelEx(&cfg, bd.total_q <= 64 ? prefix_merge_kernel<true> : prefix_merge_kernel<false>,
+                           (const RowPieces*)a.pieces, bd.total_q, (const float*)a.part_lse, (const float4*)a.part_o,
+                           out, lse);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
