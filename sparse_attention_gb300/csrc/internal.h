@@ -83,6 +83,12 @@ bool make_tmap_bf16_2d(CUtensorMap* tm, const void* base, uint64_t inner, uint64
 bool make_tmap_bf16_chunks(CUtensorMap* tm, const void* base, uint64_t chunks, uint64_t rows, uint32_t box_rows,
                            uint32_t box_chunks);
 
+// The same seen as [rows / 8][chunks][8][64], rows a multiple of 8, so that the
+// 8-row groups of a chunk lie evenly spaced however few rows a box has: box
+// {64, 8, box_chunks, box_rows / 8}, each group's chunks one after the other.
+bool make_tmap_bf16_groups(CUtensorMap* tm, const void* base, uint64_t chunks, uint64_t rows, uint32_t box_rows,
+                           uint32_t box_chunks);
+
 // make_tmap_bf16_2d for a 2-D tensor of bytes (row stride inner bytes).
 bool make_tmap_u8_2d(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner,
                      uint32_t box_rows);

@@ -570,17 +570,17 @@ __device__ __noinline__ bool any_not_finite(const Args& a, const S& s, uint64_t 
     return false;
 }
 
-// kKRows, kVRows: positions of a K box (of one chunk, or of a stage's three)
-// and of a V box (of two).  Pages of 64 rows and more, and contiguous caches:
-// boxes of 64; pages of 32: of 32; pages of 16: K boxes of 8 rows x 3 chunks,
-// whose 8-row groups stay evenly spaced in a stage as a descriptor needs them
-// (24 K and 16 V boxes a tile; boxes of one chunk of 16 rows, 36 and 32: 0.94
-// instead of 0.89 ms for 16 trees of 64 over 8,192 rows).
+// kRows: positions of a box of K (a stage's three chunks) and of V (two): 64 for
+// pages of 64 rows and more and contiguous caches; pages of 32 and 16 take
+// boxes of a page, K by 8-row groups x three chunks, which stay evenly spaced
+// in a stage as a descriptor needs them (pages of 16: 12 K and 16 V boxes a
+// tile; with K boxes of one group, 24 and 16, 155 instead of 141 us for 40
+// rows in 5 groups of 6 behind 12,001).
 //
 // kShared: behind shared prefixes.  The work is the runs that prefix_plan_kernel
 // wrote, and every piece goes out in fp32 for prefix_merge_kernel to join (but
 // whole items of sequences that share no tile).
-template <int kKRows, int kVRows, bool kShared>
+template <int kRows, bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_mla_kernel(const Args a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v) {
@@ -663,8 +663,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++segs_read;
         return ok && to.t1 > to.t0;
     };
-    constexpr int kboxes = 64 / kKRows, vboxes = kTile / kVRows;     // per stage's positions
-    constexpr int kChunksPerBox = kKRows == 32 ? 1 : kGroup;
+    constexpr int kboxes = 64 / kRows, vboxes = kTile / kRows;       // per stage's positions
+    constexpr bool kGroups = kRows < 64;         // K boxes of 8-row groups x three chunks
 
     // MMAs are issued by one elected lane, which also waits: the tensor pipe
     // takes a K chunk's four MMAs in 150 cycles, less than a warp that waits
@@ -681,7 +681,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 bool bad = false;
                 const int32_t x = x0 + lane;
                 const int32_t row =
-                    box_row(a, s, s.first_pos(s.t0 + x / kboxes) + 64 * (int)rank + (x % kboxes) * kKRows, bad);
+                    box_row(a, s, s.first_pos(s.t0 + x / kboxes) + 64 * (int)rank + (x % kboxes) * kRows, bad);
                 for (int32_t y = 0; ok && y < 32 && x0 + y < n; y += kboxes) {
                     if (x0 + y == 0) {
                         // No row for this CTA: zeros, from behind the queries.
@@ -696,18 +696,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tma_load_2d_pair(smem_u32(S.q + lane * kChunkBytes), &tm_q, lead(S.qfull), 64 * lane, q_row);
                     }
                     const uint32_t g = g0 + (x0 + y) / kboxes;
-                    const int e = lane % kboxes, c = (lane / kboxes) * kChunksPerBox;    // a box each
-                    const int32_t r = __shfl_sync(0xffffffffu, row, y + e);
+                    const int32_t r = __shfl_sync(0xffffffffu, row, (y + lane) & 31);    // a box each
 #pragma unroll 1
                     for (int gr = 0; ok && gr < kKStages; ++gr) {
                         const uint32_t bar = lead(S.kfull[gr]);
                         if (lane == 0 && (g == 0 || wait(S.kempty[gr], (g - 1) & 1)))
                             mbar_arrive_expect_tx_pair(bar, kKBytes);
                         ok = __shfl_sync(0xffffffffu, ok, 0);
-                        if (ok && c < kGroup)
-                            tma_load_3d_pair(smem_u32(S.k + gr * kKBytes + c * kChunkBytes +
-                                                      e * kKRows * 128 * kChunksPerBox),
-                                             &tm_k, bar, 0, r, kGroup * gr + c);
+                        if (ok && lane < kboxes) {
+                            const uint32_t dst = smem_u32(S.k + gr * kKBytes + lane * kRows * 128 * kGroup);
+                            if constexpr (kGroups) tma_load_4d_pair(dst, &tm_k, bar, 0, 0, kGroup * gr, r >> 3);
+                            else tma_load_3d_pair(dst, &tm_k, bar, 0, r, kGroup * gr);
+                        }
                     }
                     // Rows that no other pair reads come from HBM: the next
                     // tile's are brought to L2 while this one's are loaded
@@ -719,7 +719,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int32_t next = y + kboxes + lane;
                         const int32_t r2 = __shfl_sync(0xffffffffu, row, next & 31);
                         if (lane < kboxes && next < 32 && x0 + next < n && r2 < a.rows_total)
-                            prefetch_l2_bulk(a.kv + (int64_t)r2 * kDQK, min(kKRows, a.rows_total - r2) * 2 * kDQK);
+                            prefetch_l2_bulk(a.kv + (int64_t)r2 * kDQK, min(kRows, a.rows_total - r2) * 2 * kDQK);
                     }
                 }
             }
@@ -728,11 +728,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rank == 0) {
             // MMA: S of tile g + 1, then PV of tile g
             constexpr uint32_t kIdS = idesc_bf16_f32(128, kTile), kIdO = idesc_bf16_f32(128, 256, false, true);
-            // K stages: three chunks of 64 rows, or (boxes of 8 rows) eight
+            // K stages: three chunks of 64 rows, or (smaller pages) eight
             // groups of 8 rows x three chunks; V stages: boxes of two 64-dim
             // blocks of vrows rows
-            constexpr uint32_t ksbo = kKRows == 8 ? 1024 * kGroup : 1024;
-            constexpr uint32_t kcstep = (kKRows == 8 ? 1024 : kChunkBytes) >> 4;
+            constexpr uint32_t ksbo = kGroups ? 1024 * kGroup : 1024;
+            constexpr uint32_t kcstep = (kGroups ? 1024 : kChunkBytes) >> 4;
             // S of tile g; first / last of its segment (number seg)
             auto issue_s = [&](uint32_t g, bool first, bool last, uint32_t seg) {
                 if (first && !wait(S.qfull, seg & 1)) return;
@@ -761,7 +761,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (first && seg > 0 && !wait(S.ofree, (seg - 1) & 1)) return;
                 if (!wait(S.pfull, g & 1)) return;
                 tc_fence_after();
-                const uint64_t dp = sdesc_sw128(smem_u32(S.p), 0, 1024), dv = sdesc_sw128(smem_u32(S.v), kVRows * 128, 1024);
+                const uint64_t dp = sdesc_sw128(smem_u32(S.p), 0, 1024), dv = sdesc_sw128(smem_u32(S.v), kRows * 128, 1024);
 #pragma unroll 1
                 for (int j = 0; j < kVStages; ++j) {
                     if (!wait(S.vfull[j], g & 1)) return;
@@ -770,7 +770,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
                         mma_bf16_ss_pair(tmem + kOCol + 128 * j, dp + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3),
-                                         db + 128 * k + 128 * ((16 * k) & -kVRows) / 16, kIdO, !first || k != 0);
+                                         db + 128 * k + 128 * ((16 * k) & -kRows) / 16, kIdO, !first || k != 0);
                     mma_commit_pair(smem_u32(&S.vempty[j]));
                 }
                 mma_commit_pair(smem_u32(&S.pvdone));
@@ -805,7 +805,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool bad = false;
             for (int32_t x0 = 0; ok && x0 < n; x0 += 32) {
                 const int32_t x = x0 + lane;
-                const int32_t row = box_row(a, s, s.first_pos(s.t0) + x * kVRows, bad);
+                const int32_t row = box_row(a, s, s.first_pos(s.t0) + x * kRows, bad);
                 const bool any_bad = __any_sync(0xffffffffu, bad);
                 if (lane == 0) {
                     S.bad[seg & 3] = any_bad;
@@ -825,7 +825,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             mbar_arrive_expect_tx_pair(bar, kVBytes);
                         ok = __shfl_sync(0xffffffffu, ok, 0);
                         if (ok && lane < vboxes)
-                            tma_load_3d_pair(smem_u32(S.v + j * kVBytes + lane * kVRows * 256), &tm_v, bar, 0, r,
+                            tma_load_3d_pair(smem_u32(S.v + j * kVBytes + lane * kRows * 256), &tm_v, bar, 0, r,
                                              4 * j + 2 * (int)rank);
                     }
                 }
@@ -843,11 +843,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     // two rows at a time; boxes behind the last row are zero
                     const int32_t from = max(0, s.c - pos0) + (lane >> 4), live = min(kTile, s.len - pos0);
-                    const int32_t end = (live + kVRows - 1) & -kVRows;
+                    const int32_t end = (live + kRows - 1) & -kRows;
                     auto piece = [&](int32_t x) -> uint4* {
-                        const int32_t in = x & (kVRows - 1), blk = (lane >> 3) & 1;
+                        const int32_t in = x & (kRows - 1), blk = (lane >> 3) & 1;
                         return reinterpret_cast<uint4*>(S.v + j * kVBytes + (x - in) * 256 +
-                                                        (blk * kVRows + in) * 128 + (lane & 7) * 16);
+                                                        (blk * kRows + in) * 128 + (lane & 7) * 16);
                     };
 #pragma unroll 1
                     for (int32_t x = max(from, live + ((live ^ from) & 1)); x < end; x += 2)
@@ -1486,9 +1486,9 @@ int max_pairs() {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(tree_mla_kernel<64, 64, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem)) !=
+    if (cudaFuncSetAttribute(tree_mla_kernel<64, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem)) !=
             cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, tree_mla_kernel<64, 64, false>, &cfg) != cudaSuccess || n <= 0) {
+        cudaOccupancyMaxActiveClusters(&n, tree_mla_kernel<64, false>, &cfg) != cudaSuccess || n <= 0) {
         cudaGetLastError();
         return num_sms() / 2;
     }
@@ -1500,15 +1500,15 @@ int max_pairs() {
 // Tensor maps of the queries and of the cache, whose boxes go by its pages.
 struct TreeMaps {
     CUtensorMap q, k, v;
-    uint32_t krows;
+    uint32_t rows;
     bool ok;
     TreeMaps(const Args& a, const uint16_t* queries) {
         const int page = a.pg.table ? 1 << a.pg.shift : kTile;
-        krows = page >= 64 ? 64 : page == 32 ? 32 : 8;
-        const uint32_t kchunks = krows == 32 ? 1 : kGroup, vrows = (uint32_t)std::min(page, 64);
+        rows = (uint32_t)std::min(page, 64);
         ok = make_tmap_bf16_2d(&q, queries, kDQK, (uint64_t)a.bd.total_q * kH, 64, 64) &&
-             make_tmap_bf16_chunks(&k, a.kv, kQChunks, (uint64_t)a.rows_total, krows, kchunks) &&
-             make_tmap_bf16_chunks(&v, a.kv, kQChunks, (uint64_t)a.rows_total, vrows, 2);
+             (rows == 64 ? make_tmap_bf16_chunks(&k, a.kv, kQChunks, (uint64_t)a.rows_total, rows, kGroup)
+                          : make_tmap_bf16_groups(&k, a.kv, kQChunks, (uint64_t)a.rows_total, rows, kGroup)) &&
+             make_tmap_bf16_chunks(&v, a.kv, kQChunks, (uint64_t)a.rows_total, rows, 2);
     }
 };
 
@@ -1549,9 +1549,9 @@ cudaError_t launch_tree_mla(const BatchDev& bd, const PagesDev& pg, const uint16
     a.rows_total = pg.table ? pg.pool_pages << pg.shift : (int32_t)(bd.B * bd.stride);
     const TreeMaps maps(a, q);
     if (!maps.ok) return cudaErrorInvalidValue;
-    auto kernel = maps.krows == 64   ? tree_mla_kernel<64, 64, false>
-                  : maps.krows == 32 ? tree_mla_kernel<32, 32, false>
-                                     : tree_mla_kernel<8, 16, false>;
+    auto kernel = maps.rows == 64   ? tree_mla_kernel<64, false>
+                  : maps.rows == 32 ? tree_mla_kernel<32, false>
+                                     : tree_mla_kernel<16, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
     if (e != cudaSuccess) return e;
     // Both are programmatic dependents of the launch before them: they set up
@@ -1640,9 +1640,9 @@ cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const Pag
     a.rows_total = pg.table ? pg.pool_pages << pg.shift : (int32_t)(bd.B * bd.stride);
     const TreeMaps maps(a, q);
     if (!maps.ok) return cudaErrorInvalidValue;
-    auto kernel = maps.krows == 64   ? tree_mla_kernel<64, 64, true>
-                  : maps.krows == 32 ? tree_mla_kernel<32, 32, true>
-                                     : tree_mla_kernel<8, 16, true>;
+    auto kernel = maps.rows == 64   ? tree_mla_kernel<64, true>
+                  : maps.rows == 32 ? tree_mla_kernel<32, true>
+                                     : tree_mla_kernel<16, true>;
     constexpr size_t kSmem = sizeof(SmemOf<SharedSeg>);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
