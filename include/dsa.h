@@ -622,15 +622,14 @@ typedef struct dsa_groups {
 } dsa_groups;
 
 /* Bytes of workspace that dsa_prefix_mla_fwd needs for `batch` in `groups`
- * groups (its arrays are not read): some 263 KB a new row and sequence (fp32
- * results over the shared and over the own part before they are joined).  Host
- * only. */
+ * groups (its arrays are not read): some 40 MB for the fp32 results of what is
+ * cut between CTA pairs, 128 bytes a sequence and 8 a group.  Host only. */
 DSA_API dsa_status dsa_prefix_workspace_size(const dsa_batch* batch, const dsa_groups* groups, size_t* bytes);
 
 /* dsa_tree_mla_fwd for sequences behind shared prefixes: the same arguments,
  * results and errors, but the shared rows (rounded down to a multiple of 128)
- * are read once for each two new rows of the whole group, from the cache of its first
- * sequence with new rows, instead of once for each two of every sequence.  With pages the
+ * are read once for two new rows of the whole group, from the cache of its first
+ * sequence with new rows, instead of once for two of every sequence.  With pages the
  * sequences' block tables name the same pages there; contiguous caches hold the
  * rows once per sequence.
  *   mask  as there, or NULL: each new row sees itself and those before it

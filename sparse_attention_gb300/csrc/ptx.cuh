@@ -352,7 +352,18 @@ __device__ __forceinline__ void mma_bf16_ss_pair(uint32_t d_tmem, uint64_t a_des
         : "memory");
 }
 
-// The same with A in tensor memory: a lane per row, two consecutive K elements a
+// The same, leaving D's lanes of a CTA of the pair as they are where its mask is all ones.
+__device__ __forceinline__ void mma_bf16_ss_pair_lanes(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                       uint32_t idesc, uint32_t accumulate, uint32_t off0,
+                                                       uint32_t off1) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5, %6, %6, %6, %6}, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(off0), "r"(off1)
+        : "memory");
+}
+
+// mma_bf16_ss_pair with A in tensor memory: a lane per row, two consecutive K elements a
 // column, 8 columns an instruction, at the same address in both CTAs.
 __device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                                  uint32_t accumulate) {

@@ -48,6 +48,13 @@
 // a share's end leaves fp32 partial results, which tree_merge_kernel joins in
 // order.
 //
+// Behind shared prefixes (dsa_prefix_mla_fwd) a group's new rows are paired
+// across its sequences, so an item walks the shared tiles once and then the own
+// ones of its one or two sequences.  (Shared and own parts as items of their
+// own, all joined in fp32: 242 instead of 180 us for 61 sequences of up to 15
+// rows behind 3,774, and 263 KB of workspace a row and sequence; small calls 0-10 %
+// faster.)  Cut, joined and merged as above.
+//
 // Bounds.  A row pair's tile is 36 MMAs of N = 128 (37 cycles each) and 16 of
 // N = 256 (65): 2,372 cycles for 35.7 MFLOP, 92 % of the tensor rate; a single
 // row leaves rank 1's half empty and is bound by HBM (121 flop a byte).
@@ -71,10 +78,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTile = 128;                   // positions per tile
 constexpr int kItemCost = 3;                 // an item's start and end, in tiles
-// .. behind shared prefixes, where every item writes its results in fp32 (64 rows
-// behind 32,768, their own parts 64 short items: 206, 171, 148, 137, 139 and 142 us at 1, 2, 3,
-// 4, 5 and 7)
-constexpr int kRunItemCost = 4;
+constexpr int kApartUnits = 6;               // units a pair that are little work
+constexpr int kFewRows = 16;                 // rows of a call up to which a merge goes by rows
 constexpr int kThreads = 288;
 constexpr int kChunkBytes = 64 * 128;        // 64 rows x 64 dims
 constexpr int kQChunks = kDQK / 64;          // 9
@@ -102,36 +107,47 @@ struct Seg {
     int64_t u0;                  // the unit of tile 0, for a piece of a cut item
     __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
     __device__ int32_t first_pos(int32_t t) const { return t * kTile; }
+    __device__ bool begins() const { return true; }              // a segment is all that a pair has of an item
+    __device__ bool ends() const { return true; }
+    __device__ bool sees(uint32_t) const { return true; }
+    __device__ bool from_start() const { return t0 == 0; }
 };
 
-// Behind shared prefixes an item may begin further into its sequence.
+// Behind shared prefixes an item is two new rows of a group, and its tiles lie in
+// up to three sequences' caches: the shared ones, those of the first row's
+// sequence, and those of the second row's if that is another.  A segment is what a
+// pair has of one of them.
 struct SharedSeg : Seg {
-    int32_t base;                // tiles before the item's first
-    int32_t slot;                // where the piece goes
+    int32_t shift;               // tiles of the item before the first of this cache, less those before it there
+    int32_t from, to;            // the item's tiles that the pair has, of all three
+    uint32_t live;               // bit r: CTA r's row sees this cache
     bool ahead;                  // no other item reads its rows
-    bool all;                    // everything that its rows see: the result itself, no piece
-    __device__ int32_t first_pos(int32_t t) const { return (base + t) * kTile; }
+    __device__ bool whole() const { return from == 0 && to == tiles; }
+    __device__ int32_t first_pos(int32_t t) const { return (t - shift) * kTile; }
+    __device__ bool begins() const { return t0 == from; }
+    __device__ bool ends() const { return t1 == to; }
+    __device__ bool sees(uint32_t rank) const { return (live >> rank) & 1u; }
+    __device__ bool from_start() const { return from == 0; }
 };
 
-// Behind shared prefixes the work is a list of runs: first every group's new
-// rows over its shared tiles (whole ones only, from its first sequence's
-// cache), then every sequence's over its own.
-struct Run {
-    int32_t q0, nq, len, base;   // new rows, length of the cache, tiles before the run's first
-    int32_t b, item0;            // the sequence whose cache it reads, items before it
+// Behind shared prefixes the work is a list of runs, two a sequence: the items
+// whose rows are both its own, and the one of its last row and the next
+// sequence's first (or none), if a row is left.
+struct alignas(16) Run {
+    int32_t row, items;          // first new row, items
+    int32_t lead, base;          // whose cache holds the shared rows, tiles of them
+    int32_t b, len, n, i0;       // sequence, length of its cache, its new rows, which of them `row` is
+    int32_t b2, len2, n2;        // of the second row's sequence (n2 = 0: none)
+    int32_t rows;                // rows of an item
+    int32_t lone, pad;           // whether the shared rows are this item's alone
     int64_t u;                   // units before it
+    __device__ int32_t own() const { return (len + kTile - 1) / kTile - base; }
+    __device__ int32_t tiles() const { return base + own() + (n2 > 0 ? (len2 + kTile - 1) / kTile - base : 0); }
 };
-static_assert(sizeof(Run) == 32, "two 16-byte loads");
+static_assert(sizeof(Run) == 64, "four 16-byte loads");
 
 struct RunPlan {
     int64_t all, chunk;          // units, and those of a pair
-};
-
-// The pieces of a row's shared or own part: those of one item, in order of the
-// pairs that computed them.
-struct RowPieces {
-    int32_t slot;                // the first one's
-    int32_t count;               // twice their number, and which of the item's two rows this is
 };
 
 template <class S>
@@ -172,8 +188,8 @@ struct Args {
     // behind shared prefixes only
     const RunPlan* rplan;
     const Run* runs;
-    int32_t runs_total, runs_shared;     // all runs, and those over shared tiles
-    RowPieces* pieces;   // [2][total_q]: shared, own
+    int32_t runs_total;
+    int2* cut_rows;      // [total_q] or null: of a row of a cut item, 2 * (first pair + 1) + which of its rows, last pair
 };
 
 __device__ __forceinline__ int64_t seq_units(const SeqInfo& s) {
@@ -274,8 +290,8 @@ struct SegIter {
 struct RunIter {
     const Args& a;
     const int32_t pair;
-    int64_t lo, hi, chunk;
-    int32_t r = 0, p = -1;
+    int64_t lo, hi, chunk, u0 = 0;
+    int32_t r = 0, p = -1, at = 0, to = 0;       // run, its next item; the item's tiles that are left
     Run q{};
     __device__ RunIter(const Args& args, int32_t pair_) : a(args), pair(pair_) {
         // The last run that begins at or before lo: 32 probes at a time, the
@@ -283,8 +299,8 @@ struct RunIter {
         const int lane = (int)lane_id();
         int32_t span = a.runs_total;             // it is one of runs r .. r + span - 1
         for (bool first = true; first || span > 1; first = false) {
-            const int32_t step = (span + 31) / 32, at = r + lane * step;
-            const int64_t u = lane * step < span ? a.runs[at].u : INT64_MAX;
+            const int32_t step = (span + 31) / 32, i = r + lane * step;
+            const int64_t u = lane * step < span ? a.runs[i].u : INT64_MAX;
             if (first) {
                 const RunPlan pl = *a.rplan;
                 chunk = pl.chunk;
@@ -299,42 +315,66 @@ struct RunIter {
     }
     __device__ int32_t holder(int64_t u) const { return (int32_t)(u / chunk); }
 
-    __device__ bool next(SharedSeg& s) {
+    // The next item of the pair's share, its tiles at .. to - 1.
+    __device__ bool item(SharedSeg& s) {
         if (lo >= hi) return false;
         while (r < a.runs_total) {
-            const int32_t tiles = (q.len + kTile - 1) / kTile - q.base, per = tiles + kRunItemCost, items = (q.nq + 1) >> 1;
-            if (p < 0) p = (int32_t)min((int64_t)items, (lo - q.u) / per);
-            while (p < items) {
-                const int64_t u0 = q.u + (int64_t)p * per + kRunItemCost;
-                if (u0 - kRunItemCost >= hi) return false;
-                s.t0 = (int32_t)max((int64_t)0, min((int64_t)tiles, lo - u0));
-                s.t1 = (int32_t)max((int64_t)0, min((int64_t)tiles, hi - u0));
-                const int32_t item = p++;
-                if (s.t1 <= s.t0) continue;
-                const bool shared = r < a.runs_shared;
-                s.b = q.b;
-                s.i0 = shared ? 0 : 2 * item;
-                s.row = q.q0 + 2 * item;
-                s.rows = min(2, q.nq - 2 * item);
-                s.c = shared ? q.len : q.len - q.nq;
-                s.len = q.len;
+            const int32_t tiles = q.tiles(), per = tiles + kItemCost;
+            if (p < 0) p = (int32_t)min((int64_t)q.items, (lo - q.u) / per);
+            while (p < q.items) {
+                u0 = q.u + (int64_t)p * per + kItemCost;
+                if (u0 - kItemCost >= hi) return false;
+                at = (int32_t)max((int64_t)0, min((int64_t)tiles, lo - u0));
+                to = (int32_t)max((int64_t)0, min((int64_t)tiles, hi - u0));
+                const int32_t i = p++;
+                if (to <= at) continue;
+                s.row = q.row + 2 * i;
+                s.rows = q.rows;
                 s.tiles = tiles;
-                s.base = q.base;
-                s.ahead = q.nq <= 2;
                 s.u0 = u0;
-                s.slot = q.item0 + item + pair;
-                s.all = !shared && q.base == 0 && s.whole();
-                if (!s.all && s.t0 == 0 && cluster_rank() == 0 && (int)lane_id() < s.rows) {
-                    const int32_t last = holder(u0 + tiles - 1);
-                    a.pieces[(shared ? 0 : a.bd.total_q) + s.row + lane_id()] =
-                        RowPieces{s.slot, 2 * (last - pair + 1) + (int)lane_id()};
-                }
+                s.from = at;
+                s.to = to;
                 return true;
             }
             p = 0;
             if (++r < a.runs_total) q = a.runs[r];
         }
         return false;
+    }
+
+    __device__ bool next(SharedSeg& s) {
+        if (at >= to && !item(s)) return false;
+        // (the item's run: an item is walked to its end before the next)
+        const int32_t mid = q.base + q.own(), i = s.row - q.row;
+        s.t0 = at;
+        if (at < q.base) {
+            s.t1 = min(to, q.base);
+            s.b = q.lead;
+            s.len = s.c = q.base * kTile;
+            s.i0 = s.shift = 0;
+            s.live = 3u;
+            s.ahead = q.lone != 0;
+        } else if (at < mid) {
+            s.t1 = min(to, mid);
+            s.b = q.b;
+            s.len = q.len;
+            s.c = q.len - q.n;
+            s.i0 = q.i0 + i;
+            s.shift = 0;
+            s.live = q.n2 > 0 ? 1u : 3u;
+            s.ahead = q.n <= 2;
+        } else {
+            s.t1 = to;
+            s.b = q.b2;
+            s.len = q.len2;
+            s.c = q.len2 - q.n2;
+            s.i0 = -1;                           // CTA 1's row is its first
+            s.shift = mid - q.base;
+            s.live = 2u;
+            s.ahead = q.n2 <= 2;
+        }
+        at = s.t1;
+        return true;
     }
 };
 
@@ -578,8 +618,8 @@ __device__ __noinline__ bool any_not_finite(const Args& a, const S& s, uint64_t 
 // rows in 5 groups of 6 behind 12,001).
 //
 // kShared: behind shared prefixes.  The work is the runs that prefix_plan_kernel
-// wrote, and every piece goes out in fp32 for prefix_merge_kernel to join (but
-// whole items of sequences that share no tile).
+// wrote.  Over the own tiles of one of an item's two sequences the other CTA's
+// lanes of O are left out of the product (0 * NaN is NaN).
 template <int kRows, bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_mla_kernel(const Args a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -673,8 +713,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // then each lane issues a box.
     if (warp == 0) {
         // Q and K loads
-        uint32_t g0 = 0, seg = 0;                // tiles and segments before this one
-        for (; next_seg(s); g0 += s.t1 - s.t0, ++seg) {
+        uint32_t g0 = 0, item = 0;               // tiles and items before this one
+        for (; next_seg(s); g0 += s.t1 - s.t0, item += s.ends()) {
             // first rows of the segment's boxes, 32 at a time
             const int32_t n = (s.t1 - s.t0) * kboxes;
             for (int32_t x0 = 0; ok && x0 < n; x0 += 32) {
@@ -683,13 +723,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int32_t row =
                     box_row(a, s, s.first_pos(s.t0 + x / kboxes) + 64 * (int)rank + (x % kboxes) * kRows, bad);
                 for (int32_t y = 0; ok && y < 32 && x0 + y < n; y += kboxes) {
-                    if (x0 + y == 0) {
+                    if (x0 + y == 0 && s.begins()) {
                         // No row for this CTA: zeros, from behind the queries.
                         // Whatever lay there would do as well, but its products
                         // cost power, which holds the clock (64 x 1 row over
                         // 32,768 in a long loop: 438 us, 407 with zeros).
                         const int32_t q_row = (int)rank < s.rows ? (s.row + (int)rank) * kH : a.bd.total_q * kH;
-                        if (lane == 0 && (seg == 0 || wait(S.qempty, (seg - 1) & 1)))
+                        if (lane == 0 && (item == 0 || wait(S.qempty, (item - 1) & 1)))
                             mbar_arrive_expect_tx_pair(lead(S.qfull), (uint32_t)sizeof(S.q));
                         ok = __shfl_sync(0xffffffffu, ok, 0);
                         if (ok && lane < kQChunks)
@@ -733,9 +773,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // blocks of vrows rows
             constexpr uint32_t ksbo = kGroups ? 1024 * kGroup : 1024;
             constexpr uint32_t kcstep = (kGroups ? 1024 : kChunkBytes) >> 4;
-            // S of tile g; first / last of its segment (number seg)
-            auto issue_s = [&](uint32_t g, bool first, bool last, uint32_t seg) {
-                if (first && !wait(S.qfull, seg & 1)) return;
+            // S of tile g; first / last of what the pair has of its item (number `item`)
+            auto issue_s = [&](uint32_t g, bool first, bool last, uint32_t item) {
+                if (first && !wait(S.qfull, item & 1)) return;
                 const uint32_t buf = g & 1;
                 if (g >= 2 && !wait(S.sempty[buf], ((g >> 1) - 1) & 1)) return;
                 const uint64_t dq = sdesc_sw128(smem_u32(S.q), 0, 1024), dk = sdesc_sw128(smem_u32(S.k), 0, ksbo);
@@ -757,8 +797,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mma_commit_pair(smem_u32(&S.sfull[buf]));
                 if (last) mma_commit_pair(smem_u32(&S.qempty));
             };
-            auto issue_pv = [&](uint32_t g, bool first, uint32_t seg) {
-                if (first && seg > 0 && !wait(S.ofree, (seg - 1) & 1)) return;
+            // fresh: the first that its rows see; off0, off1: all ones where a CTA's row sees nothing of it
+            auto issue_pv = [&](uint32_t g, bool first, bool fresh, uint32_t item, uint32_t off0, uint32_t off1) {
+                if (first && item > 0 && !wait(S.ofree, (item - 1) & 1)) return;
                 if (!wait(S.pfull, g & 1)) return;
                 tc_fence_after();
                 const uint64_t dp = sdesc_sw128(smem_u32(S.p), 0, 1024), dv = sdesc_sw128(smem_u32(S.v), kRows * 128, 1024);
@@ -768,48 +809,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     const uint64_t db = dv + j * (kVBytes >> 4);
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_bf16_ss_pair(tmem + kOCol + 128 * j, dp + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3),
-                                         db + 128 * k + 128 * ((16 * k) & -kRows) / 16, kIdO, !first || k != 0);
+                    for (int k = 0; k < kTile / 16; ++k) {
+                        const uint64_t da = dp + (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3);
+                        const uint64_t dk = db + 128 * k + 128 * ((16 * k) & -kRows) / 16;
+                        if constexpr (kShared)
+                            mma_bf16_ss_pair_lanes(tmem + kOCol + 128 * j, da, dk, kIdO, !fresh || k != 0, off0, off1);
+                        else
+                            mma_bf16_ss_pair(tmem + kOCol + 128 * j, da, dk, kIdO, !fresh || k != 0);
+                    }
                     mma_commit_pair(smem_u32(&S.vempty[j]));
                 }
                 mma_commit_pair(smem_u32(&S.pvdone));
             };
             Segment n;
             bool more = next_seg(n);
-            uint32_t g = 0;
-            if (more && elect_one()) issue_s(0, true, n.t1 - n.t0 == 1, 0);
+            uint32_t g = 0, item = 0, begun = 0; // begun: bit r, CTA r's row has seen a tile
+            if (more && elect_one()) issue_s(0, true, n.t1 - n.t0 == 1 && n.ends(), 0);
             __syncwarp();
             ok = __all_sync(0xffffffffu, ok);
-            for (uint32_t seg = 0; ok && more; ++seg) {
+            while (ok && more) {
                 s = n;
                 more = next_seg(n);
                 const int32_t tiles = s.t1 - s.t0;
+                const uint32_t off0 = s.sees(0) ? 0u : ~0u, off1 = s.sees(1) ? 0u : ~0u;
+                const uint32_t live = (off0 ? 0u : 1u) | (off1 ? 0u : 2u);
+                if (s.begins()) begun = 0;
+                const bool fresh = !(begun & live);
+                begun |= live;
                 if (elect_one()) {
                     for (int32_t t = 0; ok && t < tiles; ++t) {
-                        if (t + 1 < tiles) issue_s(g + t + 1, false, t + 2 == tiles, seg);
-                        else if (more) issue_s(g + t + 1, true, n.t1 - n.t0 == 1, seg + 1);
-                        if (ok) issue_pv(g + t, t == 0, seg);
+                        if (t + 1 < tiles) issue_s(g + t + 1, false, t + 2 == tiles && s.ends(), item);
+                        else if (more) issue_s(g + t + 1, n.begins(), n.t1 - n.t0 == 1 && n.ends(), item + s.ends());
+                        if (ok) issue_pv(g + t, t == 0 && s.begins(), t == 0 && fresh, item, off0, off1);
                     }
                 }
                 __syncwarp();
                 ok = __all_sync(0xffffffffu, ok);
                 g += tiles;
+                item += s.ends();
             }
         }
     } else if (warp == 2) {
         // V loads
-        uint32_t g0 = 0, seg = 0;
-        for (; next_seg(s); g0 += s.t1 - s.t0, ++seg) {
+        uint32_t g0 = 0, item = 0;
+        bool any_bad = false;
+        for (; next_seg(s); g0 += s.t1 - s.t0, item += s.ends()) {
             const int32_t n = (s.t1 - s.t0) * vboxes;
-            bool bad = false;
+            if (s.begins()) any_bad = false;
             for (int32_t x0 = 0; ok && x0 < n; x0 += 32) {
                 const int32_t x = x0 + lane;
+                bool bad = false;
                 const int32_t row = box_row(a, s, s.first_pos(s.t0) + x * kRows, bad);
-                const bool any_bad = __any_sync(0xffffffffu, bad);
+                bad = __any_sync(0xffffffffu, bad);
+                any_bad = any_bad || (bad && s.sees(rank));
                 if (lane == 0) {
-                    S.bad[seg & 3] = any_bad;
-                    if (any_bad) latch_status(a.status, DSA_ERR_BAD_INDEX);
+                    S.bad[item & 3] = any_bad;
+                    if (bad) latch_status(a.status, DSA_ERR_BAD_INDEX);
                 }
                 __syncwarp();
                 for (int32_t y = 0; ok && y < 32 && x0 + y < n; y += vboxes) {
@@ -884,7 +939,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // softmax and epilogue: TMEM lane = tid - 128
         const int ln = tid - 128, x = ln & 63, half = ln >> 6;
         const uint32_t tl = tmem + ((uint32_t)(ln & ~31) << 16);
-        uint32_t g = 0, seg = 0, xb = 0;
+        uint32_t g = 0, seg = 0, item = 0, xb = 0;
+        float m = -INFINITY, l = 0.f;
+        bool begun = false, lost = false;        // the row has seen a tile; an infinity that its scores do not show
         auto exchange = [&](float v) -> float {
             xb ^= 1;
             S.xch[xb][ln] = v;
@@ -893,20 +950,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         // the four warps agree on each segment, since they meet at barriers
         while (!named_bar_or(1, 128, !next_seg(s))) {
-            const bool mine = (int)rank < s.rows;
+            const bool mine = (int)rank < s.rows && s.sees(rank);
             const uint64_t bits =
                 mine ? visible_bits(kShared && !a.mask
                                         ? ~0ull
                                         : __ldg(reinterpret_cast<const unsigned long long*>(a.mask) + s.row + rank),
                                     s.i0 + (int)rank)
                      : 0u;
-            if (!mine) {
+            if ((int)rank >= s.rows && s.begins()) {
                 // P of the last segment is read; zeros for this one
 #pragma unroll
                 for (int k = 0; k < 8; ++k) reinterpret_cast<uint4*>(S.p)[128 * k + ln] = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
             }
-            float m = -INFINITY, l = 0.f;
+            if (s.begins()) {
+                m = -INFINITY, l = 0.f;
+                begun = lost = false;
+            }
             for (int32_t t = s.t0; t < s.t1; ++t, ++g) {
                 const uint32_t buf = g & 1;
                 wait(S.sfull[buf], (g >> 1) & 1);
@@ -962,7 +1022,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (g > 0) wait(S.pvdone, (g - 1) & 1);
                 __syncwarp();
                 tc_fence_after();
-                if (t > s.t0 && __any_sync(0xffffffffu, f != 1.f)) {
+                if (begun && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
                     for (uint32_t c = 0; c < 256; c += 16) {
                         uint32_t o[16];
@@ -983,23 +1043,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(lead(S.pfull));
+                begun = true;
+            }
+            if constexpr (kShared) {
+                if (!s.ends()) {
+                    __syncwarp();
+                    if (mine && *reinterpret_cast<volatile uint32_t*>(&S.lost[warp - 4]) == seg + 1 &&
+                        any_not_finite(a, s, bits))
+                        lost = true;
+                    ++seg;
+                    continue;
+                }
             }
             wait(S.pvdone, (g - 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
-            const bool bad = *reinterpret_cast<volatile int32_t*>(&S.bad[seg & 3]) != 0;
-            if (mine) {
+            const bool bad = *reinterpret_cast<volatile int32_t*>(&S.bad[item & 3]) != 0;
+            if ((int)rank < s.rows) {
                 __syncwarp();
-                if (*reinterpret_cast<volatile uint32_t*>(&S.lost[warp - 4]) == seg + 1 && any_not_finite(a, s, bits))
-                    l = NAN;
+                if (mine && *reinterpret_cast<volatile uint32_t*>(&S.lost[warp - 4]) == seg + 1 &&
+                    any_not_finite(a, s, bits))
+                    lost = true;
+                if (lost) l = NAN;
                 l += exchange(l);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const float ls = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                 const int64_t head = (int64_t)(s.row + (int)rank) * kH;
-                bool whole = s.whole();
-                if constexpr (kShared) whole = s.all;
-                int64_t slot = 2 * (int64_t)pair + (s.t0 == 0 ? 1 : 0);
-                if constexpr (kShared) slot = s.slot;
+                const bool whole = s.whole();
+                const int64_t slot = 2 * (int64_t)pair + (s.from_start() ? 1 : 0);
                 if (half == 0 && ok) {
                     if (!whole) a.part_lse[slot * 128 + 64 * (int)rank + x] = bad ? INFINITY : ls;
                     else if (a.lse && !bad) a.lse[head + x] = ls;
@@ -1043,7 +1114,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 } else if (ok && !whole) {
                     // partial results stay in TMEM's order, four columns of a
-                    // warp's 32 lanes side by side
+                    // warp's 32 lanes side by side (zeros for a row that sees
+                    // none of the pair's tiles: nothing wrote its lanes)
                     float4* part = reinterpret_cast<float4*>(a.part_o) +
                                    ((slot * 2 + (int)rank) * 4 + (warp - 4)) * 64 * 32 + lane;
 #pragma unroll 2
@@ -1051,6 +1123,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         uint32_t o[32];
                         tmem_ld_32x32b_x32(tl + kOCol + c, o);
                         tmem_ld_wait();
+                        if constexpr (kShared) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = begun ? o[k] : 0u;
+                        }
 #pragma unroll
                         for (int v = 0; v < 8; ++v)
                             part[(c / 4 + v) * 32] =
@@ -1063,6 +1139,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_pair(lead(S.ofree));
             ++seg;
+            ++item;
         }
     } else {
         // the segments, and what tree_merge_kernel has to know of a cut item
@@ -1078,11 +1155,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
         };
         bool more = true;
+        int4 meta = make_int4(0, 0, 0, 0);
         if constexpr (kShared) {
             RunIter it(a, pair);
             for (uint32_t n = 0; ok && more; ++n) {
                 more = it.next(s);
                 publish(n, more);
+                if (more && s.ends() && !s.whole()) {
+                    meta = make_int4(s.row, s.rows, it.holder(s.u0 + s.tiles - 1), it.holder(s.u0));
+                    if (a.cut_rows && s.from_start() && rank == 0 && lane < s.rows)
+                        a.cut_rows[s.row + lane] = make_int2(2 * (pair + 1) + lane, meta.z);
+                }
             }
         } else {
             SegIter it(a, S.plan, pair, pairs);
@@ -1093,14 +1176,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     k += __popc(__ballot_sync(0xffffffffu, x + lane < pairs && S.plan.lo[x + lane] <= u));
                 return k - 1;
             };
-            int4 meta = make_int4(0, 0, 0, 0);
             for (uint32_t n = 0; ok && more; ++n) {
                 more = it.next(s);
                 publish(n, more);
                 if (more && !s.whole()) meta = make_int4(s.row, s.rows, holder(s.u0 + s.tiles - 1), holder(s.u0));
             }
-            if (rank == 0 && lane == 0) a.meta[pair] = meta;
         }
+        if (rank == 0 && lane == 0) a.meta[pair] = meta;
     }
     if (!ok) {
         // let copies in flight land before the CTA's shared memory goes
@@ -1116,7 +1198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-constexpr int kMergeBlocks = 16, kMergeWarps = 8;
+constexpr int kMergeBlocks = 2, kMergeWarps = 8;      // blocks of an SM, warps of a block
 
 // 16 joined columns of a lane's query row, `head` in out and lse.
 __device__ __forceinline__ void store_joined(const float (&acc)[16], float sum, float top, int w, int c, int64_t head,
@@ -1134,15 +1216,15 @@ __device__ __forceinline__ void store_joined(const float (&acc)[16], float sum, 
 
 // Joins one unit's pieces: 16 TMEM columns (from c, of warp w's quarter) of 32
 // lanes, a lane per query row, whose head is at row `head` of out.  at(e): twice
-// the slot of piece e, and which of the item's two rows this is.  A warp alone, or
-// (wide, all warps of the block) every 8th piece a warp.
+// the slot of piece e, and which of the item's two rows this is.  By a block, a
+// warp every 8th piece.
 template <class At>
-__device__ __forceinline__ void join_unit(const At& at, int pieces, bool wide, int w, int c, int64_t head,
+__device__ __forceinline__ void join_unit(const At& at, int pieces, int w, int c, int64_t head,
                                           const float* __restrict__ part_lse, const float4* __restrict__ part_o,
                                           uint16_t* __restrict__ out, float* __restrict__ lse,
                                           float (*acc_s)[18][32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int e0 = wide ? warp : 0, step = wide ? kMergeWarps : 1;
+    constexpr int step = kMergeWarps;
     const int x = 32 * (w & 1) + lane;           // the lane's head
     auto piece_lse = [&](int e) -> float { return part_lse[at(e) * 64 + x]; };
     // eight pieces' sums at a time, with a running maximum
@@ -1151,7 +1233,7 @@ __device__ __forceinline__ void join_unit(const At& at, int pieces, bool wide, i
 #pragma unroll
     for (int k = 0; k < 16; ++k) acc[k] = 0.f;
 #pragma unroll 1
-    for (int e1 = e0; e1 < pieces; e1 += 8 * step) {
+    for (int e1 = warp; e1 < pieces; e1 += 8 * step) {
         float ls[8], mx = top;
 #pragma unroll
         for (int q = 0; q < 8; ++q) ls[q] = e1 + q * step < pieces ? piece_lse(e1 + q * step) : -INFINITY;
@@ -1184,78 +1266,41 @@ __device__ __forceinline__ void join_unit(const At& at, int pieces, bool wide, i
     }
     if (bad) top = INFINITY;
     else if (nan) top = NAN;
-    if (wide) {
-        // the warps' sums, in order
+    // the warps' sums, in order
 #pragma unroll
-        for (int k = 0; k < 16; ++k) acc_s[warp][k][lane] = acc[k];
-        acc_s[warp][16][lane] = sum;
-        acc_s[warp][17][lane] = top;
-        __syncthreads();
-        if (warp == 0) {
-            float mx = top;
+    for (int k = 0; k < 16; ++k) acc_s[warp][k][lane] = acc[k];
+    acc_s[warp][16][lane] = sum;
+    acc_s[warp][17][lane] = top;
+    __syncthreads();
+    if (warp == 0) {
+        float mx = top;
 #pragma unroll
-            for (int v = 1; v < kMergeWarps; ++v) {
-                const float m = acc_s[v][17][lane];
-                if (mx != INFINITY) mx = m == INFINITY || m != m ? m : mx != mx ? mx : fmaxf(mx, m);
-            }
-            const float base = mx == -INFINITY ? 0.f : mx;
-            const float own = ex2_approx((top - base) * kLog2e);
-            sum *= own;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) acc[k] *= own;
-#pragma unroll
-            for (int v = 1; v < kMergeWarps; ++v) {
-                const float f = ex2_approx((acc_s[v][17][lane] - base) * kLog2e);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) acc[k] += f * acc_s[v][k][lane];
-                sum += f * acc_s[v][16][lane];
-            }
-            top = mx;
+        for (int v = 1; v < kMergeWarps; ++v) {
+            const float m = acc_s[v][17][lane];
+            if (mx != INFINITY) mx = m == INFINITY || m != m ? m : mx != mx ? mx : fmaxf(mx, m);
         }
-        __syncthreads();
-        if (warp != 0) return;
+        const float base = mx == -INFINITY ? 0.f : mx;
+        const float own = ex2_approx((top - base) * kLog2e);
+        sum *= own;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[k] *= own;
+#pragma unroll
+        for (int v = 1; v < kMergeWarps; ++v) {
+            const float f = ex2_approx((acc_s[v][17][lane] - base) * kLog2e);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) acc[k] += f * acc_s[v][k][lane];
+            sum += f * acc_s[v][16][lane];
+        }
+        top = mx;
     }
+    __syncthreads();
+    if (warp != 0) return;
     if (top == INFINITY) return;                 // a bad page in one of the pieces
     store_joined(acc, sum, top, w, c, head + x, out, lse);
 }
 
-// Joins the partial results of the items that chunks cut.  A unit is 16 TMEM
-// columns of a CTA's 32 lanes, a lane per query row.  Items of few pieces: the
-// 16 blocks of the pair that begins the item take a unit per warp.  Items of
-// many (one long sequence over the whole GPU: 10 MB of pieces): the blocks of
-// the pairs inside it, which begin nothing, help; a block takes a unit, its
-// warps every 8th piece (1 x 100,000 rows: 83 -> 30 us, merge included).
-__global__ void __launch_bounds__(32 * kMergeWarps)
-    tree_merge_kernel(const int4* __restrict__ meta, const float* __restrict__ part_lse,
-                      const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
-    __shared__ float acc_s[kMergeWarps][18][32];
-    const int warp = threadIdx.x >> 5;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int4 it = meta[blockIdx.x];
-    const int pair = it.w, helper = (int)blockIdx.x - pair;
-    if (it.y == 0) return;
-    // its pieces: the first pair's slot 2 pair + 1, then slots 2 p of the pairs
-    // behind it
-    const int pieces = it.z - pair + 1;
-    const bool wide = pieces > kMergeWarps;
-    if (!wide && helper > 0) return;
-    const int helpers = wide ? it.z - pair + (meta[it.z].w == pair ? 1 : 0) : 1;
-    const int units = 64 * it.y, stride = wide ? kMergeBlocks * helpers : units;
-    for (int unit = wide ? kMergeBlocks * helper + (int)blockIdx.y : kMergeWarps * (int)blockIdx.y + warp; unit < units;
-         unit += stride) {
-        const int rank = unit >> 6;
-        auto at = [&](int e) -> int64_t {
-            return 2 * (e == 0 ? 2 * (int64_t)pair + 1 : 2 * ((int64_t)pair + e)) + rank;
-        };
-        join_unit(at, pieces, wide, (unit >> 4) & 3, 16 * (unit & 15), (int64_t)(it.x + rank) * kH, part_lse, part_o, out,
-                  lse, acc_s);
-    }
-}
-
-// The same for at most 8 pieces, by a warp alone, with half of all loads on their
-// way at once: for calls of few rows, which wait for each in turn (4 rows behind
-// 2,000 20.5 -> 18.6 us; 610 rows, whose warps fill the SMs, 242 -> 254).
+// The same for at most 8 pieces, by a warp, with half of all loads on their way at
+// once.
 template <class At>
 __device__ __forceinline__ void join_few(const At& at, int pieces, int w, int c, int64_t head,
                                          const float* __restrict__ part_lse, const float4* __restrict__ part_o,
@@ -1304,74 +1349,127 @@ __device__ __forceinline__ void join_few(const At& at, int pieces, int w, int c,
     store_joined(acc, sum, top, w, c, head + x, out, lse);
 }
 
-// Joins a row's pieces, those over the group's shared tiles and then its own.
-template <bool kFewRows>
+// Joins the partial results of the items that shares cut.  A unit is 16 TMEM
+// columns of a CTA's 32 lanes, a lane per query row.  Items of at most 8 pieces
+// take a warp for each unit; those of many (one long sequence over the whole
+// GPU: 10 MB of pieces) a block, whose warps take every 8th piece (1 x 100,000
+// rows: 83 -> 30 us, merge included).  The blocks that fit the GPU at once find the
+// items themselves and share out the units of all.
+__global__ void __launch_bounds__(32 * kMergeWarps, kMergeBlocks)
+    tree_merge_kernel(const int4* __restrict__ meta, int pairs, const float* __restrict__ part_lse,
+                      const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
+    __shared__ float acc_s[kMergeWarps][18][32];
+    __shared__ int4 item_s[kMaxPairs];
+    __shared__ int32_t narrow_s[kMaxPairs + 1], wide_s[kMaxPairs + 1];   // units before each pair's item
+    const int tid = threadIdx.x, warp = tid >> 5;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (tid < 32) {
+        constexpr int kEach = kMaxPairs / 32;
+        int32_t narrow[kEach], wide[kEach], n = 0, w = 0;
+        int4 it[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) it[k] = kEach * tid + k < pairs ? meta[kEach * tid + k] : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            // rows, if the pair begins the item
+            const int32_t units = it[k].w == kEach * tid + k ? 64 * it[k].y : 0;
+            const bool many = it[k].z - it[k].w >= kMergeWarps;
+            item_s[kEach * tid + k] = it[k];
+            n += narrow[k] = many ? 0 : units;
+            w += wide[k] = many ? units : 0;
+        }
+        n = warp_scan_i32(n);
+        w = warp_scan_i32(w);
+        if (tid == 31) narrow_s[kMaxPairs] = n, wide_s[kMaxPairs] = w;
+#pragma unroll
+        for (int k = kEach - 1; k >= 0; --k) {
+            narrow_s[kEach * tid + k] = n -= narrow[k];
+            wide_s[kEach * tid + k] = w -= wide[k];
+        }
+    }
+    __syncthreads();
+    // unit u of the items that `before` counts
+    auto join = [&](const int32_t* before, int32_t u, bool many) {
+        const int pair = last_at_or_below(before, kMaxPairs, u), unit = u - before[pair], rank = unit >> 6;
+        const int4 it = item_s[pair];
+        // its pieces: the first pair's slot 2 pair + 1, then slots 2 p of the pairs
+        // behind it
+        auto at = [&](int e) -> int64_t {
+            return 2 * (e == 0 ? 2 * (int64_t)pair + 1 : 2 * ((int64_t)pair + e)) + rank;
+        };
+        const int pieces = it.z - pair + 1, w = (unit >> 4) & 3, c = 16 * (unit & 15);
+        const int64_t head = (int64_t)(it.x + rank) * kH;
+        if (many) join_unit(at, pieces, w, c, head, part_lse, part_o, out, lse, acc_s);
+        else join_few(at, pieces, w, c, head, part_lse, part_o, out, lse);
+    };
+    for (int32_t u = (int32_t)blockIdx.x; u < wide_s[kMaxPairs]; u += (int32_t)gridDim.x) join(wide_s, u, true);
+    for (int32_t u = kMergeWarps * (int32_t)blockIdx.x + warp; u < narrow_s[kMaxPairs]; u += kMergeWarps * (int32_t)gridDim.x)
+        join(narrow_s, u, false);
+}
+
+// The same by rows, without the search: for calls of few rows, where the code that
+// a block meets for the first time is what counts (4 rows behind 2,000: 9.1 -> 6.0 us).
 __global__ void __launch_bounds__(32 * kMergeWarps)
-    prefix_merge_kernel(const RowPieces* __restrict__ pieces, int32_t total_q, const float* __restrict__ part_lse,
-                        const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
+    few_merge_kernel(const int2* __restrict__ rows, const float* __restrict__ part_lse,
+                     const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
     __shared__ float acc_s[kMergeWarps][18][32];
     const int warp = threadIdx.x >> 5;
     pdl_launch_dependents();
     pdl_wait();
-    const RowPieces shared = pieces[blockIdx.x], own = pieces[total_q + blockIdx.x];
-    if (own.count == 0) return;                  // no row, or a sequence outside the bounds
-    const int first = shared.count >> 1, all = first + (own.count >> 1);
-    const bool wide = all > kMergeWarps;
-    auto at = [&](int e) -> int64_t {
-        return e < first ? 2 * ((int64_t)shared.slot + e) + (shared.count & 1)
-                         : 2 * ((int64_t)own.slot + e - first) + (own.count & 1);
-    };
+    const int2 it = rows[blockIdx.x];
+    if (it.x == 0) return;                       // a row that one pair has done, or no row
+    const int pair = (it.x >> 1) - 1, pieces = it.y - pair + 1;
+    auto at = [&](int e) -> int64_t { return 2 * (2 * ((int64_t)pair + e) + (e == 0 ? 1 : 0)) + (it.x & 1); };
     const int64_t head = (int64_t)blockIdx.x * kH;
-    if (wide) {
-        for (int unit = (int)blockIdx.y; unit < 64; unit += (int)gridDim.y)
-            join_unit(at, all, true, unit >> 4, 16 * (unit & 15), head, part_lse, part_o, out, lse, acc_s);
+    if (pieces > kMergeWarps) {
+        for (int u = (int)blockIdx.y; u < 64; u += (int)gridDim.y)
+            join_unit(at, pieces, u >> 4, 16 * (u & 15), head, part_lse, part_o, out, lse, acc_s);
     } else {
-        for (int unit = kMergeWarps * (int)blockIdx.y + warp; unit < 64; unit += kMergeWarps * (int)gridDim.y)
-            if constexpr (kFewRows) join_few(at, all, unit >> 4, 16 * (unit & 15), head, part_lse, part_o, out, lse);
-            else join_unit(at, all, false, unit >> 4, 16 * (unit & 15), head, part_lse, part_o, out, lse, acc_s);
+        for (int u = kMergeWarps * (int)blockIdx.y + warp; u < 64; u += kMergeWarps * (int)gridDim.y)
+            join_few(at, pieces, u >> 4, 16 * (u & 15), head, part_lse, part_o, out, lse);
     }
 }
 
-// The runs of a call behind shared prefixes, by the first block; the others
-// clear the rows' pieces.  A group counts if all groups together are the
-// batch in order and each of its sequences with new rows keeps the shared ones; else
-// its sequences are computed each by itself.  kFew: a thread for each run at most, so
-// that everything is loaded at once and the rest is shared memory's.
+// Blocks of a merge: those of one wave, or as many as have a unit at most.
+int merge_blocks(int pairs) { return std::min(kMergeBlocks * num_sms(), 128 * pairs); }
+
+// The runs of a call behind shared prefixes, by one block.  A group counts if all
+// groups together are the batch in order and each of its sequences with new rows
+// keeps the shared ones; else its sequences are computed each by itself.  Two rows of
+// different sequences make an item only where every sequence is within its bounds, so
+// that a group's rows lie side by side.  kFew: a thread for each sequence and group
+// at most, so that everything is loaded at once and the rest is shared memory's.
 constexpr int kPlanThreads = 1024;
 
 template <bool kFew>
 __global__ void __launch_bounds__(kPlanThreads)
     prefix_plan_kernel(const BatchDev bd, const GroupsDev gr, RunPlan* plan, Run* runs, int32_t* tiles_all,
-                       int32_t* lead_all, RowPieces* pieces, int pairs, int32_t* status) {
+                       int32_t* lead_all, int pairs, int least_shared, int2* cut_rows, int32_t* status) {
     __shared__ int64_t s_units[kPlanThreads / 32];
-    __shared__ int32_t s_items[kPlanThreads / 32], s_longest[kPlanThreads / 32];
+    __shared__ int32_t s_longest[kPlanThreads / 32];
     __shared__ int32_t s_off[kFew ? kPlanThreads + 1 : 1], s_rows[kFew ? kPlanThreads : 1], s_q[kFew ? kPlanThreads + 1 : 1],
-        s_tiles[kFew ? kPlanThreads : 1], s_lead[kFew ? kPlanThreads : 1];
+        s_ctx[kFew ? kPlanThreads : 1], s_tiles[kFew ? kPlanThreads : 1], s_lead[kFew ? kPlanThreads : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = (int)blockDim.x;
     pdl_launch_dependents();
     pdl_wait();
-    if (blockIdx.x > 0) {
-        for (int64_t i = (int64_t)(blockIdx.x - 1) * threads + tid; i < 2 * (int64_t)bd.total_q;
-             i += (int64_t)(gridDim.x - 1) * threads)
-            pieces[i] = RowPieces{0, 0};
-        return;
-    }
     // tiles that a group shares, and the sequence that they are read from
     int32_t* const tiles_of = kFew ? s_tiles : tiles_all;
     int32_t* const lead = kFew ? s_lead : lead_all;
     const int32_t* const off = kFew ? s_off : gr.off;
     const int32_t* const rows_of = kFew ? s_rows : gr.shared;
     const int32_t* const q_off = kFew ? s_q : bd.q_off;
-    const int32_t n = gr.n + bd.B;
-    // the sequence of run i >= gr.n
-    auto sequence = [&](int32_t i, SeqInfo& q) -> bool { return load_seq(bd, i - gr.n, status, q); };
+    const int32_t* const ctx_len = kFew ? s_ctx : bd.ctx_len;
     SeqInfo mine{0, 0, 0};
-    bool good = false, wrong = false;
+    bool good = false, wrong = false, broken = false;
+    if (cut_rows)
+        for (int32_t i = tid; i < bd.total_q; i += threads) cut_rows[i] = make_int2(0, 0);
     if (kFew) {
-        if (tid >= gr.n && tid < n) {
-            good = sequence(tid, mine);
-            s_q[tid - gr.n] = mine.q0;
-            if (tid == n - 1) s_q[bd.B] = mine.q0 + mine.nq;
+        if (tid < bd.B) {
+            good = load_seq(bd, tid, status, mine);
+            s_q[tid] = mine.q0;
+            s_ctx[tid] = mine.ctx;
+            if (tid == bd.B - 1) s_q[bd.B] = mine.q0 + mine.nq;
         }
         if (tid < gr.n) {
             s_off[tid] = __ldg(gr.off + tid);
@@ -1389,68 +1487,76 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     if (wrong) latch_status(status, DSA_ERR_BAD_BATCH);
     wrong = __syncthreads_or(wrong);
-    for (int32_t i = kFew ? tid : gr.n + tid; i < n && !wrong; i += threads) {
-        if (i < gr.n) continue;
-        if (!kFew) good = sequence(i, mine);
-        if (good && mine.nq == 0) continue;
-        const int g = last_at_or_below(off, gr.n, i - gr.n);
+    for (int32_t i = tid; i < bd.B; i += threads) {
+        if (!kFew) good = load_seq(bd, i, status, mine);
+        broken = broken || !good;
+        if (wrong || (good && mine.nq == 0)) continue;
+        const int g = last_at_or_below(off, gr.n, i);
         if (good && rows_of[g] <= mine.ctx - mine.nq) {
-            atomicMin(lead + g, i - gr.n);
+            atomicMin(lead + g, i);
         } else {
             latch_status(status, DSA_ERR_BAD_BATCH);
             tiles_of[g] = 0;
         }
     }
-    __syncthreads();
+    const bool alone = __syncthreads_or(broken) || wrong;
     int64_t units = 0;
-    int32_t items = 0, longest = 0;
-    for (int32_t i0 = 0; i0 < n; i0 += threads) {
+    int32_t longest = 0;
+    for (int32_t i0 = 0; i0 < bd.B; i0 += threads) {
         const int32_t i = i0 + tid;
-        Run r{0, 0, 0, 0, 0, 0, 0};
-        if (i < gr.n) {
-            if (!wrong && tiles_of[i] > 0 && lead[i] < bd.B) {
-                r.q0 = q_off[off[i]];
-                r.nq = q_off[off[i + 1]] - r.q0;
-                r.len = tiles_of[i] * kTile;
-                r.b = lead[i];
-            }
-        } else if (i < n) {
-            if (!kFew) good = sequence(i, mine);
-            r.b = i - gr.n;
+        Run inner{}, tail{};
+        if (i < bd.B) {
+            if (!kFew) good = load_seq(bd, i, status, mine);
             if (good && mine.nq > 0) {
-                r.q0 = mine.q0;
-                r.nq = mine.nq;
-                r.len = mine.ctx;
-                r.base = wrong ? 0 : tiles_of[last_at_or_below(off, gr.n, r.b)];
+                const int g = wrong ? 0 : last_at_or_below(off, gr.n, i);
+                inner.base = wrong ? 0 : tiles_of[g];
+                // the rows that may make items with this sequence's
+                const bool mixed = !alone && inner.base >= least_shared;
+                const int32_t row0 = mixed ? q_off[off[g]] : mine.q0, row1 = mixed ? q_off[off[g + 1]] : mine.q0 + mine.nq;
+                const int32_t skip = (mine.q0 - row0) & 1, rest = mine.nq - skip;
+                inner.row = mine.q0 + skip;
+                inner.items = rest >> 1;
+                inner.rows = 2;
+                inner.lead = inner.base > 0 ? lead[g] : 0;
+                inner.b = i;
+                inner.len = mine.ctx;
+                inner.n = mine.nq;
+                inner.i0 = skip;
+                inner.lone = mixed && row1 - row0 <= 2;
+                tail = inner;
+                tail.row = mine.q0 + mine.nq - 1;
+                tail.items = rest & 1;
+                tail.rows = 1;
+                tail.i0 = mine.nq - 1;
+                if (tail.items && tail.row + 1 < row1) {
+                    tail.rows = 2;
+                    tail.b2 = last_at_or_below(q_off, bd.B, tail.row + 1);
+                    tail.len2 = ctx_len[tail.b2];
+                    tail.n2 = q_off[tail.b2 + 1] - q_off[tail.b2];
+                }
             }
         }
-        const int32_t its = (r.nq + 1) >> 1, tiles = (r.len + kTile - 1) / kTile - r.base;
-        const int64_t cost = (int64_t)its * (tiles + kRunItemCost);
-        longest = max(longest, its > 0 ? tiles : 0);
-        int64_t iu = cost;
-        int32_t ii = its;
+        const int64_t cost = (int64_t)inner.items * (inner.tiles() + kItemCost);
+        const int64_t both = cost + (int64_t)tail.items * (tail.tiles() + kItemCost);
+        longest = max(longest, max(inner.items ? inner.tiles() : 0, tail.items ? tail.tiles() : 0));
+        int64_t iu = both;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t u = __shfl_up_sync(0xffffffffu, iu, o);
-            const int32_t v = __shfl_up_sync(0xffffffffu, ii, o);
-            if (lane >= o) iu += u, ii += v;
+            if (lane >= o) iu += u;
         }
-        if (lane == 31) {
-            s_units[warp] = iu;
-            s_items[warp] = ii;
-        }
+        if (lane == 31) s_units[warp] = iu;
         __syncthreads();
         int64_t bu = units;
-        int32_t bi = items;
         for (int w = 0; w < threads / 32; ++w) {
-            if (w < warp) bu += s_units[w], bi += s_items[w];
+            if (w < warp) bu += s_units[w];
             units += s_units[w];
-            items += s_items[w];
         }
-        if (i < n) {
-            r.u = bu + iu - cost;
-            r.item0 = bi + ii - its;
-            runs[i] = r;
+        if (i < bd.B) {
+            inner.u = bu + iu - both;
+            tail.u = inner.u + cost;
+            runs[2 * i] = inner;
+            runs[2 * i + 1] = tail;
         }
         if (!kFew) __syncthreads();
     }
@@ -1462,6 +1568,18 @@ __global__ void __launch_bounds__(kPlanThreads)
         const int64_t even = (units + pairs - 1) / pairs;
         *plan = RunPlan{units, max(even, (int64_t)least_chunk(longest))};
     }
+}
+
+// Tiles that a group has to share for items of two sequences.  Such an item
+// spares the second its walk over the shared tiles, but takes the own tiles of both
+// in turn, with the end of each (see the fix-up).  Where there is little work for
+// every pair, only if the shared tiles are half of the longest cache (12 rows
+// behind 440, 542 of their own: 20.8 us apart, 26.9 together; 4 behind 2,000, 40 of
+// their own: 21.9 and 20.5).
+int least_shared(const BatchDev& bd, int pairs) {
+    const int64_t items = ((int64_t)bd.total_q + std::min(bd.total_q, bd.B)) / 2;
+    const int tiles = (bd.max_ctx + kTile - 1) / kTile;
+    return items * (tiles + kItemCost) <= (int64_t)kApartUnits * pairs ? std::max(1, (tiles + 1) / 2) : 1;
 }
 
 // CTA pairs that can be resident at once on the current device.
@@ -1568,10 +1686,10 @@ cudaError_t launch_tree_mla(const BatchDev& bd, const PagesDev& pg, const uint16
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, a, maps.q, maps.k, maps.v)) != cudaSuccess) return e;
     count_launches(1);
-    cfg.gridDim = dim3((unsigned)pairs, kMergeBlocks);
+    cfg.gridDim = dim3((unsigned)merge_blocks(pairs));
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, (const int4*)a.meta, (const float*)a.part_lse,
+    e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, (const int4*)a.meta, pairs, (const float*)a.part_lse,
                            (const float4*)a.part_o, out, lse);
     if (e == cudaSuccess) count_launches(1);
     return e;
@@ -1579,17 +1697,10 @@ cudaError_t launch_tree_mla(const BatchDev& bd, const PagesDev& pg, const uint16
 
 namespace {
 
-// Pieces that a call behind shared prefixes can have: two items' worth of rows
-// each, one more for an odd one of every group and sequence, and the pairs' cuts.
-size_t prefix_slots(const BatchDev& bd, int32_t groups, int pairs) {
-    const size_t rows = (size_t)bd.total_q;
-    return (rows + std::min<size_t>(rows, groups)) / 2 + (rows + std::min<size_t>(rows, bd.B)) / 2 + 2 + pairs;
-}
-
 struct PrefixScratch {
-    size_t plan, tiles, lead, runs, pieces, lse, o, bytes;
-    PrefixScratch(const BatchDev& bd, int32_t groups, int pairs) {
-        const size_t slots = prefix_slots(bd, groups, pairs);
+    size_t plan, tiles, lead, runs, meta, cut, lse, o, bytes;
+    PrefixScratch(const BatchDev& bd, int32_t groups) {
+        const size_t slots = 2 * (size_t)std::min(num_sms() / 2, kMaxPairs);
         size_t at = 0;
         auto take = [&](size_t n) {
             const size_t mine = at;
@@ -1599,8 +1710,9 @@ struct PrefixScratch {
         plan = take(sizeof(RunPlan));
         tiles = take(sizeof(int32_t) * (size_t)groups);
         lead = take(sizeof(int32_t) * (size_t)groups);
-        runs = take(sizeof(Run) * ((size_t)groups + bd.B));
-        pieces = take(sizeof(RowPieces) * 2 * (size_t)bd.total_q);
+        runs = take(sizeof(Run) * 2 * (size_t)bd.B);
+        meta = take(sizeof(int4) * slots / 2);
+        cut = take(sizeof(int2) * std::min(bd.total_q, kFewRows));
         lse = take(sizeof(float) * 128 * slots);
         o = take(sizeof(float) * 128 * kDV * slots);
         bytes = at;
@@ -1610,14 +1722,14 @@ struct PrefixScratch {
 }  // namespace
 
 size_t prefix_mla_scratch_bytes(const BatchDev& bd, int32_t groups) {
-    return PrefixScratch(bd, groups, std::min(num_sms() / 2, kMaxPairs)).bytes;
+    return PrefixScratch(bd, groups).bytes;
 }
 
 cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const PagesDev& pg, const uint16_t* q,
                               const uint16_t* kv, const uint64_t* mask, float sm_scale, uint16_t* out, float* lse,
                               void* scratch, int32_t* status, cudaStream_t stream) {
     const int pairs = max_pairs();
-    const PrefixScratch at(bd, gr.n, std::min(num_sms() / 2, kMaxPairs));
+    const PrefixScratch at(bd, gr.n);
     uint8_t* const mem = static_cast<uint8_t*>(scratch);
     Args a{};
     a.bd = bd;
@@ -1634,9 +1746,10 @@ cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const Pag
     Run* runs = reinterpret_cast<Run*>(mem + at.runs);
     a.rplan = plan;
     a.runs = runs;
-    a.runs_total = gr.n + bd.B;
-    a.runs_shared = gr.n;
-    a.pieces = reinterpret_cast<RowPieces*>(mem + at.pieces);
+    a.runs_total = 2 * bd.B;
+    a.meta = reinterpret_cast<int4*>(mem + at.meta);
+    const bool few_rows = bd.total_q <= kFewRows;
+    a.cut_rows = few_rows ? reinterpret_cast<int2*>(mem + at.cut) : nullptr;
     a.rows_total = pg.table ? pg.pool_pages << pg.shift : (int32_t)(bd.B * bd.stride);
     const TreeMaps maps(a, q);
     if (!maps.ok) return cudaErrorInvalidValue;
@@ -1650,16 +1763,16 @@ cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const Pag
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    const int64_t n = (int64_t)gr.n + bd.B;
+    const int32_t n = std::max(gr.n, bd.B);
     const bool few = n <= kPlanThreads;
-    const int threads = few ? (int)((n + 31) / 32 * 32) : kPlanThreads;
-    cfg.gridDim = dim3(1 + (unsigned)std::min<int64_t>(64, (2 * (int64_t)bd.total_q + threads - 1) / threads));
-    cfg.blockDim = dim3(threads);
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(few ? (n + 31) / 32 * 32 : kPlanThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, few ? prefix_plan_kernel<true> : prefix_plan_kernel<false>, bd, gr, plan, runs, reinterpret_cast<int32_t*>(mem + at.tiles),
-                           reinterpret_cast<int32_t*>(mem + at.lead), a.pieces, pairs, status);
+    e = cudaLaunchKernelEx(&cfg, few ? prefix_plan_kernel<true> : prefix_plan_kernel<false>, bd, gr, plan, runs,
+                           reinterpret_cast<int32_t*>(mem + at.tiles), reinterpret_cast<int32_t*>(mem + at.lead), pairs,
+                           least_shared(bd, pairs), a.cut_rows, status);
     if (e != cudaSuccess) return e;
     count_launches(1);
     cfg.gridDim = dim3(2 * (unsigned)pairs);
@@ -1667,12 +1780,17 @@ cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const Pag
     cfg.dynamicSmemBytes = kSmem;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, a, maps.q, maps.k, maps.v)) != cudaSuccess) return e;
     count_launches(1);
-    cfg.gridDim = dim3((unsigned)bd.total_q, bd.total_q <= 16 ? 64 : 64 / kMergeWarps);
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, bd.total_q <= 64 ? prefix_merge_kernel<true> : prefix_merge_kernel<false>,
-                           (const RowPieces*)a.pieces, bd.total_q, (const float*)a.part_lse, (const float4*)a.part_o,
-                           out, lse);
+    if (few_rows) {
+        cfg.gridDim = dim3((unsigned)bd.total_q, 64);
+        e = cudaLaunchKernelEx(&cfg, few_merge_kernel, (const int2*)a.cut_rows, (const float*)a.part_lse,
+                               (const float4*)a.part_o, out, lse);
+    } else {
+        cfg.gridDim = dim3((unsigned)merge_blocks(pairs));
+        e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, (const int4*)a.meta, pairs, (const float*)a.part_lse,
+                               (const float4*)a.part_o, out, lse);
+    }
     if (e == cudaSuccess) count_launches(1);
     return e;
 }

@@ -134,6 +134,42 @@ def test_rows_stay_apart():
     assert out.isnan().all() and lse.isnan().all()
 
 
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("share", [0, 128, 1000])
+@pytest.mark.parametrize("m", [[1, 1, 1, 1], [3, 1, 2, 5]])
+def test_a_tile_of_two_sequences(share, m, page):
+    """Rows of neighbours in a group may lie in one tile: what either's own rows hold stays with it."""
+    c = [share + x for x in (3, 700, 260, 129)] + [20000]        # (work enough that rows of two sequences are put together)
+    st = Shared(c, m + [16], [0, 4, 5], [share, 0], page, seed=share + m[0])
+    q, kv = st.inputs()
+    clean, lclean = st.prefix(q, kv)
+    assert st.status() == 0
+    at = np.cumsum([0] + m)
+    check_attention(st, q, kv, clean, lclean, rows=set(range(at[4] + 1)))
+    for b in range(4):
+        for value in (float("inf"), -float("inf"), float("nan")):
+            hurt = kv.clone()
+            hurt[int(st.row(b, c[b] - 1)), 200] = value          # the last committed one, its own
+            out, lse = st.prefix(q, hurt)
+            mine = torch.zeros(st.T, dtype=torch.bool)
+            mine[at[b]:at[b + 1]] = True
+            assert torch.equal(out.cpu()[~mine], clean.cpu()[~mine]) and torch.equal(lse.cpu()[~mine], lclean.cpu()[~mine])
+            assert not out.cpu()[mine].isfinite().any(-1).all()
+
+
+@pytest.mark.parametrize("b,n,share,own,page", [(12, 1, 128, 9000, 64), (3, 1, 0, 30000, 0), (9, 3, 256, 4000, 32), (15, 1, 300, 7000, 16)])
+def test_cut_own_parts(b, n, share, own, page):
+    """Long own parts: the pairs' cuts fall into either sequence of an item."""
+    rng = np.random.default_rng(b)
+    st = Shared([share + int(x) for x in rng.integers(own // 2, own, b)], [n] * b, [0, b], [share], page, seed=b)
+    q, kv = st.inputs()
+    out, lse = st.prefix(q, kv)
+    assert st.status() == 0
+    check_attention(st, q, kv, out, lse)
+    again, _ = st.prefix(q, kv)
+    assert torch.equal(out, again)
+
+
 @pytest.mark.parametrize("first,share", [
     ([0, 2, 2], [128, 128]), ([1, 3, 4], [128, 128]), ([0, 3, 2], [128, 128]), ([0, 5, 4], [128, 128]), ([0, -1, 4], [128, 128]),
     ([0, 2, 4], [128, -1]), ([0, 2, 4], [128, 129]), ([0, 2, 4], [400, 128]), ([0, 2, 1 << 30], [128, 128]),

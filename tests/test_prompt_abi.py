@@ -91,7 +91,7 @@ def test_prompt_workspace(lib):
     assert lib.dsa_prompt_workspace_size(None, ctypes.byref(n)) == 1
     assert lib.dsa_prompt_workspace_size(ctypes.byref(_batch()), None) == 1
     assert lib.dsa_prompt_workspace_size(ctypes.byref(_batch(B=0)), ctypes.byref(n)) == 1
-    assert _ws(lib, _batch()) % 256 == 0 and _ws(lib, _batch(B=65535)) >= 256 + 4 * 65537
+    assert _ws(lib, _batch()) % 256 == 0 and _ws(lib, _batch(B=65535)) >= 256 + 4 * 65536      # an offset for each sequence and one behind them
 
 
 def _call(lib, which, b, g, x, q=P, out=P, lse=None, scale=0.0625, first=None, w=P, ws=WS, n=None):
@@ -161,8 +161,10 @@ def test_prefix_workspace(lib):
     assert [size(dict(B=0), {}), size({}, dict(n=0)), size({}, dict(n=3))] == [1, 1, 1]
     assert lib.dsa_prefix_workspace_size(ctypes.byref(_batch()), None, ctypes.byref(n)) == 1
     assert lib.dsa_prefix_workspace_size(ctypes.byref(_batch()), ctypes.byref(_groups()), None) == 1
-    # every piece of 64 sequences of one row has its place: 32 pairs of shared rows, 64 own, and the cuts
-    assert size(dict(B=64, total_q=64, max_q=1), {}) == 0 and n.value >= (32 + 64 + 76) * 4 * 128 * 513
+    # two pieces of 128 rows for each of 76 CTA pairs, and two runs a sequence
+    assert size(dict(B=64, total_q=64, max_q=1), {}) == 0 and n.value >= 2 * 76 * 4 * 128 * 513 + 64 * 128
+    small = n.value
+    assert size(dict(B=65535, total_q=65535, max_q=1), {}) == 0 and n.value >= small + (65535 - 64) * 128
 
 
 @pytest.mark.parametrize("b,r,g,kw,code", [
