@@ -351,9 +351,10 @@ DSA_API dsa_status dsa_forward_fp8(const dsa_batch* batch, const uint8_t* q8, co
  * block_table[b * max_pages + s / page_size] * page_size + s % page_size of a
  * cache of pool_pages * page_size rows, and cache_stride plays no part (it
  * must still be >= max_ctx).  The calls of steps 1 to 3 take contiguous caches
- * only, so dsa_tree_mla_fwd is the one attention over pages, for up to 64 new
- * rows a sequence; prompt rows over pages are the caller's own.  Without a
- * dsa_pages (NULL) it is row b * cache_stride + s, as in every other call.
+ * only, so attention over pages is dsa_tree_mla_fwd's and dsa_prefix_mla_fwd's,
+ * for up to 64 new rows a sequence, and dsa_prompt_mla_fwd's, over rows that
+ * dsa_mla_expand reads from them.  Without a dsa_pages (NULL) it is row
+ * b * cache_stride + s, as in every other call.
  * Every launch is sized from the host arguments alone.  Calls that may run at
  * the same time (two streams, or two captured graphs) need a workspace each.
  * The calls' results do not depend on timing: the same inputs give the same
