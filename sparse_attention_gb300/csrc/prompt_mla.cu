@@ -40,6 +40,9 @@
 // L2), and short items fill the end.  The order decides which pair computes an item,
 // never what it computes.
 //
+// Where sequences have at most 128 new rows an item is those, at M = 128 (kFew
+// below).
+//
 // Roles of a CTA's 16 warps: K loads, MMA (rank 0 only), Q and V loads, items,
 // eight softmax warps (two threads share a query row, 64 positions each),
 // four that write results (an item's O is read out under the first S and softmax of
@@ -52,7 +55,7 @@
 // slows: 16,384 tokens 4.35-4.40 ms = 2,000-2,020 TFLOP/s (cuBLAS 1,921) and
 // 5.0-5.05 ms = 1,740-1,760 (1,730 sustained); 12 prompts of 839 to 2,012 tokens
 // 0.60 ms and 0.68-0.72, 401 tiles a pair for the 319 that the mask leaves;
-// 100 tokens 12 us.
+// 100 tokens 10 us.
 #include <algorithm>
 #include <atomic>
 
@@ -65,7 +68,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTile = 128;                   // positions per tile
-constexpr int kMmaRows = 256;                // M of a pair's MMA; rows of an item, but where all have at most ..
+constexpr int kMmaRows = 256;                // rows of an item and M of a pair's MMA, but where all have at most ..
 constexpr int kFewRows = 128;                // .. these
 constexpr int kThreads = 512;
 constexpr int kSoftWarps = 8, kOutWarps = 4;
@@ -74,7 +77,7 @@ constexpr int kKBytes = 64 * 128;            // 64 rows x 64 columns
 constexpr int kQChunks = kHeadQK / 64;       // 4
 constexpr int kStages = 2;                   // whole tiles of K and of V
 constexpr uint32_t kOCol = 0, kSCol = 256;   // TMEM columns
-constexpr int kSlots = 2;                    // items published ahead
+constexpr int kMaxSlots = 8;                 // items published ahead, at most
 constexpr int kMaxPairs = 96;
 constexpr float kRescale = 8.f;              // log2
 static_assert(kTile == kExpRoom, "a sequence's room holds whole tiles");
@@ -91,12 +94,12 @@ struct Smem {
     alignas(1024) uint8_t q[kQChunks * kQBytes];
     alignas(1024) uint8_t k[kStages * kQChunks * kKBytes];
     alignas(1024) uint8_t v[kStages * 2 * kQBytes];      // two blocks of 64 columns x 128 positions
-    alignas(1024) uint8_t out[kOutWarps * 4096];
+    alignas(1024) uint8_t out[kOutWarps * 4096];         // results on their way out; kFew: P, two blocks of 64 rows x 64 positions
     alignas(8) uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
-    uint64_t qfull[kQChunks], qempty[kQChunks], sfull[2], pfull[2], pvdone, odone, lfull, invfree, ofree, itemfull[kSlots], itemempty[kSlots];
-    uint64_t numfull[kSlots], numempty[kSlots];          // item numbers on their way to rank 1
-    Item item[kSlots];
-    uint32_t number[kSlots];
+    uint64_t qfull[kQChunks], qempty[kQChunks], sfull[2], pfull[2], pvdone[2], odone[2], lfull[2], invfree[2], ofree[2], itemfull[kMaxSlots], itemempty[kMaxSlots];
+    uint64_t numfull[kMaxSlots], numempty[kMaxSlots];          // item numbers on their way to rank 1
+    Item item[kMaxSlots];
+    uint32_t number[kMaxSlots];
     float xch[2][32 * kSoftWarps];
     alignas(16) int4 seq[kThreads];                      // the plan of a batch of few sequences: first new row, how many,
     int32_t start[kThreads + 1], sums[kThreads / 32];    // .. length, first expanded row; query tiles before it
@@ -169,21 +172,32 @@ __device__ __forceinline__ Item item_of(const Args& a, const Smem& S, uint32_t n
     return it;
 }
 
-// kFew: items have 128 rows at most, 64 each CTA's.  Queries then take half the
-// shared memory and are loaded an item ahead, an item's first S goes before the
-// last PV of the item before, and pairs take every pairs-th item instead of
-// asking (an answer takes 2 us, a short item 3).  Taken where the bound on new rows
-// is 128 and below (30 prompts of 8 to 23 tokens 70 us, 79 without; 32 of 128 96,
-// 102 without; one of 100 10.5, 12.4; 32 of 33 to 100 behind up to 1,000 255, 247
-// without: HBM).  The MMAs read 128 rows all the same: what follows the queries,
-// whose products are nobody's.
+// kFew: items of 128 rows at most, 64 each CTA's, and M = 128: half the tensor work
+// of a tile, and a row's S and O in two lanes and half the columns, so that two O
+// and two S fit TMEM beside each other and an item's results are read out under the
+// next one's products.  What a short item waits for is latency, so its parts overlap those of
+// its neighbours: queries in two buffers, items published eight ahead, four softmax
+// warps an item in turn.  P goes through shared memory (as A in TMEM it would
+// need its rows once in each half of the lanes).  Pairs take every pairs-th item instead of asking
+// (an answer takes 2 us, a short item 1.4).  Taken where the bound on new rows is 128 and below (28
+// prompts of 20 to 49 tokens 41 us, 76 without; 32 of 32 45, 84 without; 8 of 8 behind
+// 445 31, 38 without; 32 of 128 96, 101 without; one of 100 10.3, 12.4; 32 of 33 to 100 behind up
+// to 1,000 227, 242 without: HBM).
 template <bool kFew>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prompt_mla_kernel(const Args a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_pe) {
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_pe,
+                      const __grid_constant__ CUtensorMap tm_q16, const __grid_constant__ CUtensorMap tm_kv16,
+                      const __grid_constant__ CUtensorMap tm_pe16) {
     constexpr int R = kFew ? kFewRows : kMmaRows, kMine = R / 2;     // rows of an item, and of a CTA
     constexpr int kQRows = kMine * 128;                              // bytes of a chunk of them
-    constexpr int kQBufs = kFew ? 2 : 1;
+    constexpr int kQBufs = kFew ? 2 : 1, kOBufs = kFew ? 2 : 1;
+    // items published ahead: of short ones the warps that write results are two
+    // behind the loads (32 prompts of 32 tokens 61 us with two, 46 with eight);
+    // a pair that asks for its items takes none too early
+    constexpr int kSlots = kFew ? kMaxSlots : 2;
+    // columns of an S and of an O: with M = 128 a row's are in two lanes
+    constexpr uint32_t kSCols = kFew ? kTile / 2 : kTile, kOCols = kFew ? kHeadV / 2 : kHeadV;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem& S = *reinterpret_cast<Smem*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -206,13 +220,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&S.sfull[i]), 1);
-            mbar_init(smem_u32(&S.pfull[i]), 2 * kSoftWarps);
+            mbar_init(smem_u32(&S.pfull[i]), 2 * kSoftWarps / kOBufs);
+            mbar_init(smem_u32(&S.pvdone[i]), 1);
         }
-        mbar_init(smem_u32(&S.pvdone), 1);
-        mbar_init(smem_u32(&S.odone), 1);
-        mbar_init(smem_u32(&S.lfull), kSoftWarps / 2);
-        mbar_init(smem_u32(&S.invfree), kOutWarps);
-        mbar_init(smem_u32(&S.ofree), 2 * kOutWarps);
+        for (int i = 0; i < kOBufs; ++i) {
+            mbar_init(smem_u32(&S.lfull[i]), kSoftWarps / (kFew ? 4 : 2));
+            mbar_init(smem_u32(&S.invfree[i]), kOutWarps);
+            mbar_init(smem_u32(&S.odone[i]), 1);
+            mbar_init(smem_u32(&S.ofree[i]), 2 * kOutWarps);
+        }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_u32(&S.itemfull[i]), 1);
             mbar_init(smem_u32(&S.itemempty[i]), kSoftWarps + kOutWarps + (rank == 0 ? 3 : 2));   // the warps that read items
@@ -227,6 +243,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
         prefetch_tmap(&tm_pe);
+        prefetch_tmap(&tm_q16);
+        prefetch_tmap(&tm_kv16);
+        prefetch_tmap(&tm_pe16);
     }
     __syncwarp();
     cluster_arrive();                            // the peer may use this CTA's barriers and TMEM ..
@@ -269,39 +288,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // K or V loads: lane 0 waits, then each lane issues a box.  Before an
         // item's V its Q, a chunk as soon as the last S of the item before (kFew:
         // of the one before that) is through with it: not before its K, which
-        // need not wait for that.  Rows behind the last new row are another
-        // sequence's or zeros: nobody reads what comes of them.
+        // need not wait for that.  kFew: a tile that the item's keys do not fill
+        // comes in boxes of 16 rows, and so do fewer than a CTA's 64 queries, since
+        // the rest of a sequence's room would be read from HBM for nothing (16
+        // prompts of 16 tokens behind 48 37 -> 31 us; in long items it is not
+        // worth the code).  What then lies in the other rows is masked or not multiplied, or
+        // becomes nobody's lanes.
         const bool k = warp == 0;
         uint64_t* const full = k ? S.kfull : S.vfull;
         uint64_t* const empty = k ? S.kempty : S.vempty;
         // K: the head's three chunks, and by lane 1 the shared one; V: two
         const int boxes = k ? 2 : 1;
         const bool pe = k && lane == 1;
-        const uint32_t bytes = k ? kQChunks * kKBytes : 2 * kQBytes;
-        const uint32_t to = smem_u32(k ? S.k : S.v) + (pe ? (kQChunks - 1) * kKBytes : 0);
+        constexpr uint32_t kBytes = kQChunks * kKBytes;          // of a stage of K, and of V
+        static_assert(kBytes == 2 * kQBytes, "");
+        const uint32_t stages = smem_u32(k ? S.k : S.v), to = stages + (pe ? (kQChunks - 1) * kKBytes : 0);
         const int32_t chunk = k ? 0 : kNope / 64 + 2 * (int)rank, row = k ? 64 * (int)rank : 0;
+        // boxes of 16 rows: the lane's chunk and place in it
+        const int wide = k ? 4 : 8, c16 = lane / wide, r16 = 16 * (lane % wide);
+        const uint32_t to16 = stages + c16 * (k ? kKBytes : kQBytes) + r16 * 128;
+        const bool pe16 = k && c16 == kQChunks - 1;
         uint32_t g = 0, seg = 0;
         for (; next_item(it); ++seg) {
-            if (!k) {
-                // the barriers of chunk q, or (kFew) of buffer seg % 2
+            if (!k && kFew) {
+                const uint32_t b = seg % kQBufs, use = seg / kQBufs, bar = lead(S.qfull[b]);
+                const int n16 = (min(kMine, max(0, it.rows - kMine * (int)rank)) + 15) / 16;
+                if (lane == 0 && (use == 0 || wait(S.qempty[b], (use - 1) & 1)))
+                    mbar_arrive_expect_tx_pair(bar, n16 * kQChunks * 16 * 128);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                const uint32_t at = smem_u32(S.q + b * kQChunks * kQRows);
+                const int32_t col = it.head * kHeadQK, first = it.row + kMine * (int)rank;
+                if (ok && n16 == kMine / 16 && lane < kQChunks)
+                    tma_load_2d_pair(at + lane * kQRows, &tm_q, bar, col + 64 * lane, first);
+                if (ok && n16 < kMine / 16 && lane < 4 * kQChunks && (lane & 3) < n16)
+                    tma_load_2d_pair(at + (lane >> 2) * kQRows + (lane & 3) * 2048, &tm_q16, bar, col + 64 * (lane >> 2),
+                                     first + 16 * (lane & 3));
+            }
+            if (!k && !kFew) {
                 for (int q = 0; ok && q < kQChunks; ++q) {
-                    const uint32_t b = kFew ? seg % kQBufs : q, use = seg / kQBufs;
-                    if (lane == 0 && (use == 0 || (kFew && q > 0) || wait(S.qempty[b], (use - 1) & 1))) {
-                        if (!kFew || q == 0) mbar_arrive_expect_tx_pair(lead(S.qfull[b]), kFew ? kQChunks * kQRows : kQRows);
-                        tma_load_2d_pair(smem_u32(S.q + (kFew ? b * kQChunks + q : q) * kQRows), &tm_q, lead(S.qfull[b]),
-                                         it.head * kHeadQK + 64 * q, it.row + kMine * (int)rank);
+                    if (lane == 0 && (seg == 0 || wait(S.qempty[q], (seg - 1) & 1))) {
+                        mbar_arrive_expect_tx_pair(lead(S.qfull[q]), kQRows);
+                        tma_load_2d_pair(smem_u32(S.q + q * kQRows), &tm_q, lead(S.qfull[q]), it.head * kHeadQK + 64 * q,
+                                         it.row + kMine * (int)rank);
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                 }
             }
             for (int32_t t = 0; ok && t < it.tiles; ++t, ++g) {
                 const uint32_t st = g % kStages, bar = lead(full[st]);
+                // 16s of the item's keys here
+                const int n16 = kFew ? min(wide, (max(0, it.pos + it.rows - t * kTile - row) + 15) / 16) : wide;
                 if (lane == 0 && (g < kStages || wait(empty[st], (g / kStages - 1) & 1)))
-                    mbar_arrive_expect_tx_pair(bar, bytes);
+                    mbar_arrive_expect_tx_pair(bar, n16 * (kBytes / wide));
                 ok = __shfl_sync(0xffffffffu, ok, 0);
-                const int32_t r = it.at + t * kTile + row;
-                if (ok && pe) tma_load_2d_pair(to + st * bytes, &tm_pe, bar, 0, r);
-                else if (ok && lane < boxes) tma_load_3d_pair(to + st * bytes, k ? &tm_k : &tm_v, bar, 0, r, it.head * (kExpRow / 64) + chunk);
+                const int32_t r = it.at + t * kTile + row, c = it.head * (kExpRow / 64) + chunk;
+                if (ok && n16 == wide) {
+                    if (pe) tma_load_2d_pair(to + st * kBytes, &tm_pe, bar, 0, r);
+                    else if (lane < boxes) tma_load_3d_pair(to + st * kBytes, k ? &tm_k : &tm_v, bar, 0, r, c);
+                } else if (ok && lane < 16 && r16 < 16 * n16) {
+                    if (pe16) tma_load_2d_pair(to16 + st * kBytes, &tm_pe16, bar, 0, r + r16);
+                    else tma_load_3d_pair(to16 + st * kBytes, &tm_kv16, bar, 0, r + r16, c + c16);
+                }
             }
         }
     } else if (warp == 1) {
@@ -312,10 +359,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // items, and the next item is read behind the last S of one: what is
             // met once an item is fetched as it goes (15 cycles an instruction),
             // and nothing else runs meanwhile.
-            constexpr uint32_t kIdS = idesc_bf16_f32(kMmaRows, kTile);
-            constexpr uint32_t kIdO = idesc_bf16_f32(kMmaRows, kHeadV, false, true);
+            constexpr uint32_t kIdS = idesc_bf16_f32(R, kTile);
+            constexpr uint32_t kIdO = idesc_bf16_f32(R, kHeadV, false, true);
             const uint64_t dq = sdesc_sw128(smem_u32(S.q), 0, 1024), dk = sdesc_sw128(smem_u32(S.k), 0, 1024);
-            const uint64_t dv = sdesc_sw128(smem_u32(S.v), kQBytes, 1024);
+            const uint64_t dv = sdesc_sw128(smem_u32(S.v), kQBytes, 1024), dp = sdesc_sw128(smem_u32(S.out), 0, 1024);
             int32_t tiles = 0, keys = 0;         // of item `seg`
             uint32_t seg = 0, n = 0;             // n: tiles whose S is issued
             auto read = [&]() {
@@ -352,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const uint64_t da = dq + ((kFew ? seg % kQBufs * kQChunks + c : c) * kQRows >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_bf16_ss_pair(tmem + kSCol + kTile * buf, da + 2 * k,
+                            mma_bf16_ss_pair(tmem + kSCol + kSCols * buf, da + 2 * k,
                                              dk + (st * kQChunks + c) * (kKBytes >> 4) + 2 * k, kIdS, (c | k) != 0);
                         if (!kFew && last) mma_commit_pair(smem_u32(&S.qempty[c]));
                     }
@@ -366,17 +413,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (pending) {
                     const uint32_t st = m % kStages;
-                    if (m_first && m_seg > 0 && !wait(S.ofree, (m_seg - 1) & 1)) break;
+                    const uint32_t ob = m_seg % kOBufs, use = m_seg / kOBufs;
+                    if (m_first && use > 0 && !wait(S.ofree[ob], (use - 1) & 1)) break;
                     if (!wait(S.vfull[st], (m / kStages) & 1)) break;
                     if (!wait(S.pfull[m & 1], (m >> 1) & 1)) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int k = 0; k < steps; ++k)
-                        mma_bf16_ts_pair(tmem + kOCol, tmem + kSCol + kTile * (m & 1) + 64 * (k >> 2) + 8 * (k & 3),
-                                         dv + st * (2 * kQBytes >> 4) + 128 * k, kIdO, !m_first || k != 0);
+                    for (int k = 0; k < steps; ++k) {
+                        const uint64_t db = dv + st * (2 * kQBytes >> 4) + 128 * k;
+                        if (kFew)
+                            mma_bf16_ss_pair(tmem + kOCol + kOCols * ob, dp + (k >> 2) * (kQRows >> 4) + 2 * (k & 3), db, kIdO,
+                                             !m_first || k != 0);
+                        else
+                            mma_bf16_ts_pair(tmem + kOCol, tmem + kSCol + kSCols * (m & 1) + 64 * (k >> 2) + 8 * (k & 3), db,
+                                             kIdO, !m_first || k != 0);
+                    }
                     mma_commit_pair(smem_u32(&S.vempty[st]));
-                    mma_commit_pair(smem_u32(&S.pvdone));
-                    if (m_last) mma_commit_pair(smem_u32(&S.odone));
+                    mma_commit_pair(smem_u32(&S.pvdone[m % kOBufs]));
+                    if (m_last) mma_commit_pair(smem_u32(&S.odone[ob]));
                 }
                 if (s_now && last) {
                     t = 0;
@@ -430,10 +484,116 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mbar_arrive(smem_u32(&S.itemfull[slot]));
             }
             __syncwarp();
-            if (it.tiles > 0 && lane < kQChunks)
+            if (kFew) {
+                if (lane < 4 * kQChunks && kMine * (int)rank + 16 * (lane & 3) < it.rows)
+                    tma_prefetch_2d(&tm_q16, it.head * kHeadQK + 64 * (lane >> 2), it.row + kMine * (int)rank + 16 * (lane & 3));
+            } else if (it.tiles > 0 && lane < kQChunks) {
                 tma_prefetch_2d(&tm_q, it.head * kHeadQK + 64 * lane, it.row + kMine * (int)rank);
+            }
             __syncwarp();
             if (it.tiles == 0) break;
+        }
+    } else if (kFew && warp < 4 + kSoftWarps) {
+        // softmax: four warps an item, in turn, so that an item's end and the next
+        // one's first tile go on side by side.  TMEM lanes x and 64 + x have row
+        // x's first and last 64 positions.
+        const int mine = (tid - 128) >> 7, ln = tid & 127, x = ln & 63, half = ln >> 6;
+        const uint32_t tl = tmem + ((uint32_t)(ln & 96) << 16);
+        float* const xch = S.xch[mine];
+        uint32_t g = 0, seg = 0, xb = 0;
+        auto exchange = [&](float v) -> float {
+            xb ^= 128;
+            xch[xb + ln] = v;
+            named_bar_sync(1 + mine, 128);
+            return xch[xb + (ln ^ 64)];
+        };
+        for (; !named_bar_or(1 + mine, 128, !next_item(it)); ++seg) {
+            if ((int)(seg & 1) != mine) {
+                // (a barrier's parity tells only two tiles apart)
+                for (int32_t t = 0; t < it.tiles; ++t, ++g) wait(S.sfull[g & 1], (g >> 1) & 1);
+                continue;
+            }
+            const int32_t first = it.pos + kMine * (int)rank;    // position of the CTA's first row
+            const int32_t live = min(kMine, it.rows - kMine * (int)rank);
+            const bool idle = (x & ~31) >= live;                 // such a warp keeps in step with the others
+            float m = -INFINITY, l = 0.f;
+            for (int32_t t = 0; t < it.tiles; ++t, ++g) {
+                const uint32_t buf = g & 1;
+                wait(S.sfull[buf], (g >> 1) & 1);
+                __syncwarp();
+                tc_fence_after();
+                if (idle) {
+                    // (what P holds there becomes nobody's lanes of O)
+                    exchange(0.f);
+                    if (lane == 0) mbar_arrive_pair(lead(S.pfull[buf]));
+                    continue;
+                }
+                uint32_t r[2][32];
+                tmem_ld_32x32b_x32(tl + kSCol + kSCols * buf, r[0]);
+                tmem_ld_32x32b_x32(tl + kSCol + kSCols * buf + 32, r[1]);
+                tmem_ld_wait();
+                if ((t + 1) * kTile - 1 > first) {
+                    const int32_t d = first + x - (t * kTile + 64 * half);       // the last column that the row sees
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        if (k > d) r[k >> 5][k & 31] = 0xFF800000u;
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 64; ++k) mx = fmaxf(mx, __uint_as_float(r[k >> 5][k & 31]));
+                mx = fmaxf(mx, exchange(mx)) * a.scale_log2;
+                const bool move = mx > m + kRescale || (m == -INFINITY && mx > m);
+                const float m_new = move ? mx : m;
+                const float f = move ? ex2_approx(m - m_new) : 1.f;
+                const float off = m_new == -INFINITY ? 0.f : m_new;
+                m = m_new;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t pk[32];
+#pragma unroll
+                for (int k = 0; k < 64; k += 2) {
+                    const float p0 = ex2_approx(fmaf(__uint_as_float(r[k >> 5][k & 31]), a.scale_log2, -off));
+                    const float p1 = ex2_approx(fmaf(__uint_as_float(r[k >> 5][(k & 31) + 1]), a.scale_log2, -off));
+                    sum[(k >> 1) & 3] += p0 + p1;
+                    pk[k >> 1] = pack_bf16x2(p0, p1);
+                }
+                l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                // P is read, O at rest (PV of tile g - 2 is done: S of tile g was issued behind it)
+                if (g > 0) wait(S.pvdone[(g - 1) & 1], ((g - 1) >> 1) & 1);
+                __syncwarp();
+                tc_fence_after();
+                if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                    const uint32_t at = tl + kOCol + kOCols * (seg % kOBufs);
+#pragma unroll 1
+                    for (uint32_t c = 0; c < kOCols; c += 16) {
+                        uint32_t v[16];
+                        tmem_ld_32x32b_x16(at + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                        tmem_st_32x32b_x16(at + c, v);
+                    }
+                    tmem_st_wait();
+                }
+                uint8_t* const to = S.out + half * kQRows + x * 128;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<uint4*>(to + ((k ^ (x & 7)) << 4)) =
+                        make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(lead(S.pfull[buf]));
+            }
+            // Every row sees itself, so l > 0 but where every score is -inf: NaN, as of the formula.
+            l += exchange(l);
+            if (half == 0) {
+                if (seg > 1) wait(S.invfree[mine], ((seg >> 1) - 1) & 1);
+                S.inv[kMine * mine + x] = rcp_approx(l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&S.lfull[mine]));
+                if (a.lse && x < live)
+                    a.lse[(int64_t)(it.row + kMine * (int)rank + x) * kH + it.head] = (m + lg2_approx(l)) * kLn2;
+            }
         }
     } else if (warp < 4 + kSoftWarps) {
         // softmax: TMEM lane = query row of this CTA
@@ -493,7 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
                 if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-                    wait(S.pvdone, (g - 1) & 1);
+                    wait(S.pvdone[0], (g - 1) & 1);
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
@@ -516,13 +676,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // Every row sees itself, so l > 0 but where every score is -inf: NaN, as of the formula.
             l += exchange(l);
             if (half == 0) {
-                if (seg > 0) wait(S.invfree, (seg - 1) & 1);
+                if (seg > 0) wait(S.invfree[0], (seg - 1) & 1);
                 S.inv[x] = rcp_approx(l);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&S.lfull));
+                if (lane == 0) mbar_arrive(smem_u32(&S.lfull[0]));
                 if (a.lse && x < live)
                     a.lse[(int64_t)(it.row + kMine * (int)rank + x) * kH + it.head] = (m + lg2_approx(l)) * kLn2;
             }
+            ++seg;
+        }
+    } else if (kFew) {
+        // results: TMEM lanes x and 64 + x have row x's first and last 128 columns
+        const int r0 = 32 * (warp & 1), half = (warp >> 1) & 1;
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const bool odd = lane & 1;
+        uint32_t seg = 0;
+        while (next_item(it)) {
+            const uint32_t ob = seg % kOBufs;
+            wait(S.lfull[ob], (seg / kOBufs) & 1);
+            wait(S.odone[ob], (seg / kOBufs) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            const float inv = S.inv[kMine * ob + r0 + lane];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.invfree[ob]));
+            const int32_t mine = it.row + kMine * (int)rank + r0, live = min(kMine, it.rows - kMine * (int)rank) - r0;
+            if (ok && live > 0) {
+                // two lanes write their two rows in turn, 32 bytes of a row at a time
+                const int32_t even = lane & ~1;
+                uint16_t* const to = a.out + ((int64_t)(mine + even) * kH + it.head) * kHeadV + 128 * half + (odd ? 8 : 0);
+#pragma unroll 1
+                for (uint32_t c = 0; c < kOCols; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(tl + kOCol + kOCols * ob + c, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        uint32_t w[8], in[4];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            w[k] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * k]) * inv,
+                                               __uint_as_float(o[16 * v + 2 * k + 1]) * inv);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) in[k] = __shfl_xor_sync(0xffffffffu, odd ? w[k] : w[4 + k], 1);
+                        if (even < live)
+                            *reinterpret_cast<uint4*>(to + c + 16 * v) =
+                                odd ? make_uint4(in[0], in[1], in[2], in[3]) : make_uint4(w[0], w[1], w[2], w[3]);
+                        if (even + 1 < live)
+                            *reinterpret_cast<uint4*>(to + (int64_t)kH * kHeadV + c + 16 * v) =
+                                odd ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(in[0], in[1], in[2], in[3]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(lead(S.ofree[ob]));
             ++seg;
         }
     } else {
@@ -533,13 +741,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint8_t* const stage = S.out + (warp & 3) * 4096;
         uint32_t seg = 0;
         while (next_item(it)) {
-            wait(S.lfull, seg & 1);
-            wait(S.odone, seg & 1);
+            wait(S.lfull[0], seg & 1);
+            wait(S.odone[0], seg & 1);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
             const float inv = S.inv[r0 + lane];
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&S.invfree));
+            if (lane == 0) mbar_arrive(smem_u32(&S.invfree[0]));
             const int32_t mine = it.row + kMine * (int)rank + r0, live = min(kMine, it.rows - kMine * (int)rank) - r0;
             if (ok && live > 0) {
                 uint16_t* const to = a.out + ((int64_t)mine * kH + it.head) * kHeadV + 8 * (lane & 7);
@@ -573,7 +781,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive_pair(lead(S.ofree));
+                mbar_arrive_pair(lead(S.ofree[0]));
             }
             ++seg;
         }
@@ -656,11 +864,14 @@ cudaError_t launch(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, 
     a.lse = lse;
     a.next = reinterpret_cast<uint32_t*>(status) + kCounterWord;
     a.status = status;
-    CUtensorMap tm_q, tm_k, tm_v, tm_pe;
+    CUtensorMap tm_q, tm_k, tm_v, tm_pe, tm_q16, tm_kv16, tm_pe16;
     if (!make_tmap_bf16_2d(&tm_q, q, (uint64_t)kH * kHeadQK, (uint64_t)bd.total_q, 64, R / 2) ||
         !make_tmap_bf16_chunks(&tm_k, x.kv, (uint64_t)kH * kExpRow / 64, (uint64_t)x.rows, 64, kNope / 64) ||
         !make_tmap_bf16_chunks(&tm_v, x.kv, (uint64_t)kH * kExpRow / 64, (uint64_t)x.rows, kTile, 2) ||
-        !make_tmap_bf16_2d(&tm_pe, x.k_pe, DSA_ROPE_DIM, (uint64_t)x.rows, 64, 64))
+        !make_tmap_bf16_2d(&tm_pe, x.k_pe, DSA_ROPE_DIM, (uint64_t)x.rows, 64, 64) ||
+        !make_tmap_bf16_2d(&tm_q16, q, (uint64_t)kH * kHeadQK, (uint64_t)bd.total_q, 64, 16) ||
+        !make_tmap_bf16_chunks(&tm_kv16, x.kv, (uint64_t)kH * kExpRow / 64, (uint64_t)x.rows, 16, 1) ||
+        !make_tmap_bf16_2d(&tm_pe16, x.k_pe, DSA_ROPE_DIM, (uint64_t)x.rows, 64, 16))
         return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -683,7 +894,7 @@ cudaError_t launch(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, 
     cfg.gridDim = dim3(2 * (unsigned)pairs);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(Smem);
-    e = cudaLaunchKernelEx(&cfg, kernel, a, tm_q, tm_k, tm_v, tm_pe);
+    e = cudaLaunchKernelEx(&cfg, kernel, a, tm_q, tm_k, tm_v, tm_pe, tm_q16, tm_kv16, tm_pe16);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }

@@ -2,8 +2,8 @@
 // rows over short contexts (a few tokens appended to each of many short
 // sequences), on the FMA pipes.
 //
-// There the tensor kernel's time is an item's way through its pipeline, 2.7 us for
-// each 76 of the 64 heads x sequences, whatever the rows are.  Here a warp takes a
+// There the tensor kernel's time is an item's way through its pipeline, 1.4 us for
+// each 76 of the 64 heads x sequences, whatever the rows are, and 9 us for the first.  Here a warp takes a
 // head and four new rows of a sequence: a lane holds 8 of a key's 256 columns
 // (512 bytes a key, one load), and 8 of the value's; four keys at a time are
 // loaded, their 16 dot products summed over the warp, and folded into the four
@@ -11,9 +11,9 @@
 // rounding of the result.  Some 30 instructions a (row, key) pair and warp, and
 // keys in turn: taken while the bounds leave at most 64 keys and 512 pairs (rows x
 // length) a sequence.  There it is the faster one (32 sequences of 1 to 4 new
-// rows behind 2 70 -> 8 us, 25 x 8 behind 5 59 -> 16, 15 x 20 40 -> 19; one of 7 10 ->
-// 4); beyond, at 1,024 pairs, it no longer is (32 x 32 76 -> 72, 16 x 16 behind 48
-// 43 -> 55, 32 x 1 behind 1,000 309 -> 513).
+// rows behind 2 38 -> 8 us, 25 x 8 behind 5 33 -> 16, 15 x 20 25 -> 19; one of 7 10 ->
+// 6); beyond, at 1,024 pairs, it is not (32 x 32 45 -> 72, 16 x 16 behind 48 27 ->
+// 55, 32 x 1 behind 1,000 288 -> 513).
 #include "internal.h"
 #include "prompt.h"
 #include "ptx.cuh"

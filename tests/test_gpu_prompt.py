@@ -212,6 +212,48 @@ def test_moving_maxima():
         assert ((lse[at][:, [0, 5, 63]].cpu().double() - z).abs() <= e + 16 * F32 * (1 + z.abs())).all()
 
 
+def test_many_items_of_few_rows():
+    """More items than CTA pairs, of one to many tiles in turn, and rows at the ends of what a CTA and a warp hold."""
+    c = [0, 900, 0, 64, 300, 0, 127, 40, 1500, 2, 250, 0, 129, 88]
+    m = [64, 1, 65, 33, 97, 128, 1, 32, 31, 127, 96, 2, 63, 40]
+    P = Prompts(c, m, seed=21, gap=128, pad=9, max_q=128)
+    x = P.filled()
+    q = P.normal(P.T + 9, H, D_HEAD).cuda()
+    out = torch.full((P.T + 9, H, D_HEAD), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((P.T + 9, H), 9.0, device="cuda")
+    dsa.prompt_mla_fwd(P.batch, q, x, SCALE, out, lse, ws=P.ws)
+    assert dsa.read_device_status(P.ws) == 0
+    check_attention(P, q, x, out, lse, heads=[0, 1, 29, 62, 63])
+    assert (out[P.T:] == 9.0).all() and (lse[P.T:] == 9.0).all()
+    for _ in range(20):                      # whatever order the pairs' parts come in
+        again = torch.zeros_like(out)
+        dsa.prompt_mla_fwd(P.batch, q, x, SCALE, again, None, ws=P.ws)
+        assert torch.equal(out[:P.T], again[:P.T])
+
+
+def test_moving_maxima_of_few_rows():
+    """test_moving_maxima for at most 128 new rows."""
+    P = Prompts([800, 803], [100, 97], seed=22, max_q=128)
+    x = P.filled()
+    q = P.normal(P.T, H, D_HEAD).cuda()
+    ramp = torch.linspace(0, 3, 900, device="cuda")
+    for b, r in ((0, ramp), (1, ramp.flip(0))):
+        lo = int(P.at[b])
+        x.k_pe[lo:lo + 900] = (r[:, None] * torch.ones(D_ROPE, device="cuda")).bfloat16()
+    q[..., 192:] = 4.0
+    out = torch.empty((P.T, H, D_HEAD), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((P.T, H), device="cuda")
+    dsa.prompt_mla_fwd(P.batch, q, x, SCALE, out, lse, ws=P.ws)
+    assert dsa.read_device_status(P.ws) == 0
+    for b in range(2):
+        ref, z, big = attention_ref(P, q, x, b, [0, 5, 63])
+        at = slice(int(P.off[b]), int(P.off[b + 1]))
+        e = 256 * F32 * 58                   # as there: the same scores
+        got, tol = out[at][:, [0, 5, 63]].cpu().double(), HALF * ref.abs() + (HALF * (1 + HALF) + 2 * e + 64 * F32) * big
+        assert ((got - ref).abs() <= tol).all()
+        assert ((lse[at][:, [0, 5, 63]].cpu().double() - z).abs() <= e + 16 * F32 * (1 + z.abs())).all()
+
+
 def test_masked_rows_do_not_leak_in_few_rows():
     """The same for the kernel of few rows over short contexts."""
     P = Prompts([5, 0, 0], [20, 9, 1], seed=16, gap=128, max_q=20, max_ctx=25)
@@ -236,6 +278,32 @@ def test_masked_rows_do_not_leak_in_few_rows():
     assert torch.equal(out[keep], out2[keep]) and torch.equal(lse[keep], lse2[keep])
     heads = torch.arange(H, device="cuda") != 9
     assert torch.equal(out[3][heads], out2[3][heads]) and out2[3, 9].isnan().all()
+
+
+def test_masked_rows_do_not_leak_in_short_items():
+    """The same for items of at most 128 rows on the tensor cores, among others."""
+    m = [20, 9, 1, 128, 70, 3] * 3
+    P = Prompts([105, 0, 300] * 6, m, seed=23, gap=128, max_q=128)
+    x = P.filled()
+    q = P.normal(P.T, H, D_HEAD).cuda()
+    out, out2 = (torch.empty((P.T, H, D_HEAD), dtype=torch.bfloat16, device="cuda") for _ in (0, 1))
+    lse, lse2 = (torch.empty((P.T, H), device="cuda") for _ in (0, 1))
+    dsa.prompt_mla_fwd(P.batch, q, x, SCALE, out, lse, ws=P.ws)
+    x.k_pe[int(P.at[0]) + 112] = float("nan")            # new row 7 of sequence 0 and later see it
+    x.kv[int(P.at[3]) + 200, 4, 192:] = torch.finfo(torch.bfloat16).max    # row 95 of sequence 3 and later
+    x.k_pe[int(P.at[4]) + 69] = float("inf")             # sequence 4's last row
+    q[int(P.off[6]) + 3, 9] = float("-inf")
+    dsa.prompt_mla_fwd(P.batch, q, x, SCALE, out2, lse2, ws=P.ws)
+    assert dsa.read_device_status(P.ws) == 0
+    hurt = torch.zeros(P.T, H, dtype=torch.bool)
+    hurt[7:20] = True
+    hurt[int(P.off[5]) - 1] = True
+    hurt[int(P.off[6]) + 3, 9] = True
+    hurt = hurt.cuda()
+    assert out2[hurt].isnan().all()
+    moved = hurt.clone()
+    moved[int(P.off[3]) + 95:int(P.off[4]), 4] = True
+    assert torch.equal(out[~moved], out2[~moved]) and torch.equal(lse[~hurt], lse2[~hurt])
 
 
 def test_masked_rows_do_not_leak():
