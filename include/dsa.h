@@ -636,7 +636,8 @@ DSA_API dsa_status dsa_prefix_workspace_size(const dsa_batch* batch, const dsa_g
  *   mask  as there, or NULL: each new row sees itself and those before it
  * Groups that are not the whole batch in order, or a shared length that is
  * negative or beyond a sequence's committed rows, latch DSA_ERR_BAD_BATCH, and every sequence
- * (of the group with that length) is computed by itself.  Three launches. */
+ * (of the group with that length) is computed by itself.  Two launches, three
+ * for more than 32 sequences. */
 DSA_API dsa_status dsa_prefix_mla_fwd(const dsa_batch* batch, const dsa_groups* groups, const dsa_pages* pages,
                                       const uint16_t* q, const uint16_t* kv, const uint64_t* mask, float sm_scale,
                                       uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);

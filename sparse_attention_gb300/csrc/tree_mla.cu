@@ -52,8 +52,7 @@
 // across its sequences, so an item walks the shared tiles once and then the own
 // ones of its one or two sequences.  (Shared and own parts as items of their
 // own, all joined in fp32: 242 instead of 180 us for 61 sequences of up to 15
-// rows behind 3,774, and 263 KB of workspace a row and sequence; small calls 0-10 %
-// faster.)  Cut, joined and merged as above.
+// rows behind 3,774, and 263 KB of workspace a row and sequence.)  Cut, joined and merged as above.
 //
 // Bounds.  A row pair's tile is 36 MMAs of N = 128 (37 cycles each) and 16 of
 // N = 256 (65): 2,372 cycles for 35.7 MFLOP, 92 % of the tensor rate; a single
@@ -187,7 +186,9 @@ struct Args {
     bool ahead;          // a sequence's rows are read by one pair only
     // behind shared prefixes only
     const RunPlan* rplan;
-    const Run* runs;
+    const Run* runs;     // null: each pair's walker plans by itself (LocalRuns)
+    GroupsDev groups;
+    int32_t least_shared;
     int32_t runs_total;
     int2* cut_rows;      // [total_q] or null: of a row of a cut item, 2 * (first pair + 1) + which of its rows, last pair
 };
@@ -286,6 +287,91 @@ struct SegIter {
     }
 };
 
+__device__ int least_chunk(int tiles);
+
+// prefix_plan_kernel's runs of at most 32 sequences and groups, by a warp: lane b
+// holds sequence b's.
+struct LocalRuns {
+    int32_t q0 = 0, nq = 0, ctx = 0, base = 0, lead = 0, skip = 0, inner = 0, tail = 0, b2 = 0, len2 = 0, n2 = 0, lone = 0;
+    int64_t u = 0, ut = 0;       // units before the first and the second run
+    bool good = false;
+
+    __device__ RunPlan make(const Args& a, int pairs) {
+        constexpr uint32_t kAll = 0xffffffffu;
+        const int lane = (int)lane_id(), G = a.groups.n;
+        const bool seq = lane < a.bd.B, grp = lane < G;
+        SeqInfo s{0, 0, 0};
+        const int32_t off0 = grp ? __ldg(a.groups.off + lane) : 0, off1 = grp ? __ldg(a.groups.off + lane + 1) : 0;
+        const int32_t shared = grp ? __ldg(a.groups.shared + lane) : 0;
+        good = seq && load_seq(a.bd, lane, a.status, s);
+        q0 = s.q0, nq = s.nq, ctx = s.ctx;
+        const bool broken = __any_sync(kAll, seq && !good);
+        const bool wrong = __any_sync(kAll, grp && (off0 < 0 || off0 > off1 || off1 > a.bd.B || (lane == 0 && off0 != 0) ||
+                                                    (lane == G - 1 && off1 != a.bd.B) || shared < 0));
+        int g = 0;
+        for (int k = 1; k < G; ++k) g += __shfl_sync(kAll, off0, k) <= lane ? 1 : 0;
+        const int32_t rows = __shfl_sync(kAll, shared, g);
+        const bool bad = seq && !wrong && !(good && (nq == 0 || rows <= ctx - nq));
+        if (bad || (wrong && lane == 0)) latch_status(a.status, DSA_ERR_BAD_BATCH);
+        const uint32_t peers = __match_any_sync(kAll, seq ? g : 32 + lane), wrongs = __ballot_sync(kAll, bad);
+        const uint32_t live = __ballot_sync(kAll, good && nq > 0) & peers, after = live & ~((2u << lane) - 1u);
+        base = wrong || (wrongs & peers) ? 0 : rows / kTile;
+        lead = live ? __ffs(live) - 1 : 0;
+        const int32_t first = __shfl_sync(kAll, q0, __ffs(peers) - 1), end = __shfl_sync(kAll, q0 + nq, 31 - __clz(peers));
+        const bool mixed = !broken && !wrong && base >= a.least_shared;
+        const int32_t row1 = mixed ? end : q0 + nq;
+        skip = mixed ? (q0 - first) & 1 : 0;
+        lone = mixed && end - first <= 2;
+        inner = good && nq > 0 ? (nq - skip) >> 1 : 0;
+        tail = good && nq > 0 ? (nq - skip) & 1 : 0;
+        b2 = after ? __ffs(after) - 1 : 0;
+        len2 = __shfl_sync(kAll, ctx, b2);
+        n2 = __shfl_sync(kAll, nq, b2);
+        if (!tail || q0 + nq >= row1) n2 = 0;
+        const Run x = run(false), y = run(true);
+        const int64_t cost = (int64_t)inner * (x.tiles() + kItemCost), both = cost + (int64_t)tail * (y.tiles() + kItemCost);
+        const int32_t longest =
+            __reduce_max_sync(kAll, max(inner ? x.tiles() : 0, tail ? y.tiles() : 0));
+        int64_t sum = both;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(kAll, sum, o);
+            if (lane >= o) sum += v;
+        }
+        u = sum - both;
+        ut = u + cost;
+        const int64_t all = __shfl_sync(kAll, sum, 31), even = (all + pairs - 1) / pairs;
+        return RunPlan{all, max(even, (int64_t)least_chunk(longest))};
+    }
+    // this lane's first or second run
+    __device__ Run run(bool second) const {
+        Run r{};
+        r.row = second ? q0 + nq - 1 : q0 + skip;
+        r.items = second ? tail : inner;
+        r.lead = lead;
+        r.base = base;
+        r.b = (int32_t)lane_id();
+        r.len = ctx;
+        r.n = nq;
+        r.i0 = second ? nq - 1 : skip;
+        r.b2 = b2;
+        r.len2 = len2;
+        r.n2 = second ? n2 : 0;
+        r.rows = second && n2 == 0 ? 1 : 2;
+        r.lone = lone;
+        r.u = second ? ut : u;
+        return r;
+    }
+    // run i, to all lanes
+    __device__ Run fetch(int32_t i) const {
+        Run r = run(i & 1);
+        int32_t* const w = reinterpret_cast<int32_t*>(&r);
+#pragma unroll
+        for (int k = 0; k < (int)(sizeof(Run) / 4); ++k) w[k] = __shfl_sync(0xffffffffu, w[k], i >> 1);
+        return r;
+    }
+};
+
 // The same over runs, by one warp: a pair has an equal share of their units.
 struct RunIter {
     const Args& a;
@@ -293,25 +379,34 @@ struct RunIter {
     int64_t lo, hi, chunk, u0 = 0;
     int32_t r = 0, p = -1, at = 0, to = 0;       // run, its next item; the item's tiles that are left
     Run q{};
-    __device__ RunIter(const Args& args, int32_t pair_) : a(args), pair(pair_) {
+    LocalRuns local;
+    __device__ RunIter(const Args& args, int32_t pair_, int32_t pairs) : a(args), pair(pair_) {
+        const int lane = (int)lane_id();
+        if (!a.runs) {
+            share(local.make(a, pairs));
+            if (lo >= hi) return;
+            r = 2 * (__popc(__ballot_sync(0xffffffffu, lane < a.bd.B && local.u <= lo)) - 1);
+            if (__shfl_sync(0xffffffffu, local.ut, r >> 1) <= lo) ++r;
+            q = local.fetch(r);
+            return;
+        }
         // The last run that begins at or before lo: 32 probes at a time, the
         // first on their way with the plan itself.
-        const int lane = (int)lane_id();
         int32_t span = a.runs_total;             // it is one of runs r .. r + span - 1
         for (bool first = true; first || span > 1; first = false) {
             const int32_t step = (span + 31) / 32, i = r + lane * step;
             const int64_t u = lane * step < span ? a.runs[i].u : INT64_MAX;
-            if (first) {
-                const RunPlan pl = *a.rplan;
-                chunk = pl.chunk;
-                lo = min(pl.all, pair * chunk);
-                hi = min(pl.all, lo + chunk);
-            }
+            if (first) share(*a.rplan);
             const int last = __popc(__ballot_sync(0xffffffffu, u <= lo)) - 1;
             r += last * step;
             span = min(step, span - last * step);
         }
         if (lo < hi) q = a.runs[r];
+    }
+    __device__ void share(const RunPlan& pl) {
+        chunk = pl.chunk;
+        lo = min(pl.all, pair * chunk);
+        hi = min(pl.all, lo + chunk);
     }
     __device__ int32_t holder(int64_t u) const { return (int32_t)(u / chunk); }
 
@@ -337,7 +432,7 @@ struct RunIter {
                 return true;
             }
             p = 0;
-            if (++r < a.runs_total) q = a.runs[r];
+            if (++r < a.runs_total) q = a.runs ? a.runs[r] : local.fetch(r);
         }
         return false;
     }
@@ -383,7 +478,7 @@ struct RunIter {
 // tiles alone on the GPU is done soonest in pieces of about sqrt(N / 4)
 // (1 x 8,000 rows: 18.9 us in pieces of 4 tiles, 23.6 of 1; 1 x 1,500: 14.7 in
 // pieces of 1, 16.9 of 2 and of 4).
-__device__ __forceinline__ int least_chunk(int tiles) {
+__device__ int least_chunk(int tiles) {
     int c = 1;
     while (4 * (c + 1) * (c + 1) <= tiles + 2) ++c;
     return c;
@@ -1157,14 +1252,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool more = true;
         int4 meta = make_int4(0, 0, 0, 0);
         if constexpr (kShared) {
-            RunIter it(a, pair);
+            RunIter it(a, pair, pairs);
+            if (!a.runs && a.cut_rows && pair == 0 && rank == 0) {
+                // rows of no sequence: nothing to join
+                for (int32_t row = lane; row < (a.bd.total_q + 31 & ~31); row += 32) {
+                    bool any = false;
+                    for (int b = 0; b < a.bd.B; ++b) {
+                        const int32_t q0 = __shfl_sync(0xffffffffu, it.local.q0, b), nq = __shfl_sync(0xffffffffu, it.local.nq, b);
+                        const int good = __shfl_sync(0xffffffffu, it.local.good ? 1 : 0, b);
+                        any |= good && q0 <= row && row < q0 + nq;
+                    }
+                    if (!any && row < a.bd.total_q) a.cut_rows[row] = make_int2(0, 0);
+                }
+            }
             for (uint32_t n = 0; ok && more; ++n) {
                 more = it.next(s);
                 publish(n, more);
-                if (more && s.ends() && !s.whole()) {
-                    meta = make_int4(s.row, s.rows, it.holder(s.u0 + s.tiles - 1), it.holder(s.u0));
+                if (more && s.ends()) {
+                    const bool cut = !s.whole();
+                    if (cut) meta = make_int4(s.row, s.rows, it.holder(s.u0 + s.tiles - 1), it.holder(s.u0));
                     if (a.cut_rows && s.from_start() && rank == 0 && lane < s.rows)
-                        a.cut_rows[s.row + lane] = make_int2(2 * (pair + 1) + lane, meta.z);
+                        a.cut_rows[s.row + lane] = cut ? make_int2(2 * (pair + 1) + lane, meta.z) : make_int2(0, 0);
                 }
             }
         } else {
@@ -1411,7 +1519,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kMergeBlocks)
 // The same by rows, without the search: for calls of few rows, where the code that
 // a block meets for the first time is what counts (4 rows behind 2,000: 9.1 -> 6.0 us).
 __global__ void __launch_bounds__(32 * kMergeWarps)
-    few_merge_kernel(const int2* __restrict__ rows, const float* __restrict__ part_lse,
+    few_merge_kernel(const int2* __restrict__ rows, int pairs, const float* __restrict__ part_lse,
                      const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
     __shared__ float acc_s[kMergeWarps][18][32];
     const int warp = threadIdx.x >> 5;
@@ -1420,6 +1528,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     const int2 it = rows[blockIdx.x];
     if (it.x == 0) return;                       // a row that one pair has done, or no row
     const int pair = (it.x >> 1) - 1, pieces = it.y - pair + 1;
+    if (pair < 0 || pieces < 2 || it.y >= pairs) return;     // (left by a call that timed out)
     auto at = [&](int e) -> int64_t { return 2 * (2 * ((int64_t)pair + e) + (e == 0 ? 1 : 0)) + (it.x & 1); };
     const int64_t head = (int64_t)blockIdx.x * kH;
     if (pieces > kMergeWarps) {
@@ -1742,10 +1851,8 @@ cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const Pag
     a.status = status;
     a.part_o = reinterpret_cast<float*>(mem + at.o);
     a.part_lse = reinterpret_cast<float*>(mem + at.lse);
-    RunPlan* plan = reinterpret_cast<RunPlan*>(mem + at.plan);
-    Run* runs = reinterpret_cast<Run*>(mem + at.runs);
-    a.rplan = plan;
-    a.runs = runs;
+    a.groups = gr;
+    a.least_shared = least_shared(bd, pairs);
     a.runs_total = 2 * bd.B;
     a.meta = reinterpret_cast<int4*>(mem + at.meta);
     const bool few_rows = bd.total_q <= kFewRows;
@@ -1764,17 +1871,24 @@ cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const Pag
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     const int32_t n = std::max(gr.n, bd.B);
-    const bool few = n <= kPlanThreads;
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(few ? (n + 31) / 32 * 32 : kPlanThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, few ? prefix_plan_kernel<true> : prefix_plan_kernel<false>, bd, gr, plan, runs,
-                           reinterpret_cast<int32_t*>(mem + at.tiles), reinterpret_cast<int32_t*>(mem + at.lead), pairs,
-                           least_shared(bd, pairs), a.cut_rows, status);
-    if (e != cudaSuccess) return e;
-    count_launches(1);
+    // (a launch of its own costs 2-4 us: 4 rows behind 2,000 20.5 -> 18.5, 2 behind 300 18.5 -> 16.6)
+    if (n > 32) {
+        RunPlan* plan = reinterpret_cast<RunPlan*>(mem + at.plan);
+        Run* runs = reinterpret_cast<Run*>(mem + at.runs);
+        a.rplan = plan;
+        a.runs = runs;
+        const bool few = n <= kPlanThreads;
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(few ? (n + 31) / 32 * 32 : kPlanThreads);
+        e = cudaLaunchKernelEx(&cfg, few ? prefix_plan_kernel<true> : prefix_plan_kernel<false>, bd, gr, plan, runs,
+                               reinterpret_cast<int32_t*>(mem + at.tiles), reinterpret_cast<int32_t*>(mem + at.lead), pairs,
+                               a.least_shared, a.cut_rows, status);
+        if (e != cudaSuccess) return e;
+        count_launches(1);
+    }
     cfg.gridDim = dim3(2 * (unsigned)pairs);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
@@ -1784,7 +1898,7 @@ cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const Pag
     cfg.dynamicSmemBytes = 0;
     if (few_rows) {
         cfg.gridDim = dim3((unsigned)bd.total_q, 64);
-        e = cudaLaunchKernelEx(&cfg, few_merge_kernel, (const int2*)a.cut_rows, (const float*)a.part_lse,
+        e = cudaLaunchKernelEx(&cfg, few_merge_kernel, (const int2*)a.cut_rows, pairs, (const float*)a.part_lse,
                                (const float4*)a.part_o, out, lse);
     } else {
         cfg.gridDim = dim3((unsigned)merge_blocks(pairs));

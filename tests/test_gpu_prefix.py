@@ -67,8 +67,12 @@ class Shared(Step):
     ([5, 6, 7], [1, 2, 3], [0, 1, 1, 3], [0, 9, 4]),           # an empty group
     ([384] * 9, [1, 2, 1, 2, 1, 2, 1, 2, 1], [0, 9], [384]),
 ])
-def test_groups(c, m, first, share, page):
-    st = Shared(c, m, first, share, page, seed=len(c) + page)
+@pytest.mark.parametrize("idle", [0, 40])                     # (more than 32 sequences are planned by a launch of their own)
+def test_groups(c, m, first, share, page, idle):
+    seed = len(c) + page
+    if idle:
+        c, m, first, share = c + [3] * idle, m + [0] * idle, first + [len(c) + idle], share + [0]
+    st = Shared(c, m, first, share, page, seed=seed)
     q, kv = st.inputs()
     out, lse = st.prefix(q, kv)
     assert st.status() == 0
@@ -174,9 +178,12 @@ def test_cut_own_parts(b, n, share, own, page):
     ([0, 2, 2], [128, 128]), ([1, 3, 4], [128, 128]), ([0, 3, 2], [128, 128]), ([0, 5, 4], [128, 128]), ([0, -1, 4], [128, 128]),
     ([0, 2, 4], [128, -1]), ([0, 2, 4], [128, 129]), ([0, 2, 4], [400, 128]), ([0, 2, 1 << 30], [128, 128]),
 ])
-def test_wrong_groups_share_nothing(first, share):
+@pytest.mark.parametrize("idle", [0, 40])
+def test_wrong_groups_share_nothing(first, share, idle):
     """Latched, and every sequence gets its attention all the same."""
-    st = Shared([200, 210, 128, 140], [1, 2, 1, 3], [0, 2, 4], [128, 128], 32, seed=6)
+    st = Shared([200, 210, 128, 140] + [2] * idle, [1, 2, 1, 3] + [0] * idle, [0, 2, 4 + idle], [128, 128], 32, seed=6)
+    if idle:
+        first = [x + (idle if 4 <= x <= 5 else 0) for x in first]
     q, kv = st.inputs()
     out, lse = st.prefix(q, kv, groups=st.make_groups(first, share))
     assert st.status() == 6
