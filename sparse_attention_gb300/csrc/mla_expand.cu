@@ -132,9 +132,11 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
 
 // Units of sequence b: none of one that breaks the bounds.
 __device__ __forceinline__ int32_t units_of(const Args& a, int b) {
+    if (b >= a.bd.B) return 0;
     SeqInfo s;
-    if (b >= a.bd.B || !load_seq(a.bd, b, a.status, s) || expanded_at(a.x, b, s.ctx, a.status) < 0) return 0;
-    const int32_t f = first_of(a, b);
+    // with the lengths, not behind them
+    const int32_t lo = __ldg(a.x.off + b), hi = __ldg(a.x.off + b + 1), f = first_of(a, b);
+    if (!load_seq(a.bd, b, a.status, s) || expanded_at(a.x, lo, hi, s.ctx, a.status) < 0) return 0;
     if (f < 0 || f > s.ctx) latch_status(a.status, DSA_ERR_BAD_BATCH);
     if (f < 0 || f >= s.ctx) return 0;
     // 64 bits: a context within 16 of 2^31

@@ -21,10 +21,10 @@ struct ExpandedDev {
     uint16_t* k_pe;
 };
 
-// Where sequence b's expanded rows begin; -1 (and a latched DSA_ERR_BAD_BATCH)
-// if its room is not aligned, leaves the buffers or is too small for ctx rows.
-__device__ __forceinline__ int32_t expanded_at(const ExpandedDev& x, int b, int32_t ctx, int32_t* status) {
-    const int32_t lo = __ldg(x.off + b), hi = __ldg(x.off + b + 1);
+// Where a sequence's expanded rows begin, whose room is lo .. hi; -1 (and a latched
+// DSA_ERR_BAD_BATCH) if that is not aligned, leaves the buffers or is too small for ctx rows.
+__device__ __forceinline__ int32_t expanded_at(const ExpandedDev& x, int32_t lo, int32_t hi, int32_t ctx,
+                                               int32_t* status) {
     const int64_t need = ((int64_t)ctx + kExpRoom - 1) / kExpRoom * kExpRoom;
     if (lo >= 0 && lo % kExpRoom == 0 && hi <= x.rows && (int64_t)hi - lo >= need) return lo;
     latch_status(status, DSA_ERR_BAD_BATCH);

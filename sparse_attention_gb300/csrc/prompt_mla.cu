@@ -122,9 +122,11 @@ struct Args {
 // Sequence b: its first new row, how many there are, its length, and where its
 // expanded rows begin; no new rows for one that breaks the bounds.
 __device__ __forceinline__ int4 sequence(const BatchDev& bd, const ExpandedDev& x, int b, int32_t* status) {
+    if (b >= bd.B) return make_int4(0, 0, 0, 0);
     SeqInfo s;
-    if (b >= bd.B || !load_seq(bd, b, status, s) || s.nq == 0) return make_int4(0, 0, 0, 0);
-    const int32_t at = expanded_at(x, b, s.ctx, status);
+    const int32_t lo = __ldg(x.off + b), hi = __ldg(x.off + b + 1);      // with the lengths, not behind them
+    if (!load_seq(bd, b, status, s) || s.nq == 0) return make_int4(0, 0, 0, 0);
+    const int32_t at = expanded_at(x, lo, hi, s.ctx, status);
     return at < 0 ? make_int4(0, 0, 0, 0) : make_int4(s.q0, s.nq, s.ctx, at);
 }
 template <int R>

@@ -42,8 +42,9 @@ __global__ void __launch_bounds__(32 * kWarps)
     pdl_launch_dependents();
     pdl_wait();
     SeqInfo s;
+    const int32_t lo = __ldg(x.off + b), hi = __ldg(x.off + b + 1);      // with the lengths, not behind them
     if (!load_seq(bd, b, status, s) || s.nq <= i0) return;
-    const int32_t at = expanded_at(x, b, s.ctx, status);
+    const int32_t at = expanded_at(x, lo, hi, s.ctx, status);
     if (at < 0) return;
     const int32_t rows = min(kRows, s.nq - i0), pos = s.ctx - s.nq + i0;     // of the first row
     // lanes 0 .. 23 hold a key's own columns, 24 .. 31 the shared ones
