@@ -78,7 +78,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTile = 128;                   // positions per tile
 constexpr int kItemCost = 3;                 // an item's start and end, in tiles
 constexpr int kApartUnits = 6;               // units a pair that are little work
-constexpr int kFewRows = 16;                 // rows of a call up to which a merge goes by rows
+constexpr int kFewRows = 64;                 // rows of a call up to which a merge goes by rows
 constexpr int kThreads = 288;
 constexpr int kChunkBytes = 64 * 128;        // 64 rows x 64 dims
 constexpr int kQChunks = kDQK / 64;          // 9
@@ -1517,7 +1517,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kMergeBlocks)
 }
 
 // The same by rows, without the search: for calls of few rows, where the code that
-// a block meets for the first time is what counts (4 rows behind 2,000: 9.1 -> 6.0 us).
+// a block meets for the first time is what counts (4 rows behind 2,000: 9.1 -> 6.0 us;
+// whole calls of 49 behind 28 22.1 -> 20.5, 55 behind 1,931 34.9 -> 33.0).
 __global__ void __launch_bounds__(32 * kMergeWarps)
     few_merge_kernel(const int2* __restrict__ rows, int pairs, const float* __restrict__ part_lse,
                      const float4* __restrict__ part_o, uint16_t* __restrict__ out, float* __restrict__ lse) {
@@ -1897,7 +1898,9 @@ cudaError_t launch_prefix_mla(const BatchDev& bd, const GroupsDev& gr, const Pag
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.dynamicSmemBytes = 0;
     if (few_rows) {
-        cfg.gridDim = dim3((unsigned)bd.total_q, 64);
+        // (a wave of blocks)
+        const int units = (kMergeBlocks * num_sms() / bd.total_q + kMergeWarps - 1) / kMergeWarps * kMergeWarps;
+        cfg.gridDim = dim3((unsigned)bd.total_q, std::clamp(units, kMergeWarps, 64));
         e = cudaLaunchKernelEx(&cfg, few_merge_kernel, (const int2*)a.cut_rows, pairs, (const float*)a.part_lse,
                                (const float4*)a.part_o, out, lse);
     } else {
