@@ -1683,9 +1683,9 @@ __global__ void __launch_bounds__(kPlanThreads)
 // Tiles that a group has to share for items of two sequences.  Such an item
 // spares the second its walk over the shared tiles, but takes the own tiles of both
 // in turn, with the end of each (see the fix-up).  Where there is little work for
-// every pair, only if the shared tiles are half of the longest cache (12 rows
-// behind 440, 542 of their own: 20.8 us apart, 26.9 together; 4 behind 2,000, 40 of
-// their own: 21.9 and 20.5).
+// every pair, only if the shared tiles are half of the longest cache (15 rows in 4
+// groups behind 188, 586 of their own: 20.6 us apart, 22.5 together; 4 behind 2,000, 40
+// of their own: 20.4 and 18.5).
 int least_shared(const BatchDev& bd, int pairs) {
     const int64_t items = ((int64_t)bd.total_q + std::min(bd.total_q, bd.B)) / 2;
     const int tiles = (bd.max_ctx + kTile - 1) / kTile;
