@@ -610,8 +610,8 @@ DSA_API dsa_status dsa_prompt_mla_fwd(const dsa_batch* batch, const uint16_t* q,
 DSA_API dsa_status dsa_mla_o_proj(int32_t total_q, const uint16_t* o_mid, const uint16_t* w_o, uint16_t* y, void* ws,
                                   size_t ws_bytes, void* stream);
 
-/* Groups of consecutive sequences that share their first rows.  off (DEVICE
- * int32 [groups + 1]): group g is sequences off[g] .. off[g+1] - 1; off[0] = 0,
+/* Groups of consecutive sequences that share their first rows, 1 to `batch` of
+ * them.  off (DEVICE int32 [groups + 1]): group g is sequences off[g] .. off[g+1] - 1; off[0] = 0,
  * ascending, off[groups] = batch.  shared (DEVICE int32 [groups]): the first
  * shared[g] positions of every sequence of group g that has new rows hold the same
  * rows, and at most its ctx_len[b] - n_b.  A sequence without a common prefix is a
