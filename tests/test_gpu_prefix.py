@@ -246,6 +246,24 @@ def test_many_sequences():
     check_attention(st, q, kv, out, lse)
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(seed):
+    rng = np.random.default_rng(100 + seed)
+    c, m, first, share = [], [], [0], []
+    for _ in range(int(rng.integers(1, 6))):
+        share.append(int(rng.choice([0, 5, 127, 128, 256, 300, 700, 1500])))
+        for _ in range(int(rng.integers(1, 13))):
+            c.append(share[-1] + int(rng.choice([0, 1, 3, 60, 127, 128, 129, 400])))
+            m.append(int(rng.choice([0, 1, 1, 1, 1, 2, 3, 5, 16, 64])))
+        first.append(len(c))
+    m[0] = max(m[0], 1)
+    st = Shared(c, m, first, share, int(rng.choice([0, 16, 32, 64, 256])), seed=seed)
+    q, kv = st.inputs()
+    out, lse = st.prefix(q, kv)
+    assert st.status() == 0
+    check_attention(st, q, kv, out, lse, rows=set(int(x) for x in rng.integers(0, st.T, 40)))
+
+
 def test_every_sequence_a_group():
     B = 300
     rng = np.random.default_rng(4)

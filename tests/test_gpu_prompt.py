@@ -212,6 +212,24 @@ def test_moving_maxima():
         assert ((lse[at][:, [0, 5, 63]].cpu().double() - z).abs() <= e + 16 * F32 * (1 + z.abs())).all()
 
 
+@pytest.mark.parametrize("most", [128, 300])              # the bound on new rows chooses the kernel
+@pytest.mark.parametrize("seed", range(5))
+def test_random_batches(seed, most):
+    rng = np.random.default_rng(200 + seed)
+    n = int(rng.integers(1, 20))
+    c = [int(x) for x in rng.choice([0, 0, 1, 5, 30, 63, 64, 100, 127, 128, 200, 500], n)]
+    m = [int(x) for x in rng.choice([0, 1, 2, 5, 16, 17, 31, 32, 33, 48, 63, 64, 65, 90, 96, 97, 127, 128], n)]
+    m[0] = max(m[0], 1)
+    P = Prompts(c, m, seed=seed, gap=128, max_q=most, max_ctx=5000)
+    x = P.filled()
+    q = P.normal(P.T, H, D_HEAD).cuda()
+    out = torch.empty((P.T, H, D_HEAD), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((P.T, H), device="cuda")
+    dsa.prompt_mla_fwd(P.batch, q, x, SCALE, out, lse, ws=P.ws)
+    assert dsa.read_device_status(P.ws) == 0
+    check_attention(P, q, x, out, lse, heads=sorted(set(int(v) for v in rng.integers(0, H, 4))))
+
+
 def test_many_items_of_few_rows():
     """More items than CTA pairs, of one to many tiles in turn, and rows at the ends of what a CTA and a warp hold."""
     c = [0, 900, 0, 64, 300, 0, 127, 40, 1500, 2, 250, 0, 129, 88]
