@@ -712,6 +712,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     uint32_t o[32];
                     tmem_ld_32x32b_x32(tl + kOCol + kOCols * ob + c, o);
                     tmem_ld_wait();
+                    if (c == kOCols - 32) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_pair(lead(S.ofree[ob]));
+                    }
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
                         uint32_t w[8], in[4];
@@ -730,9 +735,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_pair(lead(S.ofree[ob]));
+            if (!(ok && live > 0)) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(lead(S.ofree[ob]));
+            }
             ++seg;
         }
     } else {
@@ -759,6 +765,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_ld_32x32b_x32(tl + kOCol + c, o[0]);
                     tmem_ld_32x32b_x32(tl + kOCol + c + 32, o[1]);
                     tmem_ld_wait();
+                    if (c == 192) {              // O is free before its last columns are written
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_pair(lead(S.ofree[0]));
+                    }
 #pragma unroll
                     for (int v = 0; v < 8; ++v) {
                         uint32_t w[4];
@@ -780,10 +791,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive_pair(lead(S.ofree[0]));
+            if (!(ok && live > 0)) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(lead(S.ofree[0]));
             }
             ++seg;
         }
