@@ -96,7 +96,7 @@ struct Smem {
     alignas(1024) uint8_t v[kStages * 2 * kQBytes];      // two blocks of 64 columns x 128 positions
     alignas(1024) uint8_t out[kOutWarps * 4096];         // results on their way out; kFew: P, two blocks of 64 rows x 64 positions
     alignas(8) uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
-    uint64_t qfull[kQChunks], qempty[kQChunks], sfull[2], pfull[2], pvdone[2], odone[2], lfull[2], invfree[2], ofree[2], itemfull[kMaxSlots], itemempty[kMaxSlots];
+    uint64_t qfull[kQChunks], qempty[kQChunks], sfull[2], pfull[2], pvdone[2], odone[2], lfull[2], invfree[2], ofree[2], followed[2], itemfull[kMaxSlots], itemempty[kMaxSlots];
     uint64_t numfull[kMaxSlots], numempty[kMaxSlots];          // item numbers on their way to rank 1
     Item item[kMaxSlots];
     uint32_t number[kMaxSlots];
@@ -230,6 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&S.invfree[i]), kOutWarps);
             mbar_init(smem_u32(&S.odone[i]), 1);
             mbar_init(smem_u32(&S.ofree[i]), 2 * kOutWarps);
+            if (kFew) mbar_init(smem_u32(&S.followed[i]), kSoftWarps / 2);
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_u32(&S.itemfull[i]), 1);
@@ -511,8 +512,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         for (; !named_bar_or(1 + mine, 128, !next_item(it)); ++seg) {
             if ((int)(seg & 1) != mine) {
-                // (a barrier's parity tells only two tiles apart)
-                for (int32_t t = 0; t < it.tiles; ++t, ++g) wait(S.sfull[g & 1], (g >> 1) & 1);
+                // The other group's item.  Nothing holds its S back for this group, and a
+                // barrier's parity tells only two phases apart, so this group does not
+                // watch them: the other one signals when its item's last S is done.  (Its next
+                // signal comes behind this group's next item, so these phases cannot pass unseen.)
+                wait(S.followed[mine ^ 1], (seg >> 1) & 1);
+                g += it.tiles;
                 continue;
             }
             const int32_t first = it.pos + kMine * (int)rank;    // position of the CTA's first row
@@ -524,6 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 wait(S.sfull[buf], (g >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
+                if (t + 1 == it.tiles && lane == 0) mbar_arrive(smem_u32(&S.followed[mine]));
                 if (idle) {
                     // (what P holds there becomes nobody's lanes of O)
                     exchange(0.f);
