@@ -555,7 +555,9 @@ DSA_API dsa_status dsa_rope(int32_t total_q, int32_t heads, int32_t dim, const u
  * off (DEVICE int32 [batch + 1]) is ascending, each sequence's begin a
  * multiple of 128 and its room off[b+1] - off[b] at least ctx_len[b] rounded up
  * to a multiple of 128, off[batch] <= rows; a sequence that breaks this is skipped and
- * DSA_ERR_BAD_BATCH latched. */
+ * DSA_ERR_BAD_BATCH latched.  Without any rows (rows = 0; kv and k_pe may be NULL)
+ * dsa_prompt_mla_fwd does the same, and dsa_mla_expand, which has nowhere to
+ * write, returns at once and latches nothing. */
 typedef struct dsa_expanded {
     int32_t rows;
     const int32_t* off;

@@ -117,8 +117,9 @@ dsa_status dsa_prompt_mla_fwd(const dsa_batch* batch, const uint16_t* q, const d
     if (st != DSA_OK || (st = check(expanded)) != DSA_OK) return st;
     if (check_ws(ws, ws_bytes, prompt_ws(batch)) != DSA_OK) return DSA_ERR_WORKSPACE;
     if (!positive(sm_scale)) return DSA_ERR_INVALID_ARG;
-    if (batch->total_q == 0 || batch->max_q == 0 || batch->max_ctx == 0 || expanded->rows == 0) return DSA_OK;
-    if (!given(q) || !given(out) || !aligned(lse, 16)) return DSA_ERR_INVALID_ARG;
+    if (batch->total_q == 0 || batch->max_q == 0 || batch->max_ctx == 0) return DSA_OK;
+    // (without expanded rows the call only finds the sequences that have new ones)
+    if (expanded->rows > 0 && (!given(q) || !given(out) || !aligned(lse, 16))) return DSA_ERR_INVALID_ARG;
     return cuda_status(launch_prompt_mla(to_dev(batch), q, to_dev(expanded), sm_scale, out, lse, scratch_of(ws),
                                          static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)));
 }

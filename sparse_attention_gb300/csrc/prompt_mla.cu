@@ -922,7 +922,8 @@ cudaError_t launch(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, 
 // By the bounds on new rows and lengths alone, so that a captured call serves others.
 cudaError_t launch_prompt_mla(const BatchDev& bd, const uint16_t* q, const ExpandedDev& x, float sm_scale,
                               uint16_t* out, float* lse, void* scratch, int32_t* status, cudaStream_t stream) {
-    if (prompt_rows_suit(bd)) return launch_prompt_rows(bd, q, x, sm_scale, out, lse, status, stream);
+    // no expanded rows: no room holds a sequence, which that kernel's first blocks latch
+    if (x.rows == 0 || prompt_rows_suit(bd)) return launch_prompt_rows(bd, q, x, sm_scale, out, lse, status, stream);
     return bd.max_q <= kFewRows ? launch<true>(bd, q, x, sm_scale, out, lse, scratch, status, stream)
                                 : launch<false>(bd, q, x, sm_scale, out, lse, scratch, status, stream);
 }

@@ -150,7 +150,9 @@ cudaError_t launch_prompt_rows(const BatchDev& bd, const uint16_t* q, const Expa
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kH / kWarps, (unsigned)bd.B, (unsigned)((bd.max_q + kRows - 1) / kRows));
+    // (without expanded rows a sequence's first block says all)
+    cfg.gridDim = x.rows == 0 ? dim3(1, (unsigned)bd.B, 1)
+                              : dim3(kH / kWarps, (unsigned)bd.B, (unsigned)((bd.max_q + kRows - 1) / kRows));
     cfg.blockDim = dim3(32 * kWarps);
     cfg.stream = stream;
     cfg.attrs = attr;
