@@ -532,7 +532,7 @@ DSA_API dsa_status dsa_rope_table(int32_t rows, int32_t first, int32_t dim, doub
  * for i < dim/2 and (a, b) = (i, i + dim/2) or, with DSA_ROPE_NEIGHBOUR,
  * (2i, 2i + 1).  fp32 arithmetic, one rounding to bf16.
  *   x, out   bf16 (DEVICE), element (t, h, i) at t * token + h * head + i;
- *            strides >= 0 and multiples of 8; point at the first rotated column.
+ *            strides multiples of 8, 0 .. 2^36; point at the first rotated column.
  *            out = x with the same strides rotates in place; otherwise the
  *            two may not overlap (from first to last element), and no two
  *            elements of out may share a place.
@@ -541,7 +541,7 @@ DSA_API dsa_status dsa_rope_table(int32_t rows, int32_t first, int32_t dim, doub
  *            value outside [0, table_rows) does too and latches DSA_ERR_BAD_INDEX
  *   flags    DSA_ROPE_*
  * ws: at least 256 bytes.  dim a multiple of 16, 16 .. 256; total_q < 2^26;
- * heads >= 1. */
+ * heads 1 .. 65,536. */
 DSA_API dsa_status dsa_rope(int32_t total_q, int32_t heads, int32_t dim, const uint16_t* x, int64_t x_token,
                             int64_t x_head, const float* cos, const float* sin, int32_t table_rows,
                             const int32_t* positions, int32_t flags, uint16_t* out, int64_t out_token,

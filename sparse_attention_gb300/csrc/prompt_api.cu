@@ -13,14 +13,19 @@ namespace {
 
 bool good_dim(int32_t dim) { return dim >= 16 && dim <= DSA_MAX_ROPE_DIM && dim % 16 == 0; }
 
-// Bytes from a tensor's first element to behind its last.
-int64_t extent(int32_t tokens, int64_t token, int32_t heads, int64_t head, int32_t dim) {
-    return 2 * ((tokens - 1) * token + (heads - 1) * head + dim);
+constexpr int64_t kMaxStride = int64_t(1) << 36;
+constexpr int32_t kMaxRopeHeads = 1 << 16;
+
+// Bytes from a tensor's first element to behind its last.  Unsigned: 2^26 tokens and
+// 2^16 heads at the largest strides span 2^63 + 2^53 bytes.
+uint64_t extent(int32_t tokens, int64_t token, int32_t heads, int64_t head, int32_t dim) {
+    return 2 * ((uint64_t)(tokens - 1) * (uint64_t)token + (uint64_t)(heads - 1) * (uint64_t)head + (uint64_t)dim);
 }
 
-bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+// (addresses stay below 2^57, so the sums stay below 2^64)
+bool overlap(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes) {
+    const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + b_bytes && y < x + a_bytes;
 }
 
 // The two calls of the expanded form run one after another in their stream, so
@@ -58,7 +63,7 @@ dsa_status dsa_rope_table(int32_t rows, int32_t first, int32_t dim, double base,
     }
     if (rows == 0) return DSA_OK;
     if (!given(cos_t) || !given(sin_t)) return DSA_ERR_INVALID_ARG;
-    const int64_t bytes = (int64_t)rows * dim * 4;
+    const uint64_t bytes = (uint64_t)rows * (uint64_t)dim * 4;
     if (overlap(cos_t, bytes, sin_t, bytes)) return DSA_ERR_INVALID_ARG;
     return cuda_status(launch_rope_table(rows, first, dim, base, scaling, cos_t, sin_t,
                                          static_cast<cudaStream_t>(stream)));
@@ -68,13 +73,13 @@ dsa_status dsa_rope(int32_t total_q, int32_t heads, int32_t dim, const uint16_t*
                     const float* cos_t, const float* sin_t, int32_t table_rows, const int32_t* positions,
                     int32_t flags, uint16_t* out, int64_t out_token, int64_t out_head, void* ws, size_t ws_bytes,
                     void* stream) {
-    if (total_q < 0 || total_q >= (1 << 26) || heads < 1 || heads > (1 << 16) || !good_dim(dim)) return DSA_ERR_INVALID_ARG;
+    if (total_q < 0 || total_q >= (1 << 26) || heads < 1 || heads > kMaxRopeHeads || !good_dim(dim)) return DSA_ERR_INVALID_ARG;
     if (table_rows < 0 || (flags & ~(DSA_ROPE_NEIGHBOUR | DSA_ROPE_INVERSE))) return DSA_ERR_INVALID_ARG;
     if (check_ws(ws, ws_bytes, with_header(0)) != DSA_OK) return DSA_ERR_WORKSPACE;
     if (total_q == 0) return DSA_OK;
     if (!given(x) || !given(out) || !given(cos_t) || !given(sin_t) || !given(positions, 4)) return DSA_ERR_INVALID_ARG;
     for (int64_t s : {x_token, x_head, out_token, out_head})
-        if (s < 0 || s % 8 != 0 || s > (int64_t(1) << 36)) return DSA_ERR_INVALID_ARG;
+        if (s < 0 || s % 8 != 0 || s > kMaxStride) return DSA_ERR_INVALID_ARG;
     // tokens of whole heads, or heads of whole tokens
     const bool by_token = (heads == 1 || out_head >= dim) &&
                           (total_q == 1 || out_token >= (heads - 1) * out_head + dim);
