@@ -54,8 +54,7 @@
 // softmax of that.  Measured, in single calls and in a loop that the power cap
 // slows: 16,384 tokens 4.35-4.40 ms = 2,000-2,020 TFLOP/s (cuBLAS 1,921) and
 // 5.0-5.05 ms = 1,740-1,760 (1,730 sustained); 12 prompts of 839 to 2,012 tokens
-// 0.60 ms and 0.68-0.72, 401 tiles a pair for the 319 that the mask leaves;
-// 100 tokens 10 us.
+// 0.59-0.60 ms and 0.68-0.72, 401 tiles a pair for the 319 that the mask leaves.
 #include <algorithm>
 #include <atomic>
 
@@ -182,9 +181,9 @@ __device__ __forceinline__ Item item_of(const Args& a, const Smem& S, uint32_t n
 // warps an item in turn.  P goes through shared memory (as A in TMEM it would
 // need its rows once in each half of the lanes).  Pairs take every pairs-th item instead of asking
 // (an answer takes 2 us, a short item 1.4).  Taken where the bound on new rows is 128 and below (28
-// prompts of 20 to 49 tokens 41 us, 76 without; 32 of 32 45, 84 without; 8 of 8 behind
-// 445 31, 38 without; 32 of 128 96, 101 without; one of 100 10.3, 12.4; 32 of 33 to 100 behind up
-// to 1,000 227, 242 without: HBM).
+// prompts of 20 to 49 tokens 41-43 us, 75 without; 32 of 32 45, 83 without; 8 of 8 behind
+// 445 31, 38 without; 32 of 128 94-96, 101 without; one of 100 10.3, 12.4; 32 of 33 to 100 behind up
+// to 1,000 224-227, 242 without: HBM).
 template <bool kFew>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prompt_mla_kernel(const Args a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

@@ -33,8 +33,10 @@ struct Turns {
 };
 
 // cos and sin of phase / 2^64 turns: within an eighth of a turn of a quarter,
-// so the first six terms of the Taylor series leave 2e-9 of a sine and 1e-10
-// of a cosine.
+// so the Taylor series' first five terms leave 1.8e-9 of a sine, its first six 1.2e-10
+// of a cosine.  With the fp32 roundings (three in x, one at the end, the inner
+// ones weighed by what their terms add) either is off by at most 4.4 x 2^-24 of its
+// size; mscale's own rounding and its product add a 2^-24 each.
 __device__ __forceinline__ void turn(uint64_t phase, float& c, float& s) {
     const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
     const int64_t rest = (int64_t)(phase - ((uint64_t)quarter << 62));
@@ -256,7 +258,9 @@ cudaError_t launch_rope(int32_t total_q, int32_t heads, int32_t dim, const uint1
     a.pieces = dim / 16;
     a.sign = inverse ? -1.f : 1.f;
     a.status = status;
-    // few tokens: more threads in flight; many: fewer reads of the table
+    // Few tokens: more threads in flight; many: fewer reads of the table.  Rows of 64
+    // heads x 64 columns, one and four heads a thread: 64 tokens 1.5 and 2.2 us, 2,048 6.9
+    // and 7.7, 4,864 (the border) 14.4 and 14.7, 9,728 28.7 and 27.7, 32,768 89.3 and 82.0.
     const bool few = (int64_t)total_q * heads * a.pieces < (int64_t)4 * 2048 * num_sms();
     if (neighbour) return few ? launch<true, 1>(a, stream) : launch<true, 4>(a, stream);
     return few ? launch<false, 1>(a, stream) : launch<false, 4>(a, stream);

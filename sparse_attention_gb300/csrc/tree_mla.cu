@@ -712,8 +712,8 @@ __device__ __noinline__ bool any_not_finite(const Args& a, const S& s, uint64_t 
 // tile; with K boxes of one group, 24 and 16, 155 instead of 141 us for 40
 // rows in 5 groups of 6 behind 12,001).
 //
-// kShared: behind shared prefixes.  The work is the runs that prefix_plan_kernel
-// wrote.  Over the own tiles of one of an item's two sequences the other CTA's
+// kShared: behind shared prefixes.  The work is runs: those that prefix_plan_kernel
+// wrote, or, for at most 32 sequences, the walker's own (LocalRuns).  Over the own tiles of one of an item's two sequences the other CTA's
 // lanes of O are left out of the product (0 * NaN is NaN).
 template <int kRows, bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -1683,9 +1683,12 @@ __global__ void __launch_bounds__(kPlanThreads)
 // Tiles that a group has to share for items of two sequences.  Such an item
 // spares the second its walk over the shared tiles, but takes the own tiles of both
 // in turn, with the end of each (see the fix-up).  Where there is little work for
-// every pair, only if the shared tiles are half of the longest cache (15 rows in 4
-// groups behind 188, 586 of their own: 20.6 us apart, 22.5 together; 4 behind 2,000, 40
-// of their own: 20.4 and 18.5).
+// every pair, only if the shared tiles are half of the longest cache.  Apart and
+// together, one call after another: 15 rows in 4 groups behind up to 188, up to 586 of their
+// own, 16.6 and 17.0 us; 8 in 2 groups behind 1,000, 1,000 of their own, 17.5 and 18.8; 4 behind
+// 2,000, 40 or 1,500 of their own, 18.9 and 18.0, 17.3 and 16.3.  It is a rule of thumb: 24
+// behind 400, 300 of their own, would be faster together (17.8 and 17.1), 3 x 5 behind
+// 1,500 and 6 x 3 behind 700 apart (15.4 and 16.6, 16.0 and 16.9).
 int least_shared(const BatchDev& bd, int pairs) {
     const int64_t items = ((int64_t)bd.total_q + std::min(bd.total_q, bd.B)) / 2;
     const int tiles = (bd.max_ctx + kTile - 1) / kTile;
